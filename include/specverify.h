@@ -77,7 +77,8 @@ typedef enum {
     SPEC_ECUDA = 2,    /* a CUDA launch or attribute call failed */
     SPEC_ETIMEOUT = 3, /* (status[] only) a bounded device wait gave up */
     SPEC_EDATA = 4,    /* (status[] only) bad logits, tokens or tree */
-    SPEC_EBOUNDS = 5   /* (status[] only, debug builds) an index check failed; the access was skipped */
+    SPEC_EBOUNDS = 5,  /* (status[] only, debug builds) an index check failed; the access was skipped */
+    SPEC_ENOPAGES = 6  /* (status[] only) too few free pages; that sequence was left as it was */
 } spec_status;
 
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
@@ -107,7 +108,11 @@ enum {
     SPEC_MAX_TREE_C = 1024,   /* tree construction: candidates per sequence */
     SPEC_MAX_TREE_L = 32,     /*                    tokens per candidate */
     SPEC_MAX_TREE_CL = 4096,  /*                    candidates x tokens */
-    SPEC_TREE_MAX_COUNT = 1 << 20  /* multiplicities are below this */
+    SPEC_TREE_MAX_COUNT = 1 << 20, /* multiplicities are below this */
+    SPEC_MAX_HEAD_DIM = 256,  /* paged cache: elements of a head */
+    SPEC_MAX_PAGE = 256,      /*              tokens of a page */
+    SPEC_MAX_GROUP = 128,     /*              query heads on one key / value head */
+    SPEC_MAX_POOL_SEQS = 4096 /*              sequences of one resize or fork */
 };
 
 /* ------------------------------------------------------------------------
@@ -362,6 +367,144 @@ spec_status spec_verify_noalloc(const void* target, const void* draft, spec_dtyp
                                 spec_sampling sampling, uint64_t seed, uint64_t offset,
                                 int32_t* accepted, int32_t* tokens, int32_t* next_token,
                                 int32_t* status, float* probs_dbg, spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * The paged key / value cache of the target model. A verification step reads
+ * and extends it: spec_cache_append writes the drafted nodes' keys and values,
+ * spec_tree_attention lets the nodes attend to the context and to their
+ * ancestors, and after spec_verify / spec_verify_tree spec_cache_compact keeps
+ * the accepted path. ([REST] "REST: 基于检索的投机解码" scores a draft tree in
+ * one pass of the target with a tree attention mask; the cache is how a
+ * serving engine holds that pass's context.)
+ *
+ * A page holds page_size consecutive positions of one sequence. Position t of
+ * sequence b is slot t % page_size of page page_table[b][t / page_size]; the
+ * row of head h there starts at
+ *   page * page_stride + slot * token_stride + h * head_stride   (elements)
+ * in k and in v (layer y: + y * layer_stride), head_dim elements long.
+ * page_table rows are table_stride entries apart and max_pages long; entries
+ * that a sequence does not hold are -1. page_refs[page] counts the table
+ * entries that name a page; a page is free iff its count is 0.
+ *
+ * Limits: k and v 16-byte aligned, every stride a multiple of 16 bytes;
+ * page_size a power of two in 8 .. SPEC_MAX_PAGE; head_dim a multiple of 8,
+ * at most SPEC_MAX_HEAD_DIM; 1 <= B <= 65535. The struct itself is host
+ * memory, read during the call.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    void* k;
+    void* v;
+    int32_t layers, num_pages, page_size, kv_heads, head_dim;
+    int64_t layer_stride, page_stride, token_stride, head_stride; /* elements */
+} spec_cache;
+
+/* ------------------------------------------------------------------------
+ * spec_tree_attention - attention of the drafted nodes over one layer's cache.
+ * With L = cache_len[b], n = n_nodes[b] and head h of q on key / value head
+ * h / (q_heads / kv_heads):
+ *   out[b, i, h] = sum_t p_t v_t,   p_t = exp(scale q_i . k_t - lse[b, i, h]),
+ *   lse[b, i, h] = log sum_t exp(scale q_i . k_t)
+ * over the positions t < L and the nodes' positions L + j, j < n, that node i
+ * sees: mask[b][i][j] != 0, or j <= i where mask is NULL (a drafted chain; one
+ * token of plain decoding is N = 1).
+ *
+ *   q             [B, N, q_heads, head_dim], 16-byte aligned
+ *   cache         layers == 1; the nodes' own keys and values are already in it
+ *   page_table, table_stride, max_pages, cache_len [B] as above
+ *   mask          [B, N, N] uint8 (spec_tree_build's), or NULL
+ *   n_nodes       [B] int32 in 0 .. N, or NULL: N for every sequence
+ *   N             1 .. SPEC_MAX_TREE_N; q_heads a multiple of kv_heads, at most
+ *                 SPEC_MAX_GROUP times it
+ *   scale         finite
+ * Outputs:
+ *   out           [B, N, q_heads, head_dim], 16-byte aligned, q's type; zero
+ *                 for nodes i >= n and for a node that sees nothing
+ *   lse           [B, N, q_heads] float (NULL allowed); -inf for those
+ *   status        [B] SPEC_OK, or SPEC_EDATA for a length, node count or page
+ *                 out of range (that sequence's outputs are NaN); NULL allowed
+ * Scores, sums and the softmax's statistics are fp32 for both types; bf16
+ * weights are rounded to bf16 before they multiply v. What lies in unseen
+ * positions (NaN and infinities too) does not reach the outputs.
+ * ---------------------------------------------------------------------- */
+size_t spec_tree_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim, spec_dtype dtype);
+
+spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dtype dtype,
+                                const int32_t* page_table, int64_t table_stride, int max_pages,
+                                const int32_t* cache_len, const uint8_t* mask, const int32_t* n_nodes,
+                                int B, int N, int q_heads, float scale, void* out, float* lse, int32_t* status,
+                                void* workspace, size_t ws_bytes, spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_cache_append - write n_nodes[b] (NULL: N) new tokens' keys and values,
+ * k and v [B, N, kv_heads, head_dim] (16-byte aligned), to positions
+ * cache_len[b] + i of one layer (layers == 1). cache_len itself is not
+ * changed. The pages must be the sequence's already (spec_cache_resize).
+ *   status        [B] SPEC_OK, or SPEC_EDATA for a length, node count or page
+ *                 out of range (nothing is written); NULL allowed
+ * 1 <= N <= 2^20.
+ * ---------------------------------------------------------------------- */
+spec_status spec_cache_append(const void* k, const void* v, const spec_cache* cache, spec_dtype dtype,
+                              const int32_t* page_table, int64_t table_stride, int max_pages,
+                              const int32_t* cache_len, const int32_t* n_nodes, int B, int N, int32_t* status,
+                              spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_cache_compact - after verification: the entries of the accepted path's
+ * nodes moved to the positions after the context, in every layer,
+ *   position L + i  <-  position L + path_nodes[b][i],   i <= accept_len[b],
+ * and the new length L + accept_len[b] + 1 (the root, node 0, is the path's
+ * first node and context from now on).
+ *   accept_len    [B] int32 (spec_verify_tree's accept_len, spec_verify's
+ *                 accepted)
+ *   path_nodes    [B, W] int32 (spec_verify_tree's), ascending from 0; NULL
+ *                 for a chain, whose accepted entries are in place already
+ *   W             1 .. SPEC_MAX_TREE_N, above every accept_len
+ *   new_len       [B] int32 (must not overlap cache_len); -1 on SPEC_EDATA
+ *   status        [B] SPEC_OK, or SPEC_EDATA for a length, path or page out of
+ *                 range (nothing moves); NULL allowed
+ * ---------------------------------------------------------------------- */
+spec_status spec_cache_compact(const spec_cache* cache, spec_dtype dtype, const int32_t* page_table,
+                               int64_t table_stride, int max_pages, const int32_t* cache_len,
+                               const int32_t* accept_len, const int32_t* path_nodes, int B, int W,
+                               int32_t* new_len, int32_t* status, spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_cache_resize - the number of pages that sequences hold: sequence
+ * seqs[f] (NULL: f) afterwards holds ceil(tokens[f] / page_size) pages.
+ * Released pages lose one reference each; new ones are the free pages of the
+ * lowest numbers, in the order of f, and pages released in the same call can
+ * be taken by it. tokens[f] = 0 frees a sequence.
+ *   page_table    [S] rows (S = num_seqs), changed in place
+ *   page_refs     [num_pages] int32, changed in place
+ *   seqs          [F] int32, distinct, or NULL; 1 <= F <= SPEC_MAX_POOL_SEQS
+ *   status        [F] SPEC_OK; SPEC_EDATA for a sequence, token count or held
+ *                 page out of range; SPEC_ENOPAGES where the free pages do not
+ *                 reach for it beside the growing sequences before it (both:
+ *                 that sequence is left as it was); NULL allowed
+ * ---------------------------------------------------------------------- */
+spec_status spec_cache_resize(int32_t* page_table, int64_t table_stride, int max_pages, int num_seqs,
+                              int32_t* page_refs, int num_pages, int page_size, const int32_t* seqs,
+                              const int32_t* tokens, int F, int32_t* status, spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_cache_fork - sequence dst[f] becomes a copy of sequence src[f]: it
+ * shares every full page (one reference more each) and gets a page of its own,
+ * the lowest free one in the order of f, for the last page if that is partly
+ * filled, whose used slots are copied in every layer. cache_len[dst[f]] is
+ * set. A source may be forked several times in one call; the dst are distinct
+ * and hold no pages.
+ *   cache_len     [S] int32, changed in place; page_table, page_refs as above
+ *   status        [F] SPEC_OK; SPEC_EDATA for a sequence, length or page out of
+ *                 range, src[f] == dst[f], or a dst that holds pages;
+ *                 SPEC_ENOPAGES (both: dst is left as it was); NULL allowed
+ *   workspace     >= spec_cache_fork_workspace_size(F) bytes
+ * ---------------------------------------------------------------------- */
+size_t spec_cache_fork_workspace_size(int F);
+
+spec_status spec_cache_fork(const spec_cache* cache, spec_dtype dtype, int32_t* page_table, int64_t table_stride,
+                            int max_pages, int num_seqs, int32_t* page_refs, int32_t* cache_len, const int32_t* src,
+                            const int32_t* dst, int F, int32_t* status, void* workspace, size_t ws_bytes,
+                            spec_stream stream);
 
 /* Human-readable name of a status code (static storage). */
 const char* spec_status_string(spec_status s);

@@ -11,9 +11,13 @@ Entry points (same names as the C ABI in ``include/specverify.h``):
 * ``verify_tree``    greedy exact-match verification of a REST draft tree
 * ``verify_mentor``  the lossy, KL-bounded mentor variant
 * ``sample``         one draw per row from the transformed distribution
+* ``tree_attention`` attention of the drafted nodes over a paged cache
+* ``cache_append``, ``cache_compact``, ``cache_resize``, ``cache_fork``
+                     the paged cache itself, changed in place
 
 Tensors may live on the GPU (the normal case) or in (pinned) host memory; host
 inputs are copied to the current device, and outputs come back to the host.
+A paged cache, its page table and its reference counts live on the GPU.
 """
 
 import contextlib
@@ -28,8 +32,9 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 # the same library built with device-side index checks (build.py --debug)
 DEBUG_LIB_PATH = os.path.join(_HERE, "libspecverify_debug.so")
 
-SPEC_OK, SPEC_EINVAL, SPEC_ECUDA, SPEC_ETIMEOUT, SPEC_EDATA, SPEC_EBOUNDS = 0, 1, 2, 3, 4, 5
+SPEC_OK, SPEC_EINVAL, SPEC_ECUDA, SPEC_ETIMEOUT, SPEC_EDATA, SPEC_EBOUNDS, SPEC_ENOPAGES = 0, 1, 2, 3, 4, 5, 6
 SPEC_F32, SPEC_BF16 = 0, 1
+MAX_TREE_N = 1024
 PURPOSE_ACCEPT, PURPOSE_RESAMPLE, PURPOSE_DRAFT = 0, 1, 2
 
 EXPORTED = [
@@ -38,6 +43,8 @@ EXPORTED = [
     "spec_expected_tokens", "spec_walltime_factor", "spec_ops_factor", "spec_best_gamma",
     "spec_verify_mentor_workspace_size", "spec_verify_mentor",
     "spec_sample_workspace_size", "spec_sample",
+    "spec_tree_attention_workspace_size", "spec_tree_attention", "spec_cache_append", "spec_cache_compact",
+    "spec_cache_resize", "spec_cache_fork_workspace_size", "spec_cache_fork",
     "spec_philox_uniform", "spec_verify_noalloc", "spec_status_string", "spec_last_cuda_error",
     "spec_version", "spec_debug_build", "spec_debug_failures", "spec_debug_withhold_copy",
 ]
@@ -45,6 +52,13 @@ EXPORTED = [
 
 class SpecSampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("top_p", ctypes.c_float), ("top_k", ctypes.c_int32)]
+
+
+class SpecCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("layers", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class SpecError(RuntimeError):
@@ -112,6 +126,22 @@ def load_library(path=None):
         lib.spec_verify_noalloc.restype = _I
         lib.spec_philox_uniform.argtypes = [_U64, _U64, ctypes.c_uint32, ctypes.c_uint32, _I, _P, _P]
         lib.spec_philox_uniform.restype = _I
+        _C, _I64 = ctypes.POINTER(SpecCache), ctypes.c_int64
+        lib.spec_tree_attention_workspace_size.argtypes = [_I] * 6
+        lib.spec_tree_attention_workspace_size.restype = _SZ
+        lib.spec_tree_attention.argtypes = [_P, _C, _I, _P, _I64, _I, _P, _P, _P, _I, _I, _I, ctypes.c_float,
+                                            _P, _P, _P, _P, _SZ, _P]
+        lib.spec_tree_attention.restype = _I
+        lib.spec_cache_append.argtypes = [_P, _P, _C, _I, _P, _I64, _I, _P, _P, _I, _I, _P, _P]
+        lib.spec_cache_append.restype = _I
+        lib.spec_cache_compact.argtypes = [_C, _I, _P, _I64, _I, _P, _P, _P, _I, _I, _P, _P, _P]
+        lib.spec_cache_compact.restype = _I
+        lib.spec_cache_resize.argtypes = [_P, _I64, _I, _I, _P, _I, _I, _P, _P, _I, _P, _P]
+        lib.spec_cache_resize.restype = _I
+        lib.spec_cache_fork_workspace_size.argtypes = [_I]
+        lib.spec_cache_fork_workspace_size.restype = _SZ
+        lib.spec_cache_fork.argtypes = [_C, _I, _P, _I64, _I, _I, _P, _P, _P, _P, _I, _P, _P, _SZ, _P]
+        lib.spec_cache_fork.restype = _I
         lib.spec_status_string.argtypes = [_I]
         lib.spec_status_string.restype = ctypes.c_char_p
         lib.spec_last_cuda_error.argtypes = []
@@ -430,6 +460,212 @@ def philox_uniform(seed, row0, position, purpose, n, device=None):
     return out
 
 
+# ---- the paged key / value cache --------------------------------------------------
+
+_NULL = ctypes.c_void_p(0)
+
+
+def _cache_args(k_cache, v_cache, layered):
+    """The C view of k / v caches [layers, pages, page_size, heads, head_dim]
+    (one layer: no first dimension), any strides with contiguous heads."""
+    if k_cache.dim() != 4 + layered or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise SpecError("k and v caches must share a dtype and the shape "
+                        + ("[layers, " if layered else "[") + "pages, page_size, heads, head_dim]")
+    st = k_cache.stride()
+    if st != v_cache.stride() or st[-1] != 1:
+        raise SpecError("k and v caches must share their strides, with contiguous heads")
+    if not (k_cache.is_cuda and v_cache.is_cuda and k_cache.device == v_cache.device):
+        raise SpecError("the caches must be on one CUDA device")
+    sh = k_cache.shape
+    layers, layer_stride = (sh[0], st[0]) if layered else (1, 0)
+    return SpecCache(k_cache.data_ptr(), v_cache.data_ptr(), layers, sh[-4], sh[-3], sh[-2], sh[-1], layer_stride,
+                     st[-4], st[-3], st[-2])
+
+
+def _table_args(page_table, rows, device):
+    """Pointer, row stride and width of an int32 page table with `rows` rows."""
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.shape[0] != rows or \
+            page_table.device != device or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise SpecError(f"page_table must be an int32 tensor [{rows}, max_pages] on the cache's device, rows contiguous")
+    width = page_table.shape[1]
+    # a single row's stride is free to be anything
+    return page_table.data_ptr(), (page_table.stride(0) if rows > 1 else width), width
+
+
+def _in(t, device, dtype=torch.int32):
+    """An input on the device in the library's layout (copied only if it is not there yet)."""
+    if t.dtype != dtype:
+        t = t.to(dtype)
+    if t.device != device:
+        t = t.to(device, non_blocking=True)
+    t = t.contiguous()
+    # a view that starts off 16 bytes: rows are moved as 16-byte words
+    return t.clone() if t.is_floating_point() and t.data_ptr() % 16 else t
+
+
+def _owned(t, shape, device, what):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+        raise SpecError(f"{what} must be a contiguous int32 tensor {list(shape)} on the cache's device")
+    return t
+
+
+def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_nodes=None, scale=None,
+                   with_lse=False, out=None):
+    """Attention of the drafted nodes q [B, N, heads, D] over one layer's cache.
+
+    k_cache, v_cache [pages, page_size, kv_heads, D] (any strides with
+    contiguous heads) hold the nodes' keys and values already (``cache_append``).
+    Node i sees the cache_len[b] context positions and the nodes j < n_nodes[b]
+    with mask[b, i, j] != 0 (``tree_build``'s mask; None: j <= i, a chain).
+    ``scale`` defaults to 1 / sqrt(D). Returns out [B, N, heads, D], status [B]
+    and, with ``with_lse``, lse [B, N, heads]; nodes from n_nodes[b] on are
+    zero (lse -inf). ``out`` may pass preallocated outputs under these keys.
+    """
+    lib = load_library()
+    host = not q.is_cuda
+    dev = k_cache.device
+    cache = _cache_args(k_cache, v_cache, 0)
+    if q.dim() != 4 or q.shape[3] != cache.head_dim or q.shape[2] % cache.kv_heads != 0 or q.dtype != k_cache.dtype:
+        raise SpecError("q must be [B, N, heads, head_dim] of the cache's dtype, heads a multiple of kv_heads")
+    dt = _dtype_code(q)
+    B, N, Hq, D = q.shape
+    table, stride, width = _table_args(page_table, B, dev)
+    q = _in(q, dev, q.dtype)
+    lens = _in(cache_len, dev)
+    mask = None if mask is None else _in(mask, dev, torch.uint8)
+    cnt = None if n_nodes is None else _in(n_nodes, dev)
+    if lens.shape != (B,) or (mask is not None and mask.shape != (B, N, N)) or (cnt is not None and cnt.shape != (B,)):
+        raise SpecError("cache_len and n_nodes must be [B], mask [B, N, N]")
+    o = dict(out or {})
+    if "out" not in o:
+        o["out"] = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+    if "status" not in o:
+        o["status"] = torch.empty((B,), dtype=torch.int32, device=dev)
+    if with_lse and "lse" not in o:
+        o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    ws = workspace(lib.spec_tree_attention_workspace_size(B, N, Hq, cache.kv_heads, D, dt), dev, stream)
+    rc = lib.spec_tree_attention(q.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
+                                 _NULL if mask is None else mask.data_ptr(), _NULL if cnt is None else cnt.data_ptr(),
+                                 B, N, Hq, D ** -0.5 if scale is None else float(scale), o["out"].data_ptr(),
+                                 o["lse"].data_ptr() if "lse" in o else _NULL, o["status"].data_ptr(),
+                                 ws.data_ptr(), ws.numel(), stream.cuda_stream)
+    _check(rc)
+    return {n: t.cpu() for n, t in o.items()} if host else o
+
+
+def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None):
+    """Write k, v [B, N, kv_heads, D] to positions cache_len[b] + i, i < n_nodes[b]
+    (None: N), of one layer's cache [pages, page_size, kv_heads, D], in place.
+
+    The pages must be the sequences' already (``cache_resize``); cache_len is
+    not changed. Returns status [B].
+    """
+    lib = load_library()
+    dev = k_cache.device
+    cache = _cache_args(k_cache, v_cache, 0)
+    if k.dim() != 4 or k.shape != v.shape or tuple(k.shape[2:]) != (cache.kv_heads, cache.head_dim) or \
+            k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+        raise SpecError("k and v must be [B, N, kv_heads, head_dim] of the cache's dtype")
+    dt = _dtype_code(k)
+    B, N = k.shape[:2]
+    table, stride, width = _table_args(page_table, B, dev)
+    k, v, lens = _in(k, dev, k.dtype), _in(v, dev, v.dtype), _in(cache_len, dev)
+    cnt = None if n_nodes is None else _in(n_nodes, dev)
+    if lens.shape != (B,) or (cnt is not None and cnt.shape != (B,)):
+        raise SpecError("cache_len and n_nodes must be [B]")
+    status = torch.empty((B,), dtype=torch.int32, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    _check(lib.spec_cache_append(k.data_ptr(), v.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
+                                 _NULL if cnt is None else cnt.data_ptr(), B, N, status.data_ptr(),
+                                 stream.cuda_stream))
+    return {"status": status}
+
+
+def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_nodes=None):
+    """Keep an accepted path in caches [layers, pages, page_size, kv_heads, D], in
+    place: position L + i <- L + path_nodes[b, i], i <= accept_len[b].
+
+    accept_len [B] and path_nodes [B, W] are ``verify_tree``'s; None: a chain
+    (``verify``'s accepted), whose entries are in place. Returns cache_len [B]
+    = L + accept_len + 1 (-1 on a data error) and status [B].
+    """
+    lib = load_library()
+    dev = k_cache.device
+    cache = _cache_args(k_cache, v_cache, 1)
+    dt = _dtype_code(k_cache)
+    B = page_table.shape[0]
+    table, stride, width = _table_args(page_table, B, dev)
+    lens, acc = _in(cache_len, dev), _in(accept_len, dev)
+    path = None if path_nodes is None else _in(path_nodes, dev)
+    if lens.shape != (B,) or acc.shape != (B,) or (path is not None and (path.dim() != 2 or path.shape[0] != B)):
+        raise SpecError("cache_len and accept_len must be [B], path_nodes [B, W]")
+    W = MAX_TREE_N if path is None else path.shape[1]
+    o = torch.empty((2, B), dtype=torch.int32, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    _check(lib.spec_cache_compact(cache, dt, table, stride, width, lens.data_ptr(), acc.data_ptr(),
+                                  _NULL if path is None else path.data_ptr(), B, W, o.data_ptr(),
+                                  o.data_ptr() + 4 * B, stream.cuda_stream))
+    return {"cache_len": o[0], "status": o[1]}
+
+
+def cache_resize(page_table, page_refs, seqs, tokens, page_size):
+    """Pages for tokens[f] tokens of sequence seqs[f] (None: f), in place: more are
+    taken (lowest free number first), surplus ones released; 0 frees a sequence.
+
+    page_table [S, max_pages] int32 (-1: no page) and page_refs [pages] int32 (0:
+    free) are changed. Returns status [F]; SPEC_ENOPAGES where pages ran out
+    (that sequence is left as it was).
+    """
+    lib = load_library()
+    if not page_table.is_cuda:
+        raise SpecError("page_table and page_refs must be on a CUDA device")
+    dev = page_table.device
+    S = page_table.shape[0]
+    table, stride, width = _table_args(page_table, S, dev)
+    _owned(page_refs, (page_refs.numel(),), dev, "page_refs")
+    tok = _in(tokens, dev)
+    who = None if seqs is None else _in(seqs, dev)
+    F = tok.numel()
+    if tok.dim() != 1 or (who is not None and who.shape != tok.shape):
+        raise SpecError("seqs and tokens must be [F]")
+    status = torch.empty((F,), dtype=torch.int32, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    _check(lib.spec_cache_resize(table, stride, width, S, page_refs.data_ptr(), page_refs.numel(), int(page_size),
+                                 _NULL if who is None else who.data_ptr(), tok.data_ptr(), F, status.data_ptr(),
+                                 stream.cuda_stream))
+    return {"status": status}
+
+
+def cache_fork(k_cache, v_cache, page_table, cache_len, page_refs, src, dst):
+    """Sequences dst[f] as copies of src[f], in place: full pages shared, a partly
+    filled last page copied (caches [layers, pages, page_size, kv_heads, D]).
+
+    page_table [S, max_pages], cache_len [S] and page_refs [pages] are changed;
+    the dst rows must be distinct and empty. Returns status [F].
+    """
+    lib = load_library()
+    dev = k_cache.device
+    cache = _cache_args(k_cache, v_cache, 1)
+    dt = _dtype_code(k_cache)
+    S = page_table.shape[0]
+    table, stride, width = _table_args(page_table, S, dev)
+    _owned(page_refs, (cache.num_pages,), dev, "page_refs")
+    _owned(cache_len, (S,), dev, "cache_len")
+    a, z = _in(src, dev), _in(dst, dev)
+    if a.dim() != 1 or a.shape != z.shape:
+        raise SpecError("src and dst must be [F]")
+    F = a.numel()
+    status = torch.empty((F,), dtype=torch.int32, device=dev)
+    stream = torch.cuda.current_stream(dev)
+    ws = workspace(lib.spec_cache_fork_workspace_size(F), dev, stream)
+    _check(lib.spec_cache_fork(cache, dt, table, stride, width, S, page_refs.data_ptr(), cache_len.data_ptr(),
+                               a.data_ptr(), z.data_ptr(), F, status.data_ptr(), ws.data_ptr(), ws.numel(),
+                               stream.cuda_stream))
+    return {"status": status}
+
+
 __all__ = ["use_library", "DEBUG_LIB_PATH", "philox_uniform", "verify", "verify_tree", "tree_build", "acceptance_rate", "expected_tokens",
-           "walltime_factor", "ops_factor", "best_gamma", "verify_mentor", "sample", "load_library", "workspace",
-           "SpecError", "SpecSampling", "EXPORTED", "LIB_PATH"]
+           "walltime_factor", "ops_factor", "best_gamma", "verify_mentor", "sample", "tree_attention", "cache_append", "cache_compact",
+           "cache_resize", "cache_fork", "load_library", "workspace",
+           "SpecError", "SpecSampling", "SpecCache", "EXPORTED", "LIB_PATH"]

@@ -8,6 +8,8 @@
 #include <cstring>
 #include <mutex>
 
+#include "attention.cuh"
+#include "cache.cuh"
 #include "common.cuh"
 #include "specverify.h"
 
@@ -349,6 +351,7 @@ const char* spec_status_string(spec_status s) {
         case SPEC_ETIMEOUT: return "SPEC_ETIMEOUT";
         case SPEC_EDATA: return "SPEC_EDATA";
         case SPEC_EBOUNDS: return "SPEC_EBOUNDS";
+        case SPEC_ENOPAGES: return "SPEC_ENOPAGES";
     }
     return "SPEC_UNKNOWN";
 }
@@ -366,7 +369,8 @@ int spec_debug_build(void) {
 int spec_debug_failures(int* line) {
     using Reader = cudaError_t (*)(unsigned int*, unsigned int*);
     const Reader readers[] = {sv::debug_read_rows, sv::debug_read_rows_smem, sv::debug_read_argmax,
-                              sv::debug_read_mentor, sv::debug_read_beta, sv::debug_read_tree_build};
+                              sv::debug_read_mentor, sv::debug_read_beta, sv::debug_read_tree_build,
+                              sv::debug_read_attention, sv::debug_read_cache};
     long long total = 0;
     int first = 0;
     for (const Reader rd : readers) {

@@ -1,0 +1,365 @@
+// Tree attention over a paged cache on the CUDA cores, and the kernel that
+// joins partial results (attention.cuh: the mathematics and the division of
+// the work). Takes every type and head size; float32 caches and head sizes
+// that the tensor-core kernel lacks come here.
+//
+// One CTA of eight warps takes 16 rows of a unit, two a warp. Tiles of 64
+// positions (32 where a float32 head is wider than 128) of K and V are staged
+// by 16-byte asynchronous copies, two tiles deep. A lane scores two positions
+// (one) for both rows of its warp; the running
+// maximum and sum are the warp's (shuffles), the weights go through a
+// warp-private strip of shared memory, and a lane accumulates four (eight:
+// D > 128) output columns in registers. Warps meet only at the tile's arrival
+// and release. fp32 throughout.
+
+#include <algorithm>
+
+#include "attention.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int NT = 256;
+constexpr int kRows = 16;
+
+template <typename E>
+constexpr int row_bytes(int D) {  // a K row in shared memory: 16 bytes of padding against bank conflicts
+    return D * (int)sizeof(E) + 16;
+}
+
+template <typename E, int KV>
+size_t simt_smem(int D) {
+    return (size_t)2 * KV * (row_bytes<E>(D) + D * sizeof(E)) + (size_t)kRows * D * 4 + (size_t)kRows * KV * 4;
+}
+
+SV_DEV void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+SV_DEV uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+template <typename E>
+SV_DEV float4 lds4(const unsigned char* p);
+template <>
+SV_DEV float4 lds4<float>(const unsigned char* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+template <>
+SV_DEV float4 lds4<bf16_t>(const unsigned char* p) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xFFFF0000u));
+}
+
+SV_DEV float4 fma4(float a, float4 v, float4 c) {
+    return make_float4(fmaf(a, v.x, c.x), fmaf(a, v.y, c.y), fmaf(a, v.z, c.z), fmaf(a, v.w, c.w));
+}
+
+// One tile's K and V rows into a stage. Rows past the sequence's end and rows
+// of a page that does not exist are zero. Returns whether a page id was bad.
+template <typename E, int KV>
+SV_DEV bool load_tile(const AttnParams& p, int b, int h, long long pos0, long long end, unsigned char* ks,
+                      unsigned char* vs) {
+    const int vec = p.D * (int)sizeof(E) / 16;
+    const E* kc = reinterpret_cast<const E*>(p.k) + h * p.head_stride;
+    const E* vc = reinterpret_cast<const E*>(p.v) + h * p.head_stride;
+    const int ps1 = (1 << p.page_shift) - 1;
+    const int32_t* table = p.table + b * p.table_stride;
+    bool bad = false;
+    for (int i = threadIdx.x; i < KV * vec; i += NT) {
+        const int t = i / vec, c = i - t * vec;
+        const long long pos = pos0 + t;
+        unsigned char* kd = ks + t * row_bytes<E>(p.D) + c * 16;
+        unsigned char* vd = vs + (t * vec + c) * 16;
+        int id = -1;
+        if (pos < end) {
+            id = __ldg(table + (pos >> p.page_shift));
+            if (id < 0 || id >= p.num_pages) {
+                bad = true;
+                id = -1;
+            }
+        }
+        if (id >= 0) {
+            const long long at = id * p.page_stride + (pos & ps1) * p.token_stride + c * (16 / (int)sizeof(E));
+            cp16(smem_addr(kd), kc + at);
+            cp16(smem_addr(vd), vc + at);
+        } else {
+            *reinterpret_cast<uint4*>(kd) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(vd) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return bad;
+}
+
+template <typename E, int KV>
+__global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ AttnParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ AttnScan scan;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int J = KV / 32;
+    const int D = p.D, D4 = D / 4, kstride = row_bytes<E>(D);
+    unsigned char* ks = smem;
+    unsigned char* vs = ks + 2 * KV * kstride;
+    float* qs = reinterpret_cast<float*>(vs + (size_t)2 * KV * D * sizeof(E));
+    float* ws = qs + kRows * D + warp * 2 * KV;  // the warp's weights [2][KV]
+
+    attn_edges<E, NT>(p);
+    int parts = 0;
+    const long long total = attn_locate<KV, NT>(p, &scan, [&](long long t, int i) -> long long {
+        const int n = attn_parts(t, gridDim.x);
+        return i == 0 && (int)blockIdx.x < n ? attn_part(t, n, blockIdx.x) : -1;
+    });
+    parts = attn_parts(total, gridDim.x);
+    if ((int)blockIdx.x >= parts) return;
+    const long long begin = attn_part(total, parts, blockIdx.x), end = attn_part(total, parts, blockIdx.x + 1);
+    int b = scan.place[0].b;
+    long long base = scan.place[0].base;
+
+    for (long long t = begin; t < end;) {
+        AttnSeq sq = attn_seq(p, b);
+        int kt = attn_kv_tiles<KV>(sq), rt = attn_row_tiles(p, sq);
+        while (t >= base + (long long)kt * rt * p.Hkv) {
+            base += (long long)kt * rt * p.Hkv;
+            sq = attn_seq(p, ++b);
+            kt = attn_kv_tiles<KV>(sq);
+            rt = attn_row_tiles(p, sq);
+        }
+        const long long unit = (t - base) / kt;
+        const int first = (int)(t - base - unit * kt);
+        const int last = (int)min((long long)kt, first + (end - t));  // tiles [first, last) of the unit
+        const int h = (int)(unit / rt), row_base = (int)(unit - (long long)h * rt) * kRows;
+        const int rows = min(kRows, sq.n * p.G - row_base);
+        const long long len = (long long)sq.L + sq.n;
+
+        // queries, in octaves of the score
+        const E* q = reinterpret_cast<const E*>(p.q);
+        for (int i = tid; i < rows * D4; i += NT) {
+            const int r = i / D4, c = i - r * D4, node = (row_base + r) / p.G, g = (row_base + r) % p.G;
+            const E* src = q + (((long long)b * p.N + node) * (p.Hkv * p.G) + h * p.G + g) * D + c * 4;
+            float4 x = lds4<E>(reinterpret_cast<const unsigned char*>(src));
+            *reinterpret_cast<float4*>(qs + r * D + c * 4) =
+                make_float4(x.x * p.c2, x.y * p.c2, x.z * p.c2, x.w * p.c2);
+        }
+        bool bad = load_tile<E, KV>(p, b, h, (long long)first * KV, len, ks, vs);
+
+        const int r0 = warp * 2;
+        float m[2], l[2];
+        float4 acc[2][2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            m[r] = __uint_as_float(0xFF800000u);
+            l[r] = 0.f;
+            acc[r][0] = acc[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        for (int tile = first; tile < last; ++tile) {
+            const int st = (tile - first) & 1;
+            if (tile + 1 < last) {
+                bad |= load_tile<E, KV>(p, b, h, (long long)(tile + 1) * KV, len, ks + (st ^ 1) * KV * kstride,
+                                    vs + (size_t)(st ^ 1) * KV * D * sizeof(E));
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            } else {
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            }
+            __syncthreads();
+            if (r0 < rows) {
+                const unsigned char* kt0 = ks + st * KV * kstride;
+                const unsigned char* vt0 = vs + (size_t)st * KV * D * sizeof(E);
+                float s[2][J] = {};
+                const float* q0 = qs + r0 * D;
+                const float* q1 = r0 + 1 < rows ? q0 + D : q0;
+                for (int c = 0; c < D4; ++c) {
+                    const float4 a0 = *reinterpret_cast<const float4*>(q0 + c * 4);
+                    const float4 a1 = *reinterpret_cast<const float4*>(q1 + c * 4);
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        const float4 x = lds4<E>(kt0 + (lane + 32 * j) * kstride + c * 4 * sizeof(E));
+                        s[0][j] = fmaf(a0.x, x.x, fmaf(a0.y, x.y, fmaf(a0.z, x.z, fmaf(a0.w, x.w, s[0][j]))));
+                        s[1][j] = fmaf(a1.x, x.x, fmaf(a1.y, x.y, fmaf(a1.z, x.z, fmaf(a1.w, x.w, s[1][j]))));
+                    }
+                }
+                const long long pos0 = (long long)tile * KV;
+                const bool tail = pos0 + KV > sq.L;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int node = (row_base + min(r0 + r, rows - 1)) / p.G;
+                    if (tail) {
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            const long long nd = pos0 + lane + 32 * j - sq.L;
+                            const bool see = nd < 0 || (nd < sq.n && (p.mask ? __ldg(p.mask + ((long long)b * p.N + node) * p.N + nd) != 0
+                                                                             : nd <= node));
+                            if (!see) s[r][j] = __uint_as_float(0xFF800000u);
+                        }
+                    }
+                    // a NaN score makes the row NaN (fmaxf drops it, the exponential keeps it)
+                    const float mn = fmaxf(m[r], warp_max(J == 2 ? fmaxf(s[r][0], s[r][J - 1]) : s[r][0]));
+                    const float ref = mn == __uint_as_float(0xFF800000u) ? 0.f : mn;
+                    const float f = ex2(m[r] - ref);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int j = 0; j < J; ++j) {
+                        const float w = ex2(s[r][j] - ref);
+                        ws[r * KV + 32 * j + lane] = w;
+                        sum += w;
+                    }
+                    l[r] = l[r] * f + warp_sum(sum);
+                    m[r] = mn;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        acc[r][g].x *= f;
+                        acc[r][g].y *= f;
+                        acc[r][g].z *= f;
+                        acc[r][g].w *= f;
+                    }
+                }
+                __syncwarp();
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int c = lane + 32 * g;
+                    if (c < D4) {
+                        if (!tail) {
+#pragma unroll 8
+                            for (int t2 = 0; t2 < KV; ++t2) {
+                                const float4 x = lds4<E>(vt0 + ((size_t)t2 * D + c * 4) * sizeof(E));
+                                acc[0][g] = fma4(ws[t2], x, acc[0][g]);
+                                acc[1][g] = fma4(ws[KV + t2], x, acc[1][g]);
+                            }
+                        } else {
+                            // an unseen node's values may be anything: a zero weight leaves them out
+                            for (int t2 = 0; t2 < KV; ++t2) {
+                                const float4 x = lds4<E>(vt0 + ((size_t)t2 * D + c * 4) * sizeof(E));
+                                const float w0 = ws[t2], w1 = ws[KV + t2];
+                                if (w0 != 0.f) acc[0][g] = fma4(w0, x, acc[0][g]);
+                                if (w1 != 0.f) acc[1][g] = fma4(w1, x, acc[1][g]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            __syncthreads();
+        }
+        bad = __syncthreads_or(bad);
+        const bool whole = first == 0 && last == kt;
+        const int slot = 2 * blockIdx.x + (t != begin);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if (r0 + r >= rows) break;
+            if (bad) l[r] = __uint_as_float(0x7FC00000u);
+            const int node = (row_base + r0 + r) / p.G, head = h * p.G + (row_base + r0 + r) % p.G;
+            const long long row = ((long long)b * p.N + node) * (p.Hkv * p.G) + head;
+            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int c = lane + 32 * g;
+                if (c >= D4) break;
+                if (whole) {
+                    const float4 o = make_float4(acc[r][g].x * inv, acc[r][g].y * inv, acc[r][g].z * inv,
+                                                 acc[r][g].w * inv);
+                    if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
+                        store4<E>(reinterpret_cast<E*>(p.out) + row * D + c * 4, o);
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + ((long long)slot * kRows + r0 + r) * D + c * 4) = acc[r][g];
+                }
+            }
+            if (lane == 0) {
+                if (!whole)
+                    p.part_ml[(long long)slot * kRows + r0 + r] = make_float2(m[r], l[r]);
+                else if (p.lse)
+                    p.lse[row] = lse_of(m[r], l[r]);
+            }
+        }
+        t += last - first;
+    }
+}
+
+// Joins the pieces of the units that CTA parts cut. Block (c, y) looks after
+// the unit that part c starts inside of, if c is the first such part, and a
+// quarter-warp-group's rows of it: weights 2^(m_i - max m), rows' sums in
+// part order.
+template <typename E, int KV>
+__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnParams p, int main_grid) {
+    __shared__ AttnScan scan;
+    const int c = blockIdx.x + 1;
+    const long long total = attn_locate<KV, 128>(p, &scan, [&](long long t, int i) -> long long {
+        const int n = attn_parts(t, main_grid);
+        return i == 0 && c < n ? attn_part(t, n, c) : -1;
+    });
+    const int parts = attn_parts(total, main_grid);
+    if (c >= parts) return;
+    const int b = scan.place[0].b;
+    const long long base = scan.place[0].base, at = attn_part(total, parts, c);
+    const AttnSeq sq = attn_seq(p, b);
+    const int kt = attn_kv_tiles<KV>(sq), rt = attn_row_tiles(p, sq);
+    const long long unit = (at - base) / kt, ustart = base + unit * kt, uend = ustart + kt;
+    if (at == ustart || attn_part(total, parts, c - 1) > ustart) return;
+    int last = c;  // the last part with tiles of this unit
+    while (last + 1 < parts && attn_part(total, parts, last + 1) < uend) ++last;
+    const int h = (int)(unit / rt), row_base = (int)(unit - (long long)h * rt) * p.tile_rows;
+    const int rows = min(p.tile_rows, sq.n * p.G - row_base);
+    const int slot0 = 2 * (c - 1) + (attn_part(total, parts, c - 1) != ustart);
+    const int lane = threadIdx.x & 31;
+    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 4) {
+        float m = __uint_as_float(0xFF800000u);
+        for (int i = c - 1; i <= last; ++i)
+            m = fmaxf(m, p.part_ml[(long long)(i == c - 1 ? slot0 : 2 * i) * p.tile_rows + r].x);
+        const float ref = m == __uint_as_float(0xFF800000u) ? 0.f : m;
+        float l = 0.f;
+        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int i = c - 1; i <= last; ++i) {
+            const long long at_row = (long long)(i == c - 1 ? slot0 : 2 * i) * p.tile_rows + r;
+            const float2 ml = p.part_ml[at_row];
+            const float w = ex2(ml.x - ref);
+            l += w * ml.y;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int d = (lane + 32 * g) * 4;
+                if (d < p.D) acc[g] = fma4(w, *reinterpret_cast<const float4*>(p.part_o + at_row * p.D + d), acc[g]);
+            }
+        }
+        const long long row = ((long long)b * p.N + (row_base + r) / p.G) * (p.Hkv * p.G) + h * p.G + (row_base + r) % p.G;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int d = (lane + 32 * g) * 4;
+            if (d < p.D && SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
+                store4<E>(reinterpret_cast<E*>(p.out) + row * p.D + d,
+                          make_float4(acc[g].x * inv, acc[g].y * inv, acc[g].z * inv, acc[g].w * inv));
+        }
+        if (lane == 0 && p.lse) p.lse[row] = lse_of(m, l);
+    }
+}
+
+template <typename E, int KV>
+cudaError_t launch_simt(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
+    const size_t smem = simt_smem<E, KV>(p.D);
+    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<E, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    attn_simt_kernel<E, KV><<<plan.grid, NT, smem, st>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || plan.grid == 1) return e;
+    attn_combine_kernel<E, KV><<<dim3(plan.grid - 1, (kRows + 3) / 4), 128, 0, st>>>(p, plan.grid);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+int attention_simt_rows() { return kRows; }
+
+int attention_simt_kv(int dtype, int D) { return dtype == 0 && D > 128 ? 32 : 64; }
+
+cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st) {
+    if (dtype != 0) return launch_simt<bf16_t, 64>(p, plan, st);
+    return plan.kv == 64 ? launch_simt<float, 64>(p, plan, st) : launch_simt<float, 32>(p, plan, st);
+}
+
+// CTAs of an SM: what its shared memory holds, four at most.
+int attention_simt_ctas(int dtype, int D) {
+    const size_t smem = dtype != 0 ? simt_smem<bf16_t, 64>(D)
+                        : attention_simt_kv(dtype, D) == 64 ? simt_smem<float, 64>(D) : simt_smem<float, 32>(D);
+    return (int)std::max<size_t>(1, std::min<size_t>(4, (size_t)227 * 1024 / (smem + 2048)));
+}
+
+SV_DEBUG_READER(attention)
+
+}  // namespace sv

@@ -1,0 +1,202 @@
+// Shared parts of the tree-attention kernels: parameters, the division of the
+// work over the CTAs, and the record layout of partial results.
+//
+// One step's drafted nodes (N per sequence, node 0 the last context token)
+// attend to their sequence's committed context and to their ancestors:
+//   o_i = sum_t p_it v_t,  p_it = exp(s_it - lse_i),  s_it = scale q_i . k_t,
+//   lse_i = log sum_t exp(s_it),
+// t over the positions < L = cache_len[b] and the nodes' positions L + j with
+// mask[i][j] = 1 (no mask: j <= i). The rows of one key / value head are its
+// nodes' query heads, row r = node r / G, head r % G of the group of G that
+// shares it, so a key is read once for all of them.
+//
+// Division. A unit is (sequence, key / value head, row tile); its tiles are
+// the kKv-position tiles of L + n positions. All units' tiles in order form
+// one range that is cut into equal parts, one a CTA, whatever the lengths
+// are (they are known on the device only). A unit inside one part is finished
+// by its CTA; the others leave partial results (unnormalised sums with their
+// running maximum and sum) that the combine kernel joins in range order, so
+// results depend on the lengths and the grid alone, never on timing.
+#pragma once
+
+#include "common.cuh"
+
+namespace sv {
+
+struct AttnParams {
+    const void* q;    // [B, N, Hkv * G, D]
+    const void* k;    // page p, slot s, head h at p * page_stride + s * token_stride + h * head_stride
+    const void* v;
+    long long page_stride, token_stride, head_stride;  // elements
+    const int32_t* table;  // [B] rows of table_stride entries
+    long long table_stride;
+    const int32_t* cache_len;  // [B]
+    const uint8_t* mask;       // [B, N, N] or null (j <= i)
+    const int32_t* n_nodes;    // [B] or null (N)
+    int B, N, Hkv, G, D, num_pages, max_pages, page_shift;
+    int tile_rows;       // rows of a row tile
+    float c2;            // scale * log2(e): scores in octaves
+    void* out;           // [B, N, Hkv * G, D]
+    float* lse;          // [B, N, Hkv * G] or null
+    int32_t* status;     // [B] or null
+    float* part_o;       // [2 * grid][rows of a tile][D] partial sums
+    float2* part_ml;     // [2 * grid][rows of a tile] running maximum (octaves) and sum
+};
+
+// A sequence's nodes and context; n = -1: bad data.
+struct AttnSeq {
+    int n, L;
+};
+
+SV_DEV AttnSeq attn_seq(const AttnParams& p, int b) {
+    AttnSeq s;
+    s.L = __ldg(p.cache_len + b);
+    s.n = p.n_nodes ? __ldg(p.n_nodes + b) : p.N;
+    if (s.L < 0 || s.n < 0 || s.n > p.N || (long long)s.L + s.n > ((long long)p.max_pages << p.page_shift)) s.n = -1;
+    return s;
+}
+
+template <int KV>
+SV_DEV int attn_kv_tiles(const AttnSeq& s) {
+    return s.n > 0 ? (int)(((long long)s.L + s.n + KV - 1) / KV) : 0;
+}
+
+SV_DEV int attn_row_tiles(const AttnParams& p, const AttnSeq& s) {
+    return s.n > 0 ? (s.n * p.G + p.tile_rows - 1) / p.tile_rows : 0;
+}
+
+template <int KV>
+SV_DEV long long attn_seq_work(const AttnParams& p, int b) {
+    const AttnSeq s = attn_seq(p, b);
+    return (long long)attn_kv_tiles<KV>(s) * attn_row_tiles(p, s) * p.Hkv;
+}
+
+// Where tile `at` of the whole range lies: its sequence and that sequence's
+// first tile in the range; total: all tiles.
+struct AttnPlace {
+    int b;
+    long long base;
+};
+
+// Scratch of attn_locate in shared memory.
+struct AttnScan {
+    long long warp_sum[32];
+    AttnPlace place[2];
+};
+
+// Called by all NT threads of a block; `pick(total, which)` gives the tile to
+// place (which = 0, 1), -1 for none. Returns the total; places go to sc->place.
+// Each thread sums a run of sequences, one scan orders the runs.
+template <int KV, int NT, typename Pick>
+SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc, Pick pick) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int run = (p.B + NT - 1) / NT;
+    const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += attn_seq_work<KV>(p, b);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) sc->warp_sum[warp] = inc;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        const long long u = sc->warp_sum[w];
+        if (w < warp) before += u;
+        total += u;
+    }
+    long long lo = before + inc - mine;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const long long at = pick(total, i);
+        if (at >= lo && at < lo + mine) {
+            long long base = lo;
+            for (int b = b0; b < b1; ++b) {
+                const long long w = attn_seq_work<KV>(p, b);
+                if (at < base + w) {
+                    sc->place[i] = AttnPlace{b, base};
+                    break;
+                }
+                base += w;
+            }
+        }
+    }
+    __syncthreads();
+    return total;
+}
+
+// CTA c's part of `total` tiles over `parts` CTAs.
+SV_DEV long long attn_part(long long total, int parts, int c) { return total * c / parts; }
+SV_DEV int attn_parts(long long total, int grid) { return (int)(total < grid ? total : grid); }
+
+// The sequences' own checks, one sequence per CTA and turn (all NT threads):
+// status, and the rows that no unit writes: zeros (lse -inf) from the node
+// count on, NaN everywhere for a sequence with bad data. A bad page id is
+// reported here; the units that meet it make their rows NaN.
+template <typename E, int NT>
+SV_DEV void attn_edges(const AttnParams& p) {
+    const int tid = threadIdx.x;
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const AttnSeq s = attn_seq(p, b);
+        bool bad = s.n < 0;
+        if (p.status) {
+            if (s.n > 0) {
+                const int pages = (int)(((long long)s.L + s.n + (1 << p.page_shift) - 1) >> p.page_shift);
+                for (int i = tid; i < pages; i += NT) {
+                    const int id = __ldg(p.table + b * p.table_stride + i);
+                    bad |= id < 0 || id >= p.num_pages;
+                }
+            }
+            bad = __syncthreads_or(bad);
+            if (tid == 0) p.status[b] = bad ? kEData : kOk;
+        }
+        const int Hq = p.Hkv * p.G, n = max(s.n, 0);
+        const long long row0 = ((long long)b * p.N + n) * Hq, rows = (long long)(p.N - n) * Hq;
+        const long long words = rows * p.D * (long long)sizeof(E) / 16;
+        const uint32_t fill = s.n < 0 ? (sizeof(E) == 4 ? 0x7FC00000u : 0x7FC07FC0u) : 0u;
+        uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<E*>(p.out) + row0 * p.D);
+        for (long long i = tid; i < words; i += NT) o[i] = make_uint4(fill, fill, fill, fill);
+        if (p.lse)
+            for (long long i = tid; i < rows; i += NT)
+                p.lse[row0 + i] = __uint_as_float(s.n < 0 ? 0x7FC00000u : 0xFF800000u);
+    }
+}
+
+SV_DEV float lse_of(float m2, float l) {
+    return l > 0.f ? (m2 + log2f(l)) * 0.6931471805599453f : (l == 0.f ? __uint_as_float(0xFF800000u) : l + m2);
+}
+
+template <typename E>
+SV_DEV void store4(E* dst, float4 x);
+template <>
+SV_DEV void store4<float>(float* dst, float4 x) {
+    *reinterpret_cast<float4*>(dst) = x;
+}
+SV_DEV uint32_t pack_bf16(float lo, float hi) {  // round to nearest even
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <>
+SV_DEV void store4<bf16_t>(bf16_t* dst, float4 x) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+}
+
+// Host side.
+struct AttnPlan {
+    int grid, rows, kv;   // CTAs of the main kernel, rows of a tile, positions of a tile
+    bool tc;              // the tensor-core kernel
+    size_t part_o, part_ml, total;  // workspace layout
+};
+
+cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);
+int attention_simt_rows();
+int attention_simt_kv(int dtype, int D);
+int attention_simt_ctas(int dtype, int D);
+cudaError_t debug_read_attention(unsigned int* count, unsigned int* line);
+
+}  // namespace sv
