@@ -21,7 +21,7 @@ LIB = os.path.join(HERE, "libspecverify.so")
 DEBUG_LIB = os.path.join(HERE, "libspecverify_debug.so")
 SOURCES = ["csrc/api.cu", "csrc/rows.cu", "csrc/rows_smem.cu", "csrc/argmax.cu", "csrc/mentor.cu",
            "csrc/noalloc.cu", "csrc/tree_build.cu", "csrc/beta.cu", "csrc/planner.cu",
-           "csrc/attention.cu", "csrc/cache.cu", "csrc/cache_api.cu"]
+           "csrc/attention.cu", "csrc/attention_tc.cu", "csrc/cache.cu", "csrc/cache_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-Xptxas", "-v", "-I", os.path.join(ROOT, "include"), "-I", os.path.join(HERE, "csrc")]

@@ -370,7 +370,7 @@ int spec_debug_failures(int* line) {
     using Reader = cudaError_t (*)(unsigned int*, unsigned int*);
     const Reader readers[] = {sv::debug_read_rows, sv::debug_read_rows_smem, sv::debug_read_argmax,
                               sv::debug_read_mentor, sv::debug_read_beta, sv::debug_read_tree_build,
-                              sv::debug_read_attention, sv::debug_read_cache};
+                              sv::debug_read_attention, sv::debug_read_attention_tc, sv::debug_read_cache};
     long long total = 0;
     int first = 0;
     for (const Reader rd : readers) {

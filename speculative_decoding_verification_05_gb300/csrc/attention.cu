@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ A
 }
 
 // Joins the pieces of the units that CTA parts cut. Block (c, y) looks after
-// the unit that part c starts inside of, if c is the first such part, and a
-// quarter-warp-group's rows of it: weights 2^(m_i - max m), rows' sums in
+// the unit that part c starts inside of, if c is the first such part; a warp
+// takes one of its rows at a time: weights 2^(m_i - max m), the pieces' sums in
 // part order.
 template <typename E, int KV>
 __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnParams p, int main_grid) {
@@ -343,6 +343,13 @@ cudaError_t launch_simt(const AttnParams& p, const AttnPlan& plan, cudaStream_t 
 }
 
 }  // namespace
+
+cudaError_t launch_attention_combine_tc(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
+    if (plan.grid == 1) return cudaSuccess;
+    const int rows = std::min(plan.rows, p.N * p.G);
+    attn_combine_kernel<bf16_t, 128><<<dim3(plan.grid - 1, std::min(16, (rows + 3) / 4)), 128, 0, st>>>(p, plan.grid);
+    return cudaGetLastError();
+}
 
 int attention_simt_rows() { return kRows; }
 

@@ -189,7 +189,6 @@ SV_DEV void store4<bf16_t>(bf16_t* dst, float4 x) {
 // Host side.
 struct AttnPlan {
     int grid, rows, kv;   // CTAs of the main kernel, rows of a tile, positions of a tile
-    bool tc;              // the tensor-core kernel
     size_t part_o, part_ml, total;  // workspace layout
 };
 
@@ -197,6 +196,17 @@ cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan
 int attention_simt_rows();
 int attention_simt_kv(int dtype, int D);
 int attention_simt_ctas(int dtype, int D);
+// The tensor-core kernel (bf16, D 64 or 128) reads K and V through two tensor
+// maps; attention_tc_maps: false where the cache's strides have none.
+struct alignas(64) AttnMaps {
+    unsigned char bytes[256];
+};
+int attention_tc_rows();
+int attention_tc_kv();
+bool attention_tc_maps(const AttnParams& p, AttnMaps* m);
+cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const AttnMaps& m, cudaStream_t st);
+cudaError_t launch_attention_combine_tc(const AttnParams& p, const AttnPlan& plan, cudaStream_t st);
+cudaError_t debug_read_attention_tc(unsigned int* count, unsigned int* line);
 cudaError_t debug_read_attention(unsigned int* count, unsigned int* line);
 
 }  // namespace sv

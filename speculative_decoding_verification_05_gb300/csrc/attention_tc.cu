@@ -1,0 +1,772 @@
+// Tree attention over a paged cache on the tensor cores (bf16, heads of 64 and
+// 128; attention.cuh: the mathematics and the division of the work).
+//
+// One CTA an SM, a persistent part of the range each. Three groups of four
+// warps, the last two warps idle:
+//   producer   (warp 8) copies K and V tiles of 128 positions page by page
+//              (tensor copies with the 128-byte swizzle) into a ring of stages;
+//   issuer     (warp 9, one lane) issues the products: S = Q K^T into tensor
+//              memory, and O += P V with P taken from tensor memory;
+//   two groups (warps 0-3, 4-7) of 128 threads, a row each: the softmax between
+//              the two products, and the results.
+// The groups are two streams that the tensor core serves in turn, one's
+// products while the other computes its softmax:
+//   more than 128 rows  both streams go over the same tiles, each for a half of
+//                       the unit's 256 rows (a tile is read once for 256 rows);
+//   else                both have the same rows and take alternate tiles; their
+//                       sums are joined at the end.
+// S_w takes columns 128 w .. of tensor memory, P_w (bf16, two a column) its
+// first half once the group has read S_w; O_w columns 256 + 128 w. Products
+// are issued by one thread and run in its order, so S_w of the next tile, issued
+// after P_w V, cannot overtake it.
+//
+// The running maximum is only raised (and O_w scaled) when a tile exceeds it
+// by more than 8 octaves: weights stay below 2^8 and the sums far inside fp32;
+// any reference gives the same quotient. Statistics and sums are fp32, and the
+// sums l are taken before the weights are rounded to bf16 for the product with
+// V. Where a weight is more than a sixteenth of its row's sum so far, its
+// rounding would show beside the output's own: steps of 16 positions with such
+// a weight are multiplied a second time with what the rounding took (P_w's
+// second half of S_w's columns, zero elsewhere). Lighter weights' roundings
+// average out, and a long row has few heavy ones.
+//
+// Tiles that reach past the context also hold nodes and the end: a thread forms
+// its row's visibility bits, and the elements of V there that are not finite
+// are zeroed in shared memory before the product (a zero weight times an
+// infinity would be NaN in rows that do not see the node) and added to the rows
+// that do see them when the results are written.
+
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "attention.cuh"
+#include "tcgen.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int NT = 384;
+// Registers: 384 x 168 at launch, handed over as 208 to the softmax groups and
+// 88 to the third (2 x 208 + 88 = 3 x 168).
+constexpr int kGroupRegs = 208, kOtherRegs = 88;
+constexpr int kKv = 128;     // positions of a tile
+constexpr int kRows = 256;   // rows of a unit
+constexpr int kMaxStages = 10;
+constexpr float kHeavy = 4.f;  // octaves below a row's sum from which a weight is heavy
+constexpr float kSlack = 8.f;  // octaves that a score may exceed the reference by
+constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile
+
+template <int D>
+struct Shape {
+    static constexpr uint32_t kTile = kKv * D * 2;
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr size_t kSmem = 1024 + 2048 + (size_t)(2 + kStages) * kTile;
+};
+
+struct Ctl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full, s_full[2], p_full[2], o_full[2], groups, drain;
+    uint32_t loads;  // ring entries filled
+    AttnScan scan;
+    uint32_t tmem;
+    int abort;
+    int flags[2];  // of the segment (by parity): 1 V had elements that are not finite, 2 a bad page
+    uint32_t heavy[2][4];  // steps of 16 positions with heavy weights, by group and warp
+    float2 ml[128];
+};
+static_assert(sizeof(Ctl) <= 2048, "control region");
+
+// One CTA's stay in a unit: tiles [first, last) of it.
+struct Seg {
+    int b, h, row0, rows, first, last, kt, L, n;
+    long long len;
+    bool dual, whole;
+    int slot, steps;  // steps: softmax tiles of both streams together
+};
+
+// Walks a part of the range; every role walks it by itself.
+struct Walk {
+    long long t, end, begin, base;
+    int b;
+    SV_DEV bool next(const AttnParams& p, Seg* s) {
+        if (t >= end) return false;
+        AttnSeq q = attn_seq(p, b);
+        int kt = attn_kv_tiles<kKv>(q), rt = attn_row_tiles(p, q);
+        while (t >= base + (long long)kt * rt * p.Hkv) {
+            base += (long long)kt * rt * p.Hkv;
+            q = attn_seq(p, ++b);
+            kt = attn_kv_tiles<kKv>(q);
+            rt = attn_row_tiles(p, q);
+        }
+        const long long unit = (t - base) / kt;
+        s->b = b;
+        s->kt = kt;
+        s->first = (int)(t - base - unit * kt);
+        s->last = (int)min((long long)kt, s->first + (end - t));
+        s->h = (int)(unit / rt);
+        s->row0 = (int)(unit - (long long)s->h * rt) * kRows;
+        s->rows = min(kRows, q.n * p.G - s->row0);
+        s->L = q.L;
+        s->n = q.n;
+        s->len = (long long)q.L + q.n;
+        s->dual = s->rows > 128;
+        s->whole = s->first == 0 && s->last == kt;
+        s->slot = 2 * blockIdx.x + (t != begin);
+        s->steps = (s->last - s->first) * (s->dual ? 2 : 1);
+        t += s->last - s->first;
+        return true;
+    }
+};
+
+// Order of a segment's tiles in the ring (cnt tiles): the order of their first
+// use. Two streams on the same tiles: K0 V0 K1 V1 ..; on alternate tiles: K0
+// K1 V0 K2 V1 K3 ..
+SV_DEV int ring_k(const Seg& s, int i) { return s.dual ? 2 * i : i + max(0, i - 1); }
+SV_DEV int ring_v(const Seg& s, int i) { return s.dual ? 2 * i + 1 : i + min(i + 2, s.last - s.first); }
+
+// A wait by whole warps: every lane gets the same answer.
+SV_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const int* abort) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort)) != 0;
+}
+
+// ---- copies ----------------------------------------------------------------------
+
+template <int D>
+SV_DEV bool load_box(const AttnParams& p, Ctl* c, const CUtensorMap* map, uint32_t stages, const Seg& s, int tile,
+                     uint32_t ring) {
+    constexpr int NS = Shape<D>::kStages;
+    const int lane = threadIdx.x & 31, st = ring % NS;
+    const uint32_t round = ring / NS;
+    const int ps = min(1 << p.page_shift, kKv), halves = D / 64, pages = kKv / ps;
+    const int pg = lane / halves, half = lane - pg * halves;
+    const long long pos = (long long)tile * kKv + pg * ps;
+    int id = -1;
+    if (pg < pages && pos < s.len) id = __ldg(p.table + s.b * p.table_stride + (pos >> p.page_shift));
+    const bool ok = id >= 0 && id < p.num_pages;
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, ok);
+    if (round && !warp_wait(&c->empty[st], (round - 1) & 1, &c->abort)) return false;
+    if (lane == 0) mbar_expect_tx(&c->full[st], __popc(who) * (uint32_t)ps * 128);
+    __syncwarp();
+    if (ok)
+        tma_load4(stages + st * Shape<D>::kTile + half * kHalf + pg * ps * 128, map, half * 64,
+                  (int)(pos & ((1 << p.page_shift) - 1)), s.h, id, &c->full[st]);
+    return true;
+}
+
+template <int D>
+SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t stages,
+                    Walk walk) {
+    uint32_t ring = 0;
+    Seg s;
+    bool ok = true;
+    while (ok && walk.next(p, &s)) {
+        const int cnt = s.last - s.first, ahead = s.dual ? 1 : 2;
+        for (int i = -ahead; ok && i < cnt; ++i) {  // V(i), then K(i + ahead); K alone before the first V
+            if (i >= 0) ok = load_box<D>(p, c, mv, stages, s, s.first + i, ring++);
+            if (ok && i + ahead < cnt) ok = load_box<D>(p, c, mk, stages, s, s.first + i + ahead, ring++);
+        }
+    }
+    if ((threadIdx.x & 31) == 0) c->loads = ok ? ring : ring - 1;
+    if (!ok) c->abort = 1;
+}
+
+// ---- products ---------------------------------------------------------------------
+
+template <int D>
+SV_DEV bool issue_s(Ctl* c, uint32_t qs, uint32_t stages, const Seg& s, int vt, uint32_t ring0) {
+    constexpr int NS = Shape<D>::kStages;
+    constexpr uint32_t idesc = mma_idesc(kKv, false);
+    const int w = vt & 1, i = s.dual ? vt >> 1 : vt;
+    const uint32_t ring = ring0 + ring_k(s, i), st = ring % NS;
+    if (!mbar_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
+    tc_fence_after();
+    const uint32_t a = qs + (s.dual ? w * Shape<D>::kTile : 0u), b = stages + st * Shape<D>::kTile;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+        mma_ss(c->tmem + 128 * w, mma_desc(a + off, 16, 1024), mma_desc(b + off, 16, 1024), idesc, kk > 0);
+    }
+    mma_commit(&c->s_full[w]);
+    if (!s.dual || w == 1) mma_commit(&c->empty[st]);
+    return true;
+}
+
+template <int D>
+SV_DEV bool issue_o(Ctl* c, uint32_t stages, const Seg& s, int vt, uint32_t ring0, uint32_t* p_phase) {
+    constexpr int NS = Shape<D>::kStages;
+    constexpr uint32_t idesc = mma_idesc(D, true);
+    const int w = vt & 1, i = s.dual ? vt >> 1 : vt;
+    const uint32_t ring = ring0 + ring_v(s, i), st = ring % NS;
+    if (!mbar_wait(&c->p_full[w], (*p_phase >> w) & 1, &c->abort)) return false;
+    *p_phase ^= 1u << w;
+    if (!mbar_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
+    tc_fence_after();
+    const uint32_t b = stages + st * Shape<D>::kTile;
+#pragma unroll
+    for (int kk = 0; kk < kKv / 16; ++kk)
+        mma_ts(c->tmem + 256 + 128 * w, c->tmem + 128 * w + kk * 8, mma_desc(b + kk * 2048, kHalf, 1024), idesc,
+               vt >= 2 || kk > 0);
+    const volatile uint32_t* hv = c->heavy[w];
+    const uint32_t heavy = hv[0] | hv[1] | hv[2] | hv[3];
+    if (heavy)
+#pragma unroll
+        for (int kk = 0; kk < kKv / 16; ++kk)
+            if (heavy >> kk & 1)
+                mma_ts(c->tmem + 256 + 128 * w, c->tmem + 128 * w + 64 + kk * 8, mma_desc(b + kk * 2048, kHalf, 1024),
+                       idesc, true);
+    if (!s.dual || w == 1) mma_commit(&c->empty[st]);
+    if (vt + 2 >= s.steps) mma_commit(&c->o_full[w]);
+    return true;
+}
+
+template <int D>
+SV_DEV void issue(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Walk walk) {
+    uint32_t ring0 = 0, p_phase = 0, q_phase = 0;
+    Seg s;
+    bool ok = true;
+    while (ok && walk.next(p, &s)) {
+        ok = mbar_wait(&c->q_full, q_phase, &c->abort);
+        q_phase ^= 1;
+        if (ok) ok = issue_s<D>(c, qs, stages, s, 0, ring0);
+        if (ok && s.steps > 1) ok = issue_s<D>(c, qs, stages, s, 1, ring0);
+        for (int vt = 0; ok && vt < s.steps; ++vt) {
+            ok = issue_o<D>(c, stages, s, vt, ring0, &p_phase);
+            if (ok && vt + 2 < s.steps) ok = issue_s<D>(c, qs, stages, s, vt + 2, ring0);
+        }
+        ring0 += 2 * (s.last - s.first);
+    }
+    if (!ok) c->abort = 1;
+}
+
+// ---- softmax and results ------------------------------------------------------------
+
+// 32 visibility bits of a row from position p0 on. Node j of the row's own
+// sequence is at position L + j.
+SV_DEV uint32_t see_bits(const AttnParams& p, const Seg& s, int node, long long p0) {
+    const long long ctx = s.L - p0;
+    uint32_t bits = ctx >= 32 ? 0xFFFFFFFFu : ctx <= 0 ? 0u : (1u << ctx) - 1u;
+    if (bits == 0xFFFFFFFFu) return bits;
+    if (!p.mask) {
+        const long long upto = (long long)s.L + node + 1 - p0;  // the row sees positions below this
+        return upto >= 32 ? 0xFFFFFFFFu : upto <= 0 ? 0u : (1u << upto) - 1u;
+    }
+    const uint8_t* row = p.mask + ((long long)s.b * p.N + node) * p.N;
+    const uint8_t* all_end = p.mask + (long long)p.B * p.N * p.N;
+    const long long j0 = p0 - s.L;  // node of bit 0 (negative: context)
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+        const long long j = j0 + 4 * g;
+        if (j + 3 < 0 || j >= s.n) continue;
+        const uint8_t* a = row + j;
+        const uint32_t shift = ((uintptr_t)a & 3) * 8;
+        const uint8_t* down = a - ((uintptr_t)a & 3);
+        if (j >= 0 && j + 4 <= s.n && down >= p.mask && down + 8 <= all_end) {
+            const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(down));
+            const uint32_t hi = shift ? __ldg(reinterpret_cast<const uint32_t*>(down) + 1) : 0u;
+            const uint32_t four = __vsetne4(__funnelshift_r(lo, hi, shift), 0u);
+            bits |= ((four * 0x01020408u) >> 24 & 0xFu) << (4 * g);
+        } else {
+            for (int e = 0; e < 4; ++e)
+                if (j + e >= 0 && j + e < s.n && __ldg(a + e) != 0) bits |= 1u << (4 * g + e);
+        }
+    }
+    return bits;
+}
+
+// Rows of a V tile past the context: rows past the end become zero, elements
+// that are not finite too (flag 1). Thread t owns position t of the tile.
+template <int D>
+SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int tile, int t, int parity) {
+    const long long pos = (long long)tile * kKv + t;
+    if (pos < s.L) return;
+    const bool past = pos >= s.len;
+    bool found = false;
+#pragma unroll
+    for (int half = 0; half < D / 64; ++half)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = tile_addr + half * kHalf + t * 128 + ((i ^ (t & 7)) * 16);
+            uint32_t x[4] = {0u, 0u, 0u, 0u};
+            bool write = past;
+            if (!past) {
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                             : "r"(a));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if ((x[e] & 0x7F80u) == 0x7F80u) {
+                        x[e] &= 0xFFFF0000u;
+                        write = found = true;
+                    }
+                    if ((x[e] & 0x7F800000u) == 0x7F800000u) {
+                        x[e] &= 0x0000FFFFu;
+                        write = found = true;
+                    }
+                }
+            }
+            if (write)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                             : "memory");
+        }
+    if (found) atomicOr(&c->flags[parity], 1);
+}
+
+// What clean_v took out, for one row and 32 columns.
+SV_DEV void add_unclean(const AttnParams& p, const Seg& s, int node, int col0, float (&o)[32]) {
+    const int j0 = (int)max(0LL, (long long)s.first * kKv - s.L);
+    const int j1 = (int)min((long long)s.n, (long long)s.last * kKv - s.L);
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + s.h * p.head_stride + col0;
+    for (int j = j0; j < j1; ++j) {
+        const bool see = p.mask ? __ldg(p.mask + ((long long)s.b * p.N + node) * p.N + j) != 0 : j <= node;
+        if (!see) continue;
+        const long long pos = (long long)s.L + j;
+        const int id = __ldg(p.table + s.b * p.table_stride + (pos >> p.page_shift));
+        if (id < 0 || id >= p.num_pages) continue;
+        const uint16_t* row = v + id * p.page_stride + (pos & ((1 << p.page_shift) - 1)) * p.token_stride;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const uint32_t x = row[e];
+            if ((x & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float(x << 16);
+        }
+    }
+}
+
+SV_DEV uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+SV_DEV void unpack2(uint64_t r, float* x, float* y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(r)); }
+SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+constexpr float kNegInf = -__builtin_inff();
+
+template <int D>
+struct Group {
+    const AttnParams& p;
+    Ctl* c;
+    uint32_t qs, stages;
+    int w, warp, lane, t;       // group, warp of the group, lane, thread of the group = row of its tile
+    uint32_t tm_s, tm_o;        // this warp's lanes of S_w and O_w
+    uint32_t s_phase = 0, o_phase = 0, g_phase = 0;
+
+    // Both groups; false after a timeout.
+    SV_DEV bool meet() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->groups);
+        const bool ok = warp_wait(&c->groups, g_phase, &c->abort);
+        g_phase ^= 1;
+        return ok;
+    }
+
+    SV_DEV void load_q(const Seg& s) {
+        constexpr int C = D / 8;  // 16-byte words of a row
+        const int lo = s.dual ? 128 * w : 0, hi = s.dual ? min(s.rows, lo + 128) : s.rows;
+        const int start = s.dual ? t : w * 128 + t, step = s.dual ? 128 : 256;
+        const uint32_t dst = qs + (s.dual ? w * Shape<D>::kTile : 0u);
+        const uint32_t flip = p.c2 < 0.f ? 0x80008000u : 0u;
+        const int Hq = p.Hkv * p.G;
+        const char* q = reinterpret_cast<const char*>(p.q);
+        for (int i = start; i < (hi - lo) * C; i += step) {
+            const int r = i / C, ch = i - r * C, rr = s.row0 + lo + r, node = rr / p.G;
+            const long long row = ((long long)s.b * p.N + node) * Hq + s.h * p.G + (rr - node * p.G);
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + row * (D * 2)) + ch);
+            const uint32_t a = dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) * 16);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x.x ^ flip), "r"(x.y ^ flip),
+                         "r"(x.z ^ flip), "r"(x.w ^ flip)
+                         : "memory");
+        }
+    }
+
+    // One tile: S -> P, the row's maximum m (octaves) and sum l.
+    SV_DEV void softmax(const uint32_t (&see)[4], bool tail, bool first, float c2, float& m, float& l) {
+        float x[128];
+        tmem_ld128(tm_s, x);
+        if (tail) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                if (!(see[i >> 5] >> (i & 31) & 1)) x[i] = kNegInf;
+        }
+        float mx[8];  // by steps of 16 positions
+#pragma unroll
+        for (int i = 0; i < 128; ++i) mx[i >> 4] = i & 15 ? fmaxf(mx[i >> 4], x[i]) : x[i];
+        const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * c2;
+        if (first) {
+            m = mt;
+        } else {
+            const float mn = fmaxf(m, mt);
+            if (__any_sync(0xFFFFFFFFu, mn - m > kSlack)) {
+                // O_w is at rest: this tile's scores were issued after the last product into it
+                const float f = mn == kNegInf ? 1.f : ex2(m - mn);
+                m = mn;
+                l *= f;
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+                    uint32_t r[32];
+                    tmem_ld32(tm_o + k, o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * f);
+                    tmem_st32(tm_o + k, r);
+                }
+            }
+        }
+        const float ref = m == kNegInf ? 0.f : m;
+        const uint64_t cc = pack2(c2, c2), rr = pack2(-ref, -ref);
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                float& a = x[64 * k + 2 * e];
+                float& b = x[64 * k + 2 * e + 1];
+                unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[e & 3] = add2(sum[e & 3], pack2(a, b));
+                pk[e] = pack_bf16(a, b);
+            }
+            tmem_st32(tm_s + 32 * k, pk);
+        }
+        float a, b;
+        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &a, &b);
+        l += a + b;
+        // what the rounding took from the heavy weights, by steps of 16 positions
+        const float cut = __log2f(l) - kHeavy + ref;
+        uint32_t heavy = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) heavy |= mx[k] * c2 > cut ? 1u << k : 0u;
+        heavy = __reduce_or_sync(0xFFFFFFFFu, heavy);
+        if (lane == 0) c->heavy[w][warp] = heavy;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            uint32_t lo[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+            if (heavy >> k & 1)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float u = x[16 * k + 2 * e], v = x[16 * k + 2 * e + 1];
+                    const uint32_t hi = pack_bf16(u, v);
+                    lo[e] = pack_bf16(u - __uint_as_float(hi << 16), v - __uint_as_float(hi & 0xFFFF0000u));
+                }
+            tmem_st8(tm_s + 64 + 8 * k, lo);
+        }
+        tmem_wait_st();
+    }
+
+    // 32 columns of a row's result.
+    SV_DEV void put(const Seg& s, int rr, int col, const float (&o)[32], float inv) {
+        if (s.whole) {
+            const int node = (s.row0 + rr) / p.G, g = (s.row0 + rr) - node * p.G;
+            const long long row = ((long long)s.b * p.N + node) * (p.Hkv * p.G) + s.h * p.G + g;
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.out) + (row * D + col) * 2);
+            if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    dst[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv),
+                                        pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
+                                        pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
+                                        pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+        } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)s.slot * kRows + rr) * D + col);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+    }
+    SV_DEV void put_ml(const Seg& s, int rr, float m, float l) {
+        if (!s.whole) {
+            p.part_ml[(long long)s.slot * kRows + rr] = make_float2(m, l);
+        } else if (p.lse) {
+            const int node = (s.row0 + rr) / p.G, g = (s.row0 + rr) - node * p.G;
+            p.lse[((long long)s.b * p.N + node) * (p.Hkv * p.G) + s.h * p.G + g] = lse_of(m, l);
+        }
+    }
+
+    // A segment's result: each group its own rows, or group 0 both groups' sums.
+    SV_DEV bool finish(const Seg& s, int parity, float m, float l) {
+        const bool joined = !s.dual && s.steps > 1;
+        const int rr = s.dual ? 128 * w + t : t;
+        const bool mine = rr < s.rows;
+        const bool warp_on = (s.dual ? 128 * w : 0) + warp * 32 < s.rows && s.steps > w;
+        if (s.steps > w) {
+            if (!warp_wait(&c->o_full[w], o_phase, &c->abort)) return false;
+            o_phase ^= 1;
+            tc_fence_after();
+        }
+        const int fl = *reinterpret_cast<volatile int*>(&c->flags[parity]);
+        const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
+        const uint32_t box = qs + Shape<D>::kTile + t * 128;  // group 1's columns on their way to group 0
+        if (!joined) {
+            if (!warp_on) return true;
+            if (fl & 2) l = __uint_as_float(0x7FC00000u);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+            for (int k = 0; k < D; k += 32) {
+                float o[32];
+                tmem_ld32(tm_o + k, o);
+                if (mine) {
+                    if (fl & 1) add_unclean(p, s, node, k, o);
+                    put(s, rr, k, o, inv);
+                }
+            }
+            if (mine) put_ml(s, rr, m, l);
+            return true;
+        }
+        float w0 = 1.f, w1 = 0.f, inv = 0.f;
+        if (w == 1) c->ml[t] = make_float2(m, l);
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+            float o[32];
+            if (warp_on) tmem_ld32(tm_o + k, o);
+            if (w == 1 && warp_on)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(box + ((i ^ (t & 7)) * 16)), "f"(o[4 * i]),
+                                 "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3])
+                                 : "memory");
+            if (!meet()) return false;
+            if (w == 0 && warp_on) {
+                if (k == 0) {
+                    const float2 z = c->ml[t];
+                    const float mn = fmaxf(m, z.x), ref = mn == kNegInf ? 0.f : mn;
+                    w0 = ex2(m - ref);
+                    w1 = ex2(z.x - ref);
+                    m = mn;
+                    l = l * w0 + z.y * w1;
+                    if (fl & 2) l = __uint_as_float(0x7FC00000u);
+                    inv = l == 0.f ? 0.f : 1.f / l;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float4 z;
+                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                                 : "=f"(z.x), "=f"(z.y), "=f"(z.z), "=f"(z.w)
+                                 : "r"(box + ((i ^ (t & 7)) * 16)));
+                    o[4 * i] = o[4 * i] * w0 + z.x * w1;
+                    o[4 * i + 1] = o[4 * i + 1] * w0 + z.y * w1;
+                    o[4 * i + 2] = o[4 * i + 2] * w0 + z.z * w1;
+                    o[4 * i + 3] = o[4 * i + 3] * w0 + z.w * w1;
+                }
+                if (mine) {
+                    if (fl & 1) add_unclean(p, s, node, k, o);
+                    put(s, rr, k, o, inv);
+                }
+            }
+            if (!meet()) return false;
+        }
+        if (w == 0 && warp_on && mine) put_ml(s, rr, m, l);
+        return true;
+    }
+
+    SV_DEV void run(Walk walk) {
+        constexpr int NS = Shape<D>::kStages;
+        const float c2 = fabsf(p.c2);
+        uint32_t ring0 = 0;
+        int parity = 0;
+        Seg s;
+        bool ok = true;
+        while (walk.next(p, &s)) {
+            // both groups are done with the last segment's queries, flags and joined sums
+            if (!(ok = meet())) break;
+            if (w == 0 && t == 0) c->flags[parity ^ 1] = 0;
+            load_q(s);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            {   // a page that does not exist anywhere under this segment's tiles
+                const long long lo = (long long)s.first * kKv >> p.page_shift;
+                const long long hi = (min(s.len, (long long)s.last * kKv) - 1) >> p.page_shift;
+                bool bad = false;
+                for (long long i = lo + w * 128 + t; i <= hi; i += 256) {
+                    const int id = __ldg(p.table + s.b * p.table_stride + i);
+                    bad |= id < 0 || id >= p.num_pages;
+                }
+                if (bad) atomicOr(&c->flags[parity], 2);
+            }
+            mbar_arrive(&c->q_full);
+
+            float m = kNegInf, l = 0.f;
+            const int rr = s.dual ? 128 * w + t : t;
+            const bool warp_on = (s.dual ? 128 * w : 0) + warp * 32 < s.rows;
+            const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
+            for (int vt = w; vt < s.steps; vt += 2) {
+                const int i = s.dual ? vt >> 1 : vt;
+                const long long pos0 = (long long)(s.first + i) * kKv;
+                const bool tail = pos0 + kKv > s.L;
+                uint32_t see[4];
+                if (tail && warp_on)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) see[k] = see_bits(p, s, node, pos0 + 32 * k);
+                if (!(ok = warp_wait(&c->s_full[w], s_phase, &c->abort))) break;
+                s_phase ^= 1;
+                __syncwarp();
+                tc_fence_after();
+                if (!warp_on && lane == 0) c->heavy[w][warp] = 0u;
+                if (warp_on) softmax(see, tail, vt < 2, c2, m, l);
+                if (tail && (!s.dual || w == 0)) {
+                    const uint32_t ring = ring0 + ring_v(s, i);
+                    if (!(ok = warp_wait(&c->full[ring % NS], (ring / NS) & 1, &c->abort))) break;
+                    clean_v<D>(c, s, stages + ring % NS * Shape<D>::kTile, s.first + i, t, parity);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->p_full[w]);
+            }
+            if (!ok) break;
+            __syncwarp();
+            if (!(ok = finish(s, parity, m, l))) break;
+            tc_fence_before();
+            ring0 += 2 * (s.last - s.first);
+            parity ^= 1;
+        }
+        if (!ok) c->abort = 1;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(NT, 1)
+    attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mk,
+                   const __grid_constant__ CUtensorMap mv) {
+    extern __shared__ unsigned char dyn[];
+    unsigned char* mem = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023);
+    Ctl* c = reinterpret_cast<Ctl*>(mem);
+    const uint32_t qs = smem_u32(mem) + 2048, stages = qs + 2 * Shape<D>::kTile;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    attn_edges<bf16_t, NT>(p);
+    const long long total = attn_locate<kKv, NT>(p, &c->scan, [&](long long t, int i) -> long long {
+        const int n = attn_parts(t, gridDim.x);
+        return i == 0 && (int)blockIdx.x < n ? attn_part(t, n, blockIdx.x) : -1;
+    });
+    const int parts = attn_parts(total, gridDim.x);
+    if ((int)blockIdx.x >= parts) return;
+    Walk walk;
+    walk.begin = walk.t = attn_part(total, parts, blockIdx.x);
+    walk.end = attn_part(total, parts, blockIdx.x + 1);
+    walk.b = c->scan.place[0].b;
+    walk.base = c->scan.place[0].base;
+
+    if (tid == 0) {
+        for (int i = 0; i < Shape<D>::kStages; ++i) {
+            mbar_init(&c->full[i], 1);
+            mbar_init(&c->empty[i], 1);
+        }
+        mbar_init(&c->q_full, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->s_full[i], 1);
+            mbar_init(&c->p_full[i], 4);
+            mbar_init(&c->o_full[i], 1);
+            c->flags[i] = 0;
+        }
+        mbar_init(&c->groups, 8);
+        mbar_init(&c->drain, 1);
+        c->abort = 0;
+        mbar_init_fence();
+    }
+    if (warp == 9) tmem_alloc512(&c->tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c->tmem;
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupRegs));
+        const int w = warp >> 2, lanes = (warp & 3) * 32;
+        Group<D> g{p, c, qs, stages, w, warp & 3, lane, tid & 127, tmem + ((uint32_t)lanes << 16) + 128 * w,
+                   tmem + ((uint32_t)lanes << 16) + 256 + 128 * w};
+        g.run(walk);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == 8) produce<D>(p, c, &mk, &mv, stages, walk);
+        if (warp == 9 && lane == 0) issue<D>(p, c, qs, stages, walk);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (c->abort) {  // copies and products in flight end before the CTA does
+        constexpr uint32_t NS = Shape<D>::kStages;
+        if (tid == 8 * 32)
+            for (uint32_t r = c->loads > NS ? c->loads - NS : 0; r < c->loads; ++r)
+                mbar_wait(&c->full[r % NS], (r / NS) & 1, nullptr);
+        if (tid == 9 * 32) {
+            mma_commit(&c->drain);
+            mbar_wait(&c->drain, 0, nullptr);
+        }
+        __syncthreads();
+    }
+    if (warp == 9) tmem_free512(tmem);
+    if (tid == 0 && c->abort && p.status) {
+        // a wait gave up: this part's sequences are not whole
+        Seg s;
+        while (walk.next(p, &s)) atomicMax(p.status + s.b, kETimeout);
+    }
+}
+
+// The 128-byte-swizzled view of k or v that the producer copies boxes of: 64
+// elements x (page_size, at most 128) slots of one head of one page.
+bool make_map(CUtensorMap* map, const AttnParams& p, const void* base) {
+    using Encode = decltype(&cuTensorMapEncodeTiled);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (!encode) return false;
+    const int ps = 1 << p.page_shift;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)ps, (cuuint64_t)p.Hkv, (cuuint64_t)p.num_pages};
+    // the stride of an index that only takes 0 may be anything that the encoding accepts
+    const cuuint64_t any = (cuuint64_t)p.D * 2;
+    const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, p.Hkv > 1 ? (cuuint64_t)p.head_stride * 2 : any,
+                                   p.num_pages > 1 ? (cuuint64_t)p.page_stride * 2 : any};
+    for (const cuuint64_t s : strides)
+        if (s == 0 || s % 16 != 0 || s >= (1ull << 40)) return false;
+    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(ps, kKv), 1, 1}, step[4] = {1, 1, 1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+cudaError_t launch_tc(const AttnParams& p, const AttnPlan& plan, const CUtensorMap& mk, const CUtensorMap& mv,
+                      cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Shape<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    attn_tc_kernel<D><<<plan.grid, NT, Shape<D>::kSmem, st>>>(p, mk, mv);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_attention_combine_tc(p, plan, st);
+}
+
+}  // namespace
+
+int attention_tc_rows() { return kRows; }
+int attention_tc_kv() { return kKv; }
+
+bool attention_tc_maps(const AttnParams& p, AttnMaps* m) {
+    static_assert(sizeof(AttnMaps) >= 2 * sizeof(CUtensorMap), "two maps");
+    CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(m);
+    return make_map(maps, p, p.k) && make_map(maps + 1, p, p.v);
+}
+
+cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const AttnMaps& m, cudaStream_t st) {
+    const CUtensorMap* maps = reinterpret_cast<const CUtensorMap*>(&m);
+    return p.D == 128 ? launch_tc<128>(p, plan, maps[0], maps[1], st) : launch_tc<64>(p, plan, maps[0], maps[1], st);
+}
+
+SV_DEBUG_READER(attention_tc)
+
+}  // namespace sv

@@ -74,13 +74,7 @@ sv::CacheView view_of(const spec_cache* c, spec_dtype dtype) {
 }
 
 // The attention's grid and workspace: functions of the shape alone.
-sv::AttnPlan attention_plan(int D, spec_dtype dtype) {
-    sv::AttnPlan a = {};
-    const int dt = dtype == SPEC_F32 ? 0 : 1;
-    a.tc = false;
-    a.rows = sv::attention_simt_rows();
-    a.kv = sv::attention_simt_kv(dt, D);
-    a.grid = kSms * sv::attention_simt_ctas(dt, D);
+sv::AttnPlan attention_layout(sv::AttnPlan a, int D) {
     size_t o = 0;
     a.part_o = o;
     o = al(o + (size_t)2 * a.grid * a.rows * D * sizeof(float));
@@ -88,6 +82,30 @@ sv::AttnPlan attention_plan(int D, spec_dtype dtype) {
     o = al(o + (size_t)2 * a.grid * a.rows * sizeof(float2));
     a.total = o;
     return a;
+}
+
+sv::AttnPlan simt_plan(int D, spec_dtype dtype) {
+    const int dt = dtype == SPEC_F32 ? 0 : 1;
+    sv::AttnPlan a = {};
+    a.rows = sv::attention_simt_rows();
+    a.kv = sv::attention_simt_kv(dt, D);
+    a.grid = kSms * sv::attention_simt_ctas(dt, D);
+    return attention_layout(a, D);
+}
+
+sv::AttnPlan tc_plan(int D) {
+    sv::AttnPlan a = {};
+    a.rows = sv::attention_tc_rows();
+    a.kv = sv::attention_tc_kv();
+    a.grid = kSms;
+    return attention_layout(a, D);
+}
+
+bool tc_shape(int D, spec_dtype dtype) { return dtype == SPEC_BF16 && (D == 64 || D == 128); }
+
+size_t attention_bytes(int D, spec_dtype dtype) {
+    const size_t simt = simt_plan(D, dtype).total;
+    return tc_shape(D, dtype) ? std::max(simt, tc_plan(D).total) : simt;
 }
 
 bool attention_shape_ok(int B, int N, int q_heads, int kv_heads, int D) {
@@ -101,7 +119,7 @@ extern "C" {
 
 size_t spec_tree_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim, spec_dtype dtype) {
     if (!attention_shape_ok(B, N, q_heads, kv_heads, head_dim) || !dtype_ok(dtype)) return 0;
-    return attention_plan(head_dim, dtype).total;
+    return attention_bytes(head_dim, dtype);
 }
 
 spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dtype dtype,
@@ -117,8 +135,7 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
         return SPEC_EINVAL;
     const float c2 = scale * 1.4426950408889634f;
     if (!std::isfinite(scale) || !std::isfinite(c2)) return SPEC_EINVAL;
-    const sv::AttnPlan plan = attention_plan(cache->head_dim, dtype);
-    if (ws_bytes < plan.total) return SPEC_EINVAL;
+    if (ws_bytes < attention_bytes(cache->head_dim, dtype)) return SPEC_EINVAL;
     sv::AttnParams p = {};
     p.q = q;
     p.k = cache->k;
@@ -139,14 +156,26 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
     p.num_pages = cache->num_pages;
     p.max_pages = max_pages;
     p.page_shift = shift_of(cache->page_size);
-    p.tile_rows = plan.rows;
     p.c2 = c2;
     p.out = out;
     p.lse = lse;
     p.status = status;
-    p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);
-    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.part_ml);
-    return done(sv::launch_attention_simt(p, dtype == SPEC_F32 ? 0 : 1, plan, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    auto use = [&](const sv::AttnPlan& plan) {
+        p.tile_rows = plan.rows;
+        p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);
+        p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.part_ml);
+    };
+    sv::AttnMaps maps;
+    // (a zero scale would multiply a masked score of -inf by zero there)
+    if (tc_shape(p.D, dtype) && scale != 0.f && sv::attention_tc_maps(p, &maps)) {
+        const sv::AttnPlan plan = tc_plan(p.D);
+        use(plan);
+        return done(sv::launch_attention_tc(p, plan, maps, st));
+    }
+    const sv::AttnPlan plan = simt_plan(p.D, dtype);
+    use(plan);
+    return done(sv::launch_attention_simt(p, dtype == SPEC_F32 ? 0 : 1, plan, st));
 }
 
 spec_status spec_cache_append(const void* k, const void* v, const spec_cache* cache, spec_dtype dtype,
