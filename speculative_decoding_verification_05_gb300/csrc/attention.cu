@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ A
     float* qs = reinterpret_cast<float*>(vs + (size_t)2 * KV * D * sizeof(E));
     float* ws = qs + kRows * D + warp * 2 * KV;  // the warp's weights [2][KV]
 
-    attn_edges<E, NT>(p);
+    attn_edges<E>(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
     int parts = 0;
     const long long total = attn_locate<KV, NT>(p, &scan, [&](long long t, int i) -> long long {
         const int n = attn_parts(t, gridDim.x);

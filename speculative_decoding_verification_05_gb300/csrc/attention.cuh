@@ -133,35 +133,36 @@ SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc, Pick pick) {
 SV_DEV long long attn_part(long long total, int parts, int c) { return total * c / parts; }
 SV_DEV int attn_parts(long long total, int grid) { return (int)(total < grid ? total : grid); }
 
-// The sequences' own checks, one sequence per CTA and turn (all NT threads):
-// status, and the rows that no unit writes: zeros (lse -inf) from the node
-// count on, NaN everywhere for a sequence with bad data. A bad page id is
-// reported here; the units that meet it make their rows NaN.
-template <typename E, int NT>
-SV_DEV void attn_edges(const AttnParams& p) {
-    const int tid = threadIdx.x;
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+// The sequences' own checks and edges, shared out over `warps` warps of the
+// grid (this is warp `gw`; as many warps a sequence as there are): status, and
+// the rows that no unit writes, zeros (lse -inf) from the node count on and NaN
+// everywhere for a sequence with bad data. A bad page id is reported here; the
+// units that meet it make their rows NaN. late: a wait of this CTA gave up.
+template <typename E>
+SV_DEV void attn_edges(const AttnParams& p, int gw, int warps, bool late = false) {
+    const int lane = threadIdx.x & 31, team = max(1, warps / p.B), member = gw % team;
+    for (int b = gw / team; b < p.B; b += (warps + team - 1) / team) {
         const AttnSeq s = attn_seq(p, b);
-        bool bad = s.n < 0;
-        if (p.status) {
+        if (p.status && member == 0) {
+            bool bad = s.n < 0;
             if (s.n > 0) {
                 const int pages = (int)(((long long)s.L + s.n + (1 << p.page_shift) - 1) >> p.page_shift);
-                for (int i = tid; i < pages; i += NT) {
+                for (int i = lane; i < pages; i += 32) {
                     const int id = __ldg(p.table + b * p.table_stride + i);
                     bad |= id < 0 || id >= p.num_pages;
                 }
             }
-            bad = __syncthreads_or(bad);
-            if (tid == 0) p.status[b] = bad ? kEData : kOk;
+            bad = __any_sync(0xFFFFFFFFu, bad) != 0;
+            if (lane == 0) p.status[b] = bad ? kEData : late ? kETimeout : kOk;
         }
         const int Hq = p.Hkv * p.G, n = max(s.n, 0);
         const long long row0 = ((long long)b * p.N + n) * Hq, rows = (long long)(p.N - n) * Hq;
         const long long words = rows * p.D * (long long)sizeof(E) / 16;
         const uint32_t fill = s.n < 0 ? (sizeof(E) == 4 ? 0x7FC00000u : 0x7FC07FC0u) : 0u;
         uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<E*>(p.out) + row0 * p.D);
-        for (long long i = tid; i < words; i += NT) o[i] = make_uint4(fill, fill, fill, fill);
+        for (long long i = member * 32 + lane; i < words; i += team * 32) o[i] = make_uint4(fill, fill, fill, fill);
         if (p.lse)
-            for (long long i = tid; i < rows; i += NT)
+            for (long long i = member * 32 + lane; i < rows; i += team * 32)
                 p.lse[row0 + i] = __uint_as_float(s.n < 0 ? 0x7FC00000u : 0xFF800000u);
     }
 }

@@ -1,22 +1,26 @@
 // Tree attention over a paged cache on the tensor cores (bf16, heads of 64 and
 // 128; attention.cuh: the mathematics and the division of the work).
 //
-// One CTA an SM, a persistent part of the range each. Three groups of four
-// warps, the last two warps idle:
+// One CTA an SM, a persistent part of the range each, twelve warps:
 //   producer   (warp 8) copies K and V tiles of 128 positions page by page
 //              (tensor copies with the 128-byte swizzle) into a ring of stages;
-//   issuer     (warp 9, one lane) issues the products: S = Q K^T into tensor
+//   issuer     (warp 9) issues the products: S = Q K^T into tensor
 //              memory, and O += P V with P taken from tensor memory;
+//   helpers    (warps 10, 11) bring a unit's queries (while the last one's
+//              results are still being written), check its pages and write the
+//              rows that no unit covers;
 //   two groups (warps 0-3, 4-7) of 128 threads, a row each: the softmax between
 //              the two products, and the results.
 // The groups are two streams that the tensor core serves in turn, one's
 // products while the other computes its softmax:
 //   more than 128 rows  both streams go over the same tiles, each for a half of
 //                       the unit's 256 rows (a tile is read once for 256 rows);
-//   else                both have the same rows and take alternate tiles; their
-//                       sums are joined at the end.
-// S_w takes columns 128 w .. of tensor memory, P_w (bf16, two a column) its
-// first half once the group has read S_w; O_w columns 256 + 128 w. Products
+//   else                both have the same rows and take alternate tiles; group
+//                       0 joins their sums at the end (both O lie in the lanes
+//                       that it can read).
+// S_w takes columns 128 w .. of tensor memory; P_w (bf16, two a column) takes
+// its place 32 positions at a time, 16 columns of weights and 16 of residuals;
+// O_w columns 256 + 128 w. Products
 // are issued by one thread and run in its order, so S_w of the next tile, issued
 // after P_w V, cannot overtake it.
 //
@@ -26,8 +30,8 @@
 // sums l are taken before the weights are rounded to bf16 for the product with
 // V. Where a weight is more than a sixteenth of its row's sum so far, its
 // rounding would show beside the output's own: steps of 16 positions with such
-// a weight are multiplied a second time with what the rounding took (P_w's
-// second half of S_w's columns, zero elsewhere). Lighter weights' roundings
+// a weight are multiplied a second time with what the rounding took (the
+// residuals, zero elsewhere). Lighter weights' roundings
 // average out, and a long row has few heavy ones.
 //
 // Tiles that reach past the context also hold nodes and the end: a thread forms
@@ -66,13 +70,13 @@ struct Shape {
 
 struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full, s_full[2], p_full[2], o_full[2], groups, drain;
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], groups, drain;
     uint32_t loads;  // ring entries filled
     AttnScan scan;
     uint32_t tmem;
     int abort;
-    int flags[2];  // of the segment (by parity): 1 V had elements that are not finite, 2 a bad page
-    uint32_t heavy[2][4];  // steps of 16 positions with heavy weights, by group and warp
+    int flags[4];  // of a segment (its number modulo 4): 1 V had elements that are not finite, 2 a bad page
+    uint8_t heavy[2][4];  // steps of 16 positions with heavy weights, by group and warp (read as one word)
     float2 ml[128];
 };
 static_assert(sizeof(Ctl) <= 2048, "control region");
@@ -99,12 +103,13 @@ struct Walk {
             kt = attn_kv_tiles<kKv>(q);
             rt = attn_row_tiles(p, q);
         }
-        const long long unit = (t - base) / kt;
+        const long long in = t - base;
+        const long long unit = in >> 31 ? in / kt : (long long)((uint32_t)in / (uint32_t)kt);
         s->b = b;
         s->kt = kt;
-        s->first = (int)(t - base - unit * kt);
+        s->first = (int)(in - unit * kt);
         s->last = (int)min((long long)kt, s->first + (end - t));
-        s->h = (int)(unit / rt);
+        s->h = unit >> 31 ? (int)(unit / rt) : (int)((uint32_t)unit / (uint32_t)rt);
         s->row0 = (int)(unit - (long long)s->h * rt) * kRows;
         s->rows = min(kRows, q.n * p.G - s->row0);
         s->L = q.L;
@@ -125,9 +130,24 @@ struct Walk {
 SV_DEV int ring_k(const Seg& s, int i) { return s.dual ? 2 * i : i + max(0, i - 1); }
 SV_DEV int ring_v(const Seg& s, int i) { return s.dual ? 2 * i + 1 : i + min(i + 2, s.last - s.first); }
 
-// A wait by whole warps: every lane gets the same answer.
+// Waits give up after about two seconds, or once `abort` is set. They poll
+// without a suspension of their own: its wake-up costs more than these short
+// waits last.
+SV_DEV bool tc_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    uint64_t start = 0, now;
+    uint32_t n = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity)) {
+        if (++n & 0xFFu) continue;
+        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+        if (!start) start = now;
+        if (now - start > 2000000000ull || (abort && *abort)) return false;
+    }
+    return true;
+}
+// By whole warps: every lane gets the same answer.
 SV_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const int* abort) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort)) != 0;
+    return __all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort)) != 0;
 }
 
 // ---- copies ----------------------------------------------------------------------
@@ -173,66 +193,93 @@ SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CU
 
 // ---- products ---------------------------------------------------------------------
 
+// The whole warp goes through the steps and one elected lane issues: operands
+// broadcast from lane 0 are known to be the same in every lane, so that they
+// stay in uniform registers (issued by one thread from its own registers, a
+// product of 16 positions took 80 to 160 cycles to issue and 64 to run).
+SV_DEV uint32_t uni(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+SV_DEV bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <int D>
-SV_DEV bool issue_s(Ctl* c, uint32_t qs, uint32_t stages, const Seg& s, int vt, uint32_t ring0) {
-    constexpr int NS = Shape<D>::kStages;
-    constexpr uint32_t idesc = mma_idesc(kKv, false);
-    const int w = vt & 1, i = s.dual ? vt >> 1 : vt;
-    const uint32_t ring = ring0 + ring_k(s, i), st = ring % NS;
-    if (!mbar_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
+SV_DEV bool issue_s(Ctl* c, uint32_t tmem, uint32_t qs, uint32_t stages, bool dual, bool last, uint32_t w, uint32_t ring) {
+    constexpr uint32_t NS = Shape<D>::kStages, idesc = mma_idesc(kKv, false);
+    const uint32_t st = uni(ring % NS);
+    if (!warp_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
     tc_fence_after();
-    const uint32_t a = qs + (s.dual ? w * Shape<D>::kTile : 0u), b = stages + st * Shape<D>::kTile;
+    const uint32_t d = tmem + 128 * w;
+    const uint64_t a = mma_desc(qs + (dual ? w * Shape<D>::kTile : 0u), 16, 1024);
+    const uint64_t b = mma_desc(stages + st * Shape<D>::kTile, 16, 1024);
+    if (elected()) {
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-        mma_ss(c->tmem + 128 * w, mma_desc(a + off, 16, 1024), mma_desc(b + off, 16, 1024), idesc, kk > 0);
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+            mma_ss(d, a + off, b + off, idesc, kk > 0);
+        }
+        mma_commit(&c->s_full[w]);
+        if (!dual || w == 1) mma_commit(&c->empty[st]);
+        if (last) mma_commit(&c->q_empty);
     }
-    mma_commit(&c->s_full[w]);
-    if (!s.dual || w == 1) mma_commit(&c->empty[st]);
+    __syncwarp();
     return true;
 }
 
 template <int D>
-SV_DEV bool issue_o(Ctl* c, uint32_t stages, const Seg& s, int vt, uint32_t ring0, uint32_t* p_phase) {
-    constexpr int NS = Shape<D>::kStages;
-    constexpr uint32_t idesc = mma_idesc(D, true);
-    const int w = vt & 1, i = s.dual ? vt >> 1 : vt;
-    const uint32_t ring = ring0 + ring_v(s, i), st = ring % NS;
-    if (!mbar_wait(&c->p_full[w], (*p_phase >> w) & 1, &c->abort)) return false;
-    *p_phase ^= 1u << w;
-    if (!mbar_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
+SV_DEV bool issue_o(Ctl* c, uint32_t tmem, uint32_t stages, bool dual, bool first, bool last, uint32_t w, uint32_t ring,
+                    uint32_t p_phase) {
+    constexpr uint32_t NS = Shape<D>::kStages, idesc = mma_idesc(D, true);
+    const uint32_t st = uni(ring % NS);
+    if (!warp_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
+    if (!warp_wait(&c->p_full[w], p_phase, &c->abort)) return false;
     tc_fence_after();
-    const uint32_t b = stages + st * Shape<D>::kTile;
-#pragma unroll
-    for (int kk = 0; kk < kKv / 16; ++kk)
-        mma_ts(c->tmem + 256 + 128 * w, c->tmem + 128 * w + kk * 8, mma_desc(b + kk * 2048, kHalf, 1024), idesc,
-               vt >= 2 || kk > 0);
-    const volatile uint32_t* hv = c->heavy[w];
-    const uint32_t heavy = hv[0] | hv[1] | hv[2] | hv[3];
-    if (heavy)
+    uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w]);  // a byte of each warp
+    heavy |= heavy >> 16;
+    heavy = uni((heavy | heavy >> 8) & 0xFFu);
+    const uint32_t d = tmem + 256 + 128 * w, a = tmem + 128 * w;
+    const uint64_t b = mma_desc(stages + st * Shape<D>::kTile, kHalf, 1024);
+    if (elected()) {
 #pragma unroll
         for (int kk = 0; kk < kKv / 16; ++kk)
-            if (heavy >> kk & 1)
-                mma_ts(c->tmem + 256 + 128 * w, c->tmem + 128 * w + 64 + kk * 8, mma_desc(b + kk * 2048, kHalf, 1024),
-                       idesc, true);
-    if (!s.dual || w == 1) mma_commit(&c->empty[st]);
-    if (vt + 2 >= s.steps) mma_commit(&c->o_full[w]);
+            mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
+        if (heavy) {
+#pragma unroll 1
+            for (int kk = 0; kk < kKv / 16; ++kk)
+                if (heavy >> kk & 1)
+                    mma_ts(d, a + (kk >> 1) * 32 + 16 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, true);
+        }
+        if (!dual || w == 1) mma_commit(&c->empty[st]);
+        if (last) mma_commit(&c->o_full[w]);
+    }
+    __syncwarp();
     return true;
 }
 
 template <int D>
 SV_DEV void issue(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Walk walk) {
+    const uint32_t tmem = uni(c->tmem);
     uint32_t ring0 = 0, p_phase = 0, q_phase = 0;
     Seg s;
     bool ok = true;
     while (ok && walk.next(p, &s)) {
-        ok = mbar_wait(&c->q_full, q_phase, &c->abort);
+        const bool dual = uni(s.dual);
+        const int steps = (int)uni(s.steps);
+        ok = warp_wait(&c->q_full, q_phase, &c->abort);
         q_phase ^= 1;
-        if (ok) ok = issue_s<D>(c, qs, stages, s, 0, ring0);
-        if (ok && s.steps > 1) ok = issue_s<D>(c, qs, stages, s, 1, ring0);
-        for (int vt = 0; ok && vt < s.steps; ++vt) {
-            ok = issue_o<D>(c, stages, s, vt, ring0, &p_phase);
-            if (ok && vt + 2 < s.steps) ok = issue_s<D>(c, qs, stages, s, vt + 2, ring0);
+#pragma unroll 1
+        for (int vt = -2; ok && vt < steps; ++vt) {
+            const uint32_t w = uni(vt & 1);
+            if (vt >= 0) {
+                ok = issue_o<D>(c, tmem, stages, dual, vt < 2, vt + 2 >= steps, w, ring0 + ring_v(s, dual ? vt >> 1 : vt),
+                                p_phase >> w & 1);
+                p_phase ^= 1u << w;
+            }
+            if (ok && vt + 2 < steps)
+                ok = issue_s<D>(c, tmem, qs, stages, dual, vt + 3 == steps, w,
+                                ring0 + ring_k(s, dual ? (vt + 2) >> 1 : vt + 2));
         }
         ring0 += 2 * (s.last - s.first);
     }
@@ -241,75 +288,98 @@ SV_DEV void issue(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Wal
 
 // ---- softmax and results ------------------------------------------------------------
 
-// 32 visibility bits of a row from position p0 on. Node j of the row's own
-// sequence is at position L + j.
-SV_DEV uint32_t see_bits(const AttnParams& p, const Seg& s, int node, long long p0) {
-    const long long ctx = s.L - p0;
-    uint32_t bits = ctx >= 32 ? 0xFFFFFFFFu : ctx <= 0 ? 0u : (1u << ctx) - 1u;
-    if (bits == 0xFFFFFFFFu) return bits;
-    if (!p.mask) {
-        const long long upto = (long long)s.L + node + 1 - p0;  // the row sees positions below this
-        return upto >= 32 ? 0xFFFFFFFFu : upto <= 0 ? 0u : (1u << upto) - 1u;
+// Word i (4 bytes from the aligned address at or below the mask's start) with
+// the bytes outside the mask left out.
+SV_DEV uint32_t mask_edge(const uint8_t* start, long long off, long long bytes, long long i) {
+    uint32_t x = 0;
+#pragma unroll 1
+    for (int e = 0; e < 4; ++e) {
+        const long long at = 4 * i + e;
+        if (at >= off && at < off + bytes) x |= (uint32_t)__ldg(start + at) << (8 * e);
     }
-    const uint8_t* row = p.mask + ((long long)s.b * p.N + node) * p.N;
-    const uint8_t* all_end = p.mask + (long long)p.B * p.N * p.N;
-    const long long j0 = p0 - s.L;  // node of bit 0 (negative: context)
+    return x;
+}
+
+// The visibility of a tile's 128 positions for one row, 32 a word. Node j of
+// the row's own sequence is at position L + j.
+SV_DEV void see_bits(const AttnParams& p, const Seg& s, int node, long long pos0, uint4* see) {
+    const long long off = (uintptr_t)p.mask & 3, bytes = (long long)p.B * p.N * p.N;
+    const long long full0 = off ? 1 : 0, full1 = ((off + bytes) >> 2) - 1;  // first and last whole word
+    const uint8_t* start = p.mask - off;
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        const long long p0 = pos0 + 32 * k;
+        const int ctx = (int)min(32LL, max(0LL, s.L - p0));                   // bits below: context
+        const int upto = (int)min(32LL, max(0LL, (p.mask ? s.len : (long long)s.L + node + 1) - p0));  // none from here on
+        const uint32_t low = ctx == 32 ? 0xFFFFFFFFu : (1u << ctx) - 1u;
+        const uint32_t in = upto == 32 ? 0xFFFFFFFFu : (1u << upto) - 1u;
+        uint32_t bits = in;
+        if (p.mask && (in & ~low)) {
+            const long long o = off + ((long long)s.b * p.N + node) * p.N + (p0 - s.L), i0 = o >> 2;
+            const uint32_t sh = (uint32_t)(o & 3) * 8;
+            uint32_t wd[9];
+            if (full1 >= full0) {
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-        const long long j = j0 + 4 * g;
-        if (j + 3 < 0 || j >= s.n) continue;
-        const uint8_t* a = row + j;
-        const uint32_t shift = ((uintptr_t)a & 3) * 8;
-        const uint8_t* down = a - ((uintptr_t)a & 3);
-        if (j >= 0 && j + 4 <= s.n && down >= p.mask && down + 8 <= all_end) {
-            const uint32_t lo = __ldg(reinterpret_cast<const uint32_t*>(down));
-            const uint32_t hi = shift ? __ldg(reinterpret_cast<const uint32_t*>(down) + 1) : 0u;
-            const uint32_t four = __vsetne4(__funnelshift_r(lo, hi, shift), 0u);
-            bits |= ((four * 0x01020408u) >> 24 & 0xFu) << (4 * g);
-        } else {
-            for (int e = 0; e < 4; ++e)
-                if (j + e >= 0 && j + e < s.n && __ldg(a + e) != 0) bits |= 1u << (4 * g + e);
+                for (int i = 0; i < 9; ++i)
+                    wd[i] = __ldg(reinterpret_cast<const uint32_t*>(start) + min(max(i0 + i, full0), full1));
+            }
+            if (i0 < full0 || i0 + 8 > full1 || full1 < full0) {  // the mask's first or last bytes are near
+                // (few threads; indexes of the array have to be constants)
+#pragma unroll
+                for (int i = 0; i < 9; ++i)
+                    if (i0 + i < full0 || i0 + i > full1) wd[i] = mask_edge(start, off, bytes, i0 + i);
+            }
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                m |= ((__vsetne4(__funnelshift_r(wd[i], wd[i + 1], sh), 0u) * 0x01020408u) >> 24 & 0xFu) << (4 * i);
+            bits &= m;
         }
+        bits = (low & in) | (bits & ~low);
+        if (k == 0) see->x = bits;
+        if (k == 1) see->y = bits;
+        if (k == 2) see->z = bits;
+        if (k == 3) see->w = bits;
     }
-    return bits;
 }
 
 // Rows of a V tile past the context: rows past the end become zero, elements
 // that are not finite too (flag 1). Thread t owns position t of the tile.
 template <int D>
-SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int tile, int t, int parity) {
+SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int tile, int t, int slot) {
     const long long pos = (long long)tile * kKv + t;
     if (pos < s.L) return;
-    const bool past = pos >= s.len;
-    bool found = false;
+    uint32_t x[D / 64][8][4];
+    const uint32_t row = tile_addr + t * 128;
+    if (pos >= s.len) {
 #pragma unroll
-    for (int half = 0; half < D / 64; ++half)
+        for (int i = 0; i < D / 64 * 8; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(row + (i >> 3) * kHalf + (((i & 7) ^ (t & 7)) * 16)),
+                         "r"(0u)
+                         : "memory");
+        return;
+    }
+    uint32_t any = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t a = tile_addr + half * kHalf + t * 128 + ((i ^ (t & 7)) * 16);
-            uint32_t x[4] = {0u, 0u, 0u, 0u};
-            bool write = past;
-            if (!past) {
-                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                             : "r"(a));
+    for (int i = 0; i < D / 64 * 8; ++i) {
+        uint32_t(&y)[4] = x[i >> 3][i & 7];
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                     : "r"(row + (i >> 3) * kHalf + (((i & 7) ^ (t & 7)) * 16)));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if ((x[e] & 0x7F80u) == 0x7F80u) {
-                        x[e] &= 0xFFFF0000u;
-                        write = found = true;
-                    }
-                    if ((x[e] & 0x7F800000u) == 0x7F800000u) {
-                        x[e] &= 0x0000FFFFu;
-                        write = found = true;
-                    }
-                }
-            }
-            if (write)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
-                             : "memory");
-        }
-    if (found) atomicOr(&c->flags[parity], 1);
+        for (int e = 0; e < 4; ++e) any |= __vcmpeq2(y[e] & 0x7F807F80u, 0x7F807F80u);
+    }
+    if (!any) return;
+    atomicOr(&c->flags[slot], 1);
+#pragma unroll
+    for (int i = 0; i < D / 64 * 8; ++i) {
+        uint32_t(&y)[4] = x[i >> 3][i & 7];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] &= ~__vcmpeq2(y[e] & 0x7F807F80u, 0x7F807F80u);
+        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (i >> 3) * kHalf + (((i & 7) ^ (t & 7)) * 16)),
+                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                     : "memory");
+    }
 }
 
 // What clean_v took out, for one row and 32 columns.
@@ -351,11 +421,55 @@ SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
 
 constexpr float kNegInf = -__builtin_inff();
 
+// ---- queries, pages, edges -----------------------------------------------------------
+
+SV_DEV void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int D>
+SV_DEV void help(const AttnParams& p, Ctl* c, uint32_t qs, Walk walk) {
+    constexpr int C = D / 8, HT = 64;  // 16-byte words of a row, helper threads
+    const int i0 = threadIdx.x - 10 * 32, lane = threadIdx.x & 31;
+    const int Hq = p.Hkv * p.G;
+    const char* q = reinterpret_cast<const char*>(p.q);
+    uint32_t seg = 0;
+    Seg s;
+    while (walk.next(p, &s)) {
+        // (the groups are past segment seg - 3: its products' last was issued before this one's queries are free)
+        if (seg && !warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort)) {
+            c->abort = 1;
+            break;
+        }
+        if (i0 == 0) c->flags[(seg + 1) & 3] = 0;
+        for (int i = i0; i < s.rows * C; i += HT) {
+            const int r = i / C, ch = i - r * C, rr = s.row0 + r, node = rr / p.G, rt = r & 127;
+            const long long row = ((long long)s.b * p.N + node) * Hq + s.h * p.G + (rr - node * p.G);
+            cp16(qs + (r >> 7) * Shape<D>::kTile + (ch >> 3) * kHalf + rt * 128 + (((ch & 7) ^ (rt & 7)) * 16),
+                 q + row * (D * 2) + ch * 16);
+        }
+        // a page that does not exist anywhere under this segment's tiles
+        const long long lo = (long long)s.first * kKv >> p.page_shift;
+        const long long hi = (min(s.len, (long long)s.last * kKv) - 1) >> p.page_shift;
+        bool bad = false;
+        for (long long i = lo + i0; i <= hi; i += HT) {
+            const int id = __ldg(p.table + s.b * p.table_stride + i);
+            bad |= id < 0 || id >= p.num_pages;
+        }
+        if (bad) atomicOr(&c->flags[seg & 3], 2);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&c->q_full);
+        ++seg;
+    }
+}
+
 template <int D>
 struct Group {
     const AttnParams& p;
     Ctl* c;
-    uint32_t qs, stages;
+    uint32_t stages;
     int w, warp, lane, t;       // group, warp of the group, lane, thread of the group = row of its tile
     uint32_t tm_s, tm_o;        // this warp's lanes of S_w and O_w
     uint32_t s_phase = 0, o_phase = 0, g_phase = 0;
@@ -369,37 +483,34 @@ struct Group {
         return ok;
     }
 
-    SV_DEV void load_q(const Seg& s) {
-        constexpr int C = D / 8;  // 16-byte words of a row
-        const int lo = s.dual ? 128 * w : 0, hi = s.dual ? min(s.rows, lo + 128) : s.rows;
-        const int start = s.dual ? t : w * 128 + t, step = s.dual ? 128 : 256;
-        const uint32_t dst = qs + (s.dual ? w * Shape<D>::kTile : 0u);
-        const uint32_t flip = p.c2 < 0.f ? 0x80008000u : 0u;
-        const int Hq = p.Hkv * p.G;
-        const char* q = reinterpret_cast<const char*>(p.q);
-        for (int i = start; i < (hi - lo) * C; i += step) {
-            const int r = i / C, ch = i - r * C, rr = s.row0 + lo + r, node = rr / p.G;
-            const long long row = ((long long)s.b * p.N + node) * Hq + s.h * p.G + (rr - node * p.G);
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + row * (D * 2)) + ch);
-            const uint32_t a = dst + (ch >> 3) * kHalf + r * 128 + (((ch & 7) ^ (r & 7)) * 16);
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x.x ^ flip), "r"(x.y ^ flip),
-                         "r"(x.z ^ flip), "r"(x.w ^ flip)
-                         : "memory");
-        }
+    SV_DEV static void hide(float (&x)[32], const uint4& see, int k) {
+        const uint32_t bits = k == 0 ? see.x : k == 1 ? see.y : k == 2 ? see.z : see.w;
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!(bits >> i & 1)) x[i] = kNegInf;
     }
 
-    // One tile: S -> P, the row's maximum m (octaves) and sum l.
-    SV_DEV void softmax(const uint32_t (&see)[4], bool tail, bool first, float c2, float& m, float& l) {
-        float x[128];
-        tmem_ld128(tm_s, x);
-        if (tail) {
+    // One tile: S -> P, the row's maximum m (octaves) and sum l. S is read from
+    // tensor memory twice, for the maximum and for the weights, 32 positions at
+    // a time: the loops stay small (held in registers whole and unrolled, the
+    // row took two to three times as long, waiting for instructions).
+    SV_DEV void softmax(const uint4 see, bool tail, bool first, float c2, float& m, float& l) {
+        float mx[8] = {};  // by steps of 16 positions
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            float x[32];
+            tmem_ld32(tm_s + 32 * k, x);
+            if (tail) hide(x, see, k);
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-                if (!(see[i >> 5] >> (i & 31) & 1)) x[i] = kNegInf;
+            for (int i = 0; i < 6; ++i) mx[i] = mx[i + 2];
+            mx[6] = x[0];
+            mx[7] = x[16];
+#pragma unroll
+            for (int i = 1; i < 16; ++i) {
+                mx[6] = fmaxf(mx[6], x[i]);
+                mx[7] = fmaxf(mx[7], x[16 + i]);
+            }
         }
-        float mx[8];  // by steps of 16 positions
-#pragma unroll
-        for (int i = 0; i < 128; ++i) mx[i >> 4] = i & 15 ? fmaxf(mx[i >> 4], x[i]) : x[i];
         const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * c2;
         if (first) {
@@ -423,45 +534,43 @@ struct Group {
             }
         }
         const float ref = m == kNegInf ? 0.f : m;
-        const uint64_t cc = pack2(c2, c2), rr = pack2(-ref, -ref);
-        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                float& a = x[64 * k + 2 * e];
-                float& b = x[64 * k + 2 * e + 1];
-                unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
-                a = ex2(a);
-                b = ex2(b);
-                sum[e & 3] = add2(sum[e & 3], pack2(a, b));
-                pk[e] = pack_bf16(a, b);
-            }
-            tmem_st32(tm_s + 32 * k, pk);
-        }
-        float a, b;
-        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &a, &b);
-        l += a + b;
-        // what the rounding took from the heavy weights, by steps of 16 positions
-        const float cut = __log2f(l) - kHeavy + ref;
+        // steps with heavy weights (against a lower bound of the new sum)
+        const float cut = __log2f(l + ex2(mt - ref)) - kHeavy + ref;
         uint32_t heavy = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) heavy |= mx[k] * c2 > cut ? 1u << k : 0u;
         heavy = __reduce_or_sync(0xFFFFFFFFu, heavy);
-        if (lane == 0) c->heavy[w][warp] = heavy;
+        if (lane == 0) c->heavy[w][warp] = (uint8_t)heavy;
+        const uint64_t cc = pack2(c2, c2), rr = pack2(-ref, -ref);
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+            float x[32];
+            uint32_t hi[16], lo[16];
+            tmem_ld32(tm_s + 32 * k, x);
+            if (tail) hide(x, see, k);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t lo[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-            if (heavy >> k & 1)
+            for (int e = 0; e < 16; ++e) {
+                float& a = x[2 * e];
+                float& b = x[2 * e + 1];
+                unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[e & 1] = add2(sum[e & 1], pack2(a, b));
+                hi[e] = pack_bf16(a, b);
+                lo[e] = 0u;
+            }
+            if (heavy >> (2 * k) & 3)  // what the rounding took
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float u = x[16 * k + 2 * e], v = x[16 * k + 2 * e + 1];
-                    const uint32_t hi = pack_bf16(u, v);
-                    lo[e] = pack_bf16(u - __uint_as_float(hi << 16), v - __uint_as_float(hi & 0xFFFF0000u));
-                }
-            tmem_st8(tm_s + 64 + 8 * k, lo);
+                for (int e = 0; e < 16; ++e)
+                    lo[e] = pack_bf16(x[2 * e] - __uint_as_float(hi[e] << 16),
+                                      x[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+            tmem_st16(tm_s + 32 * k, hi);
+            tmem_st16(tm_s + 32 * k + 16, lo);
         }
+        float a, b;
+        unpack2(add2(sum[0], sum[1]), &a, &b);
+        l += a + b;
         tmem_wait_st();
     }
 
@@ -494,105 +603,62 @@ struct Group {
     }
 
     // A segment's result: each group its own rows, or group 0 both groups' sums.
-    SV_DEV bool finish(const Seg& s, int parity, float m, float l) {
+    SV_DEV bool finish(const Seg& s, int slot, float m, float l) {
         const bool joined = !s.dual && s.steps > 1;
         const int rr = s.dual ? 128 * w + t : t;
         const bool mine = rr < s.rows;
         const bool warp_on = (s.dual ? 128 * w : 0) + warp * 32 < s.rows && s.steps > w;
         if (s.steps > w) {
-            if (!warp_wait(&c->o_full[w], o_phase, &c->abort)) return false;
-            o_phase ^= 1;
-            tc_fence_after();
+            if (!warp_wait(&c->o_full[w], o_phase >> w & 1, &c->abort)) return false;
+            o_phase ^= 1 << w;
         }
-        const int fl = *reinterpret_cast<volatile int*>(&c->flags[parity]);
+        if (joined && w == 0 && !warp_wait(&c->o_full[1], o_phase >> 1 & 1, &c->abort)) return false;
+        if (w == 0 && s.steps > 1) o_phase ^= 2;  // a phase passed, waited for or not (the groups meet in between)
+        tc_fence_after();
+        if (!warp_on || (joined && w == 1)) return true;
+        const int fl = *reinterpret_cast<volatile int*>(&c->flags[slot]);
         const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
-        const uint32_t box = qs + Shape<D>::kTile + t * 128;  // group 1's columns on their way to group 0
-        if (!joined) {
-            if (!warp_on) return true;
-            if (fl & 2) l = __uint_as_float(0x7FC00000u);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-            for (int k = 0; k < D; k += 32) {
-                float o[32];
-                tmem_ld32(tm_o + k, o);
-                if (mine) {
-                    if (fl & 1) add_unclean(p, s, node, k, o);
-                    put(s, rr, k, o, inv);
-                }
-            }
-            if (mine) put_ml(s, rr, m, l);
-            return true;
+        float w0 = 1.f, w1 = 0.f;
+        if (joined) {
+            const volatile float2* z = &c->ml[t];
+            const float zm = z->x, zl = z->y;
+            const float mn = fmaxf(m, zm), ref = mn == kNegInf ? 0.f : mn;
+            w0 = ex2(m - ref);
+            w1 = ex2(zm - ref);
+            m = mn;
+            l = l * w0 + zl * w1;
         }
-        float w0 = 1.f, w1 = 0.f, inv = 0.f;
-        if (w == 1) c->ml[t] = make_float2(m, l);
+        if (fl & 2) l = __uint_as_float(0x7FC00000u);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
             float o[32];
-            if (warp_on) tmem_ld32(tm_o + k, o);
-            if (w == 1 && warp_on)
+            tmem_ld32(tm_o + k, o);
+            if (joined) {
+                float z[32];
+                tmem_ld32(tm_o + 128 + k, z);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(box + ((i ^ (t & 7)) * 16)), "f"(o[4 * i]),
-                                 "f"(o[4 * i + 1]), "f"(o[4 * i + 2]), "f"(o[4 * i + 3])
-                                 : "memory");
-            if (!meet()) return false;
-            if (w == 0 && warp_on) {
-                if (k == 0) {
-                    const float2 z = c->ml[t];
-                    const float mn = fmaxf(m, z.x), ref = mn == kNegInf ? 0.f : mn;
-                    w0 = ex2(m - ref);
-                    w1 = ex2(z.x - ref);
-                    m = mn;
-                    l = l * w0 + z.y * w1;
-                    if (fl & 2) l = __uint_as_float(0x7FC00000u);
-                    inv = l == 0.f ? 0.f : 1.f / l;
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float4 z;
-                    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
-                                 : "=f"(z.x), "=f"(z.y), "=f"(z.z), "=f"(z.w)
-                                 : "r"(box + ((i ^ (t & 7)) * 16)));
-                    o[4 * i] = o[4 * i] * w0 + z.x * w1;
-                    o[4 * i + 1] = o[4 * i + 1] * w0 + z.y * w1;
-                    o[4 * i + 2] = o[4 * i + 2] * w0 + z.z * w1;
-                    o[4 * i + 3] = o[4 * i + 3] * w0 + z.w * w1;
-                }
-                if (mine) {
-                    if (fl & 1) add_unclean(p, s, node, k, o);
-                    put(s, rr, k, o, inv);
-                }
+                for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + z[e] * w1;
             }
-            if (!meet()) return false;
+            if (mine) {
+                if (fl & 1) add_unclean(p, s, node, k, o);
+                put(s, rr, k, o, inv);
+            }
         }
-        if (w == 0 && warp_on && mine) put_ml(s, rr, m, l);
+        if (mine) put_ml(s, rr, m, l);
         return true;
     }
 
     SV_DEV void run(Walk walk) {
         constexpr int NS = Shape<D>::kStages;
-        const float c2 = fabsf(p.c2);
+        const float c2 = p.c2;
         uint32_t ring0 = 0;
-        int parity = 0;
+        int slot = 0;
         Seg s;
         bool ok = true;
         while (walk.next(p, &s)) {
-            // both groups are done with the last segment's queries, flags and joined sums
+            // (group 0 has read the last segment's O_1)
             if (!(ok = meet())) break;
-            if (w == 0 && t == 0) c->flags[parity ^ 1] = 0;
-            load_q(s);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            {   // a page that does not exist anywhere under this segment's tiles
-                const long long lo = (long long)s.first * kKv >> p.page_shift;
-                const long long hi = (min(s.len, (long long)s.last * kKv) - 1) >> p.page_shift;
-                bool bad = false;
-                for (long long i = lo + w * 128 + t; i <= hi; i += 256) {
-                    const int id = __ldg(p.table + s.b * p.table_stride + i);
-                    bad |= id < 0 || id >= p.num_pages;
-                }
-                if (bad) atomicOr(&c->flags[parity], 2);
-            }
-            mbar_arrive(&c->q_full);
 
             float m = kNegInf, l = 0.f;
             const int rr = s.dual ? 128 * w + t : t;
@@ -602,32 +668,31 @@ struct Group {
                 const int i = s.dual ? vt >> 1 : vt;
                 const long long pos0 = (long long)(s.first + i) * kKv;
                 const bool tail = pos0 + kKv > s.L;
-                uint32_t see[4];
-                if (tail && warp_on)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) see[k] = see_bits(p, s, node, pos0 + 32 * k);
+                uint4 see = make_uint4(0u, 0u, 0u, 0u);
+                if (tail && warp_on) see_bits(p, s, node, pos0, &see);
                 if (!(ok = warp_wait(&c->s_full[w], s_phase, &c->abort))) break;
                 s_phase ^= 1;
                 __syncwarp();
                 tc_fence_after();
-                if (!warp_on && lane == 0) c->heavy[w][warp] = 0u;
+                if (!warp_on && lane == 0) c->heavy[w][warp] = 0;
                 if (warp_on) softmax(see, tail, vt < 2, c2, m, l);
                 if (tail && (!s.dual || w == 0)) {
                     const uint32_t ring = ring0 + ring_v(s, i);
                     if (!(ok = warp_wait(&c->full[ring % NS], (ring / NS) & 1, &c->abort))) break;
-                    clean_v<D>(c, s, stages + ring % NS * Shape<D>::kTile, s.first + i, t, parity);
+                    clean_v<D>(c, s, stages + ring % NS * Shape<D>::kTile, s.first + i, t, slot);
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
+                if (w == 1 && vt + 2 >= s.steps) c->ml[t] = make_float2(m, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c->p_full[w]);
             }
             if (!ok) break;
             __syncwarp();
-            if (!(ok = finish(s, parity, m, l))) break;
+            if (!(ok = finish(s, slot, m, l))) break;
             tc_fence_before();
             ring0 += 2 * (s.last - s.first);
-            parity ^= 1;
+            slot = (slot + 1) & 3;
         }
         if (!ok) c->abort = 1;
     }
@@ -643,13 +708,16 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t qs = smem_u32(mem) + 2048, stages = qs + 2 * Shape<D>::kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    attn_edges<bf16_t, NT>(p);
     const long long total = attn_locate<kKv, NT>(p, &c->scan, [&](long long t, int i) -> long long {
         const int n = attn_parts(t, gridDim.x);
         return i == 0 && (int)blockIdx.x < n ? attn_part(t, n, blockIdx.x) : -1;
     });
     const int parts = attn_parts(total, gridDim.x);
-    if ((int)blockIdx.x >= parts) return;
+    const int edge_warp = 2 * blockIdx.x + (warp & 1), edge_warps = 2 * gridDim.x;  // warps 10 and 11 of every CTA
+    if ((int)blockIdx.x >= parts) {
+        if (warp >= 10) attn_edges<bf16_t>(p, edge_warp, edge_warps);
+        return;
+    }
     Walk walk;
     walk.begin = walk.t = attn_part(total, parts, blockIdx.x);
     walk.end = attn_part(total, parts, blockIdx.x + 1);
@@ -661,12 +729,13 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&c->full[i], 1);
             mbar_init(&c->empty[i], 1);
         }
-        mbar_init(&c->q_full, 256);
+        mbar_init(&c->q_full, 2);
+        mbar_init(&c->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->s_full[i], 1);
             mbar_init(&c->p_full[i], 4);
             mbar_init(&c->o_full[i], 1);
-            c->flags[i] = 0;
+            c->flags[2 * i] = c->flags[2 * i + 1] = 0;
         }
         mbar_init(&c->groups, 8);
         mbar_init(&c->drain, 1);
@@ -682,13 +751,17 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupRegs));
         const int w = warp >> 2, lanes = (warp & 3) * 32;
-        Group<D> g{p, c, qs, stages, w, warp & 3, lane, tid & 127, tmem + ((uint32_t)lanes << 16) + 128 * w,
+        Group<D> g{p, c, stages, w, warp & 3, lane, tid & 127, tmem + ((uint32_t)lanes << 16) + 128 * w,
                    tmem + ((uint32_t)lanes << 16) + 256 + 128 * w};
         g.run(walk);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) produce<D>(p, c, &mk, &mv, stages, walk);
-        if (warp == 9 && lane == 0) issue<D>(p, c, qs, stages, walk);
+        if (warp == 9) issue<D>(p, c, qs, stages, walk);
+        if (warp >= 10) {
+            help<D>(p, c, qs, walk);
+            attn_edges<bf16_t>(p, edge_warp, edge_warps, *reinterpret_cast<volatile int*>(&c->abort) != 0);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -698,10 +771,10 @@ __global__ void __launch_bounds__(NT, 1)
         constexpr uint32_t NS = Shape<D>::kStages;
         if (tid == 8 * 32)
             for (uint32_t r = c->loads > NS ? c->loads - NS : 0; r < c->loads; ++r)
-                mbar_wait(&c->full[r % NS], (r / NS) & 1, nullptr);
+                tc_wait(&c->full[r % NS], (r / NS) & 1, nullptr);
         if (tid == 9 * 32) {
             mma_commit(&c->drain);
-            mbar_wait(&c->drain, 0, nullptr);
+            tc_wait(&c->drain, 0, nullptr);
         }
         __syncthreads();
     }

@@ -167,8 +167,8 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
         p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.part_ml);
     };
     sv::AttnMaps maps;
-    // (a zero scale would multiply a masked score of -inf by zero there)
-    if (tc_shape(p.D, dtype) && scale != 0.f && sv::attention_tc_maps(p, &maps)) {
+    // (that kernel takes the maximum before the scale: it has to be positive)
+    if (tc_shape(p.D, dtype) && scale > 0.f && sv::attention_tc_maps(p, &maps)) {
         const sv::AttnPlan plan = tc_plan(p.D);
         use(plan);
         return done(sv::launch_attention_tc(p, plan, maps, st));
