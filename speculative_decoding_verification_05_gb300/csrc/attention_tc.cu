@@ -4,11 +4,11 @@
 // One CTA an SM, a persistent part of the range each, twelve warps:
 //   producer   (warp 8) copies K and V tiles of 128 positions page by page
 //              (tensor copies with the 128-byte swizzle) into a ring of stages;
-//   issuer     (warp 9) issues the products: S = Q K^T into tensor
-//              memory, and O += P V with P taken from tensor memory;
-//   helpers    (warps 10, 11) bring a unit's queries (while the last one's
-//              results are still being written), check its pages and write the
-//              rows that no unit covers;
+//   issuers    (warps 9, 10; one a stream) issue the products: S = Q K^T into
+//              tensor memory, and O += P V with P taken from tensor memory;
+//   helper     (warp 11) brings a unit's queries (while the last one's results
+//              are still being written), checks its pages, clears what V must
+//              not contain, and writes the rows that no unit covers;
 //   two groups (warps 0-3, 4-7) of 128 threads, a row each: the softmax between
 //              the two products, and the results.
 // The groups are two streams that the tensor core serves in turn, one's
@@ -20,9 +20,9 @@
 //                       that it can read).
 // S_w takes columns 128 w .. of tensor memory; P_w (bf16, two a column) takes
 // its place 32 positions at a time, 16 columns of weights and 16 of residuals;
-// O_w columns 256 + 128 w. Products
-// are issued by one thread and run in its order, so S_w of the next tile, issued
-// after P_w V, cannot overtake it.
+// O_w columns 256 + 128 w. A stream's
+// products are issued by one thread and run in its order, so S_w of the next
+// tile, issued after P_w V, cannot overtake it.
 //
 // The running maximum is only raised (and O_w scaled) when a tile exceeds it
 // by more than 8 octaves: weights stay below 2^8 and the sums far inside fp32;
@@ -69,8 +69,8 @@ struct Shape {
 };
 
 struct Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], groups, drain;
+    uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], ask[2], groups, drain;
     uint32_t loads;  // ring entries filled
     AttnScan scan;
     uint32_t tmem;
@@ -129,6 +129,18 @@ struct Walk {
 // K1 V0 K2 V1 K3 ..
 SV_DEV int ring_k(const Seg& s, int i) { return s.dual ? 2 * i : i + max(0, i - 1); }
 SV_DEV int ring_v(const Seg& s, int i) { return s.dual ? 2 * i + 1 : i + min(i + 2, s.last - s.first); }
+
+// Whether tile i of a segment reaches past the context; the stages that the V
+// of such tiles i in [i0, i1) lie in, a bit each (no two in the same: they are
+// neighbours).
+SV_DEV bool tail_tile(const Seg& s, int i) { return (long long)(s.first + i + 1) * kKv > s.L; }
+template <int D>
+SV_DEV uint32_t clean_stages(const Seg& s, uint32_t ring0, int i0, int i1) {
+    uint32_t bits = 0;
+    for (int i = i0; i < i1; ++i)
+        if (tail_tile(s, i)) bits ^= 1u << ((ring0 + ring_v(s, i)) % Shape<D>::kStages);
+    return bits;
+}
 
 // Waits give up after about two seconds, or once `abort` is set. They poll
 // without a suspension of their own: its wake-up costs more than these short
@@ -205,86 +217,117 @@ SV_DEV bool elected() {
     return p != 0;
 }
 
+// A stream's way along the ring. Both issuers wait for every entry in its
+// order and both release it (one's products on it, or its having seen an entry
+// that is the other's): a barrier's parity tells neighbouring rounds of a stage
+// apart and no more, so none may skip one.
 template <int D>
-SV_DEV bool issue_s(Ctl* c, uint32_t tmem, uint32_t qs, uint32_t stages, bool dual, bool last, uint32_t w, uint32_t ring) {
-    constexpr uint32_t NS = Shape<D>::kStages, idesc = mma_idesc(kKv, false);
-    const uint32_t st = uni(ring % NS);
-    if (!warp_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
-    tc_fence_after();
-    const uint32_t d = tmem + 128 * w;
-    const uint64_t a = mma_desc(qs + (dual ? w * Shape<D>::kTile : 0u), 16, 1024);
-    const uint64_t b = mma_desc(stages + st * Shape<D>::kTile, 16, 1024);
-    if (elected()) {
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-            mma_ss(d, a + off, b + off, idesc, kk > 0);
-        }
-        mma_commit(&c->s_full[w]);
-        if (!dual || w == 1) mma_commit(&c->empty[st]);
-        if (last) mma_commit(&c->q_empty);
-    }
-    __syncwarp();
-    return true;
-}
+struct Issuer {
+    static constexpr uint32_t NS = Shape<D>::kStages, kTile = Shape<D>::kTile;
+    Ctl* c;
+    uint32_t w, tmem, qs, stages;
+    uint32_t seen = 0, p_phase = 0, q_phase = 0, clean = 0;  // clean: phase of each stage's barrier
 
-template <int D>
-SV_DEV bool issue_o(Ctl* c, uint32_t tmem, uint32_t stages, bool dual, bool first, bool last, uint32_t w, uint32_t ring,
-                    uint32_t p_phase) {
-    constexpr uint32_t NS = Shape<D>::kStages, idesc = mma_idesc(D, true);
-    const uint32_t st = uni(ring % NS);
-    if (!warp_wait(&c->full[st], (ring / NS) & 1, &c->abort)) return false;
-    if (!warp_wait(&c->p_full[w], p_phase, &c->abort)) return false;
-    tc_fence_after();
-    uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w]);  // a byte of each warp
-    heavy |= heavy >> 16;
-    heavy = uni((heavy | heavy >> 8) & 0xFFu);
-    const uint32_t d = tmem + 256 + 128 * w, a = tmem + 128 * w;
-    const uint64_t b = mma_desc(stages + st * Shape<D>::kTile, kHalf, 1024);
-    if (elected()) {
-#pragma unroll
-        for (int kk = 0; kk < kKv / 16; ++kk)
-            mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
-        if (heavy) {
-#pragma unroll 1
-            for (int kk = 0; kk < kKv / 16; ++kk)
-                if (heavy >> kk & 1)
-                    mma_ts(d, a + (kk >> 1) * 32 + 16 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, true);
+    // Entry `ring` (this stream's); the other's before it are passed over.
+    SV_DEV bool reach(uint32_t ring) {
+        while (seen < ring) {
+            if (!pass()) return false;
         }
-        if (!dual || w == 1) mma_commit(&c->empty[st]);
-        if (last) mma_commit(&c->o_full[w]);
+        ++seen;
+        return warp_wait(&c->full[ring % NS], (ring / NS) & 1, &c->abort);
     }
-    __syncwarp();
-    return true;
-}
+    SV_DEV bool pass() {
+        const uint32_t st = seen % NS;
+        if (!warp_wait(&c->full[st], (seen / NS) & 1, &c->abort)) return false;
+        if (elected()) mbar_arrive(&c->empty[st]);
+        __syncwarp();
+        ++seen;
+        return true;
+    }
 
-template <int D>
-SV_DEV void issue(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Walk walk) {
-    const uint32_t tmem = uni(c->tmem);
-    uint32_t ring0 = 0, p_phase = 0, q_phase = 0;
-    Seg s;
-    bool ok = true;
-    while (ok && walk.next(p, &s)) {
-        const bool dual = uni(s.dual);
-        const int steps = (int)uni(s.steps);
-        ok = warp_wait(&c->q_full, q_phase, &c->abort);
-        q_phase ^= 1;
-#pragma unroll 1
-        for (int vt = -2; ok && vt < steps; ++vt) {
-            const uint32_t w = uni(vt & 1);
-            if (vt >= 0) {
-                ok = issue_o<D>(c, tmem, stages, dual, vt < 2, vt + 2 >= steps, w, ring0 + ring_v(s, dual ? vt >> 1 : vt),
-                                p_phase >> w & 1);
-                p_phase ^= 1u << w;
+    // S of the tile at `ring`; last: the segment's last of this stream.
+    SV_DEV bool scores(bool dual, bool last, uint32_t ring) {
+        constexpr uint32_t idesc = mma_idesc(kKv, false);
+        if (!reach(ring)) return false;
+        tc_fence_after();
+        const uint32_t st = uni(ring % NS), d = tmem + 128 * w;
+        const uint64_t a = mma_desc(qs + (dual ? w * kTile : 0u), 16, 1024), b = mma_desc(stages + st * kTile, 16, 1024);
+        if (elected()) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                mma_ss(d, a + off, b + off, idesc, kk > 0);
             }
-            if (ok && vt + 2 < steps)
-                ok = issue_s<D>(c, tmem, qs, stages, dual, vt + 3 == steps, w,
-                                ring0 + ring_k(s, dual ? (vt + 2) >> 1 : vt + 2));
+            mma_commit(&c->s_full[w]);
+            mma_commit(&c->empty[st]);
+            if (last) mma_commit(&c->q_empty);
         }
-        ring0 += 2 * (s.last - s.first);
+        __syncwarp();
+        return true;
     }
-    if (!ok) c->abort = 1;
-}
+
+    // O += P V of the tile at `ring`; tail: its V has to be cleaned first.
+    SV_DEV bool output(bool dual, bool first, bool last, bool tail, uint32_t ring) {
+        constexpr uint32_t idesc = mma_idesc(D, true);
+        if (!reach(ring)) return false;
+        const uint32_t st = uni(ring % NS);
+        if (tail && (!dual || w == 0)) {
+            if (elected()) mbar_arrive(&c->ask[w]);
+            __syncwarp();
+        }
+        if (!warp_wait(&c->p_full[w], p_phase, &c->abort)) return false;
+        p_phase ^= 1;
+        if (tail && !warp_wait(&c->clean[st], clean >> st & 1, &c->abort)) return false;
+        tc_fence_after();
+        uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w]);  // a byte of each warp
+        heavy |= heavy >> 16;
+        heavy = uni((heavy | heavy >> 8) & 0xFFu);
+        const uint32_t d = tmem + 256 + 128 * w, a = tmem + 128 * w;
+        const uint64_t b = mma_desc(stages + st * kTile, kHalf, 1024);
+        if (elected()) {
+#pragma unroll
+            for (int kk = 0; kk < kKv / 16; ++kk)
+                mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
+            if (heavy) {
+#pragma unroll 1
+                for (int kk = 0; kk < kKv / 16; ++kk)
+                    if (heavy >> kk & 1)
+                        mma_ts(d, a + (kk >> 1) * 32 + 16 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, true);
+            }
+            mma_commit(&c->empty[st]);
+            if (last) mma_commit(&c->o_full[w]);
+        }
+        __syncwarp();
+        return true;
+    }
+
+    SV_DEV void run(const AttnParams& p, Walk walk) {
+        uint32_t ring0 = 0;
+        Seg s;
+        bool ok = true;
+        while (ok && walk.next(p, &s)) {
+            const bool dual = uni(s.dual);
+            const int cnt = (int)uni(s.last - s.first);
+            const int mine = dual ? cnt : (cnt + 1 - (int)w) >> 1;  // tiles of this stream
+            ok = warp_wait(&c->q_full, q_phase, &c->abort);
+            q_phase ^= 1;
+            if (mine == 0 && elected()) mbar_arrive(&c->q_empty);
+            __syncwarp();
+#pragma unroll 1
+            for (int j = -1; ok && j < mine; ++j) {
+                const int i = dual ? j : 2 * j + (int)w, next = dual ? j + 1 : i + 2;
+                if (j >= 0) ok = output(dual, j == 0, j + 1 == mine, tail_tile(s, i), ring0 + ring_v(s, i));
+                if (ok && j + 1 < mine) ok = scores(dual, j + 2 == mine, ring0 + ring_k(s, next));
+                // (phases of the stages whose V this step's tiles have had cleaned, the other stream's too)
+                if (j >= 0) clean ^= clean_stages<D>(s, ring0, dual ? j : 2 * j, dual ? j + 1 : min(2 * j + 2, cnt));
+            }
+            if (!dual && mine < (cnt + 1) >> 1) clean ^= clean_stages<D>(s, ring0, 2 * mine, cnt);
+            ring0 += 2 * cnt;
+            while (ok && seen < ring0) ok = pass();
+        }
+        if (!ok) c->abort = 1;
+    }
+};
 
 // ---- softmax and results ------------------------------------------------------------
 
@@ -343,45 +386,6 @@ SV_DEV void see_bits(const AttnParams& p, const Seg& s, int node, long long pos0
     }
 }
 
-// Rows of a V tile past the context: rows past the end become zero, elements
-// that are not finite too (flag 1). Thread t owns position t of the tile.
-template <int D>
-SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int tile, int t, int slot) {
-    const long long pos = (long long)tile * kKv + t;
-    if (pos < s.L) return;
-    uint32_t x[D / 64][8][4];
-    const uint32_t row = tile_addr + t * 128;
-    if (pos >= s.len) {
-#pragma unroll
-        for (int i = 0; i < D / 64 * 8; ++i)
-            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(row + (i >> 3) * kHalf + (((i & 7) ^ (t & 7)) * 16)),
-                         "r"(0u)
-                         : "memory");
-        return;
-    }
-    uint32_t any = 0;
-#pragma unroll
-    for (int i = 0; i < D / 64 * 8; ++i) {
-        uint32_t(&y)[4] = x[i >> 3][i & 7];
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                     : "r"(row + (i >> 3) * kHalf + (((i & 7) ^ (t & 7)) * 16)));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) any |= __vcmpeq2(y[e] & 0x7F807F80u, 0x7F807F80u);
-    }
-    if (!any) return;
-    atomicOr(&c->flags[slot], 1);
-#pragma unroll
-    for (int i = 0; i < D / 64 * 8; ++i) {
-        uint32_t(&y)[4] = x[i >> 3][i & 7];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] &= ~__vcmpeq2(y[e] & 0x7F807F80u, 0x7F807F80u);
-        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(row + (i >> 3) * kHalf + (((i & 7) ^ (t & 7)) * 16)),
-                     "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                     : "memory");
-    }
-}
-
 // What clean_v took out, for one row and 32 columns.
 SV_DEV void add_unclean(const AttnParams& p, const Seg& s, int node, int col0, float (&o)[32]) {
     const int j0 = (int)max(0LL, (long long)s.first * kKv - s.L);
@@ -427,32 +431,65 @@ SV_DEV void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// Rows of a V tile past the context (one warp): rows past the end become zero,
+// elements that are not finite too (flag 1).
 template <int D>
-SV_DEV void help(const AttnParams& p, Ctl* c, uint32_t qs, Walk walk) {
-    constexpr int C = D / 8, HT = 64;  // 16-byte words of a row, helper threads
-    const int i0 = threadIdx.x - 10 * 32, lane = threadIdx.x & 31;
-    const int Hq = p.Hkv * p.G;
-    const char* q = reinterpret_cast<const char*>(p.q);
-    uint32_t seg = 0;
-    Seg s;
-    while (walk.next(p, &s)) {
-        // (the groups are past segment seg - 3: its products' last was issued before this one's queries are free)
-        if (seg && !warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort)) {
-            c->abort = 1;
-            break;
+SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int tile, int slot) {
+    constexpr int C = D / 8, R = 32 / C;  // 16-byte words of a row, rows at a time
+    const int lane = threadIdx.x & 31, ch = lane % C;
+    const long long pos0 = (long long)tile * kKv;
+    const int r0 = (int)max(0LL, s.L - pos0), live = (int)min((long long)kKv, s.len - pos0);
+    const uint32_t col = tile_addr + (ch >> 3) * kHalf;
+    bool found = false;
+#pragma unroll 4
+    for (int r = r0 + lane / C; r < kKv; r += R) {
+        const uint32_t a = col + r * 128 + (((ch & 7) ^ (r & 7)) * 16);
+        uint32_t y[4] = {0u, 0u, 0u, 0u}, any = 1;
+        if (r < live) {
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(a));
+            any = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t bad = __vcmpeq2(y[e] & 0x7F807F80u, 0x7F807F80u);
+                any |= bad;
+                y[e] &= ~bad;
+            }
+            found |= any != 0;
         }
-        if (i0 == 0) c->flags[(seg + 1) & 3] = 0;
-        for (int i = i0; i < s.rows * C; i += HT) {
-            const int r = i / C, ch = i - r * C, rr = s.row0 + r, node = rr / p.G, rt = r & 127;
-            const long long row = ((long long)s.b * p.N + node) * Hq + s.h * p.G + (rr - node * p.G);
+        if (any)
+            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+                         : "memory");
+    }
+    if (found) atomicOr(&c->flags[slot], 1);
+}
+
+template <int D>
+SV_DEV void help(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Walk walk) {
+    constexpr int C = D / 8, R = 32 / C;  // 16-byte words of a row, rows at a time
+    constexpr uint32_t NS = Shape<D>::kStages;
+    const int lane = threadIdx.x & 31, ch = lane % C;
+    const float inv_g = 1.f / (float)p.G;
+    const int Hq = p.Hkv * p.G;
+    uint32_t seg = 0, ring0 = 0, asked = 0;
+    Seg s;
+    bool ok = true;
+    while (ok && walk.next(p, &s)) {
+        // (the groups are past segment seg - 3: its products' last was issued before this one's queries are free)
+        if (seg && !(ok = warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort))) break;
+        if (lane == 0) c->flags[(seg + 1) & 3] = 0;
+        const char* q = reinterpret_cast<const char*>(p.q) + ((long long)s.b * p.N * Hq + s.h * p.G) * (D * 2) + ch * 16;
+#pragma unroll 4
+        for (int r = lane / C; r < s.rows; r += R) {
+            // (exact: the quotient is below 2^21 and half a unit away from the next one)
+            const int rr = s.row0 + r, node = (int)(((float)rr + 0.5f) * inv_g), rt = r & 127;
             cp16(qs + (r >> 7) * Shape<D>::kTile + (ch >> 3) * kHalf + rt * 128 + (((ch & 7) ^ (rt & 7)) * 16),
-                 q + row * (D * 2) + ch * 16);
+                 q + ((long long)node * Hq + (rr - node * p.G)) * (D * 2));
         }
         // a page that does not exist anywhere under this segment's tiles
         const long long lo = (long long)s.first * kKv >> p.page_shift;
         const long long hi = (min(s.len, (long long)s.last * kKv) - 1) >> p.page_shift;
         bool bad = false;
-        for (long long i = lo + i0; i <= hi; i += HT) {
+        for (long long i = lo + lane; i <= hi; i += 32) {
             const int id = __ldg(p.table + s.b * p.table_stride + i);
             bad |= id < 0 || id >= p.num_pages;
         }
@@ -461,15 +498,27 @@ SV_DEV void help(const AttnParams& p, Ctl* c, uint32_t qs, Walk walk) {
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->q_full);
+        const int cnt = s.last - s.first;
+        for (int i = max(0, s.L / kKv - s.first); ok && i < cnt; ++i) {
+            if (!tail_tile(s, i)) continue;
+            const uint32_t st = (ring0 + ring_v(s, i)) % NS, w = s.dual ? 0u : i & 1;
+            if (!(ok = warp_wait(&c->ask[w], asked >> w & 1, &c->abort))) break;  // (the tile is there)
+            asked ^= 1u << w;
+            clean_v<D>(c, s, stages + st * Shape<D>::kTile, s.first + i, seg & 3);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->clean[st]);
+        }
+        ring0 += 2 * cnt;
         ++seg;
     }
+    if (!ok) c->abort = 1;
 }
 
 template <int D>
 struct Group {
     const AttnParams& p;
     Ctl* c;
-    uint32_t stages;
     int w, warp, lane, t;       // group, warp of the group, lane, thread of the group = row of its tile
     uint32_t tm_s, tm_o;        // this warp's lanes of S_w and O_w
     uint32_t s_phase = 0, o_phase = 0, g_phase = 0;
@@ -650,9 +699,7 @@ struct Group {
     }
 
     SV_DEV void run(Walk walk) {
-        constexpr int NS = Shape<D>::kStages;
         const float c2 = p.c2;
-        uint32_t ring0 = 0;
         int slot = 0;
         Seg s;
         bool ok = true;
@@ -676,12 +723,6 @@ struct Group {
                 tc_fence_after();
                 if (!warp_on && lane == 0) c->heavy[w][warp] = 0;
                 if (warp_on) softmax(see, tail, vt < 2, c2, m, l);
-                if (tail && (!s.dual || w == 0)) {
-                    const uint32_t ring = ring0 + ring_v(s, i);
-                    if (!(ok = warp_wait(&c->full[ring % NS], (ring / NS) & 1, &c->abort))) break;
-                    clean_v<D>(c, s, stages + ring % NS * Shape<D>::kTile, s.first + i, t, slot);
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                }
                 if (w == 1 && vt + 2 >= s.steps) c->ml[t] = make_float2(m, l);
                 tc_fence_before();
                 __syncwarp();
@@ -691,7 +732,6 @@ struct Group {
             __syncwarp();
             if (!(ok = finish(s, slot, m, l))) break;
             tc_fence_before();
-            ring0 += 2 * (s.last - s.first);
             slot = (slot + 1) & 3;
         }
         if (!ok) c->abort = 1;
@@ -713,9 +753,8 @@ __global__ void __launch_bounds__(NT, 1)
         return i == 0 && (int)blockIdx.x < n ? attn_part(t, n, blockIdx.x) : -1;
     });
     const int parts = attn_parts(total, gridDim.x);
-    const int edge_warp = 2 * blockIdx.x + (warp & 1), edge_warps = 2 * gridDim.x;  // warps 10 and 11 of every CTA
     if ((int)blockIdx.x >= parts) {
-        if (warp >= 10) attn_edges<bf16_t>(p, edge_warp, edge_warps);
+        if (warp == 11) attn_edges<bf16_t>(p, blockIdx.x, gridDim.x);
         return;
     }
     Walk walk;
@@ -727,20 +766,26 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 0) {
         for (int i = 0; i < Shape<D>::kStages; ++i) {
             mbar_init(&c->full[i], 1);
-            mbar_init(&c->empty[i], 1);
+            mbar_init(&c->empty[i], 2);
+            mbar_init(&c->clean[i], 1);
         }
-        mbar_init(&c->q_full, 2);
-        mbar_init(&c->q_empty, 1);
+        mbar_init(&c->q_full, 1);
+        mbar_init(&c->q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->s_full[i], 1);
             mbar_init(&c->p_full[i], 4);
             mbar_init(&c->o_full[i], 1);
+            mbar_init(&c->ask[i], 1);
             c->flags[2 * i] = c->flags[2 * i + 1] = 0;
         }
         mbar_init(&c->groups, 8);
-        mbar_init(&c->drain, 1);
+        mbar_init(&c->drain, 2);
         c->abort = 0;
         mbar_init_fence();
+    }
+    if (tid == 8 * 32) {
+        tma_prefetch(&mk);
+        tma_prefetch(&mv);
     }
     if (warp == 9) tmem_alloc512(&c->tmem);
     tc_fence_before();
@@ -751,16 +796,19 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kGroupRegs));
         const int w = warp >> 2, lanes = (warp & 3) * 32;
-        Group<D> g{p, c, stages, w, warp & 3, lane, tid & 127, tmem + ((uint32_t)lanes << 16) + 128 * w,
+        Group<D> g{p, c, w, warp & 3, lane, tid & 127, tmem + ((uint32_t)lanes << 16) + 128 * w,
                    tmem + ((uint32_t)lanes << 16) + 256 + 128 * w};
         g.run(walk);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) produce<D>(p, c, &mk, &mv, stages, walk);
-        if (warp == 9) issue<D>(p, c, qs, stages, walk);
-        if (warp >= 10) {
-            help<D>(p, c, qs, walk);
-            attn_edges<bf16_t>(p, edge_warp, edge_warps, *reinterpret_cast<volatile int*>(&c->abort) != 0);
+        if (warp == 9 || warp == 10) {
+            Issuer<D> is{c, uni(warp - 9), uni(tmem), qs, stages};
+            is.run(p, walk);
+        }
+        if (warp == 11) {
+            help<D>(p, c, qs, stages, walk);
+            attn_edges<bf16_t>(p, blockIdx.x, gridDim.x, *reinterpret_cast<volatile int*>(&c->abort) != 0);
         }
     }
     __syncwarp();
@@ -772,7 +820,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (tid == 8 * 32)
             for (uint32_t r = c->loads > NS ? c->loads - NS : 0; r < c->loads; ++r)
                 tc_wait(&c->full[r % NS], (r / NS) & 1, nullptr);
-        if (tid == 9 * 32) {
+        if (tid == 9 * 32 || tid == 10 * 32) {
             mma_commit(&c->drain);
             tc_wait(&c->drain, 0, nullptr);
         }

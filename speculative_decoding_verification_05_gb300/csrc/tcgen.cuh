@@ -93,6 +93,7 @@ SV_DEV void mma_commit(uint64_t* bar) {
 }
 
 // ---- tensor copies: one box of a rank-4 tensor into shared memory.
+SV_DEV void tma_prefetch(const void* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 SV_DEV void tma_load4(uint32_t dst, const void* map, int c0, int c1, int c2, int c3, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
