@@ -21,6 +21,7 @@ namespace {
 
 constexpr int NT = 256;
 constexpr int kRows = 16;
+constexpr int kExtra = 1;  // tiles that a unit's start and end count for
 
 template <typename E>
 constexpr int row_bytes(int D) {  // a K row in shared memory: 16 bytes of padding against bank conflicts
@@ -104,31 +105,15 @@ __global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ A
     float* ws = qs + kRows * D + warp * 2 * KV;  // the warp's weights [2][KV]
 
     attn_edges<E>(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
-    int parts = 0;
-    const long long total = attn_locate<KV, NT>(p, &scan, [&](long long t, int i) -> long long {
-        const int n = attn_parts(t, gridDim.x);
-        return i == 0 && (int)blockIdx.x < n ? attn_part(t, n, blockIdx.x) : -1;
-    });
-    parts = attn_parts(total, gridDim.x);
+    asm volatile("griddepcontrol.launch_dependents;");
+    const long long total = attn_locate<KV, kExtra, NT>(p, &scan);
+    const int parts = attn_parts(total, gridDim.x);
+    if (tid == 0) attn_join<KV, kExtra>(p, scan, total, parts);
     if ((int)blockIdx.x >= parts) return;
-    const long long begin = attn_part(total, parts, blockIdx.x), end = attn_part(total, parts, blockIdx.x + 1);
-    int b = scan.place[0].b;
-    long long base = scan.place[0].base;
-
-    for (long long t = begin; t < end;) {
-        AttnSeq sq = attn_seq(p, b);
-        int kt = attn_kv_tiles<KV>(sq), rt = attn_row_tiles(p, sq);
-        while (t >= base + (long long)kt * rt * p.Hkv) {
-            base += (long long)kt * rt * p.Hkv;
-            sq = attn_seq(p, ++b);
-            kt = attn_kv_tiles<KV>(sq);
-            rt = attn_row_tiles(p, sq);
-        }
-        const long long unit = (t - base) / kt;
-        const int first = (int)(t - base - unit * kt);
-        const int last = (int)min((long long)kt, first + (end - t));  // tiles [first, last) of the unit
-        const int h = (int)(unit / rt), row_base = (int)(unit - (long long)h * rt) * kRows;
-        const int rows = min(kRows, sq.n * p.G - row_base);
+    AttnWalk<KV, kExtra> walk(scan, total, parts);
+    AttnStay sq;
+    while (walk.next(p, &sq)) {
+        const int b = sq.b, h = sq.h, first = sq.first, last = sq.last, row_base = sq.row0, rows = sq.rows;
         const long long len = (long long)sq.L + sq.n;
 
         // queries, in octaves of the score
@@ -240,8 +225,8 @@ __global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ A
             __syncthreads();
         }
         bad = __syncthreads_or(bad);
-        const bool whole = first == 0 && last == kt;
-        const int slot = 2 * blockIdx.x + (t != begin);
+        const bool whole = sq.whole;
+        const int slot = sq.slot;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             if (r0 + r >= rows) break;
@@ -269,55 +254,58 @@ __global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ A
                     p.lse[row] = lse_of(m[r], l[r]);
             }
         }
-        t += last - first;
     }
 }
 
-// Joins the pieces of the units that CTA parts cut. Block (c, y) looks after
-// the unit that part c starts inside of, if c is the first such part; a warp
-// takes one of its rows at a time: weights 2^(m_i - max m), the pieces' sums in
-// part order.
-template <typename E, int KV>
-__global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant__ AttnParams p, int main_grid) {
-    __shared__ AttnScan scan;
-    const int c = blockIdx.x + 1;
-    const long long total = attn_locate<KV, 128>(p, &scan, [&](long long t, int i) -> long long {
-        const int n = attn_parts(t, main_grid);
-        return i == 0 && c < n ? attn_part(t, n, c) : -1;
-    });
-    const int parts = attn_parts(total, main_grid);
-    if (c >= parts) return;
-    const int b = scan.place[0].b;
-    const long long base = scan.place[0].base, at = attn_part(total, parts, c);
-    const AttnSeq sq = attn_seq(p, b);
-    const int kt = attn_kv_tiles<KV>(sq), rt = attn_row_tiles(p, sq);
-    const long long unit = (at - base) / kt, ustart = base + unit * kt, uend = ustart + kt;
-    if (at == ustart || attn_part(total, parts, c - 1) > ustart) return;
-    int last = c;  // the last part with tiles of this unit
-    while (last + 1 < parts && attn_part(total, parts, last + 1) < uend) ++last;
-    const int h = (int)(unit / rt), row_base = (int)(unit - (long long)h * rt) * p.tile_rows;
-    const int rows = min(p.tile_rows, sq.n * p.G - row_base);
-    const int slot0 = 2 * (c - 1) + (attn_part(total, parts, c - 1) != ustart);
+// Joins the pieces of the units that several parts share: block (c, y) takes
+// joins[c], a warp a row: weights 2^(m_i - max m) of the pieces, a lane a piece,
+// then their sums, four columns a lane (eight: D > 128).
+template <typename E>
+__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnParams p) {
     const int lane = threadIdx.x & 31;
-    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < rows; r += gridDim.y * 4) {
-        float m = __uint_as_float(0xFF800000u);
-        for (int i = c - 1; i <= last; ++i)
-            m = fmaxf(m, p.part_ml[(long long)(i == c - 1 ? slot0 : 2 * i) * p.tile_rows + r].x);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4* src = reinterpret_cast<const int4*>(p.joins + blockIdx.x + 1);
+    const int4 u = __ldcg(src), v = __ldcg(src + 1);  // b, h, row0, rows; slot0, first, last
+    const int pieces = v.z - v.y + 2;
+    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < u.w; r += gridDim.y * 4) {
+        auto at = [&](int i) { return (long long)(i == 0 ? v.x : 2 * (v.y + i - 1)) * p.tile_rows + r; };
+        const float2 none = make_float2(__uint_as_float(0xFF800000u), 0.f);
+        float2 ml = lane < pieces ? __ldcg(p.part_ml + at(lane)) : none;
+        float m = ml.x;
+        for (int i = lane + 32; i < pieces; i += 32) m = fmaxf(m, __ldcg(p.part_ml + at(i)).x);
+        m = warp_max(m);
         const float ref = m == __uint_as_float(0xFF800000u) ? 0.f : m;
         float l = 0.f;
         float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        for (int i = c - 1; i <= last; ++i) {
-            const long long at_row = (long long)(i == c - 1 ? slot0 : 2 * i) * p.tile_rows + r;
-            const float2 ml = p.part_ml[at_row];
+        for (int i0 = 0; i0 < pieces; i0 += 32) {
+            if (i0) ml = i0 + lane < pieces ? __ldcg(p.part_ml + at(i0 + lane)) : none;
             const float w = ex2(ml.x - ref);
             l += w * ml.y;
+            const int n = min(32, pieces - i0);
+            for (int i = 0; i < n; i += 8) {
+                float4 x[8][2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int d = (lane + 32 * g) * 4;
-                if (d < p.D) acc[g] = fma4(w, *reinterpret_cast<const float4*>(p.part_o + at_row * p.D + d), acc[g]);
+                for (int k = 0; k < 8; ++k)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const int d = (lane + 32 * g) * 4;
+                        x[k][g] = i + k < n && d < p.D
+                                      ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i0 + i + k) * p.D + d))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float wk = __shfl_sync(0xFFFFFFFFu, w, (i + k) & 31);
+                    if (i + k < n) {
+                        acc[0] = fma4(wk, x[k][0], acc[0]);
+                        acc[1] = fma4(wk, x[k][1], acc[1]);
+                    }
+                }
             }
         }
-        const long long row = ((long long)b * p.N + (row_base + r) / p.G) * (p.Hkv * p.G) + h * p.G + (row_base + r) % p.G;
+        l = warp_sum(l);
+        const int rr = u.z + r, node = rr / p.G;
+        const long long row = ((long long)u.x * p.N + node) * (p.Hkv * p.G) + u.y * p.G + (rr - node * p.G);
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
@@ -330,6 +318,21 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const __grid_constant
     }
 }
 
+template <typename E>
+cudaError_t launch_join(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
+    if (plan.grid == 1) return cudaSuccess;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(plan.grid - 1, (std::min(plan.rows, p.N * p.G) + 3) / 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<E>, p);
+}
+
 template <typename E, int KV>
 cudaError_t launch_simt(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
     const size_t smem = simt_smem<E, KV>(p.D);
@@ -337,18 +340,13 @@ cudaError_t launch_simt(const AttnParams& p, const AttnPlan& plan, cudaStream_t 
     if (e != cudaSuccess) return e;
     attn_simt_kernel<E, KV><<<plan.grid, NT, smem, st>>>(p);
     e = cudaGetLastError();
-    if (e != cudaSuccess || plan.grid == 1) return e;
-    attn_combine_kernel<E, KV><<<dim3(plan.grid - 1, (kRows + 3) / 4), 128, 0, st>>>(p, plan.grid);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<E>(p, plan, st);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_combine_tc(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
-    if (plan.grid == 1) return cudaSuccess;
-    const int rows = std::min(plan.rows, p.N * p.G);
-    attn_combine_kernel<bf16_t, 128><<<dim3(plan.grid - 1, std::min(16, (rows + 3) / 4)), 128, 0, st>>>(p, plan.grid);
-    return cudaGetLastError();
+cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st) {
+    return dtype == 0 ? launch_join<float>(p, plan, st) : launch_join<bf16_t>(p, plan, st);
 }
 
 int attention_simt_rows() { return kRows; }

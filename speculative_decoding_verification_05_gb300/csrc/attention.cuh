@@ -13,7 +13,9 @@
 // Division. A unit is (sequence, key / value head, row tile); its tiles are
 // the kKv-position tiles of L + n positions. All units' tiles in order form
 // one range that is cut into equal parts, one a CTA, whatever the lengths
-// are (they are known on the device only). A unit inside one part is finished
+// are (they are known on the device only). In the range a unit counts a few
+// tiles more than it has (EX, before its tiles), for what its start and end
+// cost; a cut that falls among these is moved to the unit's start. A unit inside one part is finished
 // by its CTA; the others leave partial results (unnormalised sums with their
 // running maximum and sum) that the combine kernel joins in range order, so
 // results depend on the lengths and the grid alone, never on timing.
@@ -22,6 +24,14 @@
 #include "common.cuh"
 
 namespace sv {
+
+// A unit that several CTAs' parts share, written by the second of them.
+struct AttnJoin {
+    int b, h, row0, rows;  // rows = 0: nothing to join here
+    int slot0;             // the first piece's slot; the others' are 2 * part
+    int first, last;       // parts of the other pieces
+    int pad;
+};
 
 struct AttnParams {
     const void* q;    // [B, N, Hkv * G, D]
@@ -41,6 +51,7 @@ struct AttnParams {
     int32_t* status;     // [B] or null
     float* part_o;       // [2 * grid][rows of a tile][D] partial sums
     float2* part_ml;     // [2 * grid][rows of a tile] running maximum (octaves) and sum
+    AttnJoin* joins;     // [grid] the units to join
 };
 
 // A sequence's nodes and context; n = -1: bad data.
@@ -65,10 +76,10 @@ SV_DEV int attn_row_tiles(const AttnParams& p, const AttnSeq& s) {
     return s.n > 0 ? (s.n * p.G + p.tile_rows - 1) / p.tile_rows : 0;
 }
 
-template <int KV>
+template <int KV, int EX>
 SV_DEV long long attn_seq_work(const AttnParams& p, int b) {
     const AttnSeq s = attn_seq(p, b);
-    return (long long)attn_kv_tiles<KV>(s) * attn_row_tiles(p, s) * p.Hkv;
+    return s.n > 0 ? (long long)(attn_kv_tiles<KV>(s) + EX) * attn_row_tiles(p, s) * p.Hkv : 0;
 }
 
 // Where tile `at` of the whole range lies: its sequence and that sequence's
@@ -81,19 +92,23 @@ struct AttnPlace {
 // Scratch of attn_locate in shared memory.
 struct AttnScan {
     long long warp_sum[32];
-    AttnPlace place[2];
+    AttnPlace place;
 };
 
-// Called by all NT threads of a block; `pick(total, which)` gives the tile to
-// place (which = 0, 1), -1 for none. Returns the total; places go to sc->place.
-// Each thread sums a run of sequences, one scan orders the runs.
-template <int KV, int NT, typename Pick>
-SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc, Pick pick) {
+SV_DEV int attn_parts(long long total, int grid) { return (int)(total < grid ? total : grid); }
+// CTA c's part of `total` tiles over `parts` CTAs.
+SV_DEV long long attn_part(long long total, int parts, int c) { return total * c / parts; }
+
+// Called by all NT threads of a block: the range's length, and in sc->place
+// where this CTA's part begins (if it has one). Each thread sums a run of
+// sequences, one scan orders the runs.
+template <int KV, int EX, int NT>
+SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (p.B + NT - 1) / NT;
     const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += attn_seq_work<KV>(p, b);
+    for (int b = b0; b < b1; ++b) mine += attn_seq_work<KV, EX>(p, b);
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -110,28 +125,104 @@ SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc, Pick pick) {
         total += u;
     }
     long long lo = before + inc - mine;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const long long at = pick(total, i);
-        if (at >= lo && at < lo + mine) {
-            long long base = lo;
-            for (int b = b0; b < b1; ++b) {
-                const long long w = attn_seq_work<KV>(p, b);
-                if (at < base + w) {
-                    sc->place[i] = AttnPlace{b, base};
-                    break;
-                }
-                base += w;
+    const int parts = attn_parts(total, gridDim.x);
+    const long long at = (int)blockIdx.x < parts ? attn_part(total, parts, blockIdx.x) : -1;
+    if (at >= lo && at < lo + mine) {
+        long long base = lo;
+        for (int b = b0; b < b1; ++b) {
+            const long long w = attn_seq_work<KV, EX>(p, b);
+            if (at < base + w) {
+                sc->place = AttnPlace{b, base};
+                break;
             }
+            base += w;
         }
     }
     __syncthreads();
     return total;
 }
 
-// CTA c's part of `total` tiles over `parts` CTAs.
-SV_DEV long long attn_part(long long total, int parts, int c) { return total * c / parts; }
-SV_DEV int attn_parts(long long total, int grid) { return (int)(total < grid ? total : grid); }
+// One CTA's stay in a unit: tiles [first, last) of its kt.
+struct AttnStay {
+    int b, h, row0, rows, first, last, kt, L, n, slot;
+    long long len;
+    bool whole;
+};
+
+// Walks this CTA's part of the range.
+template <int KV, int EX>
+struct AttnWalk {
+    long long t, end, base;
+    int b, stays;
+    SV_DEV AttnWalk(const AttnScan& sc, long long total, int parts)
+        : t(attn_part(total, parts, blockIdx.x)),
+          end(attn_part(total, parts, blockIdx.x + 1)),
+          base(sc.place.base),
+          b(sc.place.b),
+          stays(0) {}
+
+    SV_DEV static long long div(long long x, int y) {
+        return x >> 31 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+    }
+
+    SV_DEV bool next(const AttnParams& p, AttnStay* s) {
+        while (t < end) {
+            AttnSeq q = attn_seq(p, b);
+            int kt = attn_kv_tiles<KV>(q), rt = attn_row_tiles(p, q);
+            while (q.n <= 0 || t >= base + (long long)(kt + EX) * rt * p.Hkv) {
+                if (q.n > 0) base += (long long)(kt + EX) * rt * p.Hkv;
+                q = attn_seq(p, ++b);
+                kt = attn_kv_tiles<KV>(q);
+                rt = attn_row_tiles(p, q);
+            }
+            const long long unit = div(t - base, kt + EX);
+            const int from = (int)(t - base - unit * (kt + EX));
+            const int to = (int)min((long long)(kt + EX), from + (end - t));
+            t += to - from;
+            s->first = max(0, from - EX);
+            s->last = max(0, to - EX);
+            if (s->first == s->last) continue;
+            s->b = b;
+            s->kt = kt;
+            s->h = (int)div(unit, rt);
+            s->row0 = (int)(unit - (long long)s->h * rt) * p.tile_rows;
+            s->rows = min(p.tile_rows, q.n * p.G - s->row0);
+            s->L = q.L;
+            s->n = q.n;
+            s->len = (long long)q.L + q.n;
+            s->whole = s->first == 0 && s->last == kt;
+            s->slot = 2 * blockIdx.x + (stays > 0);
+            ++stays;
+            return true;
+        }
+        return false;
+    }
+};
+
+// This CTA's entry of p.joins (one thread): its part begins inside a unit that
+// the part before it has the first piece of.
+template <int KV, int EX>
+SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, long long total, int parts) {
+    AttnJoin j = {};
+    const int c = blockIdx.x;
+    if (c > 0 && c < parts) {
+        const AttnSeq q = attn_seq(p, sc.place.b);
+        const int kt = attn_kv_tiles<KV>(q), rt = attn_row_tiles(p, q);
+        const long long at = attn_part(total, parts, c), before = attn_part(total, parts, c - 1);
+        const long long unit = AttnWalk<KV, EX>::div(at - sc.place.base, kt + EX);
+        const long long start = sc.place.base + unit * (kt + EX), stop = start + kt + EX;
+        if (at > start + EX && before <= start + EX) {
+            j.b = sc.place.b;
+            j.h = (int)AttnWalk<KV, EX>::div(unit, rt);
+            j.row0 = (int)(unit - (long long)j.h * rt) * p.tile_rows;
+            j.rows = min(p.tile_rows, q.n * p.G - j.row0);
+            j.slot0 = 2 * (c - 1) + (before < start);
+            j.first = j.last = c;
+            while (j.last + 1 < parts && attn_part(total, parts, j.last + 1) < stop) ++j.last;
+        }
+    }
+    p.joins[c] = j;
+}
 
 // The sequences' own checks and edges, shared out over `warps` warps of the
 // grid (this is warp `gw`; as many warps a sequence as there are): status, and
@@ -190,23 +281,23 @@ SV_DEV void store4<bf16_t>(bf16_t* dst, float4 x) {
 // Host side.
 struct AttnPlan {
     int grid, rows, kv;   // CTAs of the main kernel, rows of a tile, positions of a tile
-    size_t part_o, part_ml, total;  // workspace layout
+    size_t part_o, part_ml, joins, total;  // workspace layout
 };
 
 cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);
 int attention_simt_rows();
 int attention_simt_kv(int dtype, int D);
 int attention_simt_ctas(int dtype, int D);
-// The tensor-core kernel (bf16, D 64 or 128) reads K and V through two tensor
+// The tensor-core kernel (bf16, D 64 or 128) reads K, V and Q through tensor
 // maps; attention_tc_maps: false where the cache's strides have none.
 struct alignas(64) AttnMaps {
-    unsigned char bytes[256];
+    unsigned char bytes[384];
 };
-int attention_tc_rows();
+int attention_tc_rows(int group);
 int attention_tc_kv();
 bool attention_tc_maps(const AttnParams& p, AttnMaps* m);
 cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const AttnMaps& m, cudaStream_t st);
-cudaError_t launch_attention_combine_tc(const AttnParams& p, const AttnPlan& plan, cudaStream_t st);
+cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);
 cudaError_t debug_read_attention_tc(unsigned int* count, unsigned int* line);
 cudaError_t debug_read_attention(unsigned int* count, unsigned int* line);
 

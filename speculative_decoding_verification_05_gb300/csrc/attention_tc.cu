@@ -14,7 +14,9 @@
 // The groups are two streams that the tensor core serves in turn, one's
 // products while the other computes its softmax:
 //   more than 128 rows  both streams go over the same tiles, each for a half of
-//                       the unit's 256 rows (a tile is read once for 256 rows);
+//                       the unit's 256 rows (a tile is read once for 256 rows;
+//                       a half holds whole nodes, so fewer rows where G does
+//                       not divide 128);
 //   else                both have the same rows and take alternate tiles; group
 //                       0 joins their sums at the end (both O lie in the lanes
 //                       that it can read).
@@ -55,7 +57,6 @@ constexpr int NT = 384;
 // 88 to the third (2 x 208 + 88 = 3 x 168).
 constexpr int kGroupRegs = 208, kOtherRegs = 88;
 constexpr int kKv = 128;     // positions of a tile
-constexpr int kRows = 256;   // rows of a unit
 constexpr int kMaxStages = 10;
 constexpr float kHeavy = 4.f;  // octaves below a row's sum from which a weight is heavy
 constexpr float kSlack = 8.f;  // octaves that a score may exceed the reference by
@@ -81,45 +82,18 @@ struct Ctl {
 };
 static_assert(sizeof(Ctl) <= 2048, "control region");
 
-// One CTA's stay in a unit: tiles [first, last) of it.
-struct Seg {
-    int b, h, row0, rows, first, last, kt, L, n;
-    long long len;
-    bool dual, whole;
-    int slot, steps;  // steps: softmax tiles of both streams together
+// A stay in a unit; dual: both streams go over its tiles.
+struct Seg : AttnStay {
+    bool dual;
+    int steps;  // softmax tiles of both streams together
 };
-
-// Walks a part of the range; every role walks it by itself.
-struct Walk {
-    long long t, end, begin, base;
-    int b;
+constexpr int kExtra = 2;  // tiles that a unit's start and end count for (attention.cuh)
+struct Walk : AttnWalk<kKv, kExtra> {
+    using AttnWalk<kKv, kExtra>::AttnWalk;
     SV_DEV bool next(const AttnParams& p, Seg* s) {
-        if (t >= end) return false;
-        AttnSeq q = attn_seq(p, b);
-        int kt = attn_kv_tiles<kKv>(q), rt = attn_row_tiles(p, q);
-        while (t >= base + (long long)kt * rt * p.Hkv) {
-            base += (long long)kt * rt * p.Hkv;
-            q = attn_seq(p, ++b);
-            kt = attn_kv_tiles<kKv>(q);
-            rt = attn_row_tiles(p, q);
-        }
-        const long long in = t - base;
-        const long long unit = in >> 31 ? in / kt : (long long)((uint32_t)in / (uint32_t)kt);
-        s->b = b;
-        s->kt = kt;
-        s->first = (int)(in - unit * kt);
-        s->last = (int)min((long long)kt, s->first + (end - t));
-        s->h = unit >> 31 ? (int)(unit / rt) : (int)((uint32_t)unit / (uint32_t)rt);
-        s->row0 = (int)(unit - (long long)s->h * rt) * kRows;
-        s->rows = min(kRows, q.n * p.G - s->row0);
-        s->L = q.L;
-        s->n = q.n;
-        s->len = (long long)q.L + q.n;
-        s->dual = s->rows > 128;
-        s->whole = s->first == 0 && s->last == kt;
-        s->slot = 2 * blockIdx.x + (t != begin);
+        if (!AttnWalk<kKv, kExtra>::next(p, s)) return false;
+        s->dual = s->rows > p.tile_rows / 2;
         s->steps = (s->last - s->first) * (s->dual ? 2 : 1);
-        t += s->last - s->first;
         return true;
     }
 };
@@ -141,6 +115,10 @@ SV_DEV uint32_t clean_stages(const Seg& s, uint32_t ring0, int i0, int i1) {
         if (tail_tile(s, i)) bits ^= 1u << ((ring0 + ring_v(s, i)) % Shape<D>::kStages);
     return bits;
 }
+
+// Positions of a tile that hold anything; the product with V goes over whole
+// steps of 16 of them.
+SV_DEV int live_of(const Seg& s, int i) { return (int)min((long long)kKv, s.len - (long long)(s.first + i) * kKv); }
 
 // Waits give up after about two seconds, or once `abort` is set. They poll
 // without a suspension of their own: its wake-up costs more than these short
@@ -267,7 +245,7 @@ struct Issuer {
     }
 
     // O += P V of the tile at `ring`; tail: its V has to be cleaned first.
-    SV_DEV bool output(bool dual, bool first, bool last, bool tail, uint32_t ring) {
+    SV_DEV bool output(bool dual, bool first, bool last, bool tail, int live, uint32_t ring) {
         constexpr uint32_t idesc = mma_idesc(D, true);
         if (!reach(ring)) return false;
         const uint32_t st = uni(ring % NS);
@@ -287,7 +265,7 @@ struct Issuer {
         if (elected()) {
 #pragma unroll
             for (int kk = 0; kk < kKv / 16; ++kk)
-                mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
+                if (16 * kk < live) mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
             if (heavy) {
 #pragma unroll 1
                 for (int kk = 0; kk < kKv / 16; ++kk)
@@ -316,7 +294,8 @@ struct Issuer {
 #pragma unroll 1
             for (int j = -1; ok && j < mine; ++j) {
                 const int i = dual ? j : 2 * j + (int)w, next = dual ? j + 1 : i + 2;
-                if (j >= 0) ok = output(dual, j == 0, j + 1 == mine, tail_tile(s, i), ring0 + ring_v(s, i));
+                if (j >= 0) ok = output(dual, j == 0, j + 1 == mine, tail_tile(s, i), (int)uni(live_of(s, i)),
+                                         ring0 + ring_v(s, i));
                 if (ok && j + 1 < mine) ok = scores(dual, j + 2 == mine, ring0 + ring_k(s, next));
                 // (phases of the stages whose V this step's tiles have had cleaned, the other stream's too)
                 if (j >= 0) clean ^= clean_stages<D>(s, ring0, dual ? j : 2 * j, dual ? j + 1 : min(2 * j + 2, cnt));
@@ -425,65 +404,81 @@ SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
 
 constexpr float kNegInf = -__builtin_inff();
 
-// ---- queries, pages, edges -----------------------------------------------------------
-
-SV_DEV void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 32 bytes; in one store where they start on 32.
+SV_DEV void st32(char* dst, const uint32_t* x) {
+    if (((uintptr_t)dst & 31) == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                     "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
 }
 
-// Rows of a V tile past the context (one warp): rows past the end become zero,
-// elements that are not finite too (flag 1).
+// ---- queries, pages, edges -----------------------------------------------------------
+
+// Rows of a V tile past the context (one warp): elements that are not finite
+// become zero (flag 1), and so do the rows past the end that the product's last
+// step covers.
 template <int D>
-SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int tile, int slot) {
-    constexpr int C = D / 8, R = 32 / C;  // 16-byte words of a row, rows at a time
-    const int lane = threadIdx.x & 31, ch = lane % C;
-    const long long pos0 = (long long)tile * kKv;
-    const int r0 = (int)max(0LL, s.L - pos0), live = (int)min((long long)kKv, s.len - pos0);
+SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int i, int slot) {
+    constexpr int C = D / 8, R = 32 / C, U = 8;  // 16-byte words of a row, rows at a time, words in flight
+    const int lane = threadIdx.x & 31, ch = lane % C, live = live_of(s, i);
+    const long long ctx = s.L - (long long)(s.first + i) * kKv;
     const uint32_t col = tile_addr + (ch >> 3) * kHalf;
+    auto word = [&](int r) { return col + r * 128 + (((ch & 7) ^ (r & 7)) * 16); };
     bool found = false;
-#pragma unroll 4
-    for (int r = r0 + lane / C; r < kKv; r += R) {
-        const uint32_t a = col + r * 128 + (((ch & 7) ^ (r & 7)) * 16);
-        uint32_t y[4] = {0u, 0u, 0u, 0u}, any = 1;
-        if (r < live) {
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(a));
-            any = 0;
+    for (int r0 = (int)max(0LL, ctx) + lane / C; r0 < live; r0 += R * U) {
+        uint32_t y[U][4], any = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t bad = __vcmpeq2(y[e] & 0x7F807F80u, 0x7F807F80u);
-                any |= bad;
-                y[e] &= ~bad;
-            }
-            found |= any != 0;
+        for (int u = 0; u < U; ++u) {
+            const int r = min(r0 + u * R, live - 1);
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(y[u][0]), "=r"(y[u][1]), "=r"(y[u][2]), "=r"(y[u][3])
+                         : "r"(word(r)));
         }
-        if (any)
-            asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
-                         : "memory");
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) any |= __vcmpeq2(y[u][e] & 0x7F807F80u, 0x7F807F80u);
+        if (any) {
+            found = true;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[u][e] &= ~__vcmpeq2(y[u][e] & 0x7F807F80u, 0x7F807F80u);
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(word(min(r0 + u * R, live - 1))), "r"(y[u][0]),
+                             "r"(y[u][1]), "r"(y[u][2]), "r"(y[u][3])
+                             : "memory");
+            }
+        }
     }
+    for (int r = live + lane / C; r < ((live + 15) & ~15); r += R)
+        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(word(r)), "r"(0u) : "memory");
     if (found) atomicOr(&c->flags[slot], 1);
 }
 
 template <int D>
-SV_DEV void help(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Walk walk) {
-    constexpr int C = D / 8, R = 32 / C;  // 16-byte words of a row, rows at a time
+SV_DEV void help(const AttnParams& p, Ctl* c, const CUtensorMap* mq, uint32_t qs, uint32_t stages, Walk walk) {
     constexpr uint32_t NS = Shape<D>::kStages;
-    const int lane = threadIdx.x & 31, ch = lane % C;
-    const float inv_g = 1.f / (float)p.G;
-    const int Hq = p.Hkv * p.G;
+    const int lane = threadIdx.x & 31, nodes = 128 / p.G;  // nodes of a half
+    const uint32_t box = 128u * min(nodes, p.N) * p.G;     // bytes of 64 columns of them
     uint32_t seg = 0, ring0 = 0, asked = 0;
     Seg s;
     bool ok = true;
     while (ok && walk.next(p, &s)) {
         // (the groups are past segment seg - 3: its products' last was issued before this one's queries are free)
         if (seg && !(ok = warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort))) break;
-        if (lane == 0) c->flags[(seg + 1) & 3] = 0;
-        const char* q = reinterpret_cast<const char*>(p.q) + ((long long)s.b * p.N * Hq + s.h * p.G) * (D * 2) + ch * 16;
-#pragma unroll 4
-        for (int r = lane / C; r < s.rows; r += R) {
-            // (exact: the quotient is below 2^21 and half a unit away from the next one)
-            const int rr = s.row0 + r, node = (int)(((float)rr + 0.5f) * inv_g), rt = r & 127;
-            cp16(qs + (r >> 7) * Shape<D>::kTile + (ch >> 3) * kHalf + rt * 128 + (((ch & 7) ^ (rt & 7)) * 16),
-                 q + ((long long)node * Hq + (rr - node * p.G)) * (D * 2));
+        if (lane == 0) {
+            c->flags[(seg + 1) & 3] = 0;
+            mbar_expect_tx(&c->q_full, box * (D / 64) * (s.dual ? 2 : 1));
+        }
+        __syncwarp();
+        if (lane < D / 64 * (s.dual ? 2 : 1)) {
+            const int w = lane / (D / 64), half = lane - w * (D / 64);
+            tma_load4(qs + w * Shape<D>::kTile + half * kHalf, mq, half * 64, s.h * p.G, s.row0 / p.G + w * nodes, s.b,
+                      &c->q_full);
         }
         // a page that does not exist anywhere under this segment's tiles
         const long long lo = (long long)s.first * kKv >> p.page_shift;
@@ -494,8 +489,6 @@ SV_DEV void help(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Walk
             bad |= id < 0 || id >= p.num_pages;
         }
         if (bad) atomicOr(&c->flags[seg & 3], 2);
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
         if (lane == 0) mbar_arrive(&c->q_full);
         const int cnt = s.last - s.first;
@@ -504,7 +497,7 @@ SV_DEV void help(const AttnParams& p, Ctl* c, uint32_t qs, uint32_t stages, Walk
             const uint32_t st = (ring0 + ring_v(s, i)) % NS, w = s.dual ? 0u : i & 1;
             if (!(ok = warp_wait(&c->ask[w], asked >> w & 1, &c->abort))) break;  // (the tile is there)
             asked ^= 1u << w;
-            clean_v<D>(c, s, stages + st * Shape<D>::kTile, s.first + i, seg & 3);
+            clean_v<D>(c, s, stages + st * Shape<D>::kTile, i, seg & 3);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->clean[st]);
@@ -628,23 +621,26 @@ struct Group {
         if (s.whole) {
             const int node = (s.row0 + rr) / p.G, g = (s.row0 + rr) - node * p.G;
             const long long row = ((long long)s.b * p.N + node) * (p.Hkv * p.G) + s.h * p.G + g;
-            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<char*>(p.out) + (row * D + col) * 2);
-            if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
+            char* dst = reinterpret_cast<char*>(p.out) + (row * D + col) * 2;
+            uint32_t x[16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    dst[k] = make_uint4(pack_bf16(o[8 * k] * inv, o[8 * k + 1] * inv),
-                                        pack_bf16(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
-                                        pack_bf16(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
-                                        pack_bf16(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+            for (int k = 0; k < 16; ++k) x[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+            if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G)) {
+                st32(dst, x);
+                st32(dst + 32, x + 8);
+            }
         } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + ((long long)s.slot * kRows + rr) * D + col);
+            char* dst = reinterpret_cast<char*>(p.part_o + ((long long)s.slot * p.tile_rows + rr) * D + col);
+            uint32_t x[32];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(o[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) st32(dst + 32 * k, x + 8 * k);
         }
     }
     SV_DEV void put_ml(const Seg& s, int rr, float m, float l) {
         if (!s.whole) {
-            p.part_ml[(long long)s.slot * kRows + rr] = make_float2(m, l);
+            p.part_ml[(long long)s.slot * p.tile_rows + rr] = make_float2(m, l);
         } else if (p.lse) {
             const int node = (s.row0 + rr) / p.G, g = (s.row0 + rr) - node * p.G;
             p.lse[((long long)s.b * p.N + node) * (p.Hkv * p.G) + s.h * p.G + g] = lse_of(m, l);
@@ -654,9 +650,9 @@ struct Group {
     // A segment's result: each group its own rows, or group 0 both groups' sums.
     SV_DEV bool finish(const Seg& s, int slot, float m, float l) {
         const bool joined = !s.dual && s.steps > 1;
-        const int rr = s.dual ? 128 * w + t : t;
-        const bool mine = rr < s.rows;
-        const bool warp_on = (s.dual ? 128 * w : 0) + warp * 32 < s.rows && s.steps > w;
+        const int half = p.tile_rows / 2, rr = s.dual ? half * w + t : t;
+        const bool mine = t < half && rr < s.rows;
+        const bool warp_on = warp * 32 < half && (s.dual ? half * w : 0) + warp * 32 < s.rows && s.steps > w;
         if (s.steps > w) {
             if (!warp_wait(&c->o_full[w], o_phase >> w & 1, &c->abort)) return false;
             o_phase ^= 1 << w;
@@ -708,8 +704,8 @@ struct Group {
             if (!(ok = meet())) break;
 
             float m = kNegInf, l = 0.f;
-            const int rr = s.dual ? 128 * w + t : t;
-            const bool warp_on = (s.dual ? 128 * w : 0) + warp * 32 < s.rows;
+            const int half = p.tile_rows / 2, rr = s.dual ? half * w + t : t;
+            const bool warp_on = warp * 32 < half && (s.dual ? half * w : 0) + warp * 32 < s.rows;
             const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
             for (int vt = w; vt < s.steps; vt += 2) {
                 const int i = s.dual ? vt >> 1 : vt;
@@ -741,27 +737,22 @@ struct Group {
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
     attn_tc_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap mk,
-                   const __grid_constant__ CUtensorMap mv) {
+                   const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mq) {
     extern __shared__ unsigned char dyn[];
     unsigned char* mem = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023);
     Ctl* c = reinterpret_cast<Ctl*>(mem);
     const uint32_t qs = smem_u32(mem) + 2048, stages = qs + 2 * Shape<D>::kTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const long long total = attn_locate<kKv, NT>(p, &c->scan, [&](long long t, int i) -> long long {
-        const int n = attn_parts(t, gridDim.x);
-        return i == 0 && (int)blockIdx.x < n ? attn_part(t, n, blockIdx.x) : -1;
-    });
+    asm volatile("griddepcontrol.launch_dependents;");
+    const long long total = attn_locate<kKv, kExtra, NT>(p, &c->scan);
     const int parts = attn_parts(total, gridDim.x);
+    if (tid == 11 * 32) attn_join<kKv, kExtra>(p, c->scan, total, parts);
     if ((int)blockIdx.x >= parts) {
         if (warp == 11) attn_edges<bf16_t>(p, blockIdx.x, gridDim.x);
         return;
     }
-    Walk walk;
-    walk.begin = walk.t = attn_part(total, parts, blockIdx.x);
-    walk.end = attn_part(total, parts, blockIdx.x + 1);
-    walk.b = c->scan.place[0].b;
-    walk.base = c->scan.place[0].base;
+    Walk walk(c->scan, total, parts);
 
     if (tid == 0) {
         for (int i = 0; i < Shape<D>::kStages; ++i) {
@@ -769,7 +760,7 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&c->empty[i], 2);
             mbar_init(&c->clean[i], 1);
         }
-        mbar_init(&c->q_full, 1);
+        mbar_init(&c->q_full, 2);
         mbar_init(&c->q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->s_full[i], 1);
@@ -786,6 +777,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 8 * 32) {
         tma_prefetch(&mk);
         tma_prefetch(&mv);
+        tma_prefetch(&mq);
     }
     if (warp == 9) tmem_alloc512(&c->tmem);
     tc_fence_before();
@@ -807,7 +799,7 @@ __global__ void __launch_bounds__(NT, 1)
             is.run(p, walk);
         }
         if (warp == 11) {
-            help<D>(p, c, qs, stages, walk);
+            help<D>(p, c, &mq, qs, stages, walk);
             attn_edges<bf16_t>(p, blockIdx.x, gridDim.x, *reinterpret_cast<volatile int*>(&c->abort) != 0);
         }
     }
@@ -834,10 +826,8 @@ __global__ void __launch_bounds__(NT, 1)
     }
 }
 
-// The 128-byte-swizzled view of k or v that the producer copies boxes of: 64
-// elements x (page_size, at most 128) slots of one head of one page.
-bool make_map(CUtensorMap* map, const AttnParams& p, const void* base) {
-    using Encode = decltype(&cuTensorMapEncodeTiled);
+using Encode = decltype(&cuTensorMapEncodeTiled);
+Encode encoder() {
     static const Encode encode = [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult found;
@@ -846,46 +836,62 @@ bool make_map(CUtensorMap* map, const AttnParams& p, const void* base) {
             fn = nullptr;
         return reinterpret_cast<Encode>(fn);
     }();
-    if (!encode) return false;
+    return encode;
+}
+
+// A rank-4 bf16 tensor, copied in boxes of 64 elements x box1 x box2 with the
+// 128-byte swizzle; strides in elements.
+bool encode_map(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[4], const long long (&strides)[3],
+                cuuint32_t box1, cuuint32_t box2) {
+    cuuint64_t st[3];
+    for (int i = 0; i < 3; ++i) {
+        // the stride of an index that only takes 0 may be anything that the encoding accepts
+        st[i] = dims[i + 1] > 1 ? (cuuint64_t)strides[i] * 2 : 16;
+        if (st[i] == 0 || st[i] % 16 != 0 || st[i] >= (1ull << 40)) return false;
+    }
+    const cuuint32_t box[4] = {64, box1, box2, 1}, step[4] = {1, 1, 1, 1};
+    const Encode encode = encoder();
+    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, st, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// k or v: boxes of (page_size, at most 128) slots of one head of one page.
+bool make_map(CUtensorMap* map, const AttnParams& p, const void* base) {
     const int ps = 1 << p.page_shift;
-    const cuuint64_t dims[4] = {(cuuint64_t)p.D, (cuuint64_t)ps, (cuuint64_t)p.Hkv, (cuuint64_t)p.num_pages};
-    // the stride of an index that only takes 0 may be anything that the encoding accepts
-    const cuuint64_t any = (cuuint64_t)p.D * 2;
-    const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, p.Hkv > 1 ? (cuuint64_t)p.head_stride * 2 : any,
-                                   p.num_pages > 1 ? (cuuint64_t)p.page_stride * 2 : any};
-    for (const cuuint64_t s : strides)
-        if (s == 0 || s % 16 != 0 || s >= (1ull << 40)) return false;
-    const cuuint32_t box[4] = {64, (cuuint32_t)std::min(ps, kKv), 1, 1}, step[4] = {1, 1, 1, 1};
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return encode_map(map, base, {(cuuint64_t)p.D, (cuuint64_t)ps, (cuuint64_t)p.Hkv, (cuuint64_t)p.num_pages},
+                      {p.token_stride, p.head_stride, p.page_stride}, (cuuint32_t)std::min(ps, kKv), 1);
 }
 
 template <int D>
-cudaError_t launch_tc(const AttnParams& p, const AttnPlan& plan, const CUtensorMap& mk, const CUtensorMap& mv,
-                      cudaStream_t st) {
+cudaError_t launch_tc(const AttnParams& p, const AttnPlan& plan, const CUtensorMap* maps, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)Shape<D>::kSmem);
     if (e != cudaSuccess) return e;
-    attn_tc_kernel<D><<<plan.grid, NT, Shape<D>::kSmem, st>>>(p, mk, mv);
+    attn_tc_kernel<D><<<plan.grid, NT, Shape<D>::kSmem, st>>>(p, maps[0], maps[1], maps[2]);
     e = cudaGetLastError();
-    return e != cudaSuccess ? e : launch_attention_combine_tc(p, plan, st);
+    return e != cudaSuccess ? e : launch_attention_join(p, 1, plan, st);
 }
 
 }  // namespace
 
-int attention_tc_rows() { return kRows; }
+// Two halves of whole nodes, 128 rows at most each.
+int attention_tc_rows(int group) { return 2 * (128 / group) * group; }
 int attention_tc_kv() { return kKv; }
 
 bool attention_tc_maps(const AttnParams& p, AttnMaps* m) {
-    static_assert(sizeof(AttnMaps) >= 2 * sizeof(CUtensorMap), "two maps");
+    static_assert(sizeof(AttnMaps) >= 3 * sizeof(CUtensorMap), "three maps");
     CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(m);
-    return make_map(maps, p, p.k) && make_map(maps + 1, p, p.v);
+    const long long Hq = (long long)p.Hkv * p.G;
+    // queries: boxes of the nodes of a half, the heads of one group
+    return make_map(maps, p, p.k) && make_map(maps + 1, p, p.v) &&
+           encode_map(maps + 2, p.q, {(cuuint64_t)p.D, (cuuint64_t)Hq, (cuuint64_t)p.N, (cuuint64_t)p.B},
+                      {p.D, Hq * p.D, p.N * Hq * p.D}, (cuuint32_t)p.G, (cuuint32_t)std::min(128 / p.G, p.N));
 }
 
 cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const AttnMaps& m, cudaStream_t st) {
     const CUtensorMap* maps = reinterpret_cast<const CUtensorMap*>(&m);
-    return p.D == 128 ? launch_tc<128>(p, plan, maps[0], maps[1], st) : launch_tc<64>(p, plan, maps[0], maps[1], st);
+    return p.D == 128 ? launch_tc<128>(p, plan, maps, st) : launch_tc<64>(p, plan, maps, st);
 }
 
 SV_DEBUG_READER(attention_tc)

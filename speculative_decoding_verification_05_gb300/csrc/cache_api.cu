@@ -80,6 +80,8 @@ sv::AttnPlan attention_layout(sv::AttnPlan a, int D) {
     o = al(o + (size_t)2 * a.grid * a.rows * D * sizeof(float));
     a.part_ml = o;
     o = al(o + (size_t)2 * a.grid * a.rows * sizeof(float2));
+    a.joins = o;
+    o = al(o + (size_t)a.grid * sizeof(sv::AttnJoin));
     a.total = o;
     return a;
 }
@@ -93,9 +95,9 @@ sv::AttnPlan simt_plan(int D, spec_dtype dtype) {
     return attention_layout(a, D);
 }
 
-sv::AttnPlan tc_plan(int D) {
+sv::AttnPlan tc_plan(int D, int group) {
     sv::AttnPlan a = {};
-    a.rows = sv::attention_tc_rows();
+    a.rows = sv::attention_tc_rows(group);
     a.kv = sv::attention_tc_kv();
     a.grid = kSms;
     return attention_layout(a, D);
@@ -103,9 +105,9 @@ sv::AttnPlan tc_plan(int D) {
 
 bool tc_shape(int D, spec_dtype dtype) { return dtype == SPEC_BF16 && (D == 64 || D == 128); }
 
-size_t attention_bytes(int D, spec_dtype dtype) {
+size_t attention_bytes(int D, int group, spec_dtype dtype) {
     const size_t simt = simt_plan(D, dtype).total;
-    return tc_shape(D, dtype) ? std::max(simt, tc_plan(D).total) : simt;
+    return tc_shape(D, dtype) ? std::max(simt, tc_plan(D, group).total) : simt;
 }
 
 bool attention_shape_ok(int B, int N, int q_heads, int kv_heads, int D) {
@@ -119,7 +121,7 @@ extern "C" {
 
 size_t spec_tree_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim, spec_dtype dtype) {
     if (!attention_shape_ok(B, N, q_heads, kv_heads, head_dim) || !dtype_ok(dtype)) return 0;
-    return attention_bytes(head_dim, dtype);
+    return attention_bytes(head_dim, q_heads / kv_heads, dtype);
 }
 
 spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dtype dtype,
@@ -135,7 +137,7 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
         return SPEC_EINVAL;
     const float c2 = scale * 1.4426950408889634f;
     if (!std::isfinite(scale) || !std::isfinite(c2)) return SPEC_EINVAL;
-    if (ws_bytes < attention_bytes(cache->head_dim, dtype)) return SPEC_EINVAL;
+    if (ws_bytes < attention_bytes(cache->head_dim, q_heads / cache->kv_heads, dtype)) return SPEC_EINVAL;
     sv::AttnParams p = {};
     p.q = q;
     p.k = cache->k;
@@ -165,11 +167,12 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
         p.tile_rows = plan.rows;
         p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);
         p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.part_ml);
+        p.joins = reinterpret_cast<sv::AttnJoin*>(static_cast<char*>(workspace) + plan.joins);
     };
     sv::AttnMaps maps;
     // (that kernel takes the maximum before the scale: it has to be positive)
     if (tc_shape(p.D, dtype) && scale > 0.f && sv::attention_tc_maps(p, &maps)) {
-        const sv::AttnPlan plan = tc_plan(p.D);
+        const sv::AttnPlan plan = tc_plan(p.D, p.G);
         use(plan);
         return done(sv::launch_attention_tc(p, plan, maps, st));
     }
