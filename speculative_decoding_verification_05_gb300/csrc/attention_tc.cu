@@ -6,9 +6,10 @@
 //              (tensor copies with the 128-byte swizzle) into a ring of stages;
 //   issuers    (warps 9, 10; one a stream) issue the products: S = Q K^T into
 //              tensor memory, and O += P V with P taken from tensor memory;
-//   helper     (warp 11) brings a unit's queries (while the last one's results
-//              are still being written), checks its pages, clears what V must
-//              not contain, and writes the rows that no unit covers;
+//   helper     (warp 11) walks the part and posts each stay in a unit (a
+//              segment) for the others, brings its queries (while the last
+//              one's results are still being written), clears what V must not
+//              contain, and writes the rows that no unit covers;
 //   two groups (warps 0-3, 4-7) of 128 threads, a row each: the softmax between
 //              the two products, and the results.
 // The groups are two streams that the tensor core serves in turn, one's
@@ -69,25 +70,12 @@ struct Shape {
     static constexpr size_t kSmem = 1024 + 2048 + (size_t)(2 + kStages) * kTile;
 };
 
-struct Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], ask[2], groups, drain;
-    uint32_t loads;  // ring entries filled
-    AttnScan scan;
-    uint32_t tmem;
-    int abort;
-    int flags[4];  // of a segment (its number modulo 4): 1 V had elements that are not finite, 2 a bad page
-    uint8_t heavy[2][4];  // steps of 16 positions with heavy weights, by group and warp (read as one word)
-    float2 ml[128];
-};
-static_assert(sizeof(Ctl) <= 2048, "control region");
-
 // A stay in a unit; dual: both streams go over its tiles.
 struct Seg : AttnStay {
     bool dual;
     int steps;  // softmax tiles of both streams together
 };
-constexpr int kExtra = 2;  // tiles that a unit's start and end count for (attention.cuh)
+constexpr int kExtra = 3;  // tiles that a unit's start and end count for (attention.cuh)
 struct Walk : AttnWalk<kKv, kExtra> {
     using AttnWalk<kKv, kExtra>::AttnWalk;
     SV_DEV bool next(const AttnParams& p, Seg* s) {
@@ -97,6 +85,22 @@ struct Walk : AttnWalk<kKv, kExtra> {
         return true;
     }
 };
+
+struct Ctl {
+    uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], ask[2], groups, drain;
+    uint32_t loads;  // ring entries filled
+    AttnScan scan;
+    uint32_t tmem;
+    int abort;
+    uint64_t seg_full[4];
+    Seg seg[4];    // the helper's post: segment number modulo 4; b = -1: no more
+    int flags[4];  // of a segment: 1 V had elements that are not finite, 2 a bad page
+    int busy;      // an issuer is issuing
+    uint8_t heavy[2][4];  // steps of 16 positions with heavy weights, by group and warp (read as one word)
+    float2 ml[128];
+};
+static_assert(sizeof(Ctl) <= 2048, "control region");
 
 // Order of a segment's tiles in the ring (cnt tiles): the order of their first
 // use. Two streams on the same tiles: K0 V0 K1 V1 ..; on alternate tiles: K0
@@ -140,11 +144,18 @@ SV_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const int* abort) {
     return __all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort)) != 0;
 }
 
+// The post of segment number `seg`, null after the last (or a timeout). It
+// stays until segment seg + 3 begins.
+SV_DEV const Seg* next_seg(Ctl* c, uint32_t seg, bool* ok) {
+    *ok = warp_wait(&c->seg_full[seg & 3], (seg >> 2) & 1, &c->abort);
+    return *ok && c->seg[seg & 3].b >= 0 ? &c->seg[seg & 3] : nullptr;
+}
+
 // ---- copies ----------------------------------------------------------------------
 
 template <int D>
-SV_DEV bool load_box(const AttnParams& p, Ctl* c, const CUtensorMap* map, uint32_t stages, const Seg& s, int tile,
-                     uint32_t ring) {
+SV_DEV bool load_box(const AttnParams& p, Ctl* c, const CUtensorMap* map, uint32_t stages, const Seg& s, int slot,
+                     int tile, uint32_t ring) {
     constexpr int NS = Shape<D>::kStages;
     const int lane = threadIdx.x & 31, st = ring % NS;
     const uint32_t round = ring / NS;
@@ -155,6 +166,7 @@ SV_DEV bool load_box(const AttnParams& p, Ctl* c, const CUtensorMap* map, uint32
     if (pg < pages && pos < s.len) id = __ldg(p.table + s.b * p.table_stride + (pos >> p.page_shift));
     const bool ok = id >= 0 && id < p.num_pages;
     const unsigned who = __ballot_sync(0xFFFFFFFFu, ok);
+    if (!ok && pg < pages && pos < s.len) atomicOr(&c->flags[slot], 2);
     if (round && !warp_wait(&c->empty[st], (round - 1) & 1, &c->abort)) return false;
     if (lane == 0) mbar_expect_tx(&c->full[st], __popc(who) * (uint32_t)ps * 128);
     __syncwarp();
@@ -165,19 +177,20 @@ SV_DEV bool load_box(const AttnParams& p, Ctl* c, const CUtensorMap* map, uint32
 }
 
 template <int D>
-SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t stages,
-                    Walk walk) {
-    uint32_t ring = 0;
-    Seg s;
+SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t stages) {
+    uint32_t ring = 0, seg = 0;
     bool ok = true;
-    while (ok && walk.next(p, &s)) {
-        const int cnt = s.last - s.first, ahead = s.dual ? 1 : 2;
+    while (const Seg* at = next_seg(c, seg, &ok)) {
+        const Seg& s = *at;
+        const int cnt = s.last - s.first, ahead = s.dual ? 1 : 2, slot = seg & 3;
         for (int i = -ahead; ok && i < cnt; ++i) {  // V(i), then K(i + ahead); K alone before the first V
-            if (i >= 0) ok = load_box<D>(p, c, mv, stages, s, s.first + i, ring++);
-            if (ok && i + ahead < cnt) ok = load_box<D>(p, c, mk, stages, s, s.first + i + ahead, ring++);
+            if (i >= 0) ok = load_box<D>(p, c, mv, stages, s, slot, s.first + i, ring++);
+            if (ok && i + ahead < cnt) ok = load_box<D>(p, c, mk, stages, s, slot, s.first + i + ahead, ring++);
         }
+        if (!ok) break;
+        ++seg;
     }
-    if ((threadIdx.x & 31) == 0) c->loads = ok ? ring : ring - 1;
+    if ((threadIdx.x & 31) == 0) c->loads = ok ? ring : ring - (ring > 0);
     if (!ok) c->abort = 1;
 }
 
@@ -223,11 +236,32 @@ struct Issuer {
         return true;
     }
 
+    // One stream's products at a time: issued together, the streams' products
+    // would run in turns and both end late, and both softmaxes wait together;
+    // in blocks, one's products run during the other's softmax.
+    SV_DEV bool lock() {
+        uint64_t start = 0, now;
+        uint32_t got = 0, n = 0;
+        for (;;) {
+            if (elected()) got = atomicCAS(&c->busy, 0, 1) == 0;
+            got = __any_sync(0xFFFFFFFFu, got);
+            if (got) return true;
+            if (++n & 0xFFu) continue;
+            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+            if (!start) start = now;
+            if (__any_sync(0xFFFFFFFFu, now - start > 2000000000ull || *reinterpret_cast<volatile int*>(&c->abort)))
+                return false;
+        }
+    }
+    SV_DEV void unlock() {
+        __syncwarp();
+        if (elected()) atomicExch(&c->busy, 0);
+        __syncwarp();
+    }
+
     // S of the tile at `ring`; last: the segment's last of this stream.
-    SV_DEV bool scores(bool dual, bool last, uint32_t ring) {
+    SV_DEV void scores(bool dual, bool last, uint32_t ring) {
         constexpr uint32_t idesc = mma_idesc(kKv, false);
-        if (!reach(ring)) return false;
-        tc_fence_after();
         const uint32_t st = uni(ring % NS), d = tmem + 128 * w;
         const uint64_t a = mma_desc(qs + (dual ? w * kTile : 0u), 16, 1024), b = mma_desc(stages + st * kTile, 16, 1024);
         if (elected()) {
@@ -241,26 +275,12 @@ struct Issuer {
             if (last) mma_commit(&c->q_empty);
         }
         __syncwarp();
-        return true;
     }
 
-    // O += P V of the tile at `ring`; tail: its V has to be cleaned first.
-    SV_DEV bool output(bool dual, bool first, bool last, bool tail, int live, uint32_t ring) {
+    // O += P V of the tile at `ring`.
+    SV_DEV void output(bool first, bool last, int live, uint32_t heavy, uint32_t ring) {
         constexpr uint32_t idesc = mma_idesc(D, true);
-        if (!reach(ring)) return false;
-        const uint32_t st = uni(ring % NS);
-        if (tail && (!dual || w == 0)) {
-            if (elected()) mbar_arrive(&c->ask[w]);
-            __syncwarp();
-        }
-        if (!warp_wait(&c->p_full[w], p_phase, &c->abort)) return false;
-        p_phase ^= 1;
-        if (tail && !warp_wait(&c->clean[st], clean >> st & 1, &c->abort)) return false;
-        tc_fence_after();
-        uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w]);  // a byte of each warp
-        heavy |= heavy >> 16;
-        heavy = uni((heavy | heavy >> 8) & 0xFFu);
-        const uint32_t d = tmem + 256 + 128 * w, a = tmem + 128 * w;
+        const uint32_t st = uni(ring % NS), d = tmem + 256 + 128 * w, a = tmem + 128 * w;
         const uint64_t b = mma_desc(stages + st * kTile, kHalf, 1024);
         if (elected()) {
 #pragma unroll
@@ -276,14 +296,47 @@ struct Issuer {
             if (last) mma_commit(&c->o_full[w]);
         }
         __syncwarp();
+    }
+
+    // Step j of a segment: the product with V of this stream's tile j and the
+    // scores of its tile j + 1, as far as there are such.
+    SV_DEV bool step(const Seg& s, bool dual, int cnt, int mine, int j, uint32_t ring0) {
+        const int i = dual ? j : 2 * j + (int)w, next = dual ? j + 1 : i + 2;
+        const uint32_t rv = ring0 + ring_v(s, i), rk = ring0 + ring_k(s, next);
+        uint32_t heavy = 0;
+        if (j >= 0) {
+            if (!reach(rv)) return false;
+            const uint32_t st = uni(rv % NS);
+            const bool tail = tail_tile(s, i);
+            if (tail && (!dual || w == 0)) {  // V has to be cleaned first
+                if (elected()) mbar_arrive(&c->ask[w]);
+                __syncwarp();
+            }
+            if (j + 1 < mine && !reach(rk)) return false;
+            if (!warp_wait(&c->p_full[w], p_phase, &c->abort)) return false;
+            p_phase ^= 1;
+            if (tail && !warp_wait(&c->clean[st], clean >> st & 1, &c->abort)) return false;
+            heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w]);  // a byte of each warp
+            heavy |= heavy >> 16;
+            heavy = uni((heavy | heavy >> 8) & 0xFFu);
+        } else if (j + 1 < mine && !reach(rk)) {
+            return false;
+        }
+        if (!lock()) return false;
+        tc_fence_after();
+        if (j >= 0) output(j == 0, j + 1 == mine, (int)uni(live_of(s, i)), heavy, rv);
+        if (j + 1 < mine) scores(dual, j + 2 == mine, rk);
+        unlock();
+        // (phases of the stages whose V this step's tiles have had cleaned, the other stream's too)
+        if (j >= 0) clean ^= clean_stages<D>(s, ring0, dual ? j : 2 * j, dual ? j + 1 : min(2 * j + 2, cnt));
         return true;
     }
 
-    SV_DEV void run(const AttnParams& p, Walk walk) {
-        uint32_t ring0 = 0;
-        Seg s;
+    SV_DEV void run() {
+        uint32_t ring0 = 0, seg = 0;
         bool ok = true;
-        while (ok && walk.next(p, &s)) {
+        while (const Seg* at = next_seg(c, seg, &ok)) {
+            const Seg& s = *at;
             const bool dual = uni(s.dual);
             const int cnt = (int)uni(s.last - s.first);
             const int mine = dual ? cnt : (cnt + 1 - (int)w) >> 1;  // tiles of this stream
@@ -292,17 +345,13 @@ struct Issuer {
             if (mine == 0 && elected()) mbar_arrive(&c->q_empty);
             __syncwarp();
 #pragma unroll 1
-            for (int j = -1; ok && j < mine; ++j) {
-                const int i = dual ? j : 2 * j + (int)w, next = dual ? j + 1 : i + 2;
-                if (j >= 0) ok = output(dual, j == 0, j + 1 == mine, tail_tile(s, i), (int)uni(live_of(s, i)),
-                                         ring0 + ring_v(s, i));
-                if (ok && j + 1 < mine) ok = scores(dual, j + 2 == mine, ring0 + ring_k(s, next));
-                // (phases of the stages whose V this step's tiles have had cleaned, the other stream's too)
-                if (j >= 0) clean ^= clean_stages<D>(s, ring0, dual ? j : 2 * j, dual ? j + 1 : min(2 * j + 2, cnt));
-            }
+            for (int j = -1; ok && j < mine; ++j)
+                if (mine) ok = step(s, dual, cnt, mine, j, ring0);
             if (!dual && mine < (cnt + 1) >> 1) clean ^= clean_stages<D>(s, ring0, 2 * mine, cnt);
             ring0 += 2 * cnt;
             while (ok && seen < ring0) ok = pass();
+            if (!ok) break;
+            ++seg;
         }
         if (!ok) c->abort = 1;
     }
@@ -466,31 +515,32 @@ SV_DEV void help(const AttnParams& p, Ctl* c, const CUtensorMap* mq, uint32_t qs
     const uint32_t box = 128u * min(nodes, p.N) * p.G;     // bytes of 64 columns of them
     uint32_t seg = 0, ring0 = 0, asked = 0;
     Seg s;
-    bool ok = true;
-    while (ok && walk.next(p, &s)) {
-        // (the groups are past segment seg - 3: its products' last was issued before this one's queries are free)
-        if (seg && !(ok = warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort))) break;
+    auto post = [&](uint32_t number) {  // the next segment becomes `number`'s post
+        const bool more = walk.next(p, &s);
         if (lane == 0) {
-            c->flags[(seg + 1) & 3] = 0;
-            mbar_expect_tx(&c->q_full, box * (D / 64) * (s.dual ? 2 : 1));
+            c->flags[number & 3] = 0;
+            if (!more) s.b = -1;
+            c->seg[number & 3] = s;
+            mbar_arrive(&c->seg_full[number & 3]);
         }
+        __syncwarp();
+        return more;
+    };
+    bool ok = true, more = post(0);
+    while (ok && more) {
+        const Seg& s = c->seg[seg & 3];
+        // With the last segment's queries free, the groups have begun segment
+        // seg - 2, the issuers and the producer seg - 1: post seg + 1 takes the
+        // place of one that nobody needs.
+        if (seg && !(ok = warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort))) break;
+        if (lane == 0) mbar_expect_tx(&c->q_full, box * (D / 64) * (s.dual ? 2 : 1));
         __syncwarp();
         if (lane < D / 64 * (s.dual ? 2 : 1)) {
             const int w = lane / (D / 64), half = lane - w * (D / 64);
             tma_load4(qs + w * Shape<D>::kTile + half * kHalf, mq, half * 64, s.h * p.G, s.row0 / p.G + w * nodes, s.b,
                       &c->q_full);
         }
-        // a page that does not exist anywhere under this segment's tiles
-        const long long lo = (long long)s.first * kKv >> p.page_shift;
-        const long long hi = (min(s.len, (long long)s.last * kKv) - 1) >> p.page_shift;
-        bool bad = false;
-        for (long long i = lo + lane; i <= hi; i += 32) {
-            const int id = __ldg(p.table + s.b * p.table_stride + i);
-            bad |= id < 0 || id >= p.num_pages;
-        }
-        if (bad) atomicOr(&c->flags[seg & 3], 2);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&c->q_full);
+        more = post(seg + 1);
         const int cnt = s.last - s.first;
         for (int i = max(0, s.L / kKv - s.first); ok && i < cnt; ++i) {
             if (!tail_tile(s, i)) continue;
@@ -525,33 +575,30 @@ struct Group {
         return ok;
     }
 
-    SV_DEV static void hide(float (&x)[32], const uint4& see, int k) {
-        const uint32_t bits = k == 0 ? see.x : k == 1 ? see.y : k == 2 ? see.z : see.w;
+    SV_DEV static void hide(float (&x)[64], const uint4& see, int k) {
+        const uint32_t lo = k ? see.z : see.x, hi = k ? see.w : see.y;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (!(bits >> i & 1)) x[i] = kNegInf;
+        for (int i = 0; i < 32; ++i) {
+            if (!(lo >> i & 1)) x[i] = kNegInf;
+            if (!(hi >> i & 1)) x[32 + i] = kNegInf;
+        }
     }
 
     // One tile: S -> P, the row's maximum m (octaves) and sum l. S is read from
-    // tensor memory twice, for the maximum and for the weights, 32 positions at
+    // tensor memory twice, for the maximum and for the weights, 64 positions at
     // a time: the loops stay small (held in registers whole and unrolled, the
     // row took two to three times as long, waiting for instructions).
     SV_DEV void softmax(const uint4 see, bool tail, bool first, float c2, float& m, float& l) {
         float mx[8] = {};  // by steps of 16 positions
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-            float x[32];
-            tmem_ld32(tm_s + 32 * k, x);
+        for (int k = 0; k < 2; ++k) {
+            float x[64];
+            tmem_ld64(tm_s + 64 * k, x);
             if (tail) hide(x, see, k);
 #pragma unroll
-            for (int i = 0; i < 6; ++i) mx[i] = mx[i + 2];
-            mx[6] = x[0];
-            mx[7] = x[16];
+            for (int i = 0; i < 4; ++i) mx[i] = mx[i + 4];
 #pragma unroll
-            for (int i = 1; i < 16; ++i) {
-                mx[6] = fmaxf(mx[6], x[i]);
-                mx[7] = fmaxf(mx[7], x[16 + i]);
-            }
+            for (int i = 0; i < 64; ++i) mx[4 + (i >> 4)] = i & 15 ? fmaxf(mx[4 + (i >> 4)], x[i]) : x[i];
         }
         const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * c2;
@@ -586,29 +633,35 @@ struct Group {
         const uint64_t cc = pack2(c2, c2), rr = pack2(-ref, -ref);
         uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-            float x[32];
-            uint32_t hi[16], lo[16];
-            tmem_ld32(tm_s + 32 * k, x);
+        for (int k = 0; k < 2; ++k) {
+            float x[64];
+            tmem_ld64(tm_s + 64 * k, x);
             if (tail) hide(x, see, k);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float& a = x[2 * e];
-                float& b = x[2 * e + 1];
-                unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
-                a = ex2(a);
-                b = ex2(b);
-                sum[e & 1] = add2(sum[e & 1], pack2(a, b));
-                hi[e] = pack_bf16(a, b);
-                lo[e] = 0u;
-            }
-            if (heavy >> (2 * k) & 3)  // what the rounding took
+            for (int j = 0; j < 2; ++j) {
+                uint32_t hi[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    lo[e] = pack_bf16(x[2 * e] - __uint_as_float(hi[e] << 16),
-                                      x[2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
-            tmem_st16(tm_s + 32 * k, hi);
-            tmem_st16(tm_s + 32 * k + 16, lo);
+                for (int e = 0; e < 16; ++e) {
+                    float& a = x[32 * j + 2 * e];
+                    float& b = x[32 * j + 2 * e + 1];
+                    unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
+                    a = ex2(a);
+                    b = ex2(b);
+                    sum[e & 1] = add2(sum[e & 1], pack2(a, b));
+                    hi[e] = pack_bf16(a, b);
+                }
+                tmem_st16(tm_s + 64 * k + 32 * j, hi);
+                if (heavy >> (4 * k + 2 * j) & 3) {  // what the rounding took
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        hi[e] = pack_bf16(x[32 * j + 2 * e] - __uint_as_float(hi[e] << 16),
+                                          x[32 * j + 2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) hi[e] = 0u;
+                }
+                tmem_st16(tm_s + 64 * k + 32 * j + 16, hi);
+            }
         }
         float a, b;
         unpack2(add2(sum[0], sum[1]), &a, &b);
@@ -694,12 +747,13 @@ struct Group {
         return true;
     }
 
-    SV_DEV void run(Walk walk) {
+    SV_DEV void run() {
         const float c2 = p.c2;
-        int slot = 0;
-        Seg s;
+        uint32_t seg = 0;
         bool ok = true;
-        while (walk.next(p, &s)) {
+        while (const Seg* at = next_seg(c, seg, &ok)) {
+            const Seg& s = *at;
+            const int slot = seg & 3;
             // (group 0 has read the last segment's O_1)
             if (!(ok = meet())) break;
 
@@ -728,7 +782,7 @@ struct Group {
             __syncwarp();
             if (!(ok = finish(s, slot, m, l))) break;
             tc_fence_before();
-            slot = (slot + 1) & 3;
+            ++seg;
         }
         if (!ok) c->abort = 1;
     }
@@ -747,7 +801,7 @@ __global__ void __launch_bounds__(NT, 1)
     asm volatile("griddepcontrol.launch_dependents;");
     const long long total = attn_locate<kKv, kExtra, NT>(p, &c->scan);
     const int parts = attn_parts(total, gridDim.x);
-    if (tid == 11 * 32) attn_join<kKv, kExtra>(p, c->scan, total, parts);
+    if (tid == 10 * 32) attn_join<kKv, kExtra>(p, c->scan, total, parts);
     if ((int)blockIdx.x >= parts) {
         if (warp == 11) attn_edges<bf16_t>(p, blockIdx.x, gridDim.x);
         return;
@@ -760,7 +814,7 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&c->empty[i], 2);
             mbar_init(&c->clean[i], 1);
         }
-        mbar_init(&c->q_full, 2);
+        mbar_init(&c->q_full, 1);
         mbar_init(&c->q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->s_full[i], 1);
@@ -769,6 +823,8 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&c->ask[i], 1);
             c->flags[2 * i] = c->flags[2 * i + 1] = 0;
         }
+        for (int i = 0; i < 4; ++i) mbar_init(&c->seg_full[i], 1);
+        c->busy = 0;
         mbar_init(&c->groups, 8);
         mbar_init(&c->drain, 2);
         c->abort = 0;
@@ -790,13 +846,13 @@ __global__ void __launch_bounds__(NT, 1)
         const int w = warp >> 2, lanes = (warp & 3) * 32;
         Group<D> g{p, c, w, warp & 3, lane, tid & 127, tmem + ((uint32_t)lanes << 16) + 128 * w,
                    tmem + ((uint32_t)lanes << 16) + 256 + 128 * w};
-        g.run(walk);
+        g.run();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 8) produce<D>(p, c, &mk, &mv, stages, walk);
+        if (warp == 8) produce<D>(p, c, &mk, &mv, stages);
         if (warp == 9 || warp == 10) {
             Issuer<D> is{c, uni(warp - 9), uni(tmem), qs, stages};
-            is.run(p, walk);
+            is.run();
         }
         if (warp == 11) {
             help<D>(p, c, &mq, qs, stages, walk);
