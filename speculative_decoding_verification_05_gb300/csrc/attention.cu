@@ -258,63 +258,76 @@ __global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ A
 }
 
 // Joins the pieces of the units that several parts share: block (c, y) takes
-// joins[c], a warp a row: weights 2^(m_i - max m) of the pieces, a lane a piece,
-// then their sums, four columns a lane (eight: D > 128).
+// kJoinRows rows of joins[c]. A warp forms the weights 2^(m_i - max m) / sum of
+// a row's pieces, a lane a piece; every thread adds up four columns of a row,
+// eight pieces in flight (the first eight while the weights are formed). The
+// sums' order is that of the parts. Bound by the latency of dependent loads;
+// the pieces come from L2.
+constexpr int kJoinRows = 8, kJoinNT = 256;
+
 template <typename E>
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnParams p) {
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constant__ AttnParams p) {
+    __shared__ float weight[kJoinRows][32];
+    __shared__ float top[kJoinRows];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4* src = reinterpret_cast<const int4*>(p.joins + blockIdx.x + 1);
     const int4 u = __ldcg(src), v = __ldcg(src + 1);  // b, h, row0, rows; slot0, first, last
-    const int pieces = v.z - v.y + 2;
-    for (int r = blockIdx.y * 4 + (threadIdx.x >> 5); r < u.w; r += gridDim.y * 4) {
-        auto at = [&](int i) { return (long long)(i == 0 ? v.x : 2 * (v.y + i - 1)) * p.tile_rows + r; };
-        const float2 none = make_float2(__uint_as_float(0xFF800000u), 0.f);
-        float2 ml = lane < pieces ? __ldcg(p.part_ml + at(lane)) : none;
-        float m = ml.x;
-        for (int i = lane + 32; i < pieces; i += 32) m = fmaxf(m, __ldcg(p.part_ml + at(i)).x);
+    const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, u.w - r0);
+    if (rows <= 0) return;
+    const int pieces = v.z - v.y + 2, D4 = p.D / 4;
+    auto at = [&](int i, int r) { return (long long)(i == 0 ? v.x : 2 * (v.y + i - 1)) * p.tile_rows + r0 + r; };
+    const float2 none = make_float2(__uint_as_float(0xFF800000u), 0.f);
+    float4 x[8];
+    auto load = [&](int i0, int r, int d) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            x[k] = i0 + k < pieces ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i0 + k, r) * p.D + d))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    if (tid < rows * D4) load(0, tid / D4, tid % D4 * 4);
+    if (warp < rows) {
+        const int r = warp;
+        float2 ml = none;
+        float m = none.x, l = 0.f;
+        for (int i = lane; i < pieces; i += 32) {
+            ml = __ldcg(p.part_ml + at(i, r));
+            m = fmaxf(m, ml.x);
+        }
         m = warp_max(m);
-        const float ref = m == __uint_as_float(0xFF800000u) ? 0.f : m;
-        float l = 0.f;
-        float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-        for (int i0 = 0; i0 < pieces; i0 += 32) {
-            if (i0) ml = i0 + lane < pieces ? __ldcg(p.part_ml + at(i0 + lane)) : none;
-            const float w = ex2(ml.x - ref);
-            l += w * ml.y;
-            const int n = min(32, pieces - i0);
-            for (int i = 0; i < n; i += 8) {
-                float4 x[8][2];
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        const int d = (lane + 32 * g) * 4;
-                        x[k][g] = i + k < n && d < p.D
-                                      ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i0 + i + k) * p.D + d))
-                                      : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float wk = __shfl_sync(0xFFFFFFFFu, w, (i + k) & 31);
-                    if (i + k < n) {
-                        acc[0] = fma4(wk, x[k][0], acc[0]);
-                        acc[1] = fma4(wk, x[k][1], acc[1]);
-                    }
-                }
-            }
+        const float ref = m == none.x ? 0.f : m;
+        for (int i = lane; i < pieces; i += 32) {
+            if (pieces > 32) ml = __ldcg(p.part_ml + at(i, r));
+            l += ex2(ml.x - ref) * ml.y;
         }
         l = warp_sum(l);
-        const int rr = u.z + r, node = rr / p.G;
-        const long long row = ((long long)u.x * p.N + node) * (p.Hkv * p.G) + u.y * p.G + (rr - node * p.G);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-            const int d = (lane + 32 * g) * 4;
-            if (d < p.D && SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
-                store4<E>(reinterpret_cast<E*>(p.out) + row * p.D + d,
-                          make_float4(acc[g].x * inv, acc[g].y * inv, acc[g].z * inv, acc[g].w * inv));
+        if (pieces <= 32) weight[r][lane] = lane < pieces ? ex2(ml.x - ref) * (l == 0.f ? 0.f : 1.f / l) : 0.f;
+        if (lane == 0) {
+            if (pieces > 32) weight[r][0] = l == 0.f ? 0.f : 1.f / l;
+            top[r] = ref;
+            if (p.lse) {
+                const int rr = u.z + r0 + r, node = rr / p.G;
+                p.lse[((long long)u.x * p.N + node) * (p.Hkv * p.G) + u.y * p.G + (rr - node * p.G)] = lse_of(m, l);
+            }
         }
-        if (lane == 0 && p.lse) p.lse[row] = lse_of(m, l);
+    }
+    __syncthreads();
+    for (int j = tid; j < rows * D4; j += kJoinNT) {
+        const int r = j / D4, d = (j - r * D4) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i0 = 0; i0 < pieces; i0 += 8) {
+            if (i0 || j != tid) load(i0, r, d);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i0 + k < pieces) {
+                    const float w = pieces <= 32 ? weight[r][i0 + k]
+                                                 : weight[r][0] * ex2(__ldcg(p.part_ml + at(i0 + k, r)).x - top[r]);
+                    acc = fma4(w, x[k], acc);
+                }
+        }
+        const int rr = u.z + r0 + r, node = rr / p.G;
+        const long long row = ((long long)u.x * p.N + node) * (p.Hkv * p.G) + u.y * p.G + (rr - node * p.G);
+        if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G)) store4<E>(reinterpret_cast<E*>(p.out) + row * p.D + d, acc);
     }
 }
 
@@ -325,8 +338,8 @@ cudaError_t launch_join(const AttnParams& p, const AttnPlan& plan, cudaStream_t 
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.grid - 1, (std::min(plan.rows, p.N * p.G) + 3) / 4);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3(plan.grid - 1, (std::min(plan.rows, p.N * p.G) + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(kJoinNT);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;

@@ -490,7 +490,8 @@ SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int i, int slot) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) any |= __vcmpeq2(y[u][e] & 0x7F807F80u, 0x7F807F80u);
+            for (int e = 0; e < 4; ++e)  // an exponent of all ones carries into the sign's place
+                any |= ((y[u][e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
         if (any) {
             found = true;
 #pragma unroll
