@@ -22,7 +22,9 @@ A paged cache, its page table and its reference counts live on the GPU.
 
 import contextlib
 import ctypes
+import functools
 import os
+import struct
 import threading
 
 import torch
@@ -59,6 +61,14 @@ class SpecCache(ctypes.Structure):
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
                 ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _CacheArg:
+    """A spec_cache argument: its packed bytes, or a SpecCache."""
+
+    @staticmethod
+    def from_param(x):
+        return x if isinstance(x, bytes) else ctypes.byref(x)
 
 
 class SpecError(RuntimeError):
@@ -126,7 +136,7 @@ def load_library(path=None):
         lib.spec_verify_noalloc.restype = _I
         lib.spec_philox_uniform.argtypes = [_U64, _U64, ctypes.c_uint32, ctypes.c_uint32, _I, _P, _P]
         lib.spec_philox_uniform.restype = _I
-        _C, _I64 = ctypes.POINTER(SpecCache), ctypes.c_int64
+        _C, _I64 = _CacheArg, ctypes.c_int64
         lib.spec_tree_attention_workspace_size.argtypes = [_I] * 6
         lib.spec_tree_attention_workspace_size.restype = _SZ
         lib.spec_tree_attention.argtypes = [_P, _C, _I, _P, _I64, _I, _P, _P, _P, _I, _I, _I, ctypes.c_float,
@@ -461,52 +471,76 @@ def philox_uniform(seed, row0, position, purpose, n, device=None):
 
 
 # ---- the paged key / value cache --------------------------------------------------
+#
+# These calls run once a layer and step, so the host side is kept short: plain
+# attribute reads, one packed struct, integer pointers, cached workspace sizes.
 
-_NULL = ctypes.c_void_p(0)
+_pack_cache = struct.Struct("@QQiiiii4xqqqq").pack   # spec_cache
+_LIVE = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
+
+
+def _library():
+    return _libs.get(_current[0]) or load_library()
+
+
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _scratch(nbytes, dev, index, raw):
+    """As ``workspace``, by the stream's raw handle (the same buffers)."""
+    buf = _ws_cache.get((index, raw))
+    if buf is None or buf.numel() < nbytes:
+        buf = workspace(nbytes, dev, torch.cuda.current_stream(dev))
+    return buf
 
 
 def _cache_args(k_cache, v_cache, layered):
-    """The C view of k / v caches [layers, pages, page_size, heads, head_dim]
-    (one layer: no first dimension), any strides with contiguous heads."""
-    if k_cache.dim() != 4 + layered or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+    """The packed spec_cache of k / v caches [layers, pages, page_size, heads, head_dim]
+    (one layer: no first dimension; any strides with contiguous heads), its
+    shape and its dtype code."""
+    sh, st = k_cache.shape, k_cache.stride()
+    if len(sh) != 4 + layered or v_cache.shape != sh or v_cache.dtype != k_cache.dtype:
         raise SpecError("k and v caches must share a dtype and the shape "
                         + ("[layers, " if layered else "[") + "pages, page_size, heads, head_dim]")
-    st = k_cache.stride()
-    if st != v_cache.stride() or st[-1] != 1:
+    if v_cache.stride() != st or st[-1] != 1:
         raise SpecError("k and v caches must share their strides, with contiguous heads")
-    if not (k_cache.is_cuda and v_cache.is_cuda and k_cache.device == v_cache.device):
+    if not k_cache.is_cuda or v_cache.get_device() != k_cache.get_device():
         raise SpecError("the caches must be on one CUDA device")
-    sh = k_cache.shape
-    layers, layer_stride = (sh[0], st[0]) if layered else (1, 0)
-    return SpecCache(k_cache.data_ptr(), v_cache.data_ptr(), layers, sh[-4], sh[-3], sh[-2], sh[-1], layer_stride,
-                     st[-4], st[-3], st[-2])
+    dt = _LIVE.get(k_cache.dtype)
+    if dt is None:
+        raise SpecError(f"caches must be float32 or bfloat16, got {k_cache.dtype}")
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), sh[0] if layered else 1, sh[-4], sh[-3], sh[-2], sh[-1],
+                       st[0] if layered else 0, st[-4], st[-3], st[-2]), sh, dt
 
 
-def _table_args(page_table, rows, device):
+def _table_args(page_table, rows, index):
     """Pointer, row stride and width of an int32 page table with `rows` rows."""
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.shape[0] != rows or \
-            page_table.device != device or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+    sh = page_table.shape
+    if len(sh) != 2 or page_table.dtype is not torch.int32 or sh[0] != rows or page_table.get_device() != index or \
+            (sh[1] > 1 and page_table.stride(1) != 1):
         raise SpecError(f"page_table must be an int32 tensor [{rows}, max_pages] on the cache's device, rows contiguous")
-    width = page_table.shape[1]
     # a single row's stride is free to be anything
-    return page_table.data_ptr(), (page_table.stride(0) if rows > 1 else width), width
+    return page_table.data_ptr(), (page_table.stride(0) if rows > 1 else sh[1]), sh[1]
 
 
-def _in(t, device, dtype=torch.int32):
+def _in(t, dev, index, dtype=torch.int32):
     """An input on the device in the library's layout (copied only if it is not there yet)."""
-    if t.dtype != dtype:
-        t = t.to(dtype)
-    if t.device != device:
-        t = t.to(device, non_blocking=True)
-    t = t.contiguous()
-    # a view that starts off 16 bytes: rows are moved as 16-byte words
-    return t.clone() if t.is_floating_point() and t.data_ptr() % 16 else t
+    if t.dtype is dtype and t.get_device() == index and t.is_contiguous():
+        # a view that starts off 16 bytes: rows are moved as 16-byte words
+        return t.clone() if t.data_ptr() & 15 and t.is_floating_point() else t
+    return _in(t.to(dtype).to(dev, non_blocking=True).contiguous(), dev, index, dtype)
 
 
-def _owned(t, shape, device, what):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != device or not t.is_contiguous():
+def _owned(t, shape, index, what):
+    if t.dtype is not torch.int32 or tuple(t.shape) != shape or t.get_device() != index or not t.is_contiguous():
         raise SpecError(f"{what} must be a contiguous int32 tensor {list(shape)} on the cache's device")
-    return t
+    return t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_bytes(path, B, N, Hq, Hkv, D, dt):
+    return load_library(path).spec_tree_attention_workspace_size(B, N, Hq, Hkv, D, dt)
 
 
 def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_nodes=None, scale=None,
@@ -521,36 +555,41 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_node
     and, with ``with_lse``, lse [B, N, heads]; nodes from n_nodes[b] on are
     zero (lse -inf). ``out`` may pass preallocated outputs under these keys.
     """
-    lib = load_library()
-    host = not q.is_cuda
-    dev = k_cache.device
-    cache = _cache_args(k_cache, v_cache, 0)
-    if q.dim() != 4 or q.shape[3] != cache.head_dim or q.shape[2] % cache.kv_heads != 0 or q.dtype != k_cache.dtype:
+    lib = _library()
+    cache, sh, dt = _cache_args(k_cache, v_cache, 0)
+    if q.dim() != 4 or q.shape[3] != sh[3] or q.shape[2] % sh[2] != 0 or q.dtype is not k_cache.dtype:
         raise SpecError("q must be [B, N, heads, head_dim] of the cache's dtype, heads a multiple of kv_heads")
-    dt = _dtype_code(q)
     B, N, Hq, D = q.shape
-    table, stride, width = _table_args(page_table, B, dev)
-    q = _in(q, dev, q.dtype)
-    lens = _in(cache_len, dev)
-    mask = None if mask is None else _in(mask, dev, torch.uint8)
-    cnt = None if n_nodes is None else _in(n_nodes, dev)
-    if lens.shape != (B,) or (mask is not None and mask.shape != (B, N, N)) or (cnt is not None and cnt.shape != (B,)):
-        raise SpecError("cache_len and n_nodes must be [B], mask [B, N, N]")
-    o = dict(out or {})
+    dev, index = k_cache.device, k_cache.get_device()
+    table, stride, width = _table_args(page_table, B, index)
+    host = not q.is_cuda
+    q = _in(q, dev, index, q.dtype)
+    lens = _in(cache_len, dev, index)
+    if mask is not None:
+        mask = _in(mask, dev, index, torch.uint8)
+        if mask.shape != (B, N, N):
+            raise SpecError("mask must be [B, N, N]")
+    if n_nodes is not None:
+        n_nodes = _in(n_nodes, dev, index)
+    if lens.shape != (B,) or (n_nodes is not None and n_nodes.shape != (B,)):
+        raise SpecError("cache_len and n_nodes must be [B]")
+    o = {} if out is None else dict(out)
     if "out" not in o:
-        o["out"] = torch.empty((B, N, Hq, D), dtype=q.dtype, device=dev)
+        o["out"] = torch.empty_like(q)
     if "status" not in o:
         o["status"] = torch.empty((B,), dtype=torch.int32, device=dev)
     if with_lse and "lse" not in o:
         o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=dev)
-    stream = torch.cuda.current_stream(dev)
-    ws = workspace(lib.spec_tree_attention_workspace_size(B, N, Hq, cache.kv_heads, D, dt), dev, stream)
+    raw = _raw_stream(index)
+    ws = _scratch(_attention_bytes(_current[0], B, N, Hq, sh[2], D, dt), dev, index, raw)
     rc = lib.spec_tree_attention(q.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
-                                 _NULL if mask is None else mask.data_ptr(), _NULL if cnt is None else cnt.data_ptr(),
-                                 B, N, Hq, D ** -0.5 if scale is None else float(scale), o["out"].data_ptr(),
-                                 o["lse"].data_ptr() if "lse" in o else _NULL, o["status"].data_ptr(),
-                                 ws.data_ptr(), ws.numel(), stream.cuda_stream)
-    _check(rc)
+                                 None if mask is None else mask.data_ptr(),
+                                 None if n_nodes is None else n_nodes.data_ptr(), B, N, Hq,
+                                 D ** -0.5 if scale is None else scale, o["out"].data_ptr(),
+                                 o["lse"].data_ptr() if "lse" in o else None, o["status"].data_ptr(),
+                                 ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc)
     return {n: t.cpu() for n, t in o.items()} if host else o
 
 
@@ -561,24 +600,25 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None):
     The pages must be the sequences' already (``cache_resize``); cache_len is
     not changed. Returns status [B].
     """
-    lib = load_library()
-    dev = k_cache.device
-    cache = _cache_args(k_cache, v_cache, 0)
-    if k.dim() != 4 or k.shape != v.shape or tuple(k.shape[2:]) != (cache.kv_heads, cache.head_dim) or \
-            k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+    lib = _library()
+    cache, sh, dt = _cache_args(k_cache, v_cache, 0)
+    if k.dim() != 4 or k.shape != v.shape or k.shape[2:] != sh[2:] or k.dtype is not k_cache.dtype or \
+            v.dtype is not k_cache.dtype:
         raise SpecError("k and v must be [B, N, kv_heads, head_dim] of the cache's dtype")
-    dt = _dtype_code(k)
     B, N = k.shape[:2]
-    table, stride, width = _table_args(page_table, B, dev)
-    k, v, lens = _in(k, dev, k.dtype), _in(v, dev, v.dtype), _in(cache_len, dev)
-    cnt = None if n_nodes is None else _in(n_nodes, dev)
-    if lens.shape != (B,) or (cnt is not None and cnt.shape != (B,)):
+    dev, index = k_cache.device, k_cache.get_device()
+    table, stride, width = _table_args(page_table, B, index)
+    k, v, lens = _in(k, dev, index, k.dtype), _in(v, dev, index, v.dtype), _in(cache_len, dev, index)
+    if n_nodes is not None:
+        n_nodes = _in(n_nodes, dev, index)
+    if lens.shape != (B,) or (n_nodes is not None and n_nodes.shape != (B,)):
         raise SpecError("cache_len and n_nodes must be [B]")
     status = torch.empty((B,), dtype=torch.int32, device=dev)
-    stream = torch.cuda.current_stream(dev)
-    _check(lib.spec_cache_append(k.data_ptr(), v.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
-                                 _NULL if cnt is None else cnt.data_ptr(), B, N, status.data_ptr(),
-                                 stream.cuda_stream))
+    rc = lib.spec_cache_append(k.data_ptr(), v.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
+                               None if n_nodes is None else n_nodes.data_ptr(), B, N, status.data_ptr(),
+                               _raw_stream(index))
+    if rc:
+        _check(rc)
     return {"status": status}
 
 
@@ -590,23 +630,24 @@ def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_node
     (``verify``'s accepted), whose entries are in place. Returns cache_len [B]
     = L + accept_len + 1 (-1 on a data error) and status [B].
     """
-    lib = load_library()
-    dev = k_cache.device
-    cache = _cache_args(k_cache, v_cache, 1)
-    dt = _dtype_code(k_cache)
+    lib = _library()
+    cache, _, dt = _cache_args(k_cache, v_cache, 1)
     B = page_table.shape[0]
-    table, stride, width = _table_args(page_table, B, dev)
-    lens, acc = _in(cache_len, dev), _in(accept_len, dev)
-    path = None if path_nodes is None else _in(path_nodes, dev)
+    dev, index = k_cache.device, k_cache.get_device()
+    table, stride, width = _table_args(page_table, B, index)
+    lens, acc = _in(cache_len, dev, index), _in(accept_len, dev, index)
+    path = None if path_nodes is None else _in(path_nodes, dev, index)
     if lens.shape != (B,) or acc.shape != (B,) or (path is not None and (path.dim() != 2 or path.shape[0] != B)):
         raise SpecError("cache_len and accept_len must be [B], path_nodes [B, W]")
-    W = MAX_TREE_N if path is None else path.shape[1]
-    o = torch.empty((2, B), dtype=torch.int32, device=dev)
-    stream = torch.cuda.current_stream(dev)
-    _check(lib.spec_cache_compact(cache, dt, table, stride, width, lens.data_ptr(), acc.data_ptr(),
-                                  _NULL if path is None else path.data_ptr(), B, W, o.data_ptr(),
-                                  o.data_ptr() + 4 * B, stream.cuda_stream))
-    return {"cache_len": o[0], "status": o[1]}
+    new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    status = torch.empty((B,), dtype=torch.int32, device=dev)
+    rc = lib.spec_cache_compact(cache, dt, table, stride, width, lens.data_ptr(), acc.data_ptr(),
+                                None if path is None else path.data_ptr(), B,
+                                MAX_TREE_N if path is None else path.shape[1], new_len.data_ptr(), status.data_ptr(),
+                                _raw_stream(index))
+    if rc:
+        _check(rc)
+    return {"cache_len": new_len, "status": status}
 
 
 def cache_resize(page_table, page_refs, seqs, tokens, page_size):
@@ -617,23 +658,24 @@ def cache_resize(page_table, page_refs, seqs, tokens, page_size):
     free) are changed. Returns status [F]; SPEC_ENOPAGES where pages ran out
     (that sequence is left as it was).
     """
-    lib = load_library()
+    lib = _library()
     if not page_table.is_cuda:
         raise SpecError("page_table and page_refs must be on a CUDA device")
-    dev = page_table.device
+    dev, index = page_table.device, page_table.get_device()
     S = page_table.shape[0]
-    table, stride, width = _table_args(page_table, S, dev)
-    _owned(page_refs, (page_refs.numel(),), dev, "page_refs")
-    tok = _in(tokens, dev)
-    who = None if seqs is None else _in(seqs, dev)
-    F = tok.numel()
+    table, stride, width = _table_args(page_table, S, index)
+    pages = page_refs.numel()
+    refs = _owned(page_refs, (pages,), index, "page_refs")
+    tok = _in(tokens, dev, index)
+    who = None if seqs is None else _in(seqs, dev, index)
     if tok.dim() != 1 or (who is not None and who.shape != tok.shape):
         raise SpecError("seqs and tokens must be [F]")
+    F = tok.shape[0]
     status = torch.empty((F,), dtype=torch.int32, device=dev)
-    stream = torch.cuda.current_stream(dev)
-    _check(lib.spec_cache_resize(table, stride, width, S, page_refs.data_ptr(), page_refs.numel(), int(page_size),
-                                 _NULL if who is None else who.data_ptr(), tok.data_ptr(), F, status.data_ptr(),
-                                 stream.cuda_stream))
+    rc = lib.spec_cache_resize(table, stride, width, S, refs, pages, page_size, None if who is None else who.data_ptr(),
+                               tok.data_ptr(), F, status.data_ptr(), _raw_stream(index))
+    if rc:
+        _check(rc)
     return {"status": status}
 
 
@@ -644,24 +686,24 @@ def cache_fork(k_cache, v_cache, page_table, cache_len, page_refs, src, dst):
     page_table [S, max_pages], cache_len [S] and page_refs [pages] are changed;
     the dst rows must be distinct and empty. Returns status [F].
     """
-    lib = load_library()
-    dev = k_cache.device
-    cache = _cache_args(k_cache, v_cache, 1)
-    dt = _dtype_code(k_cache)
+    lib = _library()
+    cache, sh, dt = _cache_args(k_cache, v_cache, 1)
+    dev, index = k_cache.device, k_cache.get_device()
     S = page_table.shape[0]
-    table, stride, width = _table_args(page_table, S, dev)
-    _owned(page_refs, (cache.num_pages,), dev, "page_refs")
-    _owned(cache_len, (S,), dev, "cache_len")
-    a, z = _in(src, dev), _in(dst, dev)
+    table, stride, width = _table_args(page_table, S, index)
+    refs = _owned(page_refs, (sh[1],), index, "page_refs")
+    lens = _owned(cache_len, (S,), index, "cache_len")
+    a, z = _in(src, dev, index), _in(dst, dev, index)
     if a.dim() != 1 or a.shape != z.shape:
         raise SpecError("src and dst must be [F]")
-    F = a.numel()
+    F = a.shape[0]
     status = torch.empty((F,), dtype=torch.int32, device=dev)
-    stream = torch.cuda.current_stream(dev)
-    ws = workspace(lib.spec_cache_fork_workspace_size(F), dev, stream)
-    _check(lib.spec_cache_fork(cache, dt, table, stride, width, S, page_refs.data_ptr(), cache_len.data_ptr(),
-                               a.data_ptr(), z.data_ptr(), F, status.data_ptr(), ws.data_ptr(), ws.numel(),
-                               stream.cuda_stream))
+    raw = _raw_stream(index)
+    ws = _scratch(lib.spec_cache_fork_workspace_size(F), dev, index, raw)
+    rc = lib.spec_cache_fork(cache, dt, table, stride, width, S, refs, lens, a.data_ptr(), z.data_ptr(), F,
+                             status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+    if rc:
+        _check(rc)
     return {"status": status}
 
 

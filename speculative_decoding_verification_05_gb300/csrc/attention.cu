@@ -13,6 +13,8 @@
 // and release. fp32 throughout.
 
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "attention.cuh"
 
@@ -349,7 +351,7 @@ cudaError_t launch_join(const AttnParams& p, const AttnPlan& plan, cudaStream_t 
 template <typename E, int KV>
 cudaError_t launch_simt(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
     const size_t smem = simt_smem<E, KV>(p.D);
-    cudaError_t e = cudaFuncSetAttribute(attn_simt_kernel<E, KV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_simt_kernel<E, KV>), smem);
     if (e != cudaSuccess) return e;
     attn_simt_kernel<E, KV><<<plan.grid, NT, smem, st>>>(p);
     e = cudaGetLastError();
@@ -357,6 +359,36 @@ cudaError_t launch_simt(const AttnParams& p, const AttnPlan& plan, cudaStream_t 
 }
 
 }  // namespace
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+    constexpr int kMost = 16;
+    struct Entry {
+        std::atomic<const void*> kernel{nullptr};
+        std::atomic<size_t> bytes{0};
+        std::atomic<int> dev{-1};
+    };
+    static Entry seen[kMost];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    for (Entry& s : seen)
+        if (s.kernel.load(std::memory_order_acquire) == kernel && s.dev.load(std::memory_order_relaxed) == dev &&
+            s.bytes.load(std::memory_order_relaxed) >= bytes)
+            return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    static std::mutex mu;
+    std::lock_guard<std::mutex> g(mu);
+    for (Entry& s : seen) {
+        const void* k = s.kernel.load(std::memory_order_relaxed);
+        if (k && (k != kernel || s.dev.load(std::memory_order_relaxed) != dev)) continue;
+        s.dev.store(dev, std::memory_order_relaxed);
+        s.bytes.store(bytes, std::memory_order_relaxed);
+        s.kernel.store(kernel, std::memory_order_release);
+        break;
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st) {
     return dtype == 0 ? launch_join<float>(p, plan, st) : launch_join<bf16_t>(p, plan, st);

@@ -284,6 +284,9 @@ struct AttnPlan {
     size_t part_o, part_ml, joins, total;  // workspace layout
 };
 
+// Lets a kernel have this much dynamic shared memory (set once a device: the
+// call costs about a microsecond).
+cudaError_t allow_smem(const void* kernel, size_t bytes);
 cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);
 int attention_simt_rows();
 int attention_simt_kv(int dtype, int D);

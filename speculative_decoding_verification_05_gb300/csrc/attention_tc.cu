@@ -922,8 +922,7 @@ bool make_map(CUtensorMap* map, const AttnParams& p, const void* base) {
 
 template <int D>
 cudaError_t launch_tc(const AttnParams& p, const AttnPlan& plan, const CUtensorMap* maps, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Shape<D>::kSmem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_tc_kernel<D>), Shape<D>::kSmem);
     if (e != cudaSuccess) return e;
     attn_tc_kernel<D><<<plan.grid, NT, Shape<D>::kSmem, st>>>(p, maps[0], maps[1], maps[2]);
     e = cudaGetLastError();
