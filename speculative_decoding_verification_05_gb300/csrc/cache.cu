@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(PT) resize_kernel(const __grid_constant__ Pool
 __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PoolParams p) {
     __shared__ int offs[kMaxF + 1];
     __shared__ int scratch[PT / 32];
+    asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     auto check = [&](int f, int* len, int* full) {  // a warp: whether fork f can be made
         const int s = p.src[f], d = p.dst[f];
@@ -313,31 +314,38 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PoolPa
     }
 }
 
-// Block (x, f): the used slots of fork f's last page, every layer's K and V.
+// Block (y, f): the used slots of fork f's last page in one layer's K (y even)
+// or V. dense: a page's slots lie one after the other, heads within a slot too.
+// Bound by memory; a thread keeps eight words in flight.
+template <bool DENSE>
 __global__ void __launch_bounds__(CT) fork_copy_kernel(const __grid_constant__ CacheView c, const int4* copies) {
-    const int4 job = copies[blockIdx.y];
+    const int y = blockIdx.x >> 1;
+    char* base = (blockIdx.x & 1 ? c.v : c.k) + y * c.layer_stride;
+    const int per_head = c.row_bytes / 16, per_token = c.heads * per_head;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 job = __ldcg(copies + blockIdx.y);
     if (job.z <= 0 || job.y < 0) return;
-    const int per_head = c.row_bytes / 16, per_token = c.heads * per_head, words = job.z * per_token;
-    const long long units = (long long)c.layers * 2 * words;
-    constexpr int U = 4;
-    for (long long u0 = (long long)blockIdx.x * CT * U + threadIdx.x; u0 < units; u0 += (long long)gridDim.x * CT * U) {
+    const char* from = base + job.x * c.page_stride;
+    char* to = base + job.y * c.page_stride;
+    const int words = job.z * per_token;
+    constexpr int U = 8;
+    for (int i0 = threadIdx.x; i0 < words; i0 += CT * U) {
         uint4 x[U];
-        char* to[U];
+        long long at[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            const long long u = u0 + j * CT;
-            to[j] = nullptr;
-            if (u >= units) continue;
-            const int y = (int)(u / (2 * words)), r = (int)(u - (long long)y * 2 * words), kv = r / words;
-            const int w = r - kv * words, t = w / per_token, e = w - t * per_token, h = e / per_head;
-            char* base = (kv ? c.v : c.k) + y * c.layer_stride + t * c.token_stride + h * c.head_stride +
-                         (e - h * per_head) * 16;
-            x[j] = ldg16(base + job.x * c.page_stride);
-            to[j] = base + job.y * c.page_stride;
+            const int i = min(i0 + j * CT, words - 1);
+            if (DENSE) {
+                at[j] = (long long)i * 16;
+            } else {
+                const int t = i / per_token, e = i - t * per_token, h = e / per_head;
+                at[j] = t * c.token_stride + h * c.head_stride + (e - h * per_head) * 16;
+            }
+            x[j] = ldg16(from + at[j]);
         }
 #pragma unroll
         for (int j = 0; j < U; ++j)
-            if (to[j]) stg16(to[j], x[j]);
+            if (i0 + j * CT < words) stg16(to + at[j], x[j]);
     }
 }
 
@@ -369,9 +377,20 @@ cudaError_t launch_fork(const PoolParams& p, const CacheView& c, cudaStream_t st
     fork_kernel<<<1, PT, 0, st>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const long long units = (long long)c.layers * 2 * c.heads * (c.row_bytes / 16) << c.page_shift;
-    fork_copy_kernel<<<dim3(blocks_for(units, CT * 4, p.F), p.F), CT, 0, st>>>(c, p.copies);
-    return cudaGetLastError();
+    // starts while the bookkeeping ends (it waits for it before it reads a copy)
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * c.layers, p.F);
+    cfg.blockDim = dim3(CT);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const bool dense = c.head_stride == c.row_bytes && c.token_stride == (long long)c.heads * c.row_bytes;
+    const int4* copies = p.copies;
+    return dense ? cudaLaunchKernelEx(&cfg, fork_copy_kernel<true>, c, copies)
+                 : cudaLaunchKernelEx(&cfg, fork_copy_kernel<false>, c, copies);
 }
 
 SV_DEBUG_READER(cache)
