@@ -27,10 +27,10 @@
 // products are issued by one thread and run in its order, so S_w of the next
 // tile, issued after P_w V, cannot overtake it.
 //
-// The running maximum is only raised (and O_w scaled) when a tile exceeds it
-// by more than 8 octaves: weights stay below 2^8 and the sums far inside fp32;
-// any reference gives the same quotient. Statistics and sums are fp32, and the
-// sums l are taken before the weights are rounded to bf16 for the product with
+// Weights are formed against a whole-number reference that follows the running
+// maximum with slack (Group::softmax), so O_w is rarely scaled. Statistics and
+// sums are fp32, and the sums l are taken before the weights are rounded to
+// bf16 for the product with
 // V. Where a weight is more than a sixteenth of its row's sum so far, its
 // rounding would show beside the output's own: steps of 16 positions with such
 // a weight are multiplied a second time with what the rounding took (the
@@ -60,7 +60,8 @@ constexpr int kGroupRegs = 208, kOtherRegs = 88;
 constexpr int kKv = 128;     // positions of a tile
 constexpr int kMaxStages = 10;
 constexpr float kHeavy = 4.f;  // octaves below a row's sum from which a weight is heavy
-constexpr float kSlack = 8.f;  // octaves that a score may exceed the reference by
+constexpr float kSlack = 8.f;  // octaves of the running maximum above the reference that raise it
+constexpr float kJump = 64.f;  // of one score, within a tile
 constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile
 
 template <int D>
@@ -585,59 +586,64 @@ struct Group {
         }
     }
 
-    // One tile: S -> P, the row's maximum m (octaves) and sum l. S is read from
-    // tensor memory twice, for the maximum and for the weights, 64 positions at
-    // a time: the loops stay small (held in registers whole and unrolled, the
-    // row took two to three times as long, waiting for instructions).
-    SV_DEV void softmax(const uint4 see, bool tail, bool first, float c2, float& m, float& l) {
-        float mx[8] = {};  // by steps of 16 positions
+    // O_w (at rest during a tile's softmax) and l by a power of two.
+    SV_DEV void rescale(float f, float& l) {
+        l *= f;
 #pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-            float x[64];
-            tmem_ld64(tm_s + 64 * k, x);
-            if (tail) hide(x, see, k);
+        for (int k = 0; k < D; k += 32) {
+            float o[32];
+            uint32_t r[32];
+            tmem_ld32(tm_o + k, o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx[i] = mx[i + 4];
-#pragma unroll
-            for (int i = 0; i < 64; ++i) mx[4 + (i >> 4)] = i & 15 ? fmaxf(mx[4 + (i >> 4)], x[i]) : x[i];
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * f);
+            tmem_st32(tm_o + k, r);
         }
-        const float mt = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * c2;
-        if (first) {
-            m = mt;
-        } else {
-            const float mn = fmaxf(m, mt);
-            if (__any_sync(0xFFFFFFFFu, mn - m > kSlack)) {
-                // O_w is at rest: this tile's scores were issued after the last product into it
-                const float f = mn == kNegInf ? 1.f : ex2(m - mn);
-                m = mn;
-                l *= f;
-#pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    float o[32];
-                    uint32_t r[32];
-                    tmem_ld32(tm_o + k, o);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * f);
-                    tmem_st32(tm_o + k, r);
-                }
-            }
+    }
+
+    // A row's weights are 2^(s - ref) with a whole number for ref, at first the
+    // maximum of the first 64 positions that it sees, rounded up. Weights may
+    // exceed 1: fp32 sums and bf16 weights scale without loss, so the running
+    // maximum m need not be known before a tile's weights are formed (which
+    // took another pass over S). Before a tile, ref is raised to m where m is
+    // more than 8 octaves above it; within a tile only where a score lies more
+    // than 64 octaves above (sums stay far from overflow).
+    //
+    // One tile: S -> P, 64 positions at a time in a rolled loop (unrolled over
+    // the whole row it took twice as long, waiting for instructions).
+    SV_DEV void softmax(const uint4 see, bool tail, bool first, float c2, float& m, float& ref, float& l) {
+        if (!first && __any_sync(0xFFFFFFFFu, m - ref > kSlack)) {
+            const float to = fmaxf(ref, ceilf(m));
+            rescale(ref == to ? 1.f : ex2(ref - to), l);
+            ref = to;
         }
-        const float ref = m == kNegInf ? 0.f : m;
-        // steps with heavy weights (against a lower bound of the new sum)
-        const float cut = __log2f(l + ex2(mt - ref)) - kHeavy + ref;
+        const uint64_t cc = pack2(c2, c2);
         uint32_t heavy = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) heavy |= mx[k] * c2 > cut ? 1u << k : 0u;
-        heavy = __reduce_or_sync(0xFFFFFFFFu, heavy);
-        if (lane == 0) c->heavy[w][warp] = (uint8_t)heavy;
-        const uint64_t cc = pack2(c2, c2), rr = pack2(-ref, -ref);
-        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll 1
         for (int k = 0; k < 2; ++k) {
-            float x[64];
+            float x[64], mx[4];  // mx: by steps of 16 positions
             tmem_ld64(tm_s + 64 * k, x);
             if (tail) hide(x, see, k);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) mx[i >> 4] = i & 15 ? fmaxf(mx[i >> 4], x[i]) : x[i];
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+            if (ref == kNegInf) ref = ceilf(top);  // (nothing seen so far: all sums are zero)
+            m = fmaxf(m, top);
+            if (__any_sync(0xFFFFFFFFu, top - ref > kJump)) {
+                const float to = fmaxf(ref, ceilf(top)), f = ref == to ? 1.f : ex2(ref - to);
+                if (first) l *= f; else rescale(f, l);
+                if (k) scale_p(f);
+                ref = to;
+            }
+            const float r = ref == kNegInf ? 0.f : ref;
+            const uint64_t rr = pack2(-r, -r);
+            // steps with heavy weights (against a lower bound of the new sum)
+            const float cut = __log2f(l + ex2(top - r)) - kHeavy + r;
+            uint32_t hv = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hv |= mx[i] * c2 > cut ? 1u << i : 0u;
+            hv = __reduce_or_sync(0xFFFFFFFFu, hv);
+            heavy |= hv << (4 * k);
+            uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint32_t hi[16];
@@ -652,7 +658,7 @@ struct Group {
                     hi[e] = pack_bf16(a, b);
                 }
                 tmem_st16(tm_s + 64 * k + 32 * j, hi);
-                if (heavy >> (4 * k + 2 * j) & 3) {  // what the rounding took
+                if (hv >> (2 * j) & 3) {  // what the rounding took
 #pragma unroll
                     for (int e = 0; e < 16; ++e)
                         hi[e] = pack_bf16(x[32 * j + 2 * e] - __uint_as_float(hi[e] << 16),
@@ -663,11 +669,29 @@ struct Group {
                 }
                 tmem_st16(tm_s + 64 * k + 32 * j + 16, hi);
             }
+            float a, b;
+            unpack2(add2(sum[0], sum[1]), &a, &b);
+            l += a + b;
         }
-        float a, b;
-        unpack2(add2(sum[0], sum[1]), &a, &b);
-        l += a + b;
+        if (lane == 0) c->heavy[w][warp] = (uint8_t)heavy;
         tmem_wait_st();
+    }
+
+    // The first 64 positions' weights and residuals by a power of two.
+    SV_DEV void scale_p(float f) {
+        tmem_wait_st();
+#pragma unroll 1
+        for (int k = 0; k < 64; k += 32) {
+            float x[32];
+            uint32_t y[32];
+            tmem_ld32(tm_s + k, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const uint32_t u = __float_as_uint(x[e]);
+                y[e] = pack_bf16(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f);
+            }
+            tmem_st32(tm_s + k, y);
+        }
     }
 
     // 32 columns of a row's result.
@@ -758,7 +782,7 @@ struct Group {
             // (group 0 has read the last segment's O_1)
             if (!(ok = meet())) break;
 
-            float m = kNegInf, l = 0.f;
+            float m = kNegInf, ref = kNegInf, l = 0.f;
             const int half = p.tile_rows / 2, rr = s.dual ? half * w + t : t;
             const bool warp_on = warp * 32 < half && (s.dual ? half * w : 0) + warp * 32 < s.rows;
             const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
@@ -773,15 +797,15 @@ struct Group {
                 __syncwarp();
                 tc_fence_after();
                 if (!warp_on && lane == 0) c->heavy[w][warp] = 0;
-                if (warp_on) softmax(see, tail, vt < 2, c2, m, l);
-                if (w == 1 && vt + 2 >= s.steps) c->ml[t] = make_float2(m, l);
+                if (warp_on) softmax(see, tail, vt < 2, c2, m, ref, l);
+                if (w == 1 && vt + 2 >= s.steps) c->ml[t] = make_float2(ref, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c->p_full[w]);
             }
             if (!ok) break;
             __syncwarp();
-            if (!(ok = finish(s, slot, m, l))) break;
+            if (!(ok = finish(s, slot, ref, l))) break;
             tc_fence_before();
             ++seg;
         }
