@@ -21,11 +21,15 @@
 //   else                both have the same rows and take alternate tiles; group
 //                       0 joins their sums at the end (both O lie in the lanes
 //                       that it can read).
-// S_w takes columns 128 w .. of tensor memory; P_w (bf16, two a column) takes
-// its place 32 positions at a time, 16 columns of weights and 16 of residuals;
-// O_w columns 256 + 128 w. A stream's
-// products are issued by one thread and run in its order, so S_w of the next
-// tile, issued after P_w V, cannot overtake it.
+// A stream goes by halves of a tile, 64 positions: S of a half takes columns
+// 128 w + 64 (half) of tensor memory, and P (bf16, two a column) its place 32
+// positions at a time, 16 columns of weights and 16 of residuals; O_w columns
+// 256 + 128 w. With two halves' places, a half's scores are there before the
+// softmax of the half before is done, and the products run beside it (with one
+// place of 128 positions a stream, scores, softmax and product came one after
+// the other: 4450 cycles for two tiles of the two streams, whose products take
+// 2048). A stream's products are issued by one thread and run in its order, so
+// the scores of the next half in a place cannot overtake the product that reads it.
 //
 // Weights are formed against a whole-number reference that follows the running
 // maximum with slack (Group::softmax), so O_w is rarely scaled. Statistics and
@@ -61,8 +65,10 @@ constexpr int kKv = 128;     // positions of a tile
 constexpr int kMaxStages = 10;
 constexpr float kHeavy = 4.f;  // octaves below a row's sum from which a weight is heavy
 constexpr float kSlack = 8.f;  // octaves of the running maximum above the reference that raise it
-constexpr float kJump = 64.f;  // of one score, within a tile
+constexpr float kJump = 64.f;  // of a half's own scores above it
 constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile
+constexpr int kHalfKv = 64;            // positions of a half of a tile
+constexpr uint32_t kHalfRows = kHalfKv * 128;  // bytes from its rows to the other half's, in 64 columns
 
 template <int D>
 struct Shape {
@@ -89,7 +95,7 @@ struct Walk : AttnWalk<kKv, kExtra> {
 
 struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], ask[2], groups, drain;
+    uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv[2], o_full[2], ask[2], groups, drain;
     uint32_t loads;  // ring entries filled
     AttnScan scan;
     uint32_t tmem;
@@ -97,8 +103,7 @@ struct Ctl {
     uint64_t seg_full[4];
     Seg seg[4];    // the helper's post: segment number modulo 4; b = -1: no more
     int flags[4];  // of a segment: 1 V had elements that are not finite, 2 a bad page
-    int busy;      // an issuer is issuing
-    uint8_t heavy[2][4];  // steps of 16 positions with heavy weights, by group and warp (read as one word)
+    uint8_t heavy[2][2][4];  // steps of 16 positions with heavy weights, by group, half and warp (read as one word)
     float2 ml[128];
 };
 static_assert(sizeof(Ctl) <= 2048, "control region");
@@ -124,6 +129,14 @@ SV_DEV uint32_t clean_stages(const Seg& s, uint32_t ring0, int i0, int i1) {
 // Positions of a tile that hold anything; the product with V goes over whole
 // steps of 16 of them.
 SV_DEV int live_of(const Seg& s, int i) { return (int)min((long long)kKv, s.len - (long long)(s.first + i) * kKv); }
+
+// Halves of stream w's tiles: two each, one where nothing of the last tile's
+// second half is there.
+SV_DEV int halves_of(const Seg& s, int w) {
+    const int cnt = s.last - s.first, mine = s.dual ? cnt : (cnt + 1 - w) >> 1;
+    const bool has_last = s.dual || ((cnt - 1) & 1) == w;
+    return 2 * mine - (mine && has_last && live_of(s, cnt - 1) <= kHalfKv ? 1 : 0);
+}
 
 // Waits give up after about two seconds, or once `abort` is set. They poll
 // without a suspension of their own: its wake-up costs more than these short
@@ -237,100 +250,46 @@ struct Issuer {
         return true;
     }
 
-    // One stream's products at a time: issued together, the streams' products
-    // would run in turns and both end late, and both softmaxes wait together;
-    // in blocks, one's products run during the other's softmax.
-    SV_DEV bool lock() {
-        uint64_t start = 0, now;
-        uint32_t got = 0, n = 0;
-        for (;;) {
-            if (elected()) got = atomicCAS(&c->busy, 0, 1) == 0;
-            got = __any_sync(0xFFFFFFFFu, got);
-            if (got) return true;
-            if (++n & 0xFFu) continue;
-            asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
-            if (!start) start = now;
-            if (__any_sync(0xFFFFFFFFu, now - start > 2000000000ull || *reinterpret_cast<volatile int*>(&c->abort)))
-                return false;
-        }
-    }
-    SV_DEV void unlock() {
-        __syncwarp();
-        if (elected()) atomicExch(&c->busy, 0);
-        __syncwarp();
-    }
-
-    // S of the tile at `ring`; last: the segment's last of this stream.
-    SV_DEV void scores(bool dual, bool last, uint32_t ring) {
-        constexpr uint32_t idesc = mma_idesc(kKv, false);
-        const uint32_t st = uni(ring % NS), d = tmem + 128 * w;
-        const uint64_t a = mma_desc(qs + (dual ? w * kTile : 0u), 16, 1024), b = mma_desc(stages + st * kTile, 16, 1024);
+    // S of a half of the tile in stage st.
+    SV_DEV void scores(bool dual, int half, uint32_t st, bool done, bool last) {
+        constexpr uint32_t idesc = mma_idesc(kHalfKv, false);
+        const uint32_t d = tmem + 128 * w + 64 * half;
+        const uint64_t a = mma_desc(qs + (dual ? w * kTile : 0u), 16, 1024);
+        const uint64_t b = mma_desc(stages + st * kTile + half * kHalfRows, 16, 1024);
         if (elected()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
                 mma_ss(d, a + off, b + off, idesc, kk > 0);
             }
-            mma_commit(&c->s_full[w]);
-            mma_commit(&c->empty[st]);
+            mma_commit(&c->s_full[w][half]);
+            if (done) mma_commit(&c->empty[st]);
             if (last) mma_commit(&c->q_empty);
         }
         __syncwarp();
     }
 
-    // O += P V of the tile at `ring`.
-    SV_DEV void output(bool first, bool last, int live, uint32_t heavy, uint32_t ring) {
+    // O += P V of a half, `steps` of its 16-position steps.
+    SV_DEV void output(int half, uint32_t st, bool first, int steps, uint32_t heavy, bool done, bool last) {
         constexpr uint32_t idesc = mma_idesc(D, true);
-        const uint32_t st = uni(ring % NS), d = tmem + 256 + 128 * w, a = tmem + 128 * w;
-        const uint64_t b = mma_desc(stages + st * kTile, kHalf, 1024);
+        const uint32_t d = tmem + 256 + 128 * w, a = tmem + 128 * w + 64 * half;
+        const uint64_t b = mma_desc(stages + st * kTile + half * kHalfRows, kHalf, 1024);
         if (elected()) {
 #pragma unroll
-            for (int kk = 0; kk < kKv / 16; ++kk)
-                if (16 * kk < live) mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
+            for (int kk = 0; kk < 4; ++kk) {
+                if (kk < steps) mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
+            }
             if (heavy) {
 #pragma unroll 1
-                for (int kk = 0; kk < kKv / 16; ++kk)
+                for (int kk = 0; kk < 4; ++kk)
                     if (heavy >> kk & 1)
                         mma_ts(d, a + (kk >> 1) * 32 + 16 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, true);
             }
-            mma_commit(&c->empty[st]);
+            mma_commit(&c->pv[w]);
+            if (done) mma_commit(&c->empty[st]);
             if (last) mma_commit(&c->o_full[w]);
         }
         __syncwarp();
-    }
-
-    // Step j of a segment: the product with V of this stream's tile j and the
-    // scores of its tile j + 1, as far as there are such.
-    SV_DEV bool step(const Seg& s, bool dual, int cnt, int mine, int j, uint32_t ring0) {
-        const int i = dual ? j : 2 * j + (int)w, next = dual ? j + 1 : i + 2;
-        const uint32_t rv = ring0 + ring_v(s, i), rk = ring0 + ring_k(s, next);
-        uint32_t heavy = 0;
-        if (j >= 0) {
-            if (!reach(rv)) return false;
-            const uint32_t st = uni(rv % NS);
-            const bool tail = tail_tile(s, i);
-            if (tail && (!dual || w == 0)) {  // V has to be cleaned first
-                if (elected()) mbar_arrive(&c->ask[w]);
-                __syncwarp();
-            }
-            if (j + 1 < mine && !reach(rk)) return false;
-            if (!warp_wait(&c->p_full[w], p_phase, &c->abort)) return false;
-            p_phase ^= 1;
-            if (tail && !warp_wait(&c->clean[st], clean >> st & 1, &c->abort)) return false;
-            heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w]);  // a byte of each warp
-            heavy |= heavy >> 16;
-            heavy = uni((heavy | heavy >> 8) & 0xFFu);
-        } else if (j + 1 < mine && !reach(rk)) {
-            return false;
-        }
-        if (!lock()) return false;
-        tc_fence_after();
-        if (j >= 0) output(j == 0, j + 1 == mine, (int)uni(live_of(s, i)), heavy, rv);
-        if (j + 1 < mine) scores(dual, j + 2 == mine, rk);
-        unlock();
-        // (phases of the stages whose V this step's tiles have had cleaned, the other stream's too)
-        if (j >= 0) clean ^= clean_stages<D>(s, ring0, dual ? j : 2 * j, dual ? j + 1 : min(2 * j + 2, cnt));
-        return true;
     }
 
     SV_DEV void run() {
@@ -340,14 +299,53 @@ struct Issuer {
             const Seg& s = *at;
             const bool dual = uni(s.dual);
             const int cnt = (int)uni(s.last - s.first);
-            const int mine = dual ? cnt : (cnt + 1 - (int)w) >> 1;  // tiles of this stream
+            const int halves = (int)uni(halves_of(s, w));  // of this stream's tiles
+            uint32_t st_k = 0, st_v = 0;
             ok = warp_wait(&c->q_full, q_phase, &c->abort);
             q_phase ^= 1;
-            if (mine == 0 && elected()) mbar_arrive(&c->q_empty);
+            if (halves == 0 && elected()) mbar_arrive(&c->q_empty);
             __syncwarp();
+            // P V of half u, and then the scores of half u + 2 in its place
 #pragma unroll 1
-            for (int j = -1; ok && j < mine; ++j)
-                if (mine) ok = step(s, dual, cnt, mine, j, ring0);
+            for (int u = halves ? -2 : 0; ok && u < halves; ++u) {
+                const int half = u & 1, i = dual ? u >> 1 : 2 * (u >> 1) + (int)w;
+                if (u >= 0) {
+                    const bool tail = tail_tile(s, i);
+                    if (half == 0) {
+                        const uint32_t ring = ring0 + ring_v(s, i);
+                        if (!(ok = reach(ring))) break;
+                        st_v = uni(ring % NS);
+                        if (tail && (!dual || w == 0)) {  // V has to be cleaned first
+                            if (elected()) mbar_arrive(&c->ask[w]);
+                            __syncwarp();
+                        }
+                    }
+                    if (!(ok = warp_wait(&c->p_full[w][half], p_phase >> half & 1, &c->abort))) break;
+                    p_phase ^= 1u << half;
+                    if (tail && half == 0 && !(ok = warp_wait(&c->clean[st_v], clean >> st_v & 1, &c->abort))) break;
+                    tc_fence_after();
+                    uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w][half]);  // a byte of each warp
+                    heavy |= heavy >> 16;
+                    heavy = uni((heavy | heavy >> 8) & 0xFFu);
+                    const int steps = tail ? (int)uni((live_of(s, i) - kHalfKv * half + 15) >> 4) : 4;
+                    output(half, st_v, u == 0, steps, heavy, half == 1 || u + 1 == halves, u + 1 == halves);
+                }
+                if (u + 2 < halves) {
+                    if (half == 0) {
+                        const uint32_t ring = ring0 + ring_k(s, dual ? (u >> 1) + 1 : i + 2);
+                        if (!(ok = reach(ring))) break;
+                        st_k = uni(ring % NS);
+                        tc_fence_after();
+                    }
+                    scores(dual, half, st_k, half == 1 || u + 3 == halves, u + 3 == halves);
+                }
+                // (phases of the stages whose V these tiles have had cleaned, the other stream's too)
+                if (u >= 0 && (half == 1 || u + 1 == halves)) {
+                    const int i0 = dual ? i : i - (int)w, i1 = dual ? i + 1 : min(i0 + 2, cnt);
+                    if (tail_tile(s, i1 - 1)) clean ^= clean_stages<D>(s, ring0, i0, i1);
+                }
+            }
+            const int mine = (halves + 1) >> 1;
             if (!dual && mine < (cnt + 1) >> 1) clean ^= clean_stages<D>(s, ring0, 2 * mine, cnt);
             ring0 += 2 * cnt;
             while (ok && seen < ring0) ok = pass();
@@ -372,14 +370,14 @@ SV_DEV uint32_t mask_edge(const uint8_t* start, long long off, long long bytes, 
     return x;
 }
 
-// The visibility of a tile's 128 positions for one row, 32 a word. Node j of
-// the row's own sequence is at position L + j.
-SV_DEV void see_bits(const AttnParams& p, const Seg& s, int node, long long pos0, uint4* see) {
+// The visibility of 64 positions for one row, 32 a word. Node j of the row's
+// own sequence is at position L + j.
+SV_DEV void see_bits(const AttnParams& p, const Seg& s, int node, long long pos0, uint2* see) {
     const long long off = (uintptr_t)p.mask & 3, bytes = (long long)p.B * p.N * p.N;
     const long long full0 = off ? 1 : 0, full1 = ((off + bytes) >> 2) - 1;  // first and last whole word
     const uint8_t* start = p.mask - off;
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
         const long long p0 = pos0 + 32 * k;
         const int ctx = (int)min(32LL, max(0LL, s.L - p0));                   // bits below: context
         const int upto = (int)min(32LL, max(0LL, (p.mask ? s.len : (long long)s.L + node + 1) - p0));  // none from here on
@@ -410,8 +408,6 @@ SV_DEV void see_bits(const AttnParams& p, const Seg& s, int node, long long pos0
         bits = (low & in) | (bits & ~low);
         if (k == 0) see->x = bits;
         if (k == 1) see->y = bits;
-        if (k == 2) see->z = bits;
-        if (k == 3) see->w = bits;
     }
 }
 
@@ -566,7 +562,7 @@ struct Group {
     Ctl* c;
     int w, warp, lane, t;       // group, warp of the group, lane, thread of the group = row of its tile
     uint32_t tm_s, tm_o;        // this warp's lanes of S_w and O_w
-    uint32_t s_phase = 0, o_phase = 0, g_phase = 0;
+    uint32_t s_phase = 0, o_phase = 0, g_phase = 0, pv_count = 0;
 
     // Both groups; false after a timeout.
     SV_DEV bool meet() {
@@ -577,17 +573,20 @@ struct Group {
         return ok;
     }
 
-    SV_DEV static void hide(float (&x)[64], const uint4& see, int k) {
-        const uint32_t lo = k ? see.z : see.x, hi = k ? see.w : see.y;
+    SV_DEV static void hide(float (&x)[64], const uint2& see) {
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            if (!(lo >> i & 1)) x[i] = kNegInf;
-            if (!(hi >> i & 1)) x[32 + i] = kNegInf;
+            if (!(see.x >> i & 1)) x[i] = kNegInf;
+            if (!(see.y >> i & 1)) x[32 + i] = kNegInf;
         }
     }
 
-    // O_w (at rest during a tile's softmax) and l by a power of two.
-    SV_DEV void rescale(float f, float& l) {
+    // O_w and l by a power of two, once the product of the half before (the
+    // pv_count-th of this stream) is done: the one before that is, as its place
+    // holds this half's scores.
+    SV_DEV bool rescale(float f, float& l) {
+        if (!warp_wait(&c->pv[w], (pv_count - 1) & 1, &c->abort)) return false;
+        tc_fence_after();
         l *= f;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
@@ -598,100 +597,73 @@ struct Group {
             for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(o[e] * f);
             tmem_st32(tm_o + k, r);
         }
+        return true;
     }
 
     // A row's weights are 2^(s - ref) with a whole number for ref, at first the
-    // maximum of the first 64 positions that it sees, rounded up. Weights may
+    // maximum of the first positions that it sees, rounded up. Weights may
     // exceed 1: fp32 sums and bf16 weights scale without loss, so the running
-    // maximum m need not be known before a tile's weights are formed (which
-    // took another pass over S). Before a tile, ref is raised to m where m is
-    // more than 8 octaves above it; within a tile only where a score lies more
-    // than 64 octaves above (sums stay far from overflow).
+    // maximum m need not be known before a half's weights are formed. ref is
+    // raised to it where it is more than 8 octaves above before a half begins;
+    // for a half's own scores only where one lies more than 64 octaves above
+    // (sums stay far from overflow).
     //
-    // One tile: S -> P, 64 positions at a time in a rolled loop (unrolled over
-    // the whole row it took twice as long, waiting for instructions).
-    SV_DEV void softmax(const uint4 see, bool tail, bool first, float c2, float& m, float& ref, float& l) {
-        if (!first && __any_sync(0xFFFFFFFFu, m - ref > kSlack)) {
-            const float to = fmaxf(ref, ceilf(m));
-            rescale(ref == to ? 1.f : ex2(ref - to), l);
+    // One half: S -> P.
+    SV_DEV bool softmax(int half, const uint2 see, bool tail, bool first, float c2, float& m, float& ref, float& l) {
+        const uint32_t at = tm_s + 64 * half;
+        float x[64], mx[4];  // mx: by steps of 16 positions
+        tmem_ld64(at, x);
+        if (tail) hide(x, see);
+#pragma unroll
+        for (int i = 0; i < 64; ++i) mx[i >> 4] = i & 15 ? fmaxf(mx[i >> 4], x[i]) : x[i];
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+        if (ref == kNegInf) ref = ceilf(top);  // (nothing seen so far: all sums are zero)
+        if (!first && __any_sync(0xFFFFFFFFu, fmaxf(m - kSlack, top - kJump) > ref)) {
+            const float to = fmaxf(ref, ceilf(fmaxf(m, top)));
+            if (!rescale(ref == to ? 1.f : ex2(ref - to), l)) return false;
             ref = to;
         }
-        const uint64_t cc = pack2(c2, c2);
+        m = fmaxf(m, top);
+        const float r = ref == kNegInf ? 0.f : ref;
+        const uint64_t cc = pack2(c2, c2), rr = pack2(-r, -r);
+        // steps with heavy weights (against a lower bound of the new sum)
+        const float cut = __log2f(l + ex2(top - r)) - kHeavy + r;
         uint32_t heavy = 0;
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-            float x[64], mx[4];  // mx: by steps of 16 positions
-            tmem_ld64(tm_s + 64 * k, x);
-            if (tail) hide(x, see, k);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) mx[i >> 4] = i & 15 ? fmaxf(mx[i >> 4], x[i]) : x[i];
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
-            if (ref == kNegInf) ref = ceilf(top);  // (nothing seen so far: all sums are zero)
-            m = fmaxf(m, top);
-            if (__any_sync(0xFFFFFFFFu, top - ref > kJump)) {
-                const float to = fmaxf(ref, ceilf(top)), f = ref == to ? 1.f : ex2(ref - to);
-                if (first) l *= f; else rescale(f, l);
-                if (k) scale_p(f);
-                ref = to;
+        for (int i = 0; i < 4; ++i) heavy |= mx[i] * c2 > cut ? 1u << i : 0u;
+        heavy = __reduce_or_sync(0xFFFFFFFFu, heavy);
+        if (lane == 0) c->heavy[w][half][warp] = (uint8_t)heavy;
+        uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t hi[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float& a = x[32 * j + 2 * e];
+                float& b = x[32 * j + 2 * e + 1];
+                unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
+                a = ex2(a);
+                b = ex2(b);
+                sum[e & 1] = add2(sum[e & 1], pack2(a, b));
+                hi[e] = pack_bf16(a, b);
             }
-            const float r = ref == kNegInf ? 0.f : ref;
-            const uint64_t rr = pack2(-r, -r);
-            // steps with heavy weights (against a lower bound of the new sum)
-            const float cut = __log2f(l + ex2(top - r)) - kHeavy + r;
-            uint32_t hv = 0;
+            tmem_st16(at + 32 * j, hi);
+            if (heavy >> (2 * j) & 3) {  // what the rounding took
 #pragma unroll
-            for (int i = 0; i < 4; ++i) hv |= mx[i] * c2 > cut ? 1u << i : 0u;
-            hv = __reduce_or_sync(0xFFFFFFFFu, hv);
-            heavy |= hv << (4 * k);
-            uint64_t sum[2] = {0ull, 0ull};
+                for (int e = 0; e < 16; ++e)
+                    hi[e] = pack_bf16(x[32 * j + 2 * e] - __uint_as_float(hi[e] << 16),
+                                      x[32 * j + 2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+            } else {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t hi[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float& a = x[32 * j + 2 * e];
-                    float& b = x[32 * j + 2 * e + 1];
-                    unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
-                    a = ex2(a);
-                    b = ex2(b);
-                    sum[e & 1] = add2(sum[e & 1], pack2(a, b));
-                    hi[e] = pack_bf16(a, b);
-                }
-                tmem_st16(tm_s + 64 * k + 32 * j, hi);
-                if (hv >> (2 * j) & 3) {  // what the rounding took
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        hi[e] = pack_bf16(x[32 * j + 2 * e] - __uint_as_float(hi[e] << 16),
-                                          x[32 * j + 2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) hi[e] = 0u;
-                }
-                tmem_st16(tm_s + 64 * k + 32 * j + 16, hi);
+                for (int e = 0; e < 16; ++e) hi[e] = 0u;
             }
-            float a, b;
-            unpack2(add2(sum[0], sum[1]), &a, &b);
-            l += a + b;
+            tmem_st16(at + 32 * j + 16, hi);
         }
-        if (lane == 0) c->heavy[w][warp] = (uint8_t)heavy;
+        float a, b;
+        unpack2(add2(sum[0], sum[1]), &a, &b);
+        l += a + b;
         tmem_wait_st();
-    }
-
-    // The first 64 positions' weights and residuals by a power of two.
-    SV_DEV void scale_p(float f) {
-        tmem_wait_st();
-#pragma unroll 1
-        for (int k = 0; k < 64; k += 32) {
-            float x[32];
-            uint32_t y[32];
-            tmem_ld32(tm_s + k, x);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const uint32_t u = __float_as_uint(x[e]);
-                y[e] = pack_bf16(__uint_as_float(u << 16) * f, __uint_as_float(u & 0xFFFF0000u) * f);
-            }
-            tmem_st32(tm_s + k, y);
-        }
+        return true;
     }
 
     // 32 columns of a row's result.
@@ -786,22 +758,24 @@ struct Group {
             const int half = p.tile_rows / 2, rr = s.dual ? half * w + t : t;
             const bool warp_on = warp * 32 < half && (s.dual ? half * w : 0) + warp * 32 < s.rows;
             const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
-            for (int vt = w; vt < s.steps; vt += 2) {
-                const int i = s.dual ? vt >> 1 : vt;
-                const long long pos0 = (long long)(s.first + i) * kKv;
-                const bool tail = pos0 + kKv > s.L;
-                uint4 see = make_uint4(0u, 0u, 0u, 0u);
+            const int halves = halves_of(s, w);
+#pragma unroll 1
+            for (int u = 0; u < halves; ++u) {
+                const int half = u & 1, i = s.dual ? u >> 1 : 2 * (u >> 1) + w;
+                const long long pos0 = (long long)(s.first + i) * kKv + kHalfKv * half;
+                const bool tail = pos0 + kHalfKv > s.L;
+                uint2 see = make_uint2(0u, 0u);
                 if (tail && warp_on) see_bits(p, s, node, pos0, &see);
-                if (!(ok = warp_wait(&c->s_full[w], s_phase, &c->abort))) break;
-                s_phase ^= 1;
-                __syncwarp();
+                if (!(ok = warp_wait(&c->s_full[w][half], s_phase >> half & 1, &c->abort))) break;
+                s_phase ^= 1u << half;
                 tc_fence_after();
-                if (!warp_on && lane == 0) c->heavy[w][warp] = 0;
-                if (warp_on) softmax(see, tail, vt < 2, c2, m, ref, l);
-                if (w == 1 && vt + 2 >= s.steps) c->ml[t] = make_float2(ref, l);
+                if (!warp_on && lane == 0) c->heavy[w][half][warp] = 0;
+                if (warp_on && !(ok = softmax(half, see, tail, u == 0, c2, m, ref, l))) break;
+                ++pv_count;
+                if (w == 1 && u + 1 == halves) c->ml[t] = make_float2(ref, l);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&c->p_full[w]);
+                if (lane == 0) mbar_arrive(&c->p_full[w][half]);
             }
             if (!ok) break;
             __syncwarp();
@@ -842,14 +816,16 @@ __global__ void __launch_bounds__(NT, 1)
         mbar_init(&c->q_full, 1);
         mbar_init(&c->q_empty, 2);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&c->s_full[i], 1);
-            mbar_init(&c->p_full[i], 4);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&c->s_full[i][h], 1);
+                mbar_init(&c->p_full[i][h], 4);
+            }
+            mbar_init(&c->pv[i], 1);
             mbar_init(&c->o_full[i], 1);
             mbar_init(&c->ask[i], 1);
             c->flags[2 * i] = c->flags[2 * i + 1] = 0;
         }
         for (int i = 0; i < 4; ++i) mbar_init(&c->seg_full[i], 1);
-        c->busy = 0;
         mbar_init(&c->groups, 8);
         mbar_init(&c->drain, 2);
         c->abort = 0;
