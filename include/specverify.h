@@ -416,6 +416,7 @@ typedef struct {
  *   N             1 .. SPEC_MAX_TREE_N; q_heads a multiple of kv_heads, at most
  *                 SPEC_MAX_GROUP times it
  *   scale         finite
+ *   (kv_heads x ceil(N x group / 16) x max_pages x page_size / 32 below 2^31)
  * Outputs:
  *   out           [B, N, q_heads, head_dim], 16-byte aligned, q's type; zero
  *                 for nodes i >= n and for a node that sees nothing

@@ -108,11 +108,9 @@ __global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ A
 
     attn_edges<E>(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
     asm volatile("griddepcontrol.launch_dependents;");
-    const long long total = attn_locate<KV, kExtra, NT>(p, &scan);
-    const int parts = attn_parts(total, gridDim.x);
-    if (tid == 0) attn_join<KV, kExtra>(p, scan, total, parts);
-    if ((int)blockIdx.x >= parts) return;
-    AttnWalk<KV, kExtra> walk(scan, total, parts);
+    const AttnCut cut = attn_locate<KV, kExtra, NT>(p, &scan);
+    if (tid == 0) attn_join<KV, kExtra>(p, scan, cut);
+    AttnWalk<KV, kExtra> walk(scan, cut);
     AttnStay sq;
     while (walk.next(p, &sq)) {
         const int b = sq.b, h = sq.h, first = sq.first, last = sq.last, row_base = sq.row0, rows = sq.rows;

@@ -95,15 +95,18 @@ struct AttnScan {
     AttnPlace place;
 };
 
-SV_DEV int attn_parts(long long total, int grid) { return (int)(total < grid ? total : grid); }
-// CTA c's part of `total` tiles over `parts` CTAs.
-SV_DEV long long attn_part(long long total, int parts, int c) { return total * c / parts; }
+// The range cut into parts, one a CTA (the first `extra` one tile longer).
+struct AttnCut {
+    long long each;
+    int extra, parts;
+    SV_DEV long long at(int c) const { return each * c + min(c, extra); }
+};
 
-// Called by all NT threads of a block: the range's length, and in sc->place
-// where this CTA's part begins (if it has one). Each thread sums a run of
-// sequences, one scan orders the runs.
+// Called by all NT threads of a block: the cut range, and in sc->place where
+// this CTA's part begins (if it has one). Each thread sums a run of sequences,
+// one scan orders the runs.
 template <int KV, int EX, int NT>
-SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc) {
+SV_DEV AttnCut attn_locate(const AttnParams& p, AttnScan* sc) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (p.B + NT - 1) / NT;
     const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
@@ -125,8 +128,11 @@ SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc) {
         total += u;
     }
     long long lo = before + inc - mine;
-    const int parts = attn_parts(total, gridDim.x);
-    const long long at = (int)blockIdx.x < parts ? attn_part(total, parts, blockIdx.x) : -1;
+    AttnCut cut;
+    cut.parts = (int)min(total, (long long)gridDim.x);
+    cut.each = cut.parts ? total / cut.parts : 0;
+    cut.extra = (int)(total - cut.each * cut.parts);
+    const long long at = (int)blockIdx.x < cut.parts ? cut.at(blockIdx.x) : -1;
     if (at >= lo && at < lo + mine) {
         long long base = lo;
         for (int b = b0; b < b1; ++b) {
@@ -139,7 +145,7 @@ SV_DEV long long attn_locate(const AttnParams& p, AttnScan* sc) {
         }
     }
     __syncthreads();
-    return total;
+    return cut;
 }
 
 // One CTA's stay in a unit: tiles [first, last) of its kt.
@@ -154,17 +160,15 @@ template <int KV, int EX>
 struct AttnWalk {
     long long t, end, base;
     int b, stays;
-    SV_DEV AttnWalk(const AttnScan& sc, long long total, int parts)
-        : t(attn_part(total, parts, blockIdx.x)),
-          end(attn_part(total, parts, blockIdx.x + 1)),
-          base(sc.place.base),
-          b(sc.place.b),
-          stays(0) {}
-
-    SV_DEV static long long div(long long x, int y) {
-        return x >> 31 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+    SV_DEV AttnWalk(const AttnScan& sc, const AttnCut& cut) : t(0), end(0), base(0), b(0), stays(0) {
+        if ((int)blockIdx.x >= cut.parts) return;
+        t = cut.at(blockIdx.x);
+        end = cut.at(blockIdx.x + 1);
+        base = sc.place.base;
+        b = sc.place.b;
     }
 
+    // (a sequence's own part of the range is below 2^31)
     SV_DEV bool next(const AttnParams& p, AttnStay* s) {
         while (t < end) {
             AttnSeq q = attn_seq(p, b);
@@ -175,8 +179,8 @@ struct AttnWalk {
                 kt = attn_kv_tiles<KV>(q);
                 rt = attn_row_tiles(p, q);
             }
-            const long long unit = div(t - base, kt + EX);
-            const int from = (int)(t - base - unit * (kt + EX));
+            const uint32_t in = (uint32_t)(t - base), unit = in / (uint32_t)(kt + EX);
+            const int from = (int)(in - unit * (uint32_t)(kt + EX));
             const int to = (int)min((long long)(kt + EX), from + (end - t));
             t += to - from;
             s->first = max(0, from - EX);
@@ -184,8 +188,8 @@ struct AttnWalk {
             if (s->first == s->last) continue;
             s->b = b;
             s->kt = kt;
-            s->h = (int)div(unit, rt);
-            s->row0 = (int)(unit - (long long)s->h * rt) * p.tile_rows;
+            s->h = (int)(unit / (uint32_t)rt);
+            s->row0 = (int)(unit - (uint32_t)s->h * rt) * p.tile_rows;
             s->rows = min(p.tile_rows, q.n * p.G - s->row0);
             s->L = q.L;
             s->n = q.n;
@@ -202,23 +206,23 @@ struct AttnWalk {
 // This CTA's entry of p.joins (one thread): its part begins inside a unit that
 // the part before it has the first piece of.
 template <int KV, int EX>
-SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, long long total, int parts) {
+SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, const AttnCut& cut) {
     AttnJoin j = {};
     const int c = blockIdx.x;
-    if (c > 0 && c < parts) {
+    if (c > 0 && c < cut.parts) {
         const AttnSeq q = attn_seq(p, sc.place.b);
         const int kt = attn_kv_tiles<KV>(q), rt = attn_row_tiles(p, q);
-        const long long at = attn_part(total, parts, c), before = attn_part(total, parts, c - 1);
-        const long long unit = AttnWalk<KV, EX>::div(at - sc.place.base, kt + EX);
-        const long long start = sc.place.base + unit * (kt + EX), stop = start + kt + EX;
+        const long long at = cut.at(c), before = cut.at(c - 1);
+        const uint32_t unit = (uint32_t)(at - sc.place.base) / (uint32_t)(kt + EX);
+        const long long start = sc.place.base + (long long)unit * (kt + EX), stop = start + kt + EX;
         if (at > start + EX && before <= start + EX) {
             j.b = sc.place.b;
-            j.h = (int)AttnWalk<KV, EX>::div(unit, rt);
-            j.row0 = (int)(unit - (long long)j.h * rt) * p.tile_rows;
+            j.h = (int)(unit / (uint32_t)rt);
+            j.row0 = (int)(unit - (uint32_t)j.h * rt) * p.tile_rows;
             j.rows = min(p.tile_rows, q.n * p.G - j.row0);
             j.slot0 = 2 * (c - 1) + (before < start);
             j.first = j.last = c;
-            while (j.last + 1 < parts && attn_part(total, parts, j.last + 1) < stop) ++j.last;
+            while (j.last + 1 < cut.parts && cut.at(j.last + 1) < stop) ++j.last;
         }
     }
     p.joins[c] = j;
@@ -228,9 +232,9 @@ SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, long long total, 
 // grid (this is warp `gw`; as many warps a sequence as there are): status, and
 // the rows that no unit writes, zeros (lse -inf) from the node count on and NaN
 // everywhere for a sequence with bad data. A bad page id is reported here; the
-// units that meet it make their rows NaN. late: a wait of this CTA gave up.
+// units that meet it make their rows NaN.
 template <typename E>
-SV_DEV void attn_edges(const AttnParams& p, int gw, int warps, bool late = false) {
+SV_DEV void attn_edges(const AttnParams& p, int gw, int warps) {
     const int lane = threadIdx.x & 31, team = max(1, warps / p.B), member = gw % team;
     for (int b = gw / team; b < p.B; b += (warps + team - 1) / team) {
         const AttnSeq s = attn_seq(p, b);
@@ -244,7 +248,7 @@ SV_DEV void attn_edges(const AttnParams& p, int gw, int warps, bool late = false
                 }
             }
             bad = __any_sync(0xFFFFFFFFu, bad) != 0;
-            if (lane == 0) p.status[b] = bad ? kEData : late ? kETimeout : kOk;
+            if (lane == 0) p.status[b] = bad ? kEData : kOk;
         }
         const int Hq = p.Hkv * p.G, n = max(s.n, 0);
         const long long row0 = ((long long)b * p.N + n) * Hq, rows = (long long)(p.N - n) * Hq;

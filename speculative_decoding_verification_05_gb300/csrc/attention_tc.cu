@@ -138,19 +138,14 @@ SV_DEV int halves_of(const Seg& s, int w) {
     return 2 * mine - (mine && has_last && live_of(s, cnt - 1) <= kHalfKv ? 1 : 0);
 }
 
-// Waits give up after about two seconds, or once `abort` is set. They poll
-// without a suspension of their own: its wake-up costs more than these short
-// waits last.
+// Waits give up after some 2^22 polls (a tenth of a second and more), or once
+// `abort` is set. They poll without a suspension of their own: its wake-up costs
+// more than these short waits last.
 SV_DEV bool tc_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-    uint64_t start = 0, now;
     uint32_t n = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity)) {
-        if (++n & 0xFFu) continue;
-        asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
-        if (!start) start = now;
-        if (now - start > 2000000000ull || (abort && *abort)) return false;
-    }
+    while (!mbar_try_wait(bar, parity))
+        if (!(++n & 0xFFu) && (n >> 22 || (abort && *abort))) return false;
     return true;
 }
 // By whole warps: every lane gets the same answer.
@@ -168,43 +163,49 @@ SV_DEV const Seg* next_seg(Ctl* c, uint32_t seg, bool* ok) {
 // ---- copies ----------------------------------------------------------------------
 
 template <int D>
-SV_DEV bool load_box(const AttnParams& p, Ctl* c, const CUtensorMap* map, uint32_t stages, const Seg& s, int slot,
-                     int tile, uint32_t ring) {
-    constexpr int NS = Shape<D>::kStages;
-    const int lane = threadIdx.x & 31, st = ring % NS;
-    const uint32_t round = ring / NS;
-    const int ps = min(1 << p.page_shift, kKv), halves = D / 64, pages = kKv / ps;
-    const int pg = lane / halves, half = lane - pg * halves;
-    const long long pos = (long long)tile * kKv + pg * ps;
-    int id = -1;
-    if (pg < pages && pos < s.len) id = __ldg(p.table + s.b * p.table_stride + (pos >> p.page_shift));
-    const bool ok = id >= 0 && id < p.num_pages;
-    const unsigned who = __ballot_sync(0xFFFFFFFFu, ok);
-    if (!ok && pg < pages && pos < s.len) atomicOr(&c->flags[slot], 2);
-    if (round && !warp_wait(&c->empty[st], (round - 1) & 1, &c->abort)) return false;
-    if (lane == 0) mbar_expect_tx(&c->full[st], __popc(who) * (uint32_t)ps * 128);
-    __syncwarp();
-    if (ok)
-        tma_load4(stages + st * Shape<D>::kTile + half * kHalf + pg * ps * 128, map, half * 64,
-                  (int)(pos & ((1 << p.page_shift) - 1)), s.h, id, &c->full[st]);
-    return true;
-}
-
-template <int D>
 SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t stages) {
-    uint32_t ring = 0, seg = 0;
+    constexpr uint32_t NS = Shape<D>::kStages, halves = D / 64;
+    const int lane = threadIdx.x & 31, ps1 = (1 << p.page_shift) - 1, ps = min(ps1 + 1, kKv), pages = kKv / ps;
+    const int pg = lane / halves, half = lane % halves;
+    const uint32_t to = half * kHalf + pg * ps * 128;
+    uint32_t ring = 0, seg = 0, st = 0, free_phase = 1;  // (a first round's stages are free)
     bool ok = true;
     while (const Seg* at = next_seg(c, seg, &ok)) {
         const Seg& s = *at;
-        const int cnt = s.last - s.first, ahead = s.dual ? 1 : 2, slot = seg & 3;
-        for (int i = -ahead; ok && i < cnt; ++i) {  // V(i), then K(i + ahead); K alone before the first V
-            if (i >= 0) ok = load_box<D>(p, c, mv, stages, s, slot, s.first + i, ring++);
-            if (ok && i + ahead < cnt) ok = load_box<D>(p, c, mk, stages, s, slot, s.first + i + ahead, ring++);
+        const int cnt = s.last - s.first, ahead = s.dual ? 1 : 2, h = s.h;
+        const long long len = s.len, pos0 = (long long)s.first * kKv + pg * ps;
+        const int32_t* table = p.table + s.b * p.table_stride;
+        // V(i), then K(i + ahead); K alone before the first V
+#pragma unroll 1
+        for (int e = -2 * ahead; ok && e < 2 * cnt; ++e) {
+            const int i = (e >> 1) + (e & 1 ? ahead : 0);
+            if (i < 0 || i >= cnt || (e < 0 && !(e & 1))) continue;
+            const long long pos = pos0 + (long long)i * kKv;
+            int id = -1;
+            if (pg < pages && pos < len) {
+                id = __ldg(table + (pos >> p.page_shift));
+                if (id < 0 || id >= p.num_pages) {
+                    id = -1;
+                    atomicOr(&c->flags[seg & 3], 2);
+                }
+            }
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, id >= 0);
+            if (!(ok = warp_wait(&c->empty[st], free_phase, &c->abort))) break;
+            if (lane == 0) mbar_expect_tx(&c->full[st], __popc(who) * (uint32_t)ps * 128);
+            __syncwarp();
+            if (id >= 0)
+                tma_load4(stages + st * Shape<D>::kTile + to, e & 1 ? mk : mv, half * 64, (int)(pos & ps1), h, id,
+                          &c->full[st]);
+            ++ring;
+            if (++st == NS) {
+                st = 0;
+                free_phase ^= 1;
+            }
         }
         if (!ok) break;
         ++seg;
     }
-    if ((threadIdx.x & 31) == 0) c->loads = ok ? ring : ring - (ring > 0);
+    if (lane == 0) c->loads = ring;
     if (!ok) c->abort = 1;
 }
 
@@ -358,75 +359,72 @@ struct Issuer {
 
 // ---- softmax and results ------------------------------------------------------------
 
-// Word i (4 bytes from the aligned address at or below the mask's start) with
-// the bytes outside the mask left out.
-SV_DEV uint32_t mask_edge(const uint8_t* start, long long off, long long bytes, long long i) {
-    uint32_t x = 0;
-#pragma unroll 1
-    for (int e = 0; e < 4; ++e) {
-        const long long at = 4 * i + e;
-        if (at >= off && at < off + bytes) x |= (uint32_t)__ldg(start + at) << (8 * e);
-    }
-    return x;
-}
-
-// The visibility of 64 positions for one row, 32 a word. Node j of the row's
-// own sequence is at position L + j.
-SV_DEV void see_bits(const AttnParams& p, const Seg& s, int node, long long pos0, uint2* see) {
-    const long long off = (uintptr_t)p.mask & 3, bytes = (long long)p.B * p.N * p.N;
-    const long long full0 = off ? 1 : 0, full1 = ((off + bytes) >> 2) - 1;  // first and last whole word
-    const uint8_t* start = p.mask - off;
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
-        const long long p0 = pos0 + 32 * k;
-        const int ctx = (int)min(32LL, max(0LL, s.L - p0));                   // bits below: context
-        const int upto = (int)min(32LL, max(0LL, (p.mask ? s.len : (long long)s.L + node + 1) - p0));  // none from here on
-        const uint32_t low = ctx == 32 ? 0xFFFFFFFFu : (1u << ctx) - 1u;
-        const uint32_t in = upto == 32 ? 0xFFFFFFFFu : (1u << upto) - 1u;
-        uint32_t bits = in;
-        if (p.mask && (in & ~low)) {
-            const long long o = off + ((long long)s.b * p.N + node) * p.N + (p0 - s.L), i0 = o >> 2;
-            const uint32_t sh = (uint32_t)(o & 3) * 8;
-            uint32_t wd[9];
-            if (full1 >= full0) {
+// The visibility of 64 positions for the rows of a warp (lanes in the order of
+// their nodes), 32 a word: a node's mask bytes by the whole warp, a ballot a
+// word. Node j of the rows' own sequence is at position L + j.
+SV_DEV uint2 see_bits(const AttnParams& p, const Seg& s, int node, long long pos0) {
+    const int lane = threadIdx.x & 31;
+    const long long ctx = s.L - pos0, upto = s.len - pos0;  // context below ctx, nothing from upto on
+    const int j0 = (int)max(-64LL, -ctx);                   // node of bit 0 (negative: context)
+    uint32_t see[2];
+    if (!p.mask) {
+        const long long to = min(upto, ctx + node + 1);
 #pragma unroll
-                for (int i = 0; i < 9; ++i)
-                    wd[i] = __ldg(reinterpret_cast<const uint32_t*>(start) + min(max(i0 + i, full0), full1));
-            }
-            if (i0 < full0 || i0 + 8 > full1 || full1 < full0) {  // the mask's first or last bytes are near
-                // (few threads; indexes of the array have to be constants)
-#pragma unroll
-                for (int i = 0; i < 9; ++i)
-                    if (i0 + i < full0 || i0 + i > full1) wd[i] = mask_edge(start, off, bytes, i0 + i);
-            }
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                m |= ((__vsetne4(__funnelshift_r(wd[i], wd[i + 1], sh), 0u) * 0x01020408u) >> 24 & 0xFu) << (4 * i);
-            bits &= m;
+        for (int k = 0; k < 2; ++k) {
+            const int n = (int)min(32LL, max(0LL, to - 32 * k));
+            see[k] = n == 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
         }
-        bits = (low & in) | (bits & ~low);
-        if (k == 0) see->x = bits;
-        if (k == 1) see->y = bits;
+        return make_uint2(see[0], see[1]);
     }
+    const int first = __shfl_sync(0xFFFFFFFFu, node, 0), last = __shfl_sync(0xFFFFFFFFu, node, 31);
+    const uint8_t* row = p.mask + ((long long)s.b * p.N + first) * p.N + j0 + lane;
+    const bool c0 = j0 + lane < 0, c1 = j0 + lane + 32 < 0;                       // context
+    const bool n0 = !c0 && j0 + lane < s.n, n1 = !c1 && j0 + lane + 32 < s.n;  // a node
+    see[0] = see[1] = 0u;
+#pragma unroll 1
+    for (int m0 = first; m0 <= last; m0 += 8) {
+        uint8_t x[8], y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            x[u] = n0 && m0 + u <= last ? __ldg(row + u * p.N) : 0;
+            y[u] = n1 && m0 + u <= last ? __ldg(row + u * p.N + 32) : 0;
+        }
+        row += 8 * (long long)p.N;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint32_t a = __ballot_sync(0xFFFFFFFFu, c0 || x[u] != 0), b = __ballot_sync(0xFFFFFFFFu, c1 || y[u] != 0);
+            if (node == m0 + u) {
+                see[0] = a;
+                see[1] = b;
+            }
+        }
+    }
+    return make_uint2(see[0], see[1]);
 }
 
-// What clean_v took out, for one row and 32 columns.
-SV_DEV void add_unclean(const AttnParams& p, const Seg& s, int node, int col0, float (&o)[32]) {
+// What clean_v took out, added to a row's written results (columns [col, col +
+// cols)); rare, so it is kept small.
+SV_DEV void add_unclean(const AttnParams& p, const Seg& s, int node, char* out, int col, int cols) {
     const int j0 = (int)max(0LL, (long long)s.first * kKv - s.L);
     const int j1 = (int)min((long long)s.n, (long long)s.last * kKv - s.L);
-    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + s.h * p.head_stride + col0;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.v) + s.h * p.head_stride + col;
+#pragma unroll 1
     for (int j = j0; j < j1; ++j) {
         const bool see = p.mask ? __ldg(p.mask + ((long long)s.b * p.N + node) * p.N + j) != 0 : j <= node;
-        if (!see) continue;
         const long long pos = (long long)s.L + j;
         const int id = __ldg(p.table + s.b * p.table_stride + (pos >> p.page_shift));
-        if (id < 0 || id >= p.num_pages) continue;
+        if (!see || id < 0 || id >= p.num_pages) continue;
         const uint16_t* row = v + id * p.page_stride + (pos & ((1 << p.page_shift) - 1)) * p.token_stride;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) {
+#pragma unroll 1
+        for (int e = 0; e < cols; ++e) {
             const uint32_t x = row[e];
-            if ((x & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float(x << 16);
+            if ((x & 0x7F80u) != 0x7F80u) continue;
+            if (s.whole) {
+                uint16_t* o = reinterpret_cast<uint16_t*>(out) + e;
+                *o = (uint16_t)pack_bf16(__uint_as_float((uint32_t)*o << 16) + __uint_as_float(x << 16), 0.f);
+            } else {
+                reinterpret_cast<float*>(out)[e] += __uint_as_float(x << 16);
+            }
         }
     }
 }
@@ -450,16 +448,9 @@ SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
 
 constexpr float kNegInf = -__builtin_inff();
 
-// 32 bytes; in one store where they start on 32.
 SV_DEV void st32(char* dst, const uint32_t* x) {
-    if (((uintptr_t)dst & 31) == 0) {
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                     "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
-        reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
-    }
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
 }
 
 // ---- queries, pages, edges -----------------------------------------------------------
@@ -512,25 +503,7 @@ SV_DEV void help(const AttnParams& p, Ctl* c, const CUtensorMap* mq, uint32_t qs
     const int lane = threadIdx.x & 31, nodes = 128 / p.G;  // nodes of a half
     const uint32_t box = 128u * min(nodes, p.N) * p.G;     // bytes of 64 columns of them
     uint32_t seg = 0, ring0 = 0, asked = 0;
-    Seg s;
-    auto post = [&](uint32_t number) {  // the next segment becomes `number`'s post
-        const bool more = walk.next(p, &s);
-        if (lane == 0) {
-            c->flags[number & 3] = 0;
-            if (!more) s.b = -1;
-            c->seg[number & 3] = s;
-            mbar_arrive(&c->seg_full[number & 3]);
-        }
-        __syncwarp();
-        return more;
-    };
-    bool ok = true, more = post(0);
-    while (ok && more) {
-        const Seg& s = c->seg[seg & 3];
-        // With the last segment's queries free, the groups have begun segment
-        // seg - 2, the issuers and the producer seg - 1: post seg + 1 takes the
-        // place of one that nobody needs.
-        if (seg && !(ok = warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort))) break;
+    auto ask_q = [&](const Seg& s) {  // a segment's queries
         if (lane == 0) mbar_expect_tx(&c->q_full, box * (D / 64) * (s.dual ? 2 : 1));
         __syncwarp();
         if (lane < D / 64 * (s.dual ? 2 : 1)) {
@@ -538,22 +511,52 @@ SV_DEV void help(const AttnParams& p, Ctl* c, const CUtensorMap* mq, uint32_t qs
             tma_load4(qs + w * Shape<D>::kTile + half * kHalf, mq, half * 64, s.h * p.G, s.row0 / p.G + w * nodes, s.b,
                       &c->q_full);
         }
-        more = post(seg + 1);
+    };
+    bool ok = true, more = true;
+#pragma unroll 1
+    for (;; ++seg) {
+        // Post `seg`. With segment seg - 2's queries free (below), the groups have
+        // begun segment seg - 3, the issuers and the producer seg - 2: it takes the
+        // place of one that nobody needs.
+        Seg next;
+        const bool again = more && walk.next(p, &next);
+        if (!ok) {  // what is left of the part will not be done
+            if (!again) break;
+            if (lane == 0 && p.status) atomicMax(p.status + next.b, kETimeout);
+            continue;
+        }
+        if (lane == 0) {
+            c->flags[seg & 3] = 0;
+            if (!again) next.b = -1;
+            c->seg[seg & 3] = next;
+            mbar_arrive(&c->seg_full[seg & 3]);
+        }
+        __syncwarp();
+        more = again;
+        if (seg == 0) {
+            if (!more) break;
+            ask_q(c->seg[0]);
+            continue;
+        }
+        // the segment before it, whose queries are on their way: its V
+        const Seg& s = c->seg[(seg - 1) & 3];
         const int cnt = s.last - s.first;
+#pragma unroll 1
         for (int i = max(0, s.L / kKv - s.first); ok && i < cnt; ++i) {
             if (!tail_tile(s, i)) continue;
             const uint32_t st = (ring0 + ring_v(s, i)) % NS, w = s.dual ? 0u : i & 1;
             if (!(ok = warp_wait(&c->ask[w], asked >> w & 1, &c->abort))) break;  // (the tile is there)
             asked ^= 1u << w;
-            clean_v<D>(c, s, stages + st * Shape<D>::kTile, i, seg & 3);
+            clean_v<D>(c, s, stages + st * Shape<D>::kTile, i, (seg - 1) & 3);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->clean[st]);
         }
         ring0 += 2 * cnt;
-        ++seg;
+        if (ok && !more) break;
+        if (ok && (ok = warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort))) ask_q(c->seg[seg & 3]);
+        if (!ok) c->abort = 1;
     }
-    if (!ok) c->abort = 1;
 }
 
 template <int D>
@@ -666,27 +669,28 @@ struct Group {
         return true;
     }
 
-    // 32 columns of a row's result.
-    SV_DEV void put(const Seg& s, int rr, int col, const float (&o)[32], float inv) {
-        if (s.whole) {
-            const int node = (s.row0 + rr) / p.G, g = (s.row0 + rr) - node * p.G;
-            const long long row = ((long long)s.b * p.N + node) * (p.Hkv * p.G) + s.h * p.G + g;
-            char* dst = reinterpret_cast<char*>(p.out) + (row * D + col) * 2;
-            uint32_t x[16];
+    // A row's place in the result: bf16, or fp32 among the pieces.
+    SV_DEV char* place(const Seg& s, int rr) {
+        if (!s.whole) return reinterpret_cast<char*>(p.part_o + ((long long)s.slot * p.tile_rows + rr) * D);
+        const int node = (s.row0 + rr) / p.G, g = (s.row0 + rr) - node * p.G;
+        const long long row = ((long long)s.b * p.N + node) * (p.Hkv * p.G) + s.h * p.G + g;
+        return SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G) ? reinterpret_cast<char*>(p.out) + row * (D * 2) : nullptr;
+    }
+    // 32 columns of it.
+    SV_DEV static void put(bool whole, char* dst, const float (&o)[32], float inv) {
+        uint32_t x[32];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) x[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-            if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G)) {
-                st32(dst, x);
-                st32(dst + 32, x + 8);
+        for (int k = 0; k < 16; ++k)
+            if (whole) x[k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+            else {
+                x[2 * k] = __float_as_uint(o[2 * k]);
+                x[2 * k + 1] = __float_as_uint(o[2 * k + 1]);
             }
-        } else {
-            char* dst = reinterpret_cast<char*>(p.part_o + ((long long)s.slot * p.tile_rows + rr) * D + col);
-            uint32_t x[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(o[k]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) st32(dst + 32 * k, x + 8 * k);
-        }
+        st32(dst, x);
+        st32(dst + 32, x + 8);
+        if (whole) return;
+        st32(dst + 64, x + 16);
+        st32(dst + 96, x + 24);
     }
     SV_DEV void put_ml(const Seg& s, int rr, float m, float l) {
         if (!s.whole) {
@@ -725,6 +729,8 @@ struct Group {
         }
         if (fl & 2) l = __uint_as_float(0x7FC00000u);
         const float inv = l == 0.f ? 0.f : 1.f / l;
+        const bool whole = s.whole;
+        char* dst = mine ? place(s, rr) : nullptr;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
             float o[32];
@@ -735,11 +741,9 @@ struct Group {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + z[e] * w1;
             }
-            if (mine) {
-                if (fl & 1) add_unclean(p, s, node, k, o);
-                put(s, rr, k, o, inv);
-            }
+            if (dst) put(whole, dst + k * (whole ? 2 : 4), o, inv);
         }
+        if (dst && fl & 1) add_unclean(p, s, node, dst, 0, D);
         if (mine) put_ml(s, rr, m, l);
         return true;
     }
@@ -765,7 +769,7 @@ struct Group {
                 const long long pos0 = (long long)(s.first + i) * kKv + kHalfKv * half;
                 const bool tail = pos0 + kHalfKv > s.L;
                 uint2 see = make_uint2(0u, 0u);
-                if (tail && warp_on) see_bits(p, s, node, pos0, &see);
+                if (tail && warp_on) see = see_bits(p, s, node, pos0);
                 if (!(ok = warp_wait(&c->s_full[w][half], s_phase >> half & 1, &c->abort))) break;
                 s_phase ^= 1u << half;
                 tc_fence_after();
@@ -798,14 +802,8 @@ __global__ void __launch_bounds__(NT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     asm volatile("griddepcontrol.launch_dependents;");
-    const long long total = attn_locate<kKv, kExtra, NT>(p, &c->scan);
-    const int parts = attn_parts(total, gridDim.x);
-    if (tid == 10 * 32) attn_join<kKv, kExtra>(p, c->scan, total, parts);
-    if ((int)blockIdx.x >= parts) {
-        if (warp == 11) attn_edges<bf16_t>(p, blockIdx.x, gridDim.x);
-        return;
-    }
-    Walk walk(c->scan, total, parts);
+    const AttnCut cut = attn_locate<kKv, kExtra, NT>(p, &c->scan);
+    Walk walk(c->scan, cut);
 
     if (tid == 0) {
         for (int i = 0; i < Shape<D>::kStages; ++i) {
@@ -825,7 +823,10 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&c->ask[i], 1);
             c->flags[2 * i] = c->flags[2 * i + 1] = 0;
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&c->seg_full[i], 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&c->seg_full[i], 1);
+            c->seg[i].b = -1;
+        }
         mbar_init(&c->groups, 8);
         mbar_init(&c->drain, 2);
         c->abort = 0;
@@ -851,14 +852,16 @@ __global__ void __launch_bounds__(NT, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) produce<D>(p, c, &mk, &mv, stages);
+        if (warp == 10) {
+            if (lane == 0) attn_join<kKv, kExtra>(p, c->scan, cut);
+            __syncwarp();
+            attn_edges<bf16_t>(p, blockIdx.x, gridDim.x);
+        }
         if (warp == 9 || warp == 10) {
             Issuer<D> is{c, uni(warp - 9), uni(tmem), qs, stages};
             is.run();
         }
-        if (warp == 11) {
-            help<D>(p, c, &mq, qs, stages, walk);
-            attn_edges<bf16_t>(p, blockIdx.x, gridDim.x, *reinterpret_cast<volatile int*>(&c->abort) != 0);
-        }
+        if (warp == 11) help<D>(p, c, &mq, qs, stages, walk);
     }
     __syncwarp();
     tc_fence_before();
@@ -876,11 +879,8 @@ __global__ void __launch_bounds__(NT, 1)
         __syncthreads();
     }
     if (warp == 9) tmem_free512(tmem);
-    if (tid == 0 && c->abort && p.status) {
-        // a wait gave up: this part's sequences are not whole
-        Seg s;
-        while (walk.next(p, &s)) atomicMax(p.status + s.b, kETimeout);
-    }
+    if (tid < 4 && c->abort && p.status && c->seg[tid].b >= 0)  // a wait gave up: these segments are not whole
+        atomicMax(p.status + c->seg[tid].b, kETimeout);
 }
 
 using Encode = decltype(&cuTensorMapEncodeTiled);

@@ -137,6 +137,9 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
         return SPEC_EINVAL;
     const float c2 = scale * 1.4426950408889634f;
     if (!std::isfinite(scale) || !std::isfinite(c2)) return SPEC_EINVAL;
+    // a sequence's tiles (16 rows x 32 positions at the least) are counted in 32 bits
+    const double row_tiles = (double)cache->kv_heads * ((N * (q_heads / cache->kv_heads) + 15) / 16);
+    if (row_tiles * ((double)max_pages * cache->page_size / 32 + 8) >= 2147483648.0) return SPEC_EINVAL;
     if (ws_bytes < attention_bytes(cache->head_dim, q_heads / cache->kv_heads, dtype)) return SPEC_EINVAL;
     sv::AttnParams p = {};
     p.q = q;
