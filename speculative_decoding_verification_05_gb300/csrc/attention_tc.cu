@@ -251,46 +251,64 @@ struct Issuer {
         return true;
     }
 
-    // S of a half of the tile in stage st.
-    SV_DEV void scores(bool dual, int half, uint32_t st, bool done, bool last) {
-        constexpr uint32_t idesc = mma_idesc(kHalfKv, false);
-        const uint32_t d = tmem + 128 * w + 64 * half;
-        const uint64_t a = mma_desc(qs + (dual ? w * kTile : 0u), 16, 1024);
-        const uint64_t b = mma_desc(stages + st * kTile + half * kHalfRows, 16, 1024);
+    // The products of one step: for each half, O += P V of this stream's tile at
+    // ring entry rv (nv halves; `last` of the segment) and then, in the place
+    // that this frees, the scores of its next tile at rk (nk halves). One lane
+    // waits and issues: its few instructions between two products are what the
+    // other stream's products have to cover.
+    SV_DEV bool step(bool dual, uint32_t rv, int nv, bool first, bool last, bool tail, int live, uint32_t rk, int nk,
+                     bool last_k) {
+        constexpr uint32_t idesc_s = mma_idesc(kHalfKv, false), idesc_o = mma_idesc(D, true);
+        const uint32_t sv = uni(rv % NS), sk = uni(rk % NS);
+        const uint32_t ds = tmem + 128 * w, dp = tmem + 256 + 128 * w;
+        const uint64_t q = mma_desc(qs + (dual ? w * kTile : 0u), 16, 1024);
+        const uint64_t k = mma_desc(stages + sk * kTile, 16, 1024), v = mma_desc(stages + sv * kTile, kHalf, 1024);
+        bool ok = true;
         if (elected()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                mma_ss(d, a + off, b + off, idesc, kk > 0);
-            }
-            mma_commit(&c->s_full[w][half]);
-            if (done) mma_commit(&c->empty[st]);
-            if (last) mma_commit(&c->q_empty);
-        }
-        __syncwarp();
-    }
-
-    // O += P V of a half, `steps` of its 16-position steps.
-    SV_DEV void output(int half, uint32_t st, bool first, int steps, uint32_t heavy, bool done, bool last) {
-        constexpr uint32_t idesc = mma_idesc(D, true);
-        const uint32_t d = tmem + 256 + 128 * w, a = tmem + 128 * w + 64 * half;
-        const uint64_t b = mma_desc(stages + st * kTile + half * kHalfRows, kHalf, 1024);
-        if (elected()) {
+            for (int half = 0; half < 2; ++half) {
+                if (half < nv) {
+                    ok = tc_wait(&c->p_full[w][half], p_phase >> half & 1, &c->abort);
+                    if (tail && half == 0) ok = ok && tc_wait(&c->clean[sv], clean >> sv & 1, &c->abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w][half]);  // a byte of each warp
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                if (kk < steps) mma_ts(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, !first || kk > 0);
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (64 * half + 16 * kk < live)
+                            mma_ts(dp, ds + 64 * half + (kk >> 1) * 32 + (kk & 1) * 8, v + (half * kHalfRows + kk * 2048 >> 4),
+                                   idesc_o, !first || half > 0 || kk > 0);
+                    if (heavy) {
+                        heavy |= heavy >> 16;
+                        heavy |= heavy >> 8;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            if (heavy >> kk & 1)
+                                mma_ts(dp, ds + 64 * half + (kk >> 1) * 32 + 16 + (kk & 1) * 8,
+                                       v + (half * kHalfRows + kk * 2048 >> 4), idesc_o, true);
+                    }
+                    mma_commit(&c->pv[w]);
+                    if (half + 1 == nv) {
+                        mma_commit(&c->empty[sv]);
+                        if (last) mma_commit(&c->o_full[w]);
+                    }
+                }
+                if (half < nk) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                        mma_ss(ds + 64 * half, q + off, k + (half * kHalfRows >> 4) + off, idesc_s, kk > 0);
+                    }
+                    mma_commit(&c->s_full[w][half]);
+                    if (half + 1 == nk) {
+                        mma_commit(&c->empty[sk]);
+                        if (last_k) mma_commit(&c->q_empty);
+                    }
+                }
             }
-            if (heavy) {
-#pragma unroll 1
-                for (int kk = 0; kk < 4; ++kk)
-                    if (heavy >> kk & 1)
-                        mma_ts(d, a + (kk >> 1) * 32 + 16 + (kk & 1) * 8, b + kk * (2048 >> 4), idesc, true);
-            }
-            mma_commit(&c->pv[w]);
-            if (done) mma_commit(&c->empty[st]);
-            if (last) mma_commit(&c->o_full[w]);
         }
-        __syncwarp();
+        p_phase ^= (1u << nv) - 1u;  // (a bit a half)
+        return __all_sync(0xFFFFFFFFu, ok) != 0;
     }
 
     SV_DEV void run() {
@@ -299,54 +317,33 @@ struct Issuer {
         while (const Seg* at = next_seg(c, seg, &ok)) {
             const Seg& s = *at;
             const bool dual = uni(s.dual);
-            const int cnt = (int)uni(s.last - s.first);
-            const int halves = (int)uni(halves_of(s, w));  // of this stream's tiles
-            uint32_t st_k = 0, st_v = 0;
+            const int cnt = (int)uni(s.last - s.first), halves = (int)uni(halves_of(s, w));  // of this stream's tiles
+            const int mine = (halves + 1) >> 1;
             ok = warp_wait(&c->q_full, q_phase, &c->abort);
             q_phase ^= 1;
             if (halves == 0 && elected()) mbar_arrive(&c->q_empty);
             __syncwarp();
-            // P V of half u, and then the scores of half u + 2 in its place
 #pragma unroll 1
-            for (int u = halves ? -2 : 0; ok && u < halves; ++u) {
-                const int half = u & 1, i = dual ? u >> 1 : 2 * (u >> 1) + (int)w;
-                if (u >= 0) {
-                    const bool tail = tail_tile(s, i);
-                    if (half == 0) {
-                        const uint32_t ring = ring0 + ring_v(s, i);
-                        if (!(ok = reach(ring))) break;
-                        st_v = uni(ring % NS);
-                        if (tail && (!dual || w == 0)) {  // V has to be cleaned first
-                            if (elected()) mbar_arrive(&c->ask[w]);
-                            __syncwarp();
-                        }
+            for (int j = -1; ok && j < mine; ++j) {
+                if (!mine) continue;
+                const int i = dual ? j : 2 * j + (int)w;
+                const uint32_t rv = ring0 + ring_v(s, i), rk = ring0 + ring_k(s, dual ? j + 1 : i + 2);
+                const bool tail = j >= 0 && tail_tile(s, i);
+                if (j >= 0) {
+                    if (!(ok = reach(rv))) break;
+                    if (tail && (!dual || w == 0)) {  // V has to be cleaned first
+                        if (elected()) mbar_arrive(&c->ask[w]);
+                        __syncwarp();
                     }
-                    if (!(ok = warp_wait(&c->p_full[w][half], p_phase >> half & 1, &c->abort))) break;
-                    p_phase ^= 1u << half;
-                    if (tail && half == 0 && !(ok = warp_wait(&c->clean[st_v], clean >> st_v & 1, &c->abort))) break;
-                    tc_fence_after();
-                    uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w][half]);  // a byte of each warp
-                    heavy |= heavy >> 16;
-                    heavy = uni((heavy | heavy >> 8) & 0xFFu);
-                    const int steps = tail ? (int)uni((live_of(s, i) - kHalfKv * half + 15) >> 4) : 4;
-                    output(half, st_v, u == 0, steps, heavy, half == 1 || u + 1 == halves, u + 1 == halves);
                 }
-                if (u + 2 < halves) {
-                    if (half == 0) {
-                        const uint32_t ring = ring0 + ring_k(s, dual ? (u >> 1) + 1 : i + 2);
-                        if (!(ok = reach(ring))) break;
-                        st_k = uni(ring % NS);
-                        tc_fence_after();
-                    }
-                    scores(dual, half, st_k, half == 1 || u + 3 == halves, u + 3 == halves);
-                }
+                if (j + 1 < mine && !(ok = reach(rk))) break;
+                tc_fence_after();
+                ok = step(dual, rv, j < 0 ? 0 : min(2, halves - 2 * j), j == 0, j + 1 == mine, tail,
+                          tail ? live_of(s, i) : kKv, rk, min(2, halves - 2 * j - 2), j + 2 == mine);
                 // (phases of the stages whose V these tiles have had cleaned, the other stream's too)
-                if (u >= 0 && (half == 1 || u + 1 == halves)) {
-                    const int i0 = dual ? i : i - (int)w, i1 = dual ? i + 1 : min(i0 + 2, cnt);
-                    if (tail_tile(s, i1 - 1)) clean ^= clean_stages<D>(s, ring0, i0, i1);
-                }
+                const int i0 = dual ? j : 2 * j, i1 = dual ? j + 1 : min(2 * j + 2, cnt);
+                if (j >= 0 && tail_tile(s, i1 - 1)) clean ^= clean_stages<D>(s, ring0, i0, i1);
             }
-            const int mine = (halves + 1) >> 1;
             if (!dual && mine < (cnt + 1) >> 1) clean ^= clean_stages<D>(s, ring0, 2 * mine, cnt);
             ring0 += 2 * cnt;
             while (ok && seen < ring0) ok = pass();
