@@ -63,7 +63,7 @@ constexpr int NT = 384;
 constexpr int kGroupRegs = 208, kOtherRegs = 88;
 constexpr int kKv = 128;     // positions of a tile
 constexpr int kMaxStages = 10;
-constexpr float kHeavy = 4.f;  // octaves below a row's sum from which a weight is heavy
+constexpr float kHeavy = 4.f;  // octaves below a row's sum so far from which a weight is heavy
 constexpr float kSlack = 8.f;  // octaves of the running maximum above the reference that raise it
 constexpr float kJump = 64.f;  // of a half's own scores above it
 constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile
@@ -445,6 +445,12 @@ SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
 
 constexpr float kNegInf = -__builtin_inff();
 
+SV_DEV float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 SV_DEV void st32(char* dst, const uint32_t* x) {
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(x[0], x[1], x[2], x[3]);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(x[4], x[5], x[6], x[7]);
@@ -615,7 +621,14 @@ struct Group {
         tmem_ld64(at, x);
         if (tail) hide(x, see);
 #pragma unroll
-        for (int i = 0; i < 64; ++i) mx[i >> 4] = i & 15 ? fmaxf(mx[i >> 4], x[i]) : x[i];
+        for (int i = 0; i < 4; ++i) {
+            float a = max3(x[16 * i], x[16 * i + 1], x[16 * i + 2]), b = max3(x[16 * i + 3], x[16 * i + 4], x[16 * i + 5]);
+            a = max3(a, x[16 * i + 6], x[16 * i + 7]);
+            b = max3(b, x[16 * i + 8], x[16 * i + 9]);
+            a = max3(a, x[16 * i + 10], x[16 * i + 11]);
+            b = max3(b, x[16 * i + 12], x[16 * i + 13]);
+            mx[i] = max3(fmaxf(a, b), x[16 * i + 14], x[16 * i + 15]);
+        }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
         if (ref == kNegInf) ref = ceilf(top);  // (nothing seen so far: all sums are zero)
         if (!first && __any_sync(0xFFFFFFFFu, fmaxf(m - kSlack, top - kJump) > ref)) {
@@ -626,14 +639,7 @@ struct Group {
         m = fmaxf(m, top);
         const float r = ref == kNegInf ? 0.f : ref;
         const uint64_t cc = pack2(c2, c2), rr = pack2(-r, -r);
-        // steps with heavy weights (against a lower bound of the new sum)
-        const float cut = __log2f(l + ex2(top - r)) - kHeavy + r;
-        uint32_t heavy = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) heavy |= mx[i] * c2 > cut ? 1u << i : 0u;
-        heavy = __reduce_or_sync(0xFFFFFFFFu, heavy);
-        if (lane == 0) c->heavy[w][half][warp] = (uint8_t)heavy;
-        uint64_t sum[2] = {0ull, 0ull};
+        uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             uint32_t hi[16];
@@ -644,24 +650,35 @@ struct Group {
                 unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
                 a = ex2(a);
                 b = ex2(b);
-                sum[e & 1] = add2(sum[e & 1], pack2(a, b));
+                sum[e & 3] = add2(sum[e & 3], pack2(a, b));
                 hi[e] = pack_bf16(a, b);
             }
             tmem_st16(at + 32 * j, hi);
-            if (heavy >> (2 * j) & 3) {  // what the rounding took
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    hi[e] = pack_bf16(x[32 * j + 2 * e] - __uint_as_float(hi[e] << 16),
-                                      x[32 * j + 2 * e + 1] - __uint_as_float(hi[e] & 0xFFFF0000u));
-            } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) hi[e] = 0u;
-            }
-            tmem_st16(at + 32 * j + 16, hi);
         }
         float a, b;
-        unpack2(add2(sum[0], sum[1]), &a, &b);
+        unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &a, &b);
         l += a + b;
+        // what the rounding took from the heavy weights, by steps of 16 positions
+        const float cut = __log2f(l) - kHeavy + r;
+        uint32_t heavy = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) heavy |= mx[i] * c2 > cut ? 1u << i : 0u;
+        heavy = __reduce_or_sync(0xFFFFFFFFu, heavy);
+        if (lane == 0) c->heavy[w][half][warp] = (uint8_t)heavy;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            uint32_t lo[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) lo[e] = 0u;
+            if (heavy >> (2 * j) & 3)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float u = x[32 * j + 2 * e], v = x[32 * j + 2 * e + 1];
+                    const uint32_t hi = pack_bf16(u, v);
+                    lo[e] = pack_bf16(u - __uint_as_float(hi << 16), v - __uint_as_float(hi & 0xFFFF0000u));
+                }
+            tmem_st16(at + 32 * j + 16, lo);
+        }
         tmem_wait_st();
         return true;
     }
@@ -760,13 +777,14 @@ struct Group {
             const bool warp_on = warp * 32 < half && (s.dual ? half * w : 0) + warp * 32 < s.rows;
             const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
             const int halves = halves_of(s, w);
+            // where a half begins, and the context ends, from the start of the stream's first tile
+            const int step = s.dual ? kKv : 2 * kKv, reach = s.L - (s.first + (s.dual ? 0 : w)) * kKv;
 #pragma unroll 1
             for (int u = 0; u < halves; ++u) {
-                const int half = u & 1, i = s.dual ? u >> 1 : 2 * (u >> 1) + w;
-                const long long pos0 = (long long)(s.first + i) * kKv + kHalfKv * half;
-                const bool tail = pos0 + kHalfKv > s.L;
+                const int half = u & 1, off = kHalfKv * half + step * (u >> 1);
+                const bool tail = off + kHalfKv > reach;
                 uint2 see = make_uint2(0u, 0u);
-                if (tail && warp_on) see = see_bits(p, s, node, pos0);
+                if (tail && warp_on) see = see_bits(p, s, node, (long long)s.L - reach + off);
                 if (!(ok = warp_wait(&c->s_full[w][half], s_phase >> half & 1, &c->abort))) break;
                 s_phase ^= 1u << half;
                 tc_fence_after();
