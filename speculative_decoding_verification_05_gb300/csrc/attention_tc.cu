@@ -232,34 +232,44 @@ struct Issuer {
     static constexpr uint32_t NS = Shape<D>::kStages, kTile = Shape<D>::kTile;
     Ctl* c;
     uint32_t w, tmem, qs, stages;
-    uint32_t seen = 0, p_phase = 0, q_phase = 0, clean = 0;  // clean: phase of each stage's barrier
+    uint32_t st = 0, phase = 0, left = 0;               // the next entry's stage and round, entries left of the segment
+    uint32_t p_phase = 0, q_phase = 0, clean = 0;       // clean: phase of each stage's barrier
 
-    // Entry `ring` (this stream's); the other's before it are passed over.
-    SV_DEV bool reach(uint32_t ring) {
-        while (seen < ring) {
-            if (!pass()) return false;
+    SV_DEV bool advance() {
+        const bool ok = warp_wait(&c->full[st], phase, &c->abort);
+        --left;
+        if (++st == NS) {
+            st = 0;
+            phase ^= 1;
         }
-        ++seen;
-        return warp_wait(&c->full[ring % NS], (ring / NS) & 1, &c->abort);
+        return ok;
     }
-    SV_DEV bool pass() {
-        const uint32_t st = seen % NS;
-        if (!warp_wait(&c->full[st], (seen / NS) & 1, &c->abort)) return false;
-        if (elected()) mbar_arrive(&c->empty[st]);
-        __syncwarp();
-        ++seen;
-        return true;
+    // The next entry, this stream's: its stage.
+    SV_DEV bool take(uint32_t* stage) {
+        *stage = st;
+        return advance();
+    }
+    // The next n entries, the other stream's.
+    SV_DEV bool pass(int n) {
+        bool ok = true;
+        for (; ok && n > 0; --n) {
+            const uint32_t at = st;
+            ok = advance();
+            if (elected()) mbar_arrive(&c->empty[at]);
+            __syncwarp();
+        }
+        return ok;
     }
 
-    // The products of one step: for each half, O += P V of this stream's tile at
-    // ring entry rv (nv halves; `last` of the segment) and then, in the place
-    // that this frees, the scores of its next tile at rk (nk halves). One lane
+    // The products of one step: for each half, O += P V of this stream's tile in
+    // stage_v (nv halves; `last` of the segment) and then, in the place that
+    // this frees, the scores of its next tile in stage_k (nk halves). One lane
     // waits and issues: its few instructions between two products are what the
     // other stream's products have to cover.
-    SV_DEV bool step(bool dual, uint32_t rv, int nv, bool first, bool last, bool tail, int live, uint32_t rk, int nk,
-                     bool last_k) {
+    SV_DEV bool step(bool dual, uint32_t stage_v, int nv, bool first, bool last, bool tail, int live, uint32_t stage_k,
+                     int nk, bool last_k) {
         constexpr uint32_t idesc_s = mma_idesc(kHalfKv, false), idesc_o = mma_idesc(D, true);
-        const uint32_t sv = uni(rv % NS), sk = uni(rk % NS);
+        const uint32_t sv = uni(stage_v), sk = uni(stage_k);
         const uint32_t ds = tmem + 128 * w, dp = tmem + 256 + 128 * w;
         const uint64_t q = mma_desc(qs + (dual ? w * kTile : 0u), 16, 1024);
         const uint64_t k = mma_desc(stages + sk * kTile, 16, 1024), v = mma_desc(stages + sv * kTile, kHalf, 1024);
@@ -318,36 +328,40 @@ struct Issuer {
             const Seg& s = *at;
             const bool dual = uni(s.dual);
             const int cnt = (int)uni(s.last - s.first), halves = (int)uni(halves_of(s, w));  // of this stream's tiles
-            const int mine = (halves + 1) >> 1;
+            const int mine = (halves + 1) >> 1, tails = (int)uni(max(0, s.L / kKv - s.first));  // tiles from here on reach
+            const int live = (int)uni(live_of(s, cnt - 1));                                     // past the context
             ok = warp_wait(&c->q_full, q_phase, &c->abort);
             q_phase ^= 1;
             if (halves == 0 && elected()) mbar_arrive(&c->q_empty);
             __syncwarp();
+            left = 2 * cnt;
+            uint32_t sv = 0, sk = 0;
+            if (mine && !dual) ok = ok && pass(w);  // K0
 #pragma unroll 1
             for (int j = -1; ok && j < mine; ++j) {
                 if (!mine) continue;
                 const int i = dual ? j : 2 * j + (int)w;
-                const uint32_t rv = ring0 + ring_v(s, i), rk = ring0 + ring_k(s, dual ? j + 1 : i + 2);
-                const bool tail = j >= 0 && tail_tile(s, i);
+                const bool tail = j >= 0 && i >= tails;
                 if (j >= 0) {
-                    if (!(ok = reach(rv))) break;
+                    // between this stream's K(i) and V(i): V(i - 1) and K(i + 1)
+                    if (!dual && !(ok = pass((i > 0) + (i + 1 < cnt)))) break;
+                    if (!(ok = take(&sv))) break;
                     if (tail && (!dual || w == 0)) {  // V has to be cleaned first
                         if (elected()) mbar_arrive(&c->ask[w]);
                         __syncwarp();
                     }
                 }
-                if (j + 1 < mine && !(ok = reach(rk))) break;
+                if (j + 1 < mine && !(ok = take(&sk))) break;
                 tc_fence_after();
-                ok = step(dual, rv, j < 0 ? 0 : min(2, halves - 2 * j), j == 0, j + 1 == mine, tail,
-                          tail ? live_of(s, i) : kKv, rk, min(2, halves - 2 * j - 2), j + 2 == mine);
+                ok = step(dual, sv, j < 0 ? 0 : min(2, halves - 2 * j), j == 0, j + 1 == mine, tail,
+                          i + 1 == cnt ? live : kKv, sk, min(2, halves - 2 * j - 2), j + 2 == mine);
                 // (phases of the stages whose V these tiles have had cleaned, the other stream's too)
                 const int i0 = dual ? j : 2 * j, i1 = dual ? j + 1 : min(2 * j + 2, cnt);
-                if (j >= 0 && tail_tile(s, i1 - 1)) clean ^= clean_stages<D>(s, ring0, i0, i1);
+                if (j >= 0 && i1 > tails) clean ^= clean_stages<D>(s, ring0, i0, i1);
             }
             if (!dual && mine < (cnt + 1) >> 1) clean ^= clean_stages<D>(s, ring0, 2 * mine, cnt);
             ring0 += 2 * cnt;
-            while (ok && seen < ring0) ok = pass();
-            if (!ok) break;
+            if (!ok || !(ok = pass((int)left))) break;
             ++seg;
         }
         if (!ok) c->abort = 1;
