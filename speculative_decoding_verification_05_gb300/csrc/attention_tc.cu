@@ -629,7 +629,7 @@ struct Group {
     // (sums stay far from overflow).
     //
     // One half: S -> P.
-    SV_DEV bool softmax(int half, const uint2 see, bool tail, bool first, float c2, float& m, float& ref, float& l) {
+    SV_DEV bool softmax(int half, const uint2 see, bool tail, bool first, bool on, float c2, float& m, float& ref, float& l) {
         const uint32_t at = tm_s + 64 * half;
         float x[64], mx[4];  // mx: by steps of 16 positions
         tmem_ld64(at, x);
@@ -645,7 +645,8 @@ struct Group {
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
         if (ref == kNegInf) ref = ceilf(top);  // (nothing seen so far: all sums are zero)
-        if (!first && __any_sync(0xFFFFFFFFu, fmaxf(m - kSlack, top - kJump) > ref)) {
+        // (a lane without a row may hold anything)
+        if (!first && __any_sync(0xFFFFFFFFu, on && fmaxf(m - kSlack, top - kJump) > ref)) {
             const float to = fmaxf(ref, ceilf(fmaxf(m, top)));
             if (!rescale(ref == to ? 1.f : ex2(ref - to), l)) return false;
             ref = to;
@@ -677,7 +678,7 @@ struct Group {
         uint32_t heavy = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) heavy |= mx[i] * c2 > cut ? 1u << i : 0u;
-        heavy = __reduce_or_sync(0xFFFFFFFFu, heavy);
+        heavy = __reduce_or_sync(0xFFFFFFFFu, on ? heavy : 0u);
         if (lane == 0) c->heavy[w][half][warp] = (uint8_t)heavy;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -789,6 +790,7 @@ struct Group {
             float m = kNegInf, ref = kNegInf, l = 0.f;
             const int half = p.tile_rows / 2, rr = s.dual ? half * w + t : t;
             const bool warp_on = warp * 32 < half && (s.dual ? half * w : 0) + warp * 32 < s.rows;
+            const bool on = t < half && rr < s.rows;
             const int node = (s.row0 + min(rr, s.rows - 1)) / p.G;
             const int halves = halves_of(s, w);
             // where a half begins, and the context ends, from the start of the stream's first tile
@@ -803,7 +805,7 @@ struct Group {
                 s_phase ^= 1u << half;
                 tc_fence_after();
                 if (!warp_on && lane == 0) c->heavy[w][half][warp] = 0;
-                if (warp_on && !(ok = softmax(half, see, tail, u == 0, c2, m, ref, l))) break;
+                if (warp_on && !(ok = softmax(half, see, tail, u == 0, on, c2, m, ref, l))) break;
                 ++pv_count;
                 if (w == 1 && u + 1 == halves) c->ml[t] = make_float2(ref, l);
                 tc_fence_before();
