@@ -3,14 +3,25 @@
 // the work). Takes every type and head size; float32 caches and head sizes
 // that the tensor-core kernel lacks come here.
 //
-// One CTA of eight warps takes 16 rows of a unit, two a warp. Tiles of 64
-// positions (32 where a float32 head is wider than 128) of K and V are staged
-// by 16-byte asynchronous copies, two tiles deep. A lane scores two positions
-// (one) for both rows of its warp; the running
-// maximum and sum are the warp's (shuffles), the weights go through a
-// warp-private strip of shared memory, and a lane accumulates four (eight:
-// D > 128) output columns in registers. Warps meet only at the tile's arrival
-// and release. fp32 throughout.
+// One CTA of eight warps takes 16 rows of a unit, two a warp; where a unit has
+// fewer, the warps share out a tile's positions as well (8 rows: two warps a
+// pair of rows, half the positions each; 2 rows: eight). Tiles of 64 positions
+// (32 where a cache row is longer than 256 bytes) of K and V are staged by
+// 16-byte asynchronous copies, two tiles deep and across the stays in units. A
+// lane scores two positions, one, or a part of one's columns, for both rows of
+// its warp; the weights go through a warp-private strip of shared memory, and a
+// lane accumulates four (eight: D > 128) output columns in registers, narrow
+// heads (D <= 64) two or more positions at a time, in packed pairs. Warps meet
+// at the tile's arrival and release, and to add up what the warps of a row
+// have. fp32 throughout.
+//
+// Bound by issued instructions (some 800 a warp and tile of 64 positions, 190
+// of them products and their loads) from a few tiles a CTA on, by start-up and
+// the join below that: 8 sequences of 8 nodes, 12 heads of 64 columns, float32:
+// 9.2 us at contexts of 20, 21.0 at 760, 183 at 12000 (3.3 TB/s of K and V). With
+// two warps idle of every four there, a row maximum by shuffles each tile and
+// single products it took 24.7 and 234. Tiles of 32 positions with two, three or
+// four CTAs an SM took 254, 264 and 339.
 
 #include <algorithm>
 #include <atomic>
@@ -32,12 +43,10 @@ constexpr int row_bytes(int D) {  // a K row in shared memory: 16 bytes of paddi
 
 template <typename E, int KV>
 size_t simt_smem(int D) {
-    return (size_t)2 * KV * (row_bytes<E>(D) + D * sizeof(E)) + (size_t)kRows * D * 4 + (size_t)kRows * KV * 4;
+    return (size_t)2 * KV * (row_bytes<E>(D) + D * sizeof(E)) + (size_t)kRows * D * (2 * sizeof(E) + 4) +
+           (size_t)kRows * KV * 4;
 }
 
-SV_DEV void cp16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 SV_DEV uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 template <typename E>
@@ -53,207 +62,325 @@ SV_DEV float4 lds4<bf16_t>(const unsigned char* p) {
                        __uint_as_float(r.y & 0xFFFF0000u));
 }
 
+// Four columns in two packed pairs.
+struct Two {
+    uint64_t a, b;
+};
+SV_DEV float lo2(uint64_t x) { return __uint_as_float((uint32_t)x); }
+SV_DEV float hi2(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+SV_DEV uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+SV_DEV uint64_t mul1(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+SV_DEV Two axpy2(uint64_t ww, Two x, Two c) {
+    return Two{fma2(ww, x.a, c.a), fma2(ww, x.b, c.b)};
+}
+SV_DEV Two mul2(float f, Two x) {
+    const uint64_t ff = pack2(f, f);
+    return Two{mul1(ff, x.a), mul1(ff, x.b)};
+}
+template <typename E>
+SV_DEV Two lds4x2(const unsigned char* p) {
+    const float4 x = lds4<E>(p);
+    return Two{pack2(x.x, x.y), pack2(x.z, x.w)};
+}
+template <>
+SV_DEV Two lds4x2<float>(const unsigned char* p) {
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(p);
+    return Two{x.x, x.y};
+}
+
 SV_DEV float4 fma4(float a, float4 v, float4 c) {
     return make_float4(fmaf(a, v.x, c.x), fmaf(a, v.y, c.y), fmaf(a, v.z, c.z), fmaf(a, v.w, c.w));
 }
 
-// One tile's K and V rows into a stage. Rows past the sequence's end and rows
-// of a page that does not exist are zero. Returns whether a page id was bad.
+SV_DEV void cp16(uint32_t dst, const void* src, int bytes) {  // the rest of 16 is filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// One tile's K and V rows into a stage, 2^lv lanes a row (its 16-byte words,
+// rounded up). Rows past the sequence's end and rows of a page that does not
+// exist are zero. Returns whether a page id was bad.
 template <typename E, int KV>
-SV_DEV bool load_tile(const AttnParams& p, int b, int h, long long pos0, long long end, unsigned char* ks,
-                      unsigned char* vs) {
-    const int vec = p.D * (int)sizeof(E) / 16;
-    const E* kc = reinterpret_cast<const E*>(p.k) + h * p.head_stride;
-    const E* vc = reinterpret_cast<const E*>(p.v) + h * p.head_stride;
-    const int ps1 = (1 << p.page_shift) - 1;
-    const int32_t* table = p.table + b * p.table_stride;
+SV_DEV bool load_tile(const AttnParams& p, const AttnStay& s, int tile, uint32_t ks, uint32_t vs, int lv) {
+    const int vec = p.D * (int)sizeof(E) / 16, ps1 = (1 << p.page_shift) - 1, c = threadIdx.x & ((1 << lv) - 1);
+    if (c >= vec) return false;
+    const uint32_t pos0 = (uint32_t)tile * KV;
+    const int upto = (int)min((long long)KV, s.len - pos0);
+    const int32_t* table = p.table + s.b * p.table_stride;
+    const long long in = s.h * p.head_stride + c * (16 / (int)sizeof(E));
+    const E* kc = static_cast<const E*>(p.k) + in;
+    const E* vc = static_cast<const E*>(p.v) + in;
+    ks += c * 16;
+    vs += c * 16;
     bool bad = false;
-    for (int i = threadIdx.x; i < KV * vec; i += NT) {
-        const int t = i / vec, c = i - t * vec;
-        const long long pos = pos0 + t;
-        unsigned char* kd = ks + t * row_bytes<E>(p.D) + c * 16;
-        unsigned char* vd = vs + (t * vec + c) * 16;
-        int id = -1;
-        if (pos < end) {
-            id = __ldg(table + (pos >> p.page_shift));
-            if (id < 0 || id >= p.num_pages) {
-                bad = true;
-                id = -1;
-            }
-        }
-        if (id >= 0) {
-            const long long at = id * p.page_stride + (pos & ps1) * p.token_stride + c * (16 / (int)sizeof(E));
-            cp16(smem_addr(kd), kc + at);
-            cp16(smem_addr(vd), vc + at);
-        } else {
-            *reinterpret_cast<uint4*>(kd) = make_uint4(0u, 0u, 0u, 0u);
-            *reinterpret_cast<uint4*>(vd) = make_uint4(0u, 0u, 0u, 0u);
-        }
+#pragma unroll 4
+    for (int t = threadIdx.x >> lv; t < KV; t += NT >> lv) {
+        const uint32_t pos = pos0 + t;
+        int id = t < upto ? __ldg(table + (pos >> p.page_shift)) : 0;
+        const bool ok = (uint32_t)id < (uint32_t)p.num_pages;
+        bad |= !ok;
+        if (!ok) id = 0;
+        const long long at = id * p.page_stride + (int)(pos & ps1) * p.token_stride;
+        const int bytes = ok && t < upto ? 16 : 0;
+        cp16(ks + t * row_bytes<E>(p.D), kc + at, bytes);
+        cp16(vs + t * p.D * (int)sizeof(E), vc + at, bytes);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
     return bad;
 }
 
 template <typename E, int KV>
-__global__ void __launch_bounds__(NT) attn_simt_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(NT, 2) attn_simt_kernel(const __grid_constant__ AttnParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ AttnScan scan;
+    __shared__ float2 sums[kRows];  // running maximum and sum by part and row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    constexpr int J = KV / 32;
     const int D = p.D, D4 = D / 4, kstride = row_bytes<E>(D);
     unsigned char* ks = smem;
     unsigned char* vs = ks + 2 * KV * kstride;
-    float* qs = reinterpret_cast<float*>(vs + (size_t)2 * KV * D * sizeof(E));
-    float* ws = qs + kRows * D + warp * 2 * KV;  // the warp's weights [2][KV]
+    unsigned char* qs = vs + (size_t)2 * KV * D * sizeof(E);               // two stays' queries
+    float* os = reinterpret_cast<float*>(qs + 2 * kRows * D * sizeof(E));  // the warps' sums, by part and row
+    float* ws = os + kRows * D + warp * 2 * KV;                            // the warp's weights [2][KV]
+    const float none = __uint_as_float(0xFF800000u);
 
-    attn_edges<E>(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
+    constexpr int NG = KV == 64 ? 1 : 2;  // tiles of 64 positions have rows of 128 columns at most
+    // for the product with V a warp's lanes are PG groups of W lanes, a lane a
+    // column of four, and every group takes its share of the positions
+    const int lw = D4 <= 8 ? 3 : D4 <= 16 ? 4 : 5, W = 1 << lw, PG = 32 >> lw, pg = lane >> lw, vc = lane & (W - 1);
+    int col[NG];  // (lanes without a column go along with the last)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) col[g] = 4 * min(vc + 32 * g, D4 - 1);
+    const int lv = 32 - __clz(D * (int)sizeof(E) / 16 - 1);
+
     asm volatile("griddepcontrol.launch_dependents;");
-    const AttnCut cut = attn_locate<KV, kExtra, NT>(p, &scan);
-    if (tid == 0) attn_join<KV, kExtra>(p, scan, cut);
-    AttnWalk<KV, kExtra> walk(scan, cut);
-    AttnStay sq;
-    while (walk.next(p, &sq)) {
-        const int b = sq.b, h = sq.h, first = sq.first, last = sq.last, row_base = sq.row0, rows = sq.rows;
-        const long long len = (long long)sq.L + sq.n;
+    const AttnCut cut = attn_locate<KV, NT>(p, &scan);
+    AttnWalk<KV> walk(scan, cut);
 
-        // queries, in octaves of the score
-        const E* q = reinterpret_cast<const E*>(p.q);
-        for (int i = tid; i < rows * D4; i += NT) {
-            const int r = i / D4, c = i - r * D4, node = (row_base + r) / p.G, g = (row_base + r) % p.G;
-            const E* src = q + (((long long)b * p.N + node) * (p.Hkv * p.G) + h * p.G + g) * D + c * 4;
-            float4 x = lds4<E>(reinterpret_cast<const unsigned char*>(src));
-            *reinterpret_cast<float4*>(qs + r * D + c * 4) =
-                make_float4(x.x * p.c2, x.y * p.c2, x.z * p.c2, x.w * p.c2);
+    // One flat sequence of tiles, whatever stays they belong to: a tile's copies
+    // go out, then the one before it is worked on.
+    AttnStay sq = {}, next = {};  // that of the tile worked on, of the tile copied
+    int tile = 0, ahead = 0;      // of sq, of next
+    bool bad, next_bad = false, have = false, more = true;
+    // A row's weights are 2^(s - ref), ref the maximum so far, raised only where a
+    // score lies more than 8 octaves above it (fp32 sums scale without loss); a
+    // lane's l is the sum of its own positions' weights.
+    float ref[2], l[2];
+    Two acc[2][NG];
+#pragma unroll 1
+    for (int st = 0, qb = 0; more; st ^= 1) {
+        const bool fresh = ahead >= next.last;
+        bad = next_bad;
+        if (fresh) {
+            more = walk.next(p, &next);
+            ahead = next.first;
+            next_bad = false;
         }
-        bool bad = load_tile<E, KV>(p, b, h, (long long)first * KV, len, ks, vs);
-
-        const int r0 = warp * 2;
-        float m[2], l[2];
-        float4 acc[2][2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            m[r] = __uint_as_float(0xFF800000u);
-            l[r] = 0.f;
-            acc[r][0] = acc[r][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        for (int tile = first; tile < last; ++tile) {
-            const int st = (tile - first) & 1;
-            if (tile + 1 < last) {
-                bad |= load_tile<E, KV>(p, b, h, (long long)(tile + 1) * KV, len, ks + (st ^ 1) * KV * kstride,
-                                    vs + (size_t)(st ^ 1) * KV * D * sizeof(E));
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
-            } else {
-                asm volatile("cp.async.wait_group 0;" ::: "memory");
-            }
-            __syncthreads();
-            if (r0 < rows) {
-                const unsigned char* kt0 = ks + st * KV * kstride;
-                const unsigned char* vt0 = vs + (size_t)st * KV * D * sizeof(E);
-                float s[2][J] = {};
-                const float* q0 = qs + r0 * D;
-                const float* q1 = r0 + 1 < rows ? q0 + D : q0;
-                for (int c = 0; c < D4; ++c) {
-                    const float4 a0 = *reinterpret_cast<const float4*>(q0 + c * 4);
-                    const float4 a1 = *reinterpret_cast<const float4*>(q1 + c * 4);
-#pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        const float4 x = lds4<E>(kt0 + (lane + 32 * j) * kstride + c * 4 * sizeof(E));
-                        s[0][j] = fmaf(a0.x, x.x, fmaf(a0.y, x.y, fmaf(a0.z, x.z, fmaf(a0.w, x.w, s[0][j]))));
-                        s[1][j] = fmaf(a1.x, x.x, fmaf(a1.y, x.y, fmaf(a1.z, x.z, fmaf(a1.w, x.w, s[1][j]))));
-                    }
+        if (more) {
+            next_bad |= load_tile<E, KV>(p, next, ahead, smem_addr(ks) + st * KV * kstride,
+                                         smem_addr(vs) + st * KV * D * (int)sizeof(E), lv);
+            if (fresh) {
+                const int vec = D * (int)sizeof(E) / 16;
+                const E* q = static_cast<const E*>(p.q);
+#pragma unroll 1
+                for (int i = tid; i < next.rows * vec; i += NT) {
+                    const int r = i / vec, c = i - r * vec, node = (next.row0 + r) / p.G, g = (next.row0 + r) - node * p.G;
+                    const long long row = ((long long)next.b * p.N + node) * (p.Hkv * p.G) + next.h * p.G + g;
+                    cp16(smem_addr(qs) + ((qb ^ 1) * kRows * vec + i) * 16, q + row * D + c * (16 / (int)sizeof(E)), 16);
                 }
-                const long long pos0 = (long long)tile * KV;
-                const bool tail = pos0 + KV > sq.L;
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (!have) {  // while the first tile is on its way
+            if (tid == 0) attn_join<KV>(p, scan, cut);
+            attn_edges<E>(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
+        } else {
+            const int rows = sq.rows, sd = st ^ 1;
+            // pairs of rows, rounded up to 2^lg; a tile's positions shared out over 8 >> lg warps, P each
+            const int lg = rows <= 2 ? 0 : 32 - __clz((rows - 1) >> 1), part = warp >> lg, r0 = 2 * (warp - (part << lg));
+            const int lp = (KV == 64 ? 3 : 2) + lg, P = 1 << lp, LP = max(1, 32 >> lp), pos_l = lane & (P - 1), dq = lane >> lp;
+            if (tile == sq.first) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int node = (row_base + min(r0 + r, rows - 1)) / p.G;
-                    if (tail) {
+                    ref[r] = none;
+                    l[r] = 0.f;
+                    for (int g = 0; g < NG; ++g) acc[r][g] = Two{0ull, 0ull};
+                }
+            }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            const long long pos0 = (long long)tile * KV + part * P;
+            if (r0 < rows && pos0 < sq.len) {
+                const unsigned char* k0 = ks + (sd * KV + part * P + pos_l) * kstride;
+                const unsigned char* vt0 = vs + ((size_t)(sd * KV + part * P) * D) * sizeof(E);
+                const unsigned char* q0 = qs + (qb * kRows + r0) * D * sizeof(E);
+                const unsigned char* q1 = r0 + 1 < rows ? q0 + D * sizeof(E) : q0;
+                const bool two = KV == 64 && P == 64;
+                uint64_t d[2][2] = {};  // even and odd columns' sums
+                auto dot = [&](int j, uint64_t& d0, uint64_t& d1, int c) {
+                    const Two a0 = lds4x2<E>(q0 + c * 4 * sizeof(E)), a1 = lds4x2<E>(q1 + c * 4 * sizeof(E));
+                    const Two x = lds4x2<E>(k0 + j * 32 * kstride + c * 4 * sizeof(E));
+                    d0 = fma2(a0.a, x.a, fma2(a0.b, x.b, d0));
+                    d1 = fma2(a1.a, x.a, fma2(a1.b, x.b, d1));
+                };
+                if (two) {
+#pragma unroll 4
+                    for (int c = 0; c < D4; ++c) {
+                        dot(0, d[0][0], d[1][0], c);
+                        dot(1, d[0][1], d[1][1], c);
+                    }
+                } else {
+#pragma unroll 4
+                    for (int c = dq; c < D4; c += LP) dot(0, d[0][0], d[1][0], c);
+                }
+                float s[2][2];
 #pragma unroll
-                        for (int j = 0; j < J; ++j) {
-                            const long long nd = pos0 + lane + 32 * j - sq.L;
-                            const bool see = nd < 0 || (nd < sq.n && (p.mask ? __ldg(p.mask + ((long long)b * p.N + node) * p.N + nd) != 0
-                                                                             : nd <= node));
-                            if (!see) s[r][j] = __uint_as_float(0xFF800000u);
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) s[r][j] = lo2(d[r][j]) + hi2(d[r][j]);
+                for (int o = P; o < 32; o <<= 1) {
+                    s[0][0] += __shfl_xor_sync(0xFFFFFFFFu, s[0][0], o);
+                    s[1][0] += __shfl_xor_sync(0xFFFFFFFFu, s[1][0], o);
+                }
+                const int ctx = (int)min((long long)P, sq.L - pos0);  // of these positions
+                const bool tail = ctx < P;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    s[r][0] *= p.c2;
+                    s[r][1] *= p.c2;
+                    if (tail) {
+                        const int node = (sq.row0 + min(r0 + r, rows - 1)) / p.G;
+                        const uint8_t* mask = p.mask ? p.mask + ((long long)sq.b * p.N + node) * p.N : nullptr;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int nd = pos_l + 32 * j - ctx;
+                            if (nd >= 0 && (nd >= sq.n || (mask ? __ldg(mask + nd) == 0 : nd > node))) s[r][j] = none;
                         }
                     }
-                    // a NaN score makes the row NaN (fmaxf drops it, the exponential keeps it)
-                    const float mn = fmaxf(m[r], warp_max(J == 2 ? fmaxf(s[r][0], s[r][J - 1]) : s[r][0]));
-                    const float ref = mn == __uint_as_float(0xFF800000u) ? 0.f : mn;
-                    const float f = ex2(m[r] - ref);
-                    float sum = 0.f;
+                    if (!two) s[r][1] = none;
+                    // (a NaN score raises nothing and makes the row NaN)
+                    const float top = fmaxf(s[r][0], s[r][1]);
+                    if (__any_sync(0xFFFFFFFFu, top > ref[r] + 8.f)) {
+                        const float to = fmaxf(ref[r], warp_max(top)), f = ex2(ref[r] - to);
+                        ref[r] = to;
+                        l[r] *= f;
 #pragma unroll
-                    for (int j = 0; j < J; ++j) {
-                        const float w = ex2(s[r][j] - ref);
-                        ws[r * KV + 32 * j + lane] = w;
-                        sum += w;
+                        for (int g = 0; g < NG; ++g) acc[r][g] = mul2(f, acc[r][g]);
                     }
-                    l[r] = l[r] * f + warp_sum(sum);
-                    m[r] = mn;
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        acc[r][g].x *= f;
-                        acc[r][g].y *= f;
-                        acc[r][g].z *= f;
-                        acc[r][g].w *= f;
-                    }
+                    const float base = ref[r] == none ? 0.f : ref[r];
+                    const float w0 = ex2(s[r][0] - base), w1 = ex2(s[r][1] - base);
+                    ws[r * KV + pos_l] = w0;  // (lanes of one position write the same)
+                    if (two) ws[r * KV + pos_l + 32] = w1;
+                    l[r] += w0 + w1;
                 }
                 __syncwarp();
+                if (!tail) {
+#pragma unroll 2
+                    for (int t2 = 4 * pg; t2 < P; t2 += 4 * PG) {
+                        const float4 w0 = *reinterpret_cast<const float4*>(ws + t2);
+                        const float4 w1 = *reinterpret_cast<const float4*>(ws + KV + t2);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int c = lane + 32 * g;
-                    if (c < D4) {
-                        if (!tail) {
-#pragma unroll 8
-                            for (int t2 = 0; t2 < KV; ++t2) {
-                                const float4 x = lds4<E>(vt0 + ((size_t)t2 * D + c * 4) * sizeof(E));
-                                acc[0][g] = fma4(ws[t2], x, acc[0][g]);
-                                acc[1][g] = fma4(ws[KV + t2], x, acc[1][g]);
+                        for (int g = 0; g < NG; ++g) {
+                            const unsigned char* v = vt0 + (t2 * D + col[g]) * sizeof(E);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const Two x = lds4x2<E>(v + e * D * sizeof(E));
+                                const float a = e == 0 ? w0.x : e == 1 ? w0.y : e == 2 ? w0.z : w0.w;
+                                const float b = e == 0 ? w1.x : e == 1 ? w1.y : e == 2 ? w1.z : w1.w;
+                                acc[0][g] = axpy2(pack2(a, a), x, acc[0][g]);
+                                acc[1][g] = axpy2(pack2(b, b), x, acc[1][g]);
                             }
-                        } else {
-                            // an unseen node's values may be anything: a zero weight leaves them out
-                            for (int t2 = 0; t2 < KV; ++t2) {
-                                const float4 x = lds4<E>(vt0 + ((size_t)t2 * D + c * 4) * sizeof(E));
-                                const float w0 = ws[t2], w1 = ws[KV + t2];
-                                if (w0 != 0.f) acc[0][g] = fma4(w0, x, acc[0][g]);
-                                if (w1 != 0.f) acc[1][g] = fma4(w1, x, acc[1][g]);
-                            }
+                        }
+                    }
+                } else {
+                    // an unseen node's values may be anything: a zero weight leaves them out
+                    const Two zero = {0ull, 0ull};
+#pragma unroll 2
+                    for (int t2 = pg; t2 < P; t2 += PG) {
+                        const float w0 = ws[t2], w1 = ws[KV + t2];
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const Two x = lds4x2<E>(vt0 + (t2 * D + col[g]) * sizeof(E));
+                            acc[0][g] = axpy2(pack2(w0, w0), w0 != 0.f ? x : zero, acc[0][g]);
+                            acc[1][g] = axpy2(pack2(w1, w1), w1 != 0.f ? x : zero, acc[1][g]);
                         }
                     }
                 }
                 __syncwarp();
             }
             __syncthreads();
-        }
-        bad = __syncthreads_or(bad);
-        const bool whole = sq.whole;
-        const int slot = sq.slot;
+            if (tile + 1 == sq.last) {
+                if (r0 < rows) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if (r0 + r >= rows) break;
-            if (bad) l[r] = __uint_as_float(0x7FC00000u);
-            const int node = (row_base + r0 + r) / p.G, head = h * p.G + (row_base + r0 + r) % p.G;
-            const long long row = ((long long)b * p.N + node) * (p.Hkv * p.G) + head;
-            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+                    for (int r = 0; r < 2; ++r) {
+                        const int at = (part << (lg + 1)) + r0 + r;
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const int c = lane + 32 * g;
-                if (c >= D4) break;
-                if (whole) {
-                    const float4 o = make_float4(acc[r][g].x * inv, acc[r][g].y * inv, acc[r][g].z * inv,
-                                                 acc[r][g].w * inv);
-                    if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
-                        store4<E>(reinterpret_cast<E*>(p.out) + row * D + c * 4, o);
-                } else {
-                    *reinterpret_cast<float4*>(p.part_o + ((long long)slot * kRows + r0 + r) * D + c * 4) = acc[r][g];
+                        for (int g = 0; g < NG; ++g) {
+                            float4 a = make_float4(lo2(acc[r][g].a), hi2(acc[r][g].a), lo2(acc[r][g].b), hi2(acc[r][g].b));
+#pragma unroll 1
+                            for (int o = W; o < 32; o <<= 1) {
+                                a.x += __shfl_xor_sync(0xFFFFFFFFu, a.x, o);
+                                a.y += __shfl_xor_sync(0xFFFFFFFFu, a.y, o);
+                                a.z += __shfl_xor_sync(0xFFFFFFFFu, a.z, o);
+                                a.w += __shfl_xor_sync(0xFFFFFFFFu, a.w, o);
+                            }
+                            if (pg == 0 && vc + 32 * g < D4) *reinterpret_cast<float4*>(os + at * D + (vc + 32 * g) * 4) = a;
+                        }
+                        const float sum = warp_sum(lane < P ? l[r] : 0.f);
+                        if (lane == 0) sums[at] = make_float2(ref[r], sum);
+                    }
+                }
+                bad = __syncthreads_or(bad);
+#pragma unroll 1
+                for (int i = tid; i < rows * D4; i += NT) {
+                    const int r = i / D4, c = i - r * D4;
+                    float mr = none, lr = 0.f;
+#pragma unroll 1
+                    for (int at = r; at < kRows; at += 2 << lg) mr = fmaxf(mr, sums[at].x);
+                    const float ref = mr == none ? 0.f : mr;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+                    for (int at = r; at < kRows; at += 2 << lg) {
+                        const float f = ex2(sums[at].x - ref);
+                        lr += sums[at].y * f;
+                        o = fma4(f, *reinterpret_cast<const float4*>(os + at * D + c * 4), o);
+                    }
+                    if (bad) lr = __uint_as_float(0x7FC00000u);
+                    const int node = (sq.row0 + r) / p.G, head = sq.h * p.G + (sq.row0 + r) - node * p.G;
+                    const long long row = ((long long)sq.b * p.N + node) * (p.Hkv * p.G) + head;
+                    if (sq.whole) {
+                        const float inv = lr == 0.f ? 0.f : 1.f / lr;
+                        if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
+                            store4<E>(reinterpret_cast<E*>(p.out) + row * D + c * 4,
+                                      make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+                        if (c == 0 && p.lse) p.lse[row] = lse_of(mr, lr);
+                    } else {
+                        const long long at = (long long)sq.slot * kRows + r;
+                        *reinterpret_cast<float4*>(p.part_o + at * D + c * 4) = o;
+                        if (c == 0) p.part_ml[at] = make_float2(mr, lr);
+                    }
                 }
             }
-            if (lane == 0) {
-                if (!whole)
-                    p.part_ml[(long long)slot * kRows + r0 + r] = make_float2(m[r], l[r]);
-                else if (p.lse)
-                    p.lse[row] = lse_of(m[r], l[r]);
-            }
         }
+        if (fresh) {
+            sq = next;
+            tile = next.first;
+            qb ^= 1;
+        } else {
+            ++tile;
+        }
+        ++ahead;
+        have = true;
     }
 }
 
@@ -290,12 +417,14 @@ __global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constan
         const int r = warp;
         float2 ml = none;
         float m = none.x, l = 0.f;
+#pragma unroll 1
         for (int i = lane; i < pieces; i += 32) {
             ml = __ldcg(p.part_ml + at(i, r));
             m = fmaxf(m, ml.x);
         }
         m = warp_max(m);
         const float ref = m == none.x ? 0.f : m;
+#pragma unroll 1
         for (int i = lane; i < pieces; i += 32) {
             if (pieces > 32) ml = __ldcg(p.part_ml + at(i, r));
             l += ex2(ml.x - ref) * ml.y;
@@ -312,9 +441,11 @@ __global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constan
         }
     }
     __syncthreads();
+#pragma unroll 1
     for (int j = tid; j < rows * D4; j += kJoinNT) {
         const int r = j / D4, d = (j - r * D4) * 4;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
         for (int i0 = 0; i0 < pieces; i0 += 8) {
             if (i0 || j != tid) load(i0, r, d);
 #pragma unroll
@@ -394,18 +525,21 @@ cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan
 
 int attention_simt_rows() { return kRows; }
 
-int attention_simt_kv(int dtype, int D) { return dtype == 0 && D > 128 ? 32 : 64; }
+int attention_simt_extra() { return kExtra; }
+
+int attention_simt_kv(int dtype, int D) { return D * (dtype == 0 ? 4 : 2) > 256 ? 32 : 64; }
 
 cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st) {
-    if (dtype != 0) return launch_simt<bf16_t, 64>(p, plan, st);
+    if (dtype != 0) return plan.kv == 64 ? launch_simt<bf16_t, 64>(p, plan, st) : launch_simt<bf16_t, 32>(p, plan, st);
     return plan.kv == 64 ? launch_simt<float, 64>(p, plan, st) : launch_simt<float, 32>(p, plan, st);
 }
 
-// CTAs of an SM: what its shared memory holds, four at most.
+// CTAs of an SM: what its shared memory and its registers hold.
 int attention_simt_ctas(int dtype, int D) {
-    const size_t smem = dtype != 0 ? simt_smem<bf16_t, 64>(D)
-                        : attention_simt_kv(dtype, D) == 64 ? simt_smem<float, 64>(D) : simt_smem<float, 32>(D);
-    return (int)std::max<size_t>(1, std::min<size_t>(4, (size_t)227 * 1024 / (smem + 2048)));
+    const bool wide = attention_simt_kv(dtype, D) == 64;
+    const size_t smem = dtype != 0 ? (wide ? simt_smem<bf16_t, 64>(D) : simt_smem<bf16_t, 32>(D))
+                                   : (wide ? simt_smem<float, 64>(D) : simt_smem<float, 32>(D));
+    return (int)std::max<size_t>(1, std::min<size_t>(2, (size_t)227 * 1024 / (smem + 2048)));
 }
 
 SV_DEBUG_READER(attention)

@@ -14,7 +14,7 @@
 // the kKv-position tiles of L + n positions. All units' tiles in order form
 // one range that is cut into equal parts, one a CTA, whatever the lengths
 // are (they are known on the device only). In the range a unit counts a few
-// tiles more than it has (EX, before its tiles), for what its start and end
+// tiles more than it has (`extra`, before its tiles), for what its start and end
 // cost; a cut that falls among these is moved to the unit's start. A unit inside one part is finished
 // by its CTA; the others leave partial results (unnormalised sums with their
 // running maximum and sum) that the combine kernel joins in range order, so
@@ -45,6 +45,7 @@ struct AttnParams {
     const int32_t* n_nodes;    // [B] or null (N)
     int B, N, Hkv, G, D, num_pages, max_pages, page_shift;
     int tile_rows;       // rows of a row tile
+    int extra;           // tiles that a unit's start and end count for
     float c2;            // scale * log2(e): scores in octaves
     void* out;           // [B, N, Hkv * G, D]
     float* lse;          // [B, N, Hkv * G] or null
@@ -76,10 +77,10 @@ SV_DEV int attn_row_tiles(const AttnParams& p, const AttnSeq& s) {
     return s.n > 0 ? (s.n * p.G + p.tile_rows - 1) / p.tile_rows : 0;
 }
 
-template <int KV, int EX>
+template <int KV>
 SV_DEV long long attn_seq_work(const AttnParams& p, int b) {
     const AttnSeq s = attn_seq(p, b);
-    return s.n > 0 ? (long long)(attn_kv_tiles<KV>(s) + EX) * attn_row_tiles(p, s) * p.Hkv : 0;
+    return s.n > 0 ? (long long)(attn_kv_tiles<KV>(s) + p.extra) * attn_row_tiles(p, s) * p.Hkv : 0;
 }
 
 // Where tile `at` of the whole range lies: its sequence and that sequence's
@@ -105,13 +106,14 @@ struct AttnCut {
 // Called by all NT threads of a block: the cut range, and in sc->place where
 // this CTA's part begins (if it has one). Each thread sums a run of sequences,
 // one scan orders the runs.
-template <int KV, int EX, int NT>
+template <int KV, int NT>
 SV_DEV AttnCut attn_locate(const AttnParams& p, AttnScan* sc) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (p.B + NT - 1) / NT;
     const int b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += attn_seq_work<KV, EX>(p, b);
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) mine += attn_seq_work<KV>(p, b);
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -135,8 +137,9 @@ SV_DEV AttnCut attn_locate(const AttnParams& p, AttnScan* sc) {
     const long long at = (int)blockIdx.x < cut.parts ? cut.at(blockIdx.x) : -1;
     if (at >= lo && at < lo + mine) {
         long long base = lo;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
-            const long long w = attn_seq_work<KV, EX>(p, b);
+            const long long w = attn_seq_work<KV>(p, b);
             if (at < base + w) {
                 sc->place = AttnPlace{b, base};
                 break;
@@ -156,7 +159,7 @@ struct AttnStay {
 };
 
 // Walks this CTA's part of the range.
-template <int KV, int EX>
+template <int KV>
 struct AttnWalk {
     long long t, end, base;
     int b, stays;
@@ -170,21 +173,23 @@ struct AttnWalk {
 
     // (a sequence's own part of the range is below 2^31)
     SV_DEV bool next(const AttnParams& p, AttnStay* s) {
+#pragma unroll 1
         while (t < end) {
             AttnSeq q = attn_seq(p, b);
             int kt = attn_kv_tiles<KV>(q), rt = attn_row_tiles(p, q);
-            while (q.n <= 0 || t >= base + (long long)(kt + EX) * rt * p.Hkv) {
-                if (q.n > 0) base += (long long)(kt + EX) * rt * p.Hkv;
+#pragma unroll 1
+            while (q.n <= 0 || t >= base + (long long)(kt + p.extra) * rt * p.Hkv) {
+                if (q.n > 0) base += (long long)(kt + p.extra) * rt * p.Hkv;
                 q = attn_seq(p, ++b);
                 kt = attn_kv_tiles<KV>(q);
                 rt = attn_row_tiles(p, q);
             }
-            const uint32_t in = (uint32_t)(t - base), unit = in / (uint32_t)(kt + EX);
-            const int from = (int)(in - unit * (uint32_t)(kt + EX));
-            const int to = (int)min((long long)(kt + EX), from + (end - t));
+            const uint32_t in = (uint32_t)(t - base), unit = in / (uint32_t)(kt + p.extra);
+            const int from = (int)(in - unit * (uint32_t)(kt + p.extra));
+            const int to = (int)min((long long)(kt + p.extra), from + (end - t));
             t += to - from;
-            s->first = max(0, from - EX);
-            s->last = max(0, to - EX);
+            s->first = max(0, from - p.extra);
+            s->last = max(0, to - p.extra);
             if (s->first == s->last) continue;
             s->b = b;
             s->kt = kt;
@@ -205,7 +210,7 @@ struct AttnWalk {
 
 // This CTA's entry of p.joins (one thread): its part begins inside a unit that
 // the part before it has the first piece of.
-template <int KV, int EX>
+template <int KV>
 SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, const AttnCut& cut) {
     AttnJoin j = {};
     const int c = blockIdx.x;
@@ -213,15 +218,16 @@ SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, const AttnCut& cu
         const AttnSeq q = attn_seq(p, sc.place.b);
         const int kt = attn_kv_tiles<KV>(q), rt = attn_row_tiles(p, q);
         const long long at = cut.at(c), before = cut.at(c - 1);
-        const uint32_t unit = (uint32_t)(at - sc.place.base) / (uint32_t)(kt + EX);
-        const long long start = sc.place.base + (long long)unit * (kt + EX), stop = start + kt + EX;
-        if (at > start + EX && before <= start + EX) {
+        const uint32_t unit = (uint32_t)(at - sc.place.base) / (uint32_t)(kt + p.extra);
+        const long long start = sc.place.base + (long long)unit * (kt + p.extra), stop = start + kt + p.extra;
+        if (at > start + p.extra && before <= start + p.extra) {
             j.b = sc.place.b;
             j.h = (int)(unit / (uint32_t)rt);
             j.row0 = (int)(unit - (uint32_t)j.h * rt) * p.tile_rows;
             j.rows = min(p.tile_rows, q.n * p.G - j.row0);
             j.slot0 = 2 * (c - 1) + (before < start);
             j.first = j.last = c;
+#pragma unroll 1
             while (j.last + 1 < cut.parts && cut.at(j.last + 1) < stop) ++j.last;
         }
     }
@@ -236,12 +242,14 @@ SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, const AttnCut& cu
 template <typename E>
 SV_DEV void attn_edges(const AttnParams& p, int gw, int warps) {
     const int lane = threadIdx.x & 31, team = max(1, warps / p.B), member = gw % team;
+#pragma unroll 1
     for (int b = gw / team; b < p.B; b += (warps + team - 1) / team) {
         const AttnSeq s = attn_seq(p, b);
         if (p.status && member == 0) {
             bool bad = s.n < 0;
             if (s.n > 0) {
                 const int pages = (int)(((long long)s.L + s.n + (1 << p.page_shift) - 1) >> p.page_shift);
+#pragma unroll 1
                 for (int i = lane; i < pages; i += 32) {
                     const int id = __ldg(p.table + b * p.table_stride + i);
                     bad |= id < 0 || id >= p.num_pages;
@@ -255,8 +263,10 @@ SV_DEV void attn_edges(const AttnParams& p, int gw, int warps) {
         const long long words = rows * p.D * (long long)sizeof(E) / 16;
         const uint32_t fill = s.n < 0 ? (sizeof(E) == 4 ? 0x7FC00000u : 0x7FC07FC0u) : 0u;
         uint4* o = reinterpret_cast<uint4*>(reinterpret_cast<E*>(p.out) + row0 * p.D);
+#pragma unroll 1
         for (long long i = member * 32 + lane; i < words; i += team * 32) o[i] = make_uint4(fill, fill, fill, fill);
         if (p.lse)
+#pragma unroll 1
             for (long long i = member * 32 + lane; i < rows; i += team * 32)
                 p.lse[row0 + i] = __uint_as_float(s.n < 0 ? 0x7FC00000u : 0xFF800000u);
     }
@@ -285,6 +295,7 @@ SV_DEV void store4<bf16_t>(bf16_t* dst, float4 x) {
 // Host side.
 struct AttnPlan {
     int grid, rows, kv;   // CTAs of the main kernel, rows of a tile, positions of a tile
+    int extra;            // AttnParams::extra
     size_t part_o, part_ml, joins, total;  // workspace layout
 };
 
@@ -295,6 +306,7 @@ cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan
 int attention_simt_rows();
 int attention_simt_kv(int dtype, int D);
 int attention_simt_ctas(int dtype, int D);
+int attention_simt_extra();
 // The tensor-core kernel (bf16, D 64 or 128) reads K, V and Q through tensor
 // maps; attention_tc_maps: false where the cache's strides have none.
 struct alignas(64) AttnMaps {
@@ -302,6 +314,7 @@ struct alignas(64) AttnMaps {
 };
 int attention_tc_rows(int group);
 int attention_tc_kv();
+int attention_tc_extra(int group, int N);
 bool attention_tc_maps(const AttnParams& p, AttnMaps* m);
 cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const AttnMaps& m, cudaStream_t st);
 cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);

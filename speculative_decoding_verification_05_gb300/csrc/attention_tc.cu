@@ -63,6 +63,7 @@ constexpr int NT = 384;
 constexpr int kGroupRegs = 208, kOtherRegs = 88;
 constexpr int kKv = 128;     // positions of a tile
 constexpr int kMaxStages = 10;
+constexpr int kExtra = 3, kExtraDual = 6;
 constexpr float kHeavy = 4.f;  // octaves below a row's sum so far from which a weight is heavy
 constexpr float kSlack = 8.f;  // octaves of the running maximum above the reference that raise it
 constexpr float kJump = 64.f;  // of a half's own scores above it
@@ -82,11 +83,10 @@ struct Seg : AttnStay {
     bool dual;
     int steps;  // softmax tiles of both streams together
 };
-constexpr int kExtra = 3;  // tiles that a unit's start and end count for (attention.cuh)
-struct Walk : AttnWalk<kKv, kExtra> {
-    using AttnWalk<kKv, kExtra>::AttnWalk;
+struct Walk : AttnWalk<kKv> {
+    using AttnWalk<kKv>::AttnWalk;
     SV_DEV bool next(const AttnParams& p, Seg* s) {
-        if (!AttnWalk<kKv, kExtra>::next(p, s)) return false;
+        if (!AttnWalk<kKv>::next(p, s)) return false;
         s->dual = s->rows > p.tile_rows / 2;
         s->steps = (s->last - s->first) * (s->dual ? 2 : 1);
         return true;
@@ -111,7 +111,6 @@ static_assert(sizeof(Ctl) <= 2048, "control region");
 // Order of a segment's tiles in the ring (cnt tiles): the order of their first
 // use. Two streams on the same tiles: K0 V0 K1 V1 ..; on alternate tiles: K0
 // K1 V0 K2 V1 K3 ..
-SV_DEV int ring_k(const Seg& s, int i) { return s.dual ? 2 * i : i + max(0, i - 1); }
 SV_DEV int ring_v(const Seg& s, int i) { return s.dual ? 2 * i + 1 : i + min(i + 2, s.last - s.first); }
 
 // Whether tile i of a segment reaches past the context; the stages that the V
@@ -833,7 +832,7 @@ __global__ void __launch_bounds__(NT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     asm volatile("griddepcontrol.launch_dependents;");
-    const AttnCut cut = attn_locate<kKv, kExtra, NT>(p, &c->scan);
+    const AttnCut cut = attn_locate<kKv, NT>(p, &c->scan);
     Walk walk(c->scan, cut);
 
     if (tid == 0) {
@@ -884,7 +883,7 @@ __global__ void __launch_bounds__(NT, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) produce<D>(p, c, &mk, &mv, stages);
         if (warp == 10) {
-            if (lane == 0) attn_join<kKv, kExtra>(p, c->scan, cut);
+            if (lane == 0) attn_join<kKv>(p, c->scan, cut);
             __syncwarp();
             attn_edges<bf16_t>(p, blockIdx.x, gridDim.x);
         }
@@ -963,6 +962,10 @@ cudaError_t launch_tc(const AttnParams& p, const AttnPlan& plan, const CUtensorM
 }  // namespace
 
 // Two halves of whole nodes, 128 rows at most each.
+// What a unit's start and end cost, in tiles: more where both streams go over
+// the same tiles and each row block is finished by its own group.
+int attention_tc_extra(int group, int N) { return N * group > attention_tc_rows(group) / 2 ? kExtraDual : kExtra; }
+
 int attention_tc_rows(int group) { return 2 * (128 / group) * group; }
 int attention_tc_kv() { return kKv; }
 

@@ -92,14 +92,16 @@ sv::AttnPlan simt_plan(int D, spec_dtype dtype) {
     a.rows = sv::attention_simt_rows();
     a.kv = sv::attention_simt_kv(dt, D);
     a.grid = kSms * sv::attention_simt_ctas(dt, D);
+    a.extra = sv::attention_simt_extra();
     return attention_layout(a, D);
 }
 
-sv::AttnPlan tc_plan(int D, int group) {
+sv::AttnPlan tc_plan(int D, int group, int N) {
     sv::AttnPlan a = {};
     a.rows = sv::attention_tc_rows(group);
     a.kv = sv::attention_tc_kv();
     a.grid = kSms;
+    a.extra = sv::attention_tc_extra(group, N);
     return attention_layout(a, D);
 }
 
@@ -107,7 +109,7 @@ bool tc_shape(int D, spec_dtype dtype) { return dtype == SPEC_BF16 && (D == 64 |
 
 size_t attention_bytes(int D, int group, spec_dtype dtype) {
     const size_t simt = simt_plan(D, dtype).total;
-    return tc_shape(D, dtype) ? std::max(simt, tc_plan(D, group).total) : simt;
+    return tc_shape(D, dtype) ? std::max(simt, tc_plan(D, group, 1).total) : simt;
 }
 
 bool attention_shape_ok(int B, int N, int q_heads, int kv_heads, int D) {
@@ -168,6 +170,7 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     auto use = [&](const sv::AttnPlan& plan) {
         p.tile_rows = plan.rows;
+        p.extra = plan.extra;
         p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);
         p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.part_ml);
         p.joins = reinterpret_cast<sv::AttnJoin*>(static_cast<char*>(workspace) + plan.joins);
@@ -175,7 +178,7 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
     sv::AttnMaps maps;
     // (that kernel takes the maximum before the scale: it has to be positive)
     if (tc_shape(p.D, dtype) && scale > 0.f && sv::attention_tc_maps(p, &maps)) {
-        const sv::AttnPlan plan = tc_plan(p.D, p.G);
+        const sv::AttnPlan plan = tc_plan(p.D, p.G, N);
         use(plan);
         return done(sv::launch_attention_tc(p, plan, maps, st));
     }
