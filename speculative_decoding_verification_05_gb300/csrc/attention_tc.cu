@@ -174,32 +174,42 @@ SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CU
         const int cnt = s.last - s.first, ahead = s.dual ? 1 : 2, h = s.h;
         const long long len = s.len, pos0 = (long long)s.first * kKv + pg * ps;
         const int32_t* table = p.table + s.b * p.table_stride;
-        // V(i), then K(i + ahead); K alone before the first V
-#pragma unroll 1
-        for (int e = -2 * ahead; ok && e < 2 * cnt; ++e) {
-            const int i = (e >> 1) + (e & 1 ? ahead : 0);
-            if (i < 0 || i >= cnt || (e < 0 && !(e & 1))) continue;
+        auto look = [&](int i) {  // this lane's page of tile i
             const long long pos = pos0 + (long long)i * kKv;
-            int id = -1;
-            if (pg < pages && pos < len) {
-                id = __ldg(table + (pos >> p.page_shift));
-                if (id < 0 || id >= p.num_pages) {
-                    id = -1;
-                    atomicOr(&c->flags[seg & 3], 2);
-                }
+            return pg < pages && i >= 0 && i < cnt && pos < len ? __ldg(table + (pos >> p.page_shift)) : -1;
+        };
+        auto entry = [&](int id, int i, const CUtensorMap* map) {
+            if (i < 0 || i >= cnt) return;
+            const long long pos = pos0 + (long long)i * kKv;
+            const bool there = pg < pages && pos < len;
+            if (there && (uint32_t)id >= (uint32_t)p.num_pages) {
+                id = -1;
+                atomicOr(&c->flags[seg & 3], 2);
             }
-            const unsigned who = __ballot_sync(0xFFFFFFFFu, id >= 0);
-            if (!(ok = warp_wait(&c->empty[st], free_phase, &c->abort))) break;
+            const unsigned who = __ballot_sync(0xFFFFFFFFu, there && id >= 0);
+            if (!(ok = warp_wait(&c->empty[st], free_phase, &c->abort))) return;
             if (lane == 0) mbar_expect_tx(&c->full[st], __popc(who) * (uint32_t)ps * 128);
             __syncwarp();
-            if (id >= 0)
-                tma_load4(stages + st * Shape<D>::kTile + to, e & 1 ? mk : mv, half * 64, (int)(pos & ps1), h, id,
-                          &c->full[st]);
+            if (there && id >= 0)
+                tma_load4(stages + st * Shape<D>::kTile + to, map, half * 64, (int)(pos & ps1), h, id, &c->full[st]);
             ++ring;
             if (++st == NS) {
                 st = 0;
                 free_phase ^= 1;
             }
+        };
+        // V(i), then K(i + ahead); the pages of four tiles are known or on their way
+        int id0 = -1, id1 = look(1 - ahead), id2 = look(2 - ahead), id3 = look(3 - ahead);
+#pragma unroll 1
+        for (int i = -ahead; ok && i < cnt; ++i) {
+            const int next = look(i + 4);
+#pragma unroll 1
+            for (int k = 0; ok && k < 2; ++k)
+                entry(k == 0 ? id0 : s.dual ? id1 : id2, k == 0 ? i : i + ahead, k == 0 ? mv : mk);
+            id0 = id1;
+            id1 = id2;
+            id2 = id3;
+            id3 = next;
         }
         if (!ok) break;
         ++seg;
