@@ -493,7 +493,7 @@ SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int i, int slot) {
     auto word = [&](int r) { return col + r * 128 + (((ch & 7) ^ (r & 7)) * 16); };
     bool found = false;
     for (int r0 = (int)max(0LL, ctx) + lane / C; r0 < live; r0 += R * U) {
-        uint32_t y[U][4], any = 0;
+        uint32_t y[U][4], zero[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int r = min(r0 + u * R, live - 1);
@@ -504,9 +504,9 @@ SV_DEV void clean_v(Ctl* c, const Seg& s, uint32_t tile_addr, int i, int slot) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)  // an exponent of all ones carries into the sign's place
-                any |= ((y[u][e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-        if (any) {
+            for (int e = 0; e < 4; ++e)  // 0 + 0 x stays 0 unless x is not finite
+                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(zero[e]) : "r"(y[u][e]), "r"(0u));
+        if ((zero[0] | zero[1]) | (zero[2] | zero[3])) {
             found = true;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
