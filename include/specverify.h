@@ -39,10 +39,12 @@
  *    malformed tree; that sequence's outputs are then all -1. -inf alone is
  *    an ordinary zero-probability logit. SPEC_ETIMEOUT: a bounded device
  *    wait gave up. Kernels never wait on other CTAs (every hand-off between
- *    CTAs is a last-arriver counter); only the warps of one CTA of the
- *    shared-memory row path wait on one another (bounded, about a second),
- *    and when one such wait gives up, the rows that CTA had left are
- *    reported with SPEC_ETIMEOUT (outputs -1).
+ *    CTAs is a last-arriver counter or the end of a kernel); only the warps
+ *    of one CTA of the shared-memory row path and of the attention on the
+ *    tensor cores wait on one another (bounded, about a second at the most),
+ *    and when one such wait gives up, what that CTA had left is reported with
+ *    SPEC_ETIMEOUT (rows: outputs -1; attention: the sequences whose outputs
+ *    are incomplete).
  *  - Workspace: a device buffer of at least the size the matching
  *    *_workspace_size() function returns, 256-byte aligned, owned by the
  *    caller. Its content on entry does not matter: each call clears the small
@@ -423,9 +425,11 @@ typedef struct {
  *   lse           [B, N, q_heads] float (NULL allowed); -inf for those
  *   status        [B] SPEC_OK, or SPEC_EDATA for a length, node count or page
  *                 out of range (that sequence's outputs are NaN); NULL allowed
- * Scores, sums and the softmax's statistics are fp32 for both types; bf16
- * weights are rounded to bf16 before they multiply v. What lies in unseen
- * positions (NaN and infinities too) does not reach the outputs.
+ * Scores, sums and the softmax's statistics are fp32 for both types. On the
+ * tensor cores (bf16, head_dim 64 or 128, scale > 0) weights are rounded to
+ * bf16 before they multiply v, but those above a sixteenth of their row's sum
+ * keep 16 bits. What lies in unseen positions (NaN and infinities too) does
+ * not reach the outputs.
  * ---------------------------------------------------------------------- */
 size_t spec_tree_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim, spec_dtype dtype);
 

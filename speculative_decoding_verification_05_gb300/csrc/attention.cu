@@ -388,8 +388,11 @@ __global__ void __launch_bounds__(NT, 2) attn_simt_kernel(const __grid_constant_
 // kJoinRows rows of joins[c]. A warp forms the weights 2^(m_i - max m) / sum of
 // a row's pieces, a lane a piece; every thread adds up four columns of a row,
 // eight pieces in flight (the first eight while the weights are formed). The
-// sums' order is that of the parts. Bound by the latency of dependent loads;
-// the pieces come from L2.
+// sums' order is that of the parts. Bound by the latency of dependent loads
+// (the pieces come from L2): 3.3 us of a call of 8 chains, 12 heads of 64
+// columns, in 151 x 1 blocks that start while the main kernel ends. Rows a
+// block: 8, one a warp for the weights; all columns of a row in one block, so
+// that its weights are formed once.
 constexpr int kJoinRows = 8, kJoinNT = 256;
 
 template <typename E>

@@ -17,7 +17,7 @@
 // tiles more than it has (`extra`, before its tiles), for what its start and end
 // cost; a cut that falls among these is moved to the unit's start. A unit inside one part is finished
 // by its CTA; the others leave partial results (unnormalised sums with their
-// running maximum and sum) that the combine kernel joins in range order, so
+// running maximum and sum) that the join kernel adds up in range order, so
 // results depend on the lengths and the grid alone, never on timing.
 #pragma once
 

@@ -8,8 +8,8 @@
 //              tensor memory, and O += P V with P taken from tensor memory;
 //   helper     (warp 11) walks the part and posts each stay in a unit (a
 //              segment) for the others, brings its queries (while the last
-//              one's results are still being written), clears what V must not
-//              contain, and writes the rows that no unit covers;
+//              one's results are still being written) and clears what V must
+//              not contain (warp 10 first writes the rows that no unit covers);
 //   two groups (warps 0-3, 4-7) of 128 threads, a row each: the softmax between
 //              the two products, and the results.
 // The groups are two streams that the tensor core serves in turn, one's
@@ -34,18 +34,33 @@
 // Weights are formed against a whole-number reference that follows the running
 // maximum with slack (Group::softmax), so O_w is rarely scaled. Statistics and
 // sums are fp32, and the sums l are taken before the weights are rounded to
-// bf16 for the product with
-// V. Where a weight is more than a sixteenth of its row's sum so far, its
+// bf16 for the product with V. Where a weight is more than a sixteenth of its row's sum so far, its
 // rounding would show beside the output's own: steps of 16 positions with such
 // a weight are multiplied a second time with what the rounding took (the
-// residuals, zero elsewhere). Lighter weights' roundings
-// average out, and a long row has few heavy ones.
+// residuals, zero elsewhere). Lighter weights' roundings average out, and a
+// long row has few heavy ones.
 //
 // Tiles that reach past the context also hold nodes and the end: a thread forms
 // its row's visibility bits, and the elements of V there that are not finite
 // are zeroed in shared memory before the product (a zero weight times an
 // infinity would be NaN in rows that do not see the node) and added to the rows
 // that do see them when the results are written.
+
+// What bounds it. One token of 64 sequences, contexts to 8192, 8 key heads of 4
+// query heads, 128 columns: memory (174 us, 6.2 TB/s of K and V). With 64 or
+// more rows the softmax: a warp takes some 400 instructions a half, which at
+// one or two warps a scheduler last 1300 to 1900 cycles, mostly of instruction
+// latency; the tensor pipe is 36 to 50 % busy. 16 trees of 64 nodes, contexts
+// to 1900, 32 heads of one query head (64 rows, half of the product's 128):
+// 83.5 us (3.6 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 112.8 us (0.60
+// PFLOP/s); a tree of 61 nodes over 100003 positions, 8 heads of 4: 106.5 us.
+// Around that a launch takes some 13000 cycles to its first scores (the cut,
+// the first lookup, the first copies) and a unit 4000 to 6000 for its end.
+// Small pages cost copies: an entry of pages of 16 is 16 of them, and heads of
+// 64 columns (16 KB an entry) read 3.7 TB/s at pages of 16, 4.2 at 128. Code
+// size counts too: the warps' paths together are larger than the instruction
+// caches near them, and more unrolling anywhere slowed everything (loops are
+// rolled and paths shared for it).
 
 #include <cuda.h>
 
@@ -971,11 +986,14 @@ cudaError_t launch_tc(const AttnParams& p, const AttnPlan& plan, const CUtensorM
 
 }  // namespace
 
-// Two halves of whole nodes, 128 rows at most each.
 // What a unit's start and end cost, in tiles: more where both streams go over
-// the same tiles and each row block is finished by its own group.
+// the same tiles. Measured with 2, 3 and 5 (32 heads of 64 rows, alternate
+// tiles): 97.2, 89.4, 91.6 us; with 3, 5, 6 and 8 (same tiles): 118.4, 117.5,
+// 116.8, 118.5 (8 heads of 512 rows) and 114.7, 111.9, 110.4, 109.9 (one tree
+// of 244 rows over 100003 positions).
 int attention_tc_extra(int group, int N) { return N * group > attention_tc_rows(group) / 2 ? kExtraDual : kExtra; }
 
+// Two halves of whole nodes, 128 rows at most each.
 int attention_tc_rows(int group) { return 2 * (128 / group) * group; }
 int attention_tc_kv() { return kKv; }
 

@@ -214,6 +214,28 @@ def test_random_history():
         np.testing.assert_array_equal(np.bincount(held, minlength=90), p.refs)
 
 
+@pytest.mark.parametrize("pages", [4095, 4097, 8200, 32771, 70000, 131072])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_free_pages_anywhere_in_a_pool(pages, shift):
+    """The lowest free numbers, wherever they lie: windows and stretches without any, the last page, odd addresses."""
+    rng = np.random.default_rng(pages + shift)
+    free = np.unique(np.concatenate([rng.integers(0, pages, 40), rng.integers(max(0, pages - 50), pages, 9), [pages - 1],
+                                     np.arange(pages // 2, min(pages, pages // 2 + 30))]))
+    refs = np.ones(pages, np.int32)
+    refs[free] = 0
+    store = torch.ones(pages + 1, dtype=torch.int32, device="cuda")
+    dr = store[shift:shift + pages].copy_(torch.from_numpy(refs))
+    for tokens in ([16 * 20, 0, 5, 16 * 30], [16 * len(free), 0, 0, 0], [0, 0, 0, 16 * len(free) + 1], [16, 16, 16 * 39, 16]):
+        table = np.full((4, len(free) + 2), -1, np.int32)
+        dt, r = _dev(table), refs.copy()
+        dr.copy_(torch.from_numpy(refs))
+        want = paged.grow(table, r, [0, 1, 2, 3], tokens, 16)
+        got = sv.cache_resize(dt, dr, None, torch.tensor(tokens, dtype=torch.int32), 16)["status"].tolist()
+        assert got == want
+        np.testing.assert_array_equal(dt.cpu().numpy(), table)
+        np.testing.assert_array_equal(dr.cpu().numpy(), r)
+
+
 def test_large_pool_takes_the_last_pages():
     p = Pool(3, 300, 70001, layers=1, ps=8)
     p.refs[:69000] = 1
