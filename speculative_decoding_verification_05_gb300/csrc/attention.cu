@@ -385,83 +385,113 @@ __global__ void __launch_bounds__(NT, 2) attn_simt_kernel(const __grid_constant_
 }
 
 // Joins the pieces of the units that several parts share: block (c, y) takes
-// kJoinRows rows of joins[c]. A warp forms the weights 2^(m_i - max m) / sum of
-// a row's pieces, a lane a piece; every thread adds up four columns of a row,
-// eight pieces in flight (the first eight while the weights are formed). The
-// sums' order is that of the parts. Bound by the latency of dependent loads
-// (the pieces come from L2): 3.3 us of a call of 8 chains, 12 heads of 64
-// columns, in 151 x 1 blocks that start while the main kernel ends. Rows a
-// block: 8, one a warp for the weights; all columns of a row in one block, so
-// that its weights are formed once.
-constexpr int kJoinRows = 8, kJoinNT = 256;
+// JR rows of joins[c]. A row's weights 2^(m_i - max m) / sum of its pieces are
+// formed by 256 / JR lanes; a thread adds up four columns of JR / 8 rows (128
+// columns), eight loads in flight, the first of them while the weights are
+// formed. The sums' order is that of the parts. With few rows (JR = 8) it is
+// bound by the latency of dependent loads (the pieces come from L2), and a
+// thread's eight loads are a row's pieces; with many (JR = 32) by instructions,
+// and they are two pieces of four rows, so that a block's start is shared by
+// more. Calls with JR = 8 and 32: 16 trees of 512 rows 112.8 and 101.8 us; 16 of
+// 64 rows and 32 heads 83.2 and 81.7; one chain of 20 rows 13.7 and 15.6; one
+// tree of 244 rows in 19 pieces 106.5 and 111.7 (8 units: 64 blocks).
+constexpr int kJoinNT = 256;
+constexpr int kJoinFew = 152 * 4;  // blocks of 8 rows that an SM runs side by side
 
-template <typename E>
+template <typename E, int JR>
 __global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constant__ AttnParams p) {
-    __shared__ float weight[kJoinRows][32];
-    __shared__ float top[kJoinRows];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int LANES = kJoinNT / JR, RT = JR / 8, PT = 8 / RT, MOST = 32;  // MOST: weights of a row that are kept
+    __shared__ float weight[JR][MOST];
+    __shared__ float top[JR];
+    __shared__ long long out_row[JR];
+    const int tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4* src = reinterpret_cast<const int4*>(p.joins + blockIdx.x + 1);
     const int4 u = __ldcg(src), v = __ldcg(src + 1);  // b, h, row0, rows; slot0, first, last
-    const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, u.w - r0);
+    const int r0 = blockIdx.y * JR, rows = min(JR, u.w - r0);
     if (rows <= 0) return;
-    const int pieces = v.z - v.y + 2, D4 = p.D / 4;
+    const int pieces = v.z - v.y + 2, D4 = p.D / 4, lw = D4 <= 1 ? 0 : 32 - __clz(D4 - 1);
+    const int step = kJoinNT >> lw, d = (tid & ((1 << lw) - 1)) * 4;  // rows at a time, this thread's columns
     auto at = [&](int i, int r) { return (long long)(i == 0 ? v.x : 2 * (v.y + i - 1)) * p.tile_rows + r0 + r; };
-    const float2 none = make_float2(__uint_as_float(0xFF800000u), 0.f);
-    float4 x[8];
-    auto load = [&](int i0, int r, int d) {
+    float4 x[RT][PT];
+    auto load = [&](int ra, int i0) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            x[k] = i0 + k < pieces ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i0 + k, r) * p.D + d))
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < RT; ++k)
+#pragma unroll
+            for (int e = 0; e < PT; ++e)
+                x[k][e] = ra + k * step < rows && i0 + e < pieces
+                              ? __ldcg(reinterpret_cast<const float4*>(p.part_o + at(i0 + e, ra + k * step) * p.D + d))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
     };
-    if (tid < rows * D4) load(0, tid / D4, tid % D4 * 4);
-    if (warp < rows) {
-        const int r = warp;
-        float2 ml = none;
+    const int ra0 = d < p.D ? tid >> lw : rows;
+    load(ra0, 0);
+    {
+        const int r = tid / LANES, lane = tid % LANES;
+        const float2 none = make_float2(__uint_as_float(0xFF800000u), 0.f);
         float m = none.x, l = 0.f;
+        float2 ml = none;
 #pragma unroll 1
-        for (int i = lane; i < pieces; i += 32) {
+        for (int i = lane; r < rows && i < pieces; i += LANES) {
             ml = __ldcg(p.part_ml + at(i, r));
             m = fmaxf(m, ml.x);
         }
-        m = warp_max(m);
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         const float ref = m == none.x ? 0.f : m;
 #pragma unroll 1
-        for (int i = lane; i < pieces; i += 32) {
-            if (pieces > 32) ml = __ldcg(p.part_ml + at(i, r));
-            l += ex2(ml.x - ref) * ml.y;
+        for (int i = lane; r < rows && i < pieces; i += LANES) {
+            if (pieces > LANES) ml = __ldcg(p.part_ml + at(i, r));
+            const float w = ex2(ml.x - ref);
+            if (i < MOST) weight[r][i] = w;
+            l += w * ml.y;
         }
-        l = warp_sum(l);
-        if (pieces <= 32) weight[r][lane] = lane < pieces ? ex2(ml.x - ref) * (l == 0.f ? 0.f : 1.f / l) : 0.f;
-        if (lane == 0) {
-            if (pieces > 32) weight[r][0] = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int o = LANES / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        if (lane == 0 && r < rows) {
+            const int rr = u.z + r0 + r, node = rr / p.G;
+            const long long row = ((long long)u.x * p.N + node) * (p.Hkv * p.G) + u.y * p.G + (rr - node * p.G);
+            out_row[r] = row;
             top[r] = ref;
-            if (p.lse) {
-                const int rr = u.z + r0 + r, node = rr / p.G;
-                p.lse[((long long)u.x * p.N + node) * (p.Hkv * p.G) + u.y * p.G + (rr - node * p.G)] = lse_of(m, l);
-            }
+            if (p.lse) p.lse[row] = lse_of(m, l);
+        }
+        __syncwarp();
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int i = lane; r < rows && i < min(pieces, MOST); i += LANES) weight[r][i] *= inv;
+        if (pieces > MOST && r < rows) {  // kept for the pieces past MOST: the sum's inverse
+            __syncwarp();
+            if (lane == 0) weight[r][0] = inv;
         }
     }
     __syncthreads();
 #pragma unroll 1
-    for (int j = tid; j < rows * D4; j += kJoinNT) {
-        const int r = j / D4, d = (j - r * D4) * 4;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-        for (int i0 = 0; i0 < pieces; i0 += 8) {
-            if (i0 || j != tid) load(i0, r, d);
+    for (int ra = ra0; ra < rows; ra += RT * step) {
+        float4 acc[RT];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (i0 + k < pieces) {
-                    const float w = pieces <= 32 ? weight[r][i0 + k]
-                                                 : weight[r][0] * ex2(__ldcg(p.part_ml + at(i0 + k, r)).x - top[r]);
-                    acc = fma4(w, x[k], acc);
-                }
+        for (int k = 0; k < RT; ++k) acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i0 = 0; i0 < pieces; i0 += PT) {
+            if (i0 || ra != ra0) load(ra, i0);
+#pragma unroll
+            for (int k = 0; k < RT; ++k) {
+                const int r = ra + k * step;
+                if (r >= rows) break;
+#pragma unroll
+                for (int e = 0; e < PT; ++e)
+                    if (i0 + e < pieces) {
+                        const float w = pieces <= MOST ? weight[r][i0 + e]
+                                                       : weight[r][0] * ex2(__ldcg(p.part_ml + at(i0 + e, r)).x - top[r]);
+                        acc[k] = fma4(w, x[k][e], acc[k]);
+                    }
+            }
         }
-        const int rr = u.z + r0 + r, node = rr / p.G;
-        const long long row = ((long long)u.x * p.N + node) * (p.Hkv * p.G) + u.y * p.G + (rr - node * p.G);
-        if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G)) store4<E>(reinterpret_cast<E*>(p.out) + row * p.D + d, acc);
+#pragma unroll
+        for (int k = 0; k < RT; ++k) {
+            const int r = ra + k * step;
+            if (r >= rows) break;
+            if (SV_IN(out_row[r], (long long)p.B * p.N * p.Hkv * p.G))
+                store4<E>(reinterpret_cast<E*>(p.out) + out_row[r] * p.D + d, acc[k]);
+        }
     }
 }
 
@@ -471,13 +501,17 @@ cudaError_t launch_join(const AttnParams& p, const AttnPlan& plan, cudaStream_t 
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
+    const int rows = std::min(plan.rows, p.N * p.G);
+    // (a join a unit at the most)
+    const long long units = (long long)p.B * p.Hkv * ((p.N * p.G + plan.rows - 1) / plan.rows);
+    const bool many = std::min<long long>(units, plan.grid - 1) * ((rows + 7) / 8) > kJoinFew;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(plan.grid - 1, (std::min(plan.rows, p.N * p.G) + kJoinRows - 1) / kJoinRows);
+    cfg.gridDim = dim3(plan.grid - 1, many ? (rows + 31) / 32 : (rows + 7) / 8);
     cfg.blockDim = dim3(kJoinNT);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_join_kernel<E>, p);
+    return many ? cudaLaunchKernelEx(&cfg, attn_join_kernel<E, 32>, p) : cudaLaunchKernelEx(&cfg, attn_join_kernel<E, 8>, p);
 }
 
 template <typename E, int KV>

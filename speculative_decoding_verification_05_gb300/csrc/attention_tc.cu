@@ -52,8 +52,8 @@
 // one or two warps a scheduler last 1300 to 1900 cycles, mostly of instruction
 // latency; the tensor pipe is 36 to 50 % busy. 16 trees of 64 nodes, contexts
 // to 1900, 32 heads of one query head (64 rows, half of the product's 128):
-// 83.5 us (3.6 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 112.8 us (0.60
-// PFLOP/s); a tree of 61 nodes over 100003 positions, 8 heads of 4: 106.5 us.
+// 81.8 us (3.7 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 102 us (0.66
+// PFLOP/s); a tree of 61 nodes over 100003 positions, 8 heads of 4: 106 us.
 // Around that a launch takes some 13000 cycles to its first scores (the cut,
 // the first lookup, the first copies) and a unit 4000 to 6000 for its end.
 // Small pages cost copies: an entry of pages of 16 is 16 of them, and heads of
