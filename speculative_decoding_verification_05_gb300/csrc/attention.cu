@@ -35,6 +35,7 @@ namespace {
 constexpr int NT = 256;
 constexpr int kRows = 16;
 constexpr int kExtra = 1;  // tiles that a unit's start and end count for
+constexpr int kWhole = 2;  // tiles of a unit that is not split
 
 template <typename E>
 constexpr int row_bytes(int D) {  // a K row in shared memory: 16 bytes of padding against bank conflicts
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constan
 
 template <typename E>
 cudaError_t launch_join(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
-    if (plan.grid == 1) return cudaSuccess;
+    if (plan.whole) return cudaSuccess;
     cudaLaunchAttribute attr = {};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
@@ -563,6 +564,7 @@ cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan
 int attention_simt_rows() { return kRows; }
 
 int attention_simt_extra() { return kExtra; }
+int attention_simt_whole() { return kWhole; }
 
 int attention_simt_kv(int dtype, int D) { return D * (dtype == 0 ? 4 : 2) > 256 ? 32 : 64; }
 

@@ -18,7 +18,9 @@
 // cost; a cut that falls among these is moved to the unit's start. A unit inside one part is finished
 // by its CTA; the others leave partial results (unnormalised sums with their
 // running maximum and sum) that the join kernel adds up in range order, so
-// results depend on the lengths and the grid alone, never on timing.
+// results depend on the lengths and the grid alone, never on timing. Where there
+// are no more units than parts and a sequence can only have a few tiles (the
+// page table's width), a unit is one part's: nothing is left to join then.
 #pragma once
 
 #include "common.cuh"
@@ -46,6 +48,7 @@ struct AttnParams {
     int B, N, Hkv, G, D, num_pages, max_pages, page_shift;
     int tile_rows;       // rows of a row tile
     int extra;           // tiles that a unit's start and end count for
+    int whole;           // a unit is its first part's, all of it
     float c2;            // scale * log2(e): scores in octaves
     void* out;           // [B, N, Hkv * G, D]
     float* lse;          // [B, N, Hkv * G] or null
@@ -188,8 +191,8 @@ struct AttnWalk {
             const int from = (int)(in - unit * (uint32_t)(kt + p.extra));
             const int to = (int)min((long long)(kt + p.extra), from + (end - t));
             t += to - from;
-            s->first = max(0, from - p.extra);
-            s->last = max(0, to - p.extra);
+            s->first = p.whole ? 0 : max(0, from - p.extra);
+            s->last = p.whole ? (from == 0 ? kt : 0) : max(0, to - p.extra);
             if (s->first == s->last) continue;
             s->b = b;
             s->kt = kt;
@@ -295,7 +298,7 @@ SV_DEV void store4<bf16_t>(bf16_t* dst, float4 x) {
 // Host side.
 struct AttnPlan {
     int grid, rows, kv;   // CTAs of the main kernel, rows of a tile, positions of a tile
-    int extra;            // AttnParams::extra
+    int extra, whole;     // AttnParams::extra, whole
     size_t part_o, part_ml, joins, total;  // workspace layout
 };
 
@@ -307,6 +310,7 @@ int attention_simt_rows();
 int attention_simt_kv(int dtype, int D);
 int attention_simt_ctas(int dtype, int D);
 int attention_simt_extra();
+int attention_simt_whole();
 // The tensor-core kernel (bf16, D 64 or 128) reads K, V and Q through tensor
 // maps; attention_tc_maps: false where the cache's strides have none.
 struct alignas(64) AttnMaps {
@@ -315,6 +319,7 @@ struct alignas(64) AttnMaps {
 int attention_tc_rows(int group);
 int attention_tc_kv();
 int attention_tc_extra(int group, int N);
+int attention_tc_whole();
 bool attention_tc_maps(const AttnParams& p, AttnMaps* m);
 cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const AttnMaps& m, cudaStream_t st);
 cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);

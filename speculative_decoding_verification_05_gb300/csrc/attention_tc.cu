@@ -79,6 +79,7 @@ constexpr int kGroupRegs = 208, kOtherRegs = 88;
 constexpr int kKv = 128;     // positions of a tile
 constexpr int kMaxStages = 10;
 constexpr int kExtra = 3, kExtraDual = 6;
+constexpr int kWhole = 4;  // tiles of a unit that is not split
 constexpr float kHeavy = 4.f;  // octaves below a row's sum so far from which a weight is heavy
 constexpr float kSlack = 8.f;  // octaves of the running maximum above the reference that raise it
 constexpr float kJump = 64.f;  // of a half's own scores above it
@@ -996,6 +997,7 @@ int attention_tc_extra(int group, int N) { return N * group > attention_tc_rows(
 // Two halves of whole nodes, 128 rows at most each.
 int attention_tc_rows(int group) { return 2 * (128 / group) * group; }
 int attention_tc_kv() { return kKv; }
+int attention_tc_whole() { return kWhole; }
 
 bool attention_tc_maps(const AttnParams& p, AttnMaps* m) {
     static_assert(sizeof(AttnMaps) >= 3 * sizeof(CUtensorMap), "three maps");

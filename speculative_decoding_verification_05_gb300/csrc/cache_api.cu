@@ -171,18 +171,31 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
     auto use = [&](const sv::AttnPlan& plan) {
         p.tile_rows = plan.rows;
         p.extra = plan.extra;
+        p.whole = plan.whole;
         p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.part_o);
         p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + plan.part_ml);
         p.joins = reinterpret_cast<sv::AttnJoin*>(static_cast<char*>(workspace) + plan.joins);
     };
+    // Whole units: no more of them than CTAs, of `most` tiles at the most, and not
+    // so few that a shared unit's part would be three tiles less (a join costs as
+    // much). bf16, units of 8 rows and 128 columns, split and whole: 96 of 2 tiles
+    // 16.1 and 12.8 us, of 4 19.5 and 16.1; 8 of 4 tiles 13.3 and 14.7. float32
+    // tiles take longer than a join: 96 units of 2 tiles (64 columns) 12.0 and
+    // 10.0, of 4 14.0 and 17.8.
+    auto whole = [&](sv::AttnPlan plan, int most) {
+        const double units = (double)B * p.Hkv * ((N * p.G + plan.rows - 1) / plan.rows);
+        const double tiles = std::ceil((double)max_pages * cache->page_size / plan.kv);
+        plan.whole = units <= plan.grid && tiles <= most && tiles - units * (tiles + plan.extra) / plan.grid <= 3.0;
+        return plan;
+    };
     sv::AttnMaps maps;
     // (that kernel takes the maximum before the scale: it has to be positive)
     if (tc_shape(p.D, dtype) && scale > 0.f && sv::attention_tc_maps(p, &maps)) {
-        const sv::AttnPlan plan = tc_plan(p.D, p.G, N);
+        const sv::AttnPlan plan = whole(tc_plan(p.D, p.G, N), sv::attention_tc_whole());
         use(plan);
         return done(sv::launch_attention_tc(p, plan, maps, st));
     }
-    const sv::AttnPlan plan = simt_plan(p.D, dtype);
+    const sv::AttnPlan plan = whole(simt_plan(p.D, dtype), sv::attention_simt_whole());
     use(plan);
     return done(sv::launch_attention_simt(p, dtype == SPEC_F32 ? 0 : 1, plan, st));
 }

@@ -46,6 +46,28 @@ def test_many_units_a_core(i, dtype):
     paged.assert_attention(got, c.expected(), f"batch {i}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,H,G,hi,ps", [(1, 1, 1, 1, 60, 16), (12, 3, 8, 1, 400, 16), (19, 5, 8, 2, 100, 32),
+                                            (20, 5, 8, 2, 100, 32), (2, 60, 8, 8, 430, 64), (38, 2, 4, 4, 120, 128),
+                                            (30, 1, 5, 4, 511, 256)])
+def test_few_short_units(B, N, H, G, hi, ps, dtype):
+    """Units of a few tiles, up to as many as there are cores: split and whole ones, and the same sequences in a
+    table whose width allows for long ones."""
+    for D in (64, 128):
+        c = paged.Case(700 + B, _lens(B, B, hi), N, H, G, D, ps, dtype, True)
+        want = c.expected()
+        a = c.args()
+        got = sv.tree_attention(with_lse=True, **a)
+        assert got["status"].tolist() == [0] * B
+        paged.assert_attention(got, want, f"B {B} D {D}")
+        wide = torch.full((B, 3000), -1, dtype=torch.int32, device="cuda")
+        wide[:, :c.M] = a["page_table"]
+        a["page_table"] = wide
+        got = sv.tree_attention(with_lse=True, **a)
+        assert got["status"].tolist() == [0] * B
+        paged.assert_attention(got, want, f"B {B} D {D}, wide table")
+
+
 @pytest.mark.parametrize("rows", range(1, 18))
 def test_every_row_count_of_a_core_tile(rows):
     """float32: the warps' shares of rows and positions; head sizes of one and two column blocks a lane."""
