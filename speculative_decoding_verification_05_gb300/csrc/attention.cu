@@ -1,5 +1,5 @@
-// Tree attention over a paged cache on the CUDA cores, and the kernel that
-// joins partial results (attention.cuh: the mathematics and the division of
+// Tree attention over a paged cache on the CUDA cores, in two kernels for few and
+// for many rows, and the kernel that joins partial results (attention.cuh: the mathematics and the division of
 // the work). Takes every type and head size; float32 caches and head sizes
 // that the tensor-core kernel lacks come here.
 //
@@ -385,6 +385,244 @@ __global__ void __launch_bounds__(NT, 2) attn_simt_kernel(const __grid_constant_
     }
 }
 
+// ---- many rows ---------------------------------------------------------------------
+//
+// Units of more rows: 64 a CTA, in register tiles. Thread (ty, tx) of 16 x 16 has
+// rows 4 ty .. 4 ty + 3: first their scores at positions tx + 16 j of a tile (four
+// rows by four positions, so that eight loads of four columns serve 64 products),
+// then their outputs' columns 4 (tx + 16 g). The rows of a thread are the same
+// both times, and the weights pass between the 16 threads of a row through shared
+// memory of their warp's own: warps meet at a tile's arrival and release
+// alone. Bound by the products (a packed one takes two cycles of its pipe) and the
+// weights' moves into pairs beside them: 16 trees of 60 nodes, 8 heads of 4 query
+// heads of 128 columns, contexts to 1000, float32: 403 us, 29 TFLOP/s (821 us with
+// 16 rows a CTA); 16 nodes, 8 x 8 heads, 20000 positions: 301 us, 35 TFLOP/s (687).
+constexpr int kMany = 64;
+
+template <typename E, int KV>
+size_t many_smem(int D) {
+    return (size_t)2 * KV * (row_bytes<E>(D) + D * sizeof(E)) + (size_t)kMany * row_bytes<E>(D) +
+           (size_t)KV * (kMany + 4) * 4;
+}
+
+template <typename E, int KV, int NG>
+__global__ void __launch_bounds__(NT, NG == 1 ? 2 : 1) attn_many_kernel(const __grid_constant__ AttnParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ AttnScan scan;
+    constexpr int J = KV / 16, PS = kMany + 4;
+    const int tid = threadIdx.x, warp = tid >> 5, tx = tid & 15, ty = tid >> 4;
+    const int D = p.D, D4 = D / 4, stride = row_bytes<E>(D);
+    unsigned char* ks = smem;
+    unsigned char* vs = ks + 2 * KV * stride;
+    unsigned char* qs = vs + (size_t)2 * KV * D * sizeof(E);
+    float* ws = reinterpret_cast<float*>(qs + kMany * stride) + 4 * ty;  // weights [KV][PS], this thread's rows
+    const float none = __uint_as_float(0xFF800000u);
+    int col[NG];  // (threads without a column go along with the last)
+#pragma unroll
+    for (int g = 0; g < NG; ++g) col[g] = 4 * min(tx + 16 * g, D4 - 1);
+    const int lv = 32 - __clz(D * (int)sizeof(E) / 16 - 1);
+
+    asm volatile("griddepcontrol.launch_dependents;");
+    const AttnCut cut = attn_locate<KV, NT>(p, &scan);
+    AttnWalk<KV> walk(scan, cut);
+
+    AttnStay sq = {}, next = {};  // that of the tile worked on, of the tile copied
+    int tile = 0, ahead = 0;      // of sq, of next
+    bool bad, next_bad = false, have = false, more = true;
+    float ref[4], l[4];  // (as above: weights against a maximum with slack, a thread's own sums)
+    Two acc[4][NG];
+#pragma unroll 1
+    for (int st = 0; more; st ^= 1) {
+        const bool fresh = ahead >= next.last;
+        bad = next_bad;
+        if (fresh) {
+            more = walk.next(p, &next);
+            ahead = next.first;
+            next_bad = false;
+        }
+        if (more) {
+            next_bad |= load_tile<E, KV>(p, next, ahead, smem_addr(ks) + st * KV * stride,
+                                         smem_addr(vs) + st * KV * D * (int)sizeof(E), lv);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (!have) {  // while the first tile is on its way
+            if (tid == 0) attn_join<KV>(p, scan, cut);
+            attn_edges<E>(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
+        } else {
+            if (tile == sq.first) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    ref[r] = none;
+                    l[r] = 0.f;
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) acc[r][g] = Two{0ull, 0ull};
+                }
+            }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncthreads();
+            if (warp * 8 < sq.rows) {
+                const long long pos0 = (long long)tile * KV;
+                const unsigned char* q0 = qs + 4 * ty * stride;
+                const unsigned char* k0 = ks + ((st ^ 1) * KV + tx) * stride;
+                const unsigned char* v0 = vs + (size_t)(st ^ 1) * KV * D * sizeof(E);
+                float s[4][J];
+                {
+                    uint64_t d[4][J] = {};  // even and odd columns' sums
+#pragma unroll 2
+                    for (int c = 0; c < D4; ++c) {
+                        Two a[4], x[J];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) a[r] = lds4x2<E>(q0 + r * stride + c * 4 * sizeof(E));
+#pragma unroll
+                        for (int j = 0; j < J; ++j) x[j] = lds4x2<E>(k0 + 16 * j * stride + c * 4 * sizeof(E));
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int j = 0; j < J; ++j) d[r][j] = fma2(a[r].a, x[j].a, fma2(a[r].b, x[j].b, d[r][j]));
+                    }
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int j = 0; j < J; ++j) s[r][j] = (lo2(d[r][j]) + hi2(d[r][j])) * p.c2;
+                }
+                const bool tail = pos0 + KV > sq.L;
+                if (tail) {
+                    const int ctx = (int)max(-(1LL << 30), sq.L - pos0);  // context among these positions
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int node = (sq.row0 + min(4 * ty + r, sq.rows - 1)) / p.G;
+                        const uint8_t* mask = p.mask ? p.mask + ((long long)sq.b * p.N + node) * p.N : nullptr;
+#pragma unroll
+                        for (int j = 0; j < J; ++j) {
+                            const int nd = tx + 16 * j - ctx;
+                            if (nd >= 0 && (nd >= sq.n || (mask ? __ldg(mask + nd) == 0 : nd > node))) s[r][j] = none;
+                        }
+                    }
+                }
+                float top[4];
+                bool raise = false;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    top[r] = s[r][0];
+#pragma unroll
+                    for (int j = 1; j < J; ++j) top[r] = fmaxf(top[r], s[r][j]);
+                    raise |= top[r] > ref[r] + 8.f;
+                }
+                if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float to = top[r];
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) to = fmaxf(to, __shfl_xor_sync(0xFFFFFFFFu, to, o));
+                        to = fmaxf(to, ref[r]);
+                        const float f = to == none ? 1.f : ex2(ref[r] - to);
+                        ref[r] = to;
+                        l[r] *= f;
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) acc[r][g] = mul2(f, acc[r][g]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    float w[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        w[r] = ex2(s[r][j] - (ref[r] == none ? 0.f : ref[r]));
+                        l[r] += w[r];
+                    }
+                    *reinterpret_cast<float4*>(ws + (tx + 16 * j) * PS) = make_float4(w[0], w[1], w[2], w[3]);
+                }
+                __syncwarp();
+                if (!tail) {
+#pragma unroll 4
+                    for (int t = 0; t < KV; ++t) {
+                        const float4 w = *reinterpret_cast<const float4*>(ws + t * PS);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const Two x = lds4x2<E>(v0 + (t * D + col[g]) * sizeof(E));
+                            acc[0][g] = axpy2(pack2(w.x, w.x), x, acc[0][g]);
+                            acc[1][g] = axpy2(pack2(w.y, w.y), x, acc[1][g]);
+                            acc[2][g] = axpy2(pack2(w.z, w.z), x, acc[2][g]);
+                            acc[3][g] = axpy2(pack2(w.w, w.w), x, acc[3][g]);
+                        }
+                    }
+                } else {
+                    // an unseen node's values may be anything: a zero weight leaves them out
+                    const Two zero = {0ull, 0ull};
+#pragma unroll 1
+                    for (int t = 0; t < KV; ++t) {
+                        const float4 w = *reinterpret_cast<const float4*>(ws + t * PS);
+#pragma unroll
+                        for (int g = 0; g < NG; ++g) {
+                            const Two x = lds4x2<E>(v0 + (t * D + col[g]) * sizeof(E));
+                            acc[0][g] = axpy2(pack2(w.x, w.x), w.x != 0.f ? x : zero, acc[0][g]);
+                            acc[1][g] = axpy2(pack2(w.y, w.y), w.y != 0.f ? x : zero, acc[1][g]);
+                            acc[2][g] = axpy2(pack2(w.z, w.z), w.z != 0.f ? x : zero, acc[2][g]);
+                            acc[3][g] = axpy2(pack2(w.w, w.w), w.w != 0.f ? x : zero, acc[3][g]);
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            if (tile + 1 < sq.last) {
+                __syncthreads();
+            } else {
+                bad = __syncthreads_or(bad);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int rr = 4 * ty + r;
+#pragma unroll
+                    for (int o = 8; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], o);
+                    if (rr >= sq.rows) continue;
+                    if (bad) l[r] = __uint_as_float(0x7FC00000u);
+                    const int node = (sq.row0 + rr) / p.G, head = sq.h * p.G + (sq.row0 + rr) - node * p.G;
+                    const long long row = ((long long)sq.b * p.N + node) * (p.Hkv * p.G) + head;
+                    const long long part = (long long)sq.slot * kMany + rr;
+                    const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) {
+                        if (tx + 16 * g >= D4) continue;
+                        if (sq.whole) {
+                            const Two o = mul2(inv, acc[r][g]);
+                            if (SV_IN(row, (long long)p.B * p.N * p.Hkv * p.G))
+                                store4<E>(reinterpret_cast<E*>(p.out) + row * D + col[g],
+                                          make_float4(lo2(o.a), hi2(o.a), lo2(o.b), hi2(o.b)));
+                        } else {
+                            const Two o = acc[r][g];
+                            *reinterpret_cast<float4*>(p.part_o + part * D + col[g]) =
+                                make_float4(lo2(o.a), hi2(o.a), lo2(o.b), hi2(o.b));
+                        }
+                    }
+                    if (tx == 0) {
+                        if (!sq.whole) p.part_ml[part] = make_float2(ref[r], l[r]);
+                        else if (p.lse) p.lse[row] = lse_of(ref[r], l[r]);
+                    }
+                }
+            }
+        }
+        if (fresh) {
+            sq = next;
+            tile = next.first;
+            // (the last stay's queries are done with)
+            if (more) {
+                const int vec = D * (int)sizeof(E) / 16;
+                const E* q = static_cast<const E*>(p.q);
+#pragma unroll 1
+                for (int i = tid; i < sq.rows * vec; i += NT) {
+                    const int r = i / vec, c = i - r * vec, node = (sq.row0 + r) / p.G, g = (sq.row0 + r) - node * p.G;
+                    const long long row = ((long long)sq.b * p.N + node) * (p.Hkv * p.G) + sq.h * p.G + g;
+                    cp16(smem_addr(qs) + r * stride + c * 16, q + row * D + c * (16 / (int)sizeof(E)), 16);
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            }
+        } else {
+            ++tile;
+        }
+        ++ahead;
+        have = true;
+    }
+}
+
 // Joins the pieces of the units that several parts share: block (c, y) takes
 // JR rows of joins[c]. A row's weights 2^(m_i - max m) / sum of its pieces are
 // formed by 256 / JR lanes; a thread adds up four columns of JR / 8 rows (128
@@ -561,24 +799,48 @@ cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan
     return dtype == 0 ? launch_join<float>(p, plan, st) : launch_join<bf16_t>(p, plan, st);
 }
 
-int attention_simt_rows() { return kRows; }
+int attention_simt_rows(bool many) { return many ? kMany : kRows; }
+// Which of the two kernels. float32, 8 sequences, 8 heads, contexts to 1000, of
+// 16 and of 64 rows a CTA: 128 columns, 17 rows 58.8 and 47.9 us, 48 rows 90.0
+// and 66.7; 64 columns, 24 rows 28.8 and 31.9, 48 rows 42.2 and 46.9, and 4
+// sequences of 300 rows, contexts to 2000, 240 and 178.
+bool attention_simt_many(int rows, int D) { return rows >= (D > 64 ? kRows + 1 : kMany); }
 
 int attention_simt_extra() { return kExtra; }
 int attention_simt_whole() { return kWhole; }
 
-int attention_simt_kv(int dtype, int D) { return D * (dtype == 0 ? 4 : 2) > 256 ? 32 : 64; }
+int attention_simt_kv(int dtype, int D, bool many) { return D * (dtype == 0 ? 4 : 2) > (many ? 512 : 256) ? 32 : 64; }
+
+template <typename E, int KV, int NG>
+cudaError_t launch_many(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
+    const size_t smem = many_smem<E, KV>(p.D);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_many_kernel<E, KV, NG>), smem);
+    if (e != cudaSuccess) return e;
+    attn_many_kernel<E, KV, NG><<<plan.grid, NT, smem, st>>>(p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_join<E>(p, plan, st);
+}
+
+template <typename E>
+cudaError_t launch_cores(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
+    if (plan.rows == kRows) return plan.kv == 64 ? launch_simt<E, 64>(p, plan, st) : launch_simt<E, 32>(p, plan, st);
+    if (p.D <= 64) return launch_many<E, 64, 1>(p, plan, st);
+    if (p.D <= 128) return launch_many<E, 64, 2>(p, plan, st);
+    return launch_many<E, sizeof(E) == 4 ? 32 : 64, 4>(p, plan, st);
+}
 
 cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st) {
-    if (dtype != 0) return plan.kv == 64 ? launch_simt<bf16_t, 64>(p, plan, st) : launch_simt<bf16_t, 32>(p, plan, st);
-    return plan.kv == 64 ? launch_simt<float, 64>(p, plan, st) : launch_simt<float, 32>(p, plan, st);
+    return dtype == 0 ? launch_cores<float>(p, plan, st) : launch_cores<bf16_t>(p, plan, st);
 }
 
 // CTAs of an SM: what its shared memory and its registers hold.
-int attention_simt_ctas(int dtype, int D) {
-    const bool wide = attention_simt_kv(dtype, D) == 64;
-    const size_t smem = dtype != 0 ? (wide ? simt_smem<bf16_t, 64>(D) : simt_smem<bf16_t, 32>(D))
-                                   : (wide ? simt_smem<float, 64>(D) : simt_smem<float, 32>(D));
-    return (int)std::max<size_t>(1, std::min<size_t>(2, (size_t)227 * 1024 / (smem + 2048)));
+int attention_simt_ctas(int dtype, int D, bool many) {
+    const bool wide = attention_simt_kv(dtype, D, many) == 64;
+    size_t smem;
+    if (many) smem = dtype != 0 ? many_smem<bf16_t, 64>(D) : wide ? many_smem<float, 64>(D) : many_smem<float, 32>(D);
+    else if (dtype != 0) smem = wide ? simt_smem<bf16_t, 64>(D) : simt_smem<bf16_t, 32>(D);
+    else smem = wide ? simt_smem<float, 64>(D) : simt_smem<float, 32>(D);
+    return (int)std::max<size_t>(1, std::min<size_t>(many && D > 64 ? 1 : 2, (size_t)227 * 1024 / (smem + 2048)));
 }
 
 SV_DEBUG_READER(attention)

@@ -306,9 +306,10 @@ struct AttnPlan {
 // call costs about a microsecond).
 cudaError_t allow_smem(const void* kernel, size_t bytes);
 cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);
-int attention_simt_rows();
-int attention_simt_kv(int dtype, int D);
-int attention_simt_ctas(int dtype, int D);
+bool attention_simt_many(int rows, int D);
+int attention_simt_rows(bool many);
+int attention_simt_kv(int dtype, int D, bool many);
+int attention_simt_ctas(int dtype, int D, bool many);
 int attention_simt_extra();
 int attention_simt_whole();
 // The tensor-core kernel (bf16, D 64 or 128) reads K, V and Q through tensor

@@ -86,12 +86,12 @@ sv::AttnPlan attention_layout(sv::AttnPlan a, int D) {
     return a;
 }
 
-sv::AttnPlan simt_plan(int D, spec_dtype dtype) {
+sv::AttnPlan simt_plan(int D, spec_dtype dtype, bool many) {
     const int dt = dtype == SPEC_F32 ? 0 : 1;
     sv::AttnPlan a = {};
-    a.rows = sv::attention_simt_rows();
-    a.kv = sv::attention_simt_kv(dt, D);
-    a.grid = kSms * sv::attention_simt_ctas(dt, D);
+    a.rows = sv::attention_simt_rows(many);
+    a.kv = sv::attention_simt_kv(dt, D, many);
+    a.grid = kSms * sv::attention_simt_ctas(dt, D, many);
     a.extra = sv::attention_simt_extra();
     return attention_layout(a, D);
 }
@@ -108,7 +108,7 @@ sv::AttnPlan tc_plan(int D, int group, int N) {
 bool tc_shape(int D, spec_dtype dtype) { return dtype == SPEC_BF16 && (D == 64 || D == 128); }
 
 size_t attention_bytes(int D, int group, spec_dtype dtype) {
-    const size_t simt = simt_plan(D, dtype).total;
+    const size_t simt = std::max(simt_plan(D, dtype, false).total, simt_plan(D, dtype, true).total);
     return tc_shape(D, dtype) ? std::max(simt, tc_plan(D, group, 1).total) : simt;
 }
 
@@ -195,7 +195,7 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
         use(plan);
         return done(sv::launch_attention_tc(p, plan, maps, st));
     }
-    const sv::AttnPlan plan = whole(simt_plan(p.D, dtype), sv::attention_simt_whole());
+    const sv::AttnPlan plan = whole(simt_plan(p.D, dtype, sv::attention_simt_many(N * p.G, p.D)), sv::attention_simt_whole());
     use(plan);
     return done(sv::launch_attention_simt(p, dtype == SPEC_F32 ? 0 : 1, plan, st));
 }

@@ -46,6 +46,26 @@ def test_many_units_a_core(i, dtype):
     paged.assert_attention(got, c.expected(), f"batch {i}")
 
 
+@pytest.mark.parametrize("N,G", [(20, 1), (9, 7), (64, 1), (65, 1), (33, 4)])
+@pytest.mark.parametrize("D", [8, 64, 72, 136, 192, 256])
+def test_many_rows_on_the_cuda_cores(D, N, G):
+    """Row tiles that are partly filled, head sizes of every column grouping, few and many keys, both types."""
+    for dtype in ("f32", "bf16"):
+        c = paged.Case(800 + N, [0, 1, 63, 64, 200, 700], N, 2, G, D, 16, dtype, True, counts=[N, 1, N - 1, N, 0, N])
+        got = sv.tree_attention(with_lse=True, **c.args())
+        assert got["status"].tolist() == [0] * 6
+        paged.assert_attention(got, c.expected(), f"D {D} N {N} G {G} {dtype}")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_scales_that_are_not_positive(scale):
+    for D, dtype in ((64, "bf16"), (128, "bf16"), (128, "f32")):
+        c = paged.Case(850, [90, 0, 300], 30, 2, 3, D, 16, dtype, True, counts=[30, 9, 1])
+        c.scale = scale
+        got = sv.tree_attention(with_lse=True, **c.args())
+        paged.assert_attention(got, c.expected(), f"D {D} {dtype} {scale}")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,N,H,G,hi,ps", [(1, 1, 1, 1, 60, 16), (12, 3, 8, 1, 400, 16), (19, 5, 8, 2, 100, 32),
                                             (20, 5, 8, 2, 100, 32), (2, 60, 8, 8, 430, 64), (38, 2, 4, 4, 120, 128),
