@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(NT, 2) attn_simt_kernel(const __grid_constant_
 // then their outputs' columns 4 (tx + 16 g). The rows of a thread are the same
 // both times, and the weights pass between the 16 threads of a row through shared
 // memory of their warp's own: warps meet at a tile's arrival and release
-// alone. Bound by the products (a packed one takes two cycles of its pipe) and the
-// weights' moves into pairs beside them: 16 trees of 60 nodes, 8 heads of 4 query
+// alone. Bound by latency at two warps a scheduler (the products' pipe is 49 % busy,
+// shared memory 54 %): 16 trees of 60 nodes, 8 heads of 4 query
 // heads of 128 columns, contexts to 1000, float32: 403 us, 29 TFLOP/s (821 us with
 // 16 rows a CTA); 16 nodes, 8 x 8 heads, 20000 positions: 301 us, 35 TFLOP/s (687).
 constexpr int kMany = 64;
