@@ -426,10 +426,10 @@ typedef struct {
  *   status        [B] SPEC_OK, or SPEC_EDATA for a length, node count or page
  *                 out of range (that sequence's outputs are NaN); NULL allowed
  * Scores, sums and the softmax's statistics are fp32 for both types. On the
- * tensor cores (bf16, head_dim 64 or 128, scale > 0) weights are rounded to
- * bf16 before they multiply v, but those above a sixteenth of their row's sum
- * keep 16 bits. What lies in unseen positions (NaN and infinities too) does
- * not reach the outputs.
+ * tensor cores (bf16, head_dim 64 or 128, scale > 0) 16 bits of a weight count
+ * where it multiplies v. What lies in unseen positions (NaN and infinities too)
+ * does not reach the outputs; an infinity in v at a position that a row sees
+ * does, with its sign.
  * ---------------------------------------------------------------------- */
 size_t spec_tree_attention_workspace_size(int B, int N, int q_heads, int kv_heads, int head_dim, spec_dtype dtype);
 

@@ -23,7 +23,7 @@
 //                       that it can read).
 // A stream goes by halves of a tile, 64 positions: S of a half takes columns
 // 128 w + 64 (half) of tensor memory, and P (bf16, two a column) its place 32
-// positions at a time, 16 columns of weights and 16 of residuals; O_w columns
+// positions at a time, 16 columns of the weights' first parts and 16 of the second; O_w columns
 // 256 + 128 w. With two halves' places, a half's scores are there before the
 // softmax of the half before is done, and the products run beside it (with one
 // place of 128 positions a stream, scores, softmax and product came one after
@@ -33,12 +33,15 @@
 //
 // Weights are formed against a whole-number reference that follows the running
 // maximum with slack (Group::softmax), so O_w is rarely scaled. Statistics and
-// sums are fp32, and the sums l are taken before the weights are rounded to
-// bf16 for the product with V. Where a weight is more than a sixteenth of its row's sum so far, its
-// rounding would show beside the output's own: steps of 16 positions with such
-// a weight are multiplied a second time with what the rounding took (the
-// residuals, zero elsewhere). Lighter weights' roundings average out, and a
-// long row has few heavy ones.
+// sums are fp32. For the product with V a weight goes as two bf16 numbers, its
+// upper 16 bits and what they leave, so that V is multiplied twice: 16 bits of
+// a weight count (off by 2^-16 of it at the most). One bf16 weight would be off
+// by 2^-9, as much as the output's own rounding, and that does not average out
+// against the output: over values of mean zero both become smaller alike
+// (error of the outputs, against that of their rounding alone, with one
+// rounded weight where none is above a sixteenth of its row's sum: 1.38 times
+// at 900 positions, 1.12 at 20000). Neither part is negative, and neither is
+// zero unless the weight is, so that an infinity in V keeps its sign in every row.
 //
 // Tiles that reach past the context also hold nodes and the end: a thread forms
 // its row's visibility bits, and the elements of V there that are not finite
@@ -47,13 +50,15 @@
 // that do see them when the results are written.
 
 // What bounds it. One token of 64 sequences, contexts to 8192, 8 key heads of 4
-// query heads, 128 columns: memory (174 us, 6.2 TB/s of K and V). With 64 or
+// query heads, 128 columns: memory (172 us, 6.2 TB/s of K and V). With 64 or
 // more rows the softmax: a warp takes some 400 instructions a half, which at
 // one or two warps a scheduler last 1300 to 1900 cycles, mostly of instruction
 // latency; the tensor pipe is 36 to 50 % busy. 16 trees of 64 nodes, contexts
 // to 1900, 32 heads of one query head (64 rows, half of the product's 128):
-// 81.8 us (3.7 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 102 us (0.66
-// PFLOP/s); a tree of 61 nodes over 100003 positions, 8 heads of 4: 106 us.
+// 79.7 us (3.7 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 110 us (0.61
+// PFLOP/s); a tree of 61 nodes over 100003 positions, 8 heads of 4: 124 us
+// (weights of one bf16 number, and a second only where it was heavy: 82.1, 103
+// and 106).
 // Around that a launch takes some 13000 cycles to its first scores (the cut,
 // the first lookup, the first copies) and a unit 4000 to 6000 for its end.
 // Small pages cost copies: an entry of pages of 16 is 16 of them, and heads of
@@ -80,7 +85,7 @@ constexpr int kKv = 128;     // positions of a tile
 constexpr int kMaxStages = 10;
 constexpr int kExtra = 3, kExtraDual = 6;
 constexpr int kWhole = 4;  // tiles of a unit that is not split
-constexpr float kHeavy = 4.f;  // octaves below a row's sum so far from which a weight is heavy
+constexpr float kKeep = 1.f + 0x1p-20f;  // a weight's second part is kKeep of it less its first
 constexpr float kSlack = 8.f;  // octaves of the running maximum above the reference that raise it
 constexpr float kJump = 64.f;  // of a half's own scores above it
 constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile
@@ -119,7 +124,6 @@ struct Ctl {
     uint64_t seg_full[4];
     Seg seg[4];    // the helper's post: segment number modulo 4; b = -1: no more
     int flags[4];  // of a segment: 1 V had elements that are not finite, 2 a bad page
-    uint8_t heavy[2][2][4];  // steps of 16 positions with heavy weights, by group, half and warp (read as one word)
     float2 ml[128];
 };
 static_assert(sizeof(Ctl) <= 2048, "control region");
@@ -307,21 +311,14 @@ struct Issuer {
                     if (tail && half == 0) ok = ok && tc_wait(&c->clean[sv], clean >> sv & 1, &c->abort);
                     if (!ok) break;
                     tc_fence_after();
-                    uint32_t heavy = *reinterpret_cast<volatile uint32_t*>(c->heavy[w][half]);  // a byte of each warp
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        if (64 * half + 16 * kk < live)
-                            mma_ts(dp, ds + 64 * half + (kk >> 1) * 32 + (kk & 1) * 8, v + (half * kHalfRows + kk * 2048 >> 4),
-                                   idesc_o, !first || half > 0 || kk > 0);
-                    if (heavy) {
-                        heavy |= heavy >> 16;
-                        heavy |= heavy >> 8;
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            if (heavy >> kk & 1)
-                                mma_ts(dp, ds + 64 * half + (kk >> 1) * 32 + 16 + (kk & 1) * 8,
-                                       v + (half * kHalfRows + kk * 2048 >> 4), idesc_o, true);
-                    }
+                        if (64 * half + 16 * kk < live) {
+                            const uint32_t a = ds + 64 * half + (kk >> 1) * 32 + (kk & 1) * 8;
+                            const uint64_t b = v + (half * kHalfRows + kk * 2048 >> 4);
+                            mma_ts(dp, a, b, idesc_o, !first || half > 0 || kk > 0);
+                            mma_ts(dp, a + 16, b, idesc_o, true);
+                        }
                     mma_commit(&c->pv[w]);
                     if (half + 1 == nv) {
                         mma_commit(&c->empty[sv]);
@@ -656,7 +653,7 @@ struct Group {
     // One half: S -> P.
     SV_DEV bool softmax(int half, const uint2 see, bool tail, bool first, bool on, float c2, float& m, float& ref, float& l) {
         const uint32_t at = tm_s + 64 * half;
-        float x[64], mx[4];  // mx: by steps of 16 positions
+        float x[64], mx[4];
         tmem_ld64(at, x);
         if (tail) hide(x, see);
 #pragma unroll
@@ -678,47 +675,31 @@ struct Group {
         }
         m = fmaxf(m, top);
         const float r = ref == kNegInf ? 0.f : ref;
-        const uint64_t cc = pack2(c2, c2), rr = pack2(-r, -r);
+        const uint64_t cc = pack2(c2, c2), rr = pack2(-r, -r), keep = pack2(kKeep, kKeep);
         uint64_t sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            uint32_t hi[16];
+            uint32_t parts[32];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-                float& a = x[32 * j + 2 * e];
-                float& b = x[32 * j + 2 * e + 1];
-                unpack2(fma2(pack2(a, b), cc, rr), &a, &b);
+                float a, b, c, d;
+                unpack2(fma2(pack2(x[32 * j + 2 * e], x[32 * j + 2 * e + 1]), cc, rr), &a, &b);
                 a = ex2(a);
                 b = ex2(b);
-                sum[e & 3] = add2(sum[e & 3], pack2(a, b));
-                hi[e] = pack_bf16(a, b);
+                const uint64_t w = pack2(a, b);
+                sum[e & 3] = add2(sum[e & 3], w);
+                const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+                parts[e] = __byte_perm(ua, ub, 0x7632);  // the upper halves
+                const uint64_t upper = pack2(__uint_as_float((ua & 0xFFFF0000u) | 0x80000000u),
+                                             __uint_as_float((ub & 0xFFFF0000u) | 0x80000000u));
+                unpack2(fma2(w, keep, upper), &c, &d);
+                parts[16 + e] = pack_bf16(c, d);
             }
-            tmem_st16(at + 32 * j, hi);
+            tmem_st32(at + 32 * j, parts);
         }
         float a, b;
         unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), &a, &b);
         l += a + b;
-        // what the rounding took from the heavy weights, by steps of 16 positions
-        const float cut = __log2f(l) - kHeavy + r;
-        uint32_t heavy = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) heavy |= mx[i] * c2 > cut ? 1u << i : 0u;
-        heavy = __reduce_or_sync(0xFFFFFFFFu, on ? heavy : 0u);
-        if (lane == 0) c->heavy[w][half][warp] = (uint8_t)heavy;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            uint32_t lo[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) lo[e] = 0u;
-            if (heavy >> (2 * j) & 3)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float u = x[32 * j + 2 * e], v = x[32 * j + 2 * e + 1];
-                    const uint32_t hi = pack_bf16(u, v);
-                    lo[e] = pack_bf16(u - __uint_as_float(hi << 16), v - __uint_as_float(hi & 0xFFFF0000u));
-                }
-            tmem_st16(at + 32 * j + 16, lo);
-        }
         tmem_wait_st();
         return true;
     }
@@ -829,7 +810,6 @@ struct Group {
                 if (!(ok = warp_wait(&c->s_full[w][half], s_phase >> half & 1, &c->abort))) break;
                 s_phase ^= 1u << half;
                 tc_fence_after();
-                if (!warp_on && lane == 0) c->heavy[w][half][warp] = 0;
                 if (warp_on && !(ok = softmax(half, see, tail, u == 0, on, c2, m, ref, l))) break;
                 ++pv_count;
                 if (w == 1 && u + 1 == halves) c->ml[t] = make_float2(ref, l);
