@@ -506,7 +506,8 @@ __global__ void __launch_bounds__(NT, NG == 1 ? 2 : 1) attn_many_kernel(const __
                     top[r] = s[r][0];
 #pragma unroll
                     for (int j = 1; j < J; ++j) top[r] = fmaxf(top[r], s[r][j]);
-                    raise |= top[r] > ref[r] + 8.f;
+                    // (an absent row's queries are whatever lay there: it takes no part in the vote)
+                    raise |= 4 * ty + r < sq.rows && top[r] > ref[r] + 8.f;
                 }
                 if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
