@@ -86,8 +86,7 @@ constexpr int kMaxStages = 10;
 constexpr int kExtra = 3, kExtraDual = 6;
 constexpr int kWhole = 4;  // tiles of a unit that is not split
 constexpr float kKeep = 1.f + 0x1p-20f;  // a weight's second part is kKeep of it less its first
-constexpr float kSlack = 8.f;  // octaves of the running maximum above the reference that raise it
-constexpr float kJump = 64.f;  // of a half's own scores above it
+constexpr float kSlack = 8.f;  // octaves of a score above the reference that raise it
 constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile
 constexpr int kHalfKv = 64;            // positions of a half of a tile
 constexpr uint32_t kHalfRows = kHalfKv * 128;  // bytes from its rows to the other half's, in 64 columns
@@ -644,11 +643,11 @@ struct Group {
 
     // A row's weights are 2^(s - ref) with a whole number for ref, at first the
     // maximum of the first positions that it sees, rounded up. Weights may
-    // exceed 1: fp32 sums and bf16 weights scale without loss, so the running
-    // maximum m need not be known before a half's weights are formed. ref is
-    // raised to it where it is more than 8 octaves above before a half begins;
-    // for a half's own scores only where one lies more than 64 octaves above
-    // (sums stay far from overflow).
+    // exceed 1: fp32 sums and bf16 weights scale without loss. ref is raised to
+    // the running maximum m where a score of the half lies more than 8 octaves
+    // above it, so a weight is 2^8 at the most, and sums stay in range for values
+    // up to 2^119 / T (with weights to 2^64 before ref followed, values above 2^56
+    // could overflow).
     //
     // One half: S -> P.
     SV_DEV bool softmax(int half, const uint2 see, bool tail, bool first, bool on, float c2, float& m, float& ref, float& l) {
@@ -668,7 +667,7 @@ struct Group {
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
         if (ref == kNegInf) ref = ceilf(top);  // (nothing seen so far: all sums are zero)
         // (a lane without a row may hold anything)
-        if (!first && __any_sync(0xFFFFFFFFu, on && fmaxf(m - kSlack, top - kJump) > ref)) {
+        if (!first && __any_sync(0xFFFFFFFFu, on && top - kSlack > ref)) {
             const float to = fmaxf(ref, ceilf(fmaxf(m, top)));
             if (!rescale(ref == to ? 1.f : ex2(ref - to), l)) return false;
             ref = to;

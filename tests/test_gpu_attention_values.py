@@ -52,3 +52,21 @@ def test_outputs_are_as_exact_as_their_type(lens, N, G, D, q_scale):
     off = sv.tree_attention(**c.args())["out"].double().cpu() - want
     rounding = want.bfloat16().double() - want
     assert off.square().mean().sqrt() <= 1.02 * rounding.square().mean().sqrt()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("octaves", [3, 10, 30, 60])
+def test_values_near_the_largest(D, octaves, dtype):
+    """Values of 2^100: weighted sums stay in range wherever the scores jump, in
+    the middle of a tile or at its edges, since a weight is at most 2^8 before
+    its row's reference follows (2^8 x 2^100 x 600 terms < 2^127)."""
+    for at in (64, 130, 191, 500):
+        c = paged.Case(33, [600], 4, 1, 2, D, 16, dtype, False, q_scale=0.0)
+        c.q[..., 0] = 1.0
+        for t in range(604):
+            row = c.k[c.table[0, t // 16], t % 16, 0]
+            row[0] = octaves * math.log(2.0) * D ** 0.5 if t >= at else 0.0
+        c.v = (c.v.float().clamp(-4, 4) * 2.0 ** 98).to(c.v.dtype)
+        got = sv.tree_attention(with_lse=True, **c.args())
+        paged.assert_attention(got, c.expected(), f"jump at {at}")
