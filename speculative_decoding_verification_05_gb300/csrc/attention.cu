@@ -24,10 +24,10 @@
 // four CTAs an SM took 254, 264 and 339.
 
 #include <algorithm>
-#include <atomic>
-#include <mutex>
 
 #include "attention.cuh"
+#include "per_device.h"
+#include "specverify.h"
 
 namespace sv {
 namespace {
@@ -756,44 +756,24 @@ cudaError_t launch_join(const AttnParams& p, const AttnPlan& plan, cudaStream_t 
 
 template <typename E, int KV>
 cudaError_t launch_simt(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
-    const size_t smem = simt_smem<E, KV>(p.D);
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_simt_kernel<E, KV>), smem);
+    constexpr int widest = KV == 64 ? 256 / (int)sizeof(E) : SPEC_MAX_HEAD_DIM;  // (attention_simt_kv)
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_simt_kernel<E, KV>), simt_smem<E, KV>(widest));
     if (e != cudaSuccess) return e;
-    attn_simt_kernel<E, KV><<<plan.grid, NT, smem, st>>>(p);
+    attn_simt_kernel<E, KV><<<plan.grid, NT, simt_smem<E, KV>(p.D), st>>>(p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join<E>(p, plan, st);
 }
 
 }  // namespace
 
-cudaError_t allow_smem(const void* kernel, size_t bytes) {
-    constexpr int kMost = 16;
-    struct Entry {
-        std::atomic<const void*> kernel{nullptr};
-        std::atomic<size_t> bytes{0};
-        std::atomic<int> dev{-1};
-    };
-    static Entry seen[kMost];
+cudaError_t allow_smem(const void* kernel, size_t most) {
+    static OncePerDevice once;
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    for (Entry& s : seen)
-        if (s.kernel.load(std::memory_order_acquire) == kernel && s.dev.load(std::memory_order_relaxed) == dev &&
-            s.bytes.load(std::memory_order_relaxed) >= bytes)
-            return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-    static std::mutex mu;
-    std::lock_guard<std::mutex> g(mu);
-    for (Entry& s : seen) {
-        const void* k = s.kernel.load(std::memory_order_relaxed);
-        if (k && (k != kernel || s.dev.load(std::memory_order_relaxed) != dev)) continue;
-        s.dev.store(dev, std::memory_order_relaxed);
-        s.bytes.store(bytes, std::memory_order_relaxed);
-        s.kernel.store(kernel, std::memory_order_release);
-        break;
-    }
-    return cudaSuccess;
+    return (cudaError_t)once.run(kernel, dev, [&] {
+        return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    });
 }
 
 cudaError_t launch_attention_join(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st) {
@@ -814,10 +794,9 @@ int attention_simt_kv(int dtype, int D, bool many) { return D * (dtype == 0 ? 4 
 
 template <typename E, int KV, int NG>
 cudaError_t launch_many(const AttnParams& p, const AttnPlan& plan, cudaStream_t st) {
-    const size_t smem = many_smem<E, KV>(p.D);
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_many_kernel<E, KV, NG>), smem);
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(attn_many_kernel<E, KV, NG>), many_smem<E, KV>(64 * NG));
     if (e != cudaSuccess) return e;
-    attn_many_kernel<E, KV, NG><<<plan.grid, NT, smem, st>>>(p);
+    attn_many_kernel<E, KV, NG><<<plan.grid, NT, many_smem<E, KV>(p.D), st>>>(p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : launch_join<E>(p, plan, st);
 }

@@ -302,9 +302,9 @@ struct AttnPlan {
     size_t part_o, part_ml, joins, total;  // workspace layout
 };
 
-// Lets a kernel have this much dynamic shared memory (set once a device: the
-// call costs about a microsecond).
-cudaError_t allow_smem(const void* kernel, size_t bytes);
+// Lets a kernel have its most dynamic shared memory, the same for every call
+// (set once a device: it takes about a microsecond).
+cudaError_t allow_smem(const void* kernel, size_t most);
 cudaError_t launch_attention_simt(const AttnParams& p, int dtype, const AttnPlan& plan, cudaStream_t st);
 bool attention_simt_many(int rows, int D);
 int attention_simt_rows(bool many);
