@@ -17,12 +17,14 @@ Entry points (same names as the C ABI in ``include/specverify.h``):
 
 Tensors may live on the GPU (the normal case) or in (pinned) host memory; host
 inputs are copied to the current device, and outputs come back to the host.
-A paged cache, its page table and its reference counts live on the GPU.
+A paged cache, its page table and its reference counts live on the GPU; a call
+runs on their device, whichever is current.
 """
 
 import contextlib
 import ctypes
 import functools
+import inspect
 import os
 import struct
 import threading
@@ -192,6 +194,23 @@ def _check(rc):
         raise SpecError(msg)
 
 
+def _on_device_of(name):
+    """The call runs with the device of its tensor `name` current: a launch goes
+    to the current device, and the default stream's handle is the same on all."""
+    def wrap(fn):
+        at = list(inspect.signature(fn).parameters).index(name)
+
+        @functools.wraps(fn)
+        def call(*args, **kw):
+            t = args[at] if len(args) > at else kw.get(name)
+            if getattr(t, "is_cuda", False) and t.get_device() != torch.cuda.current_device():
+                with torch.cuda.device(t.get_device()):
+                    return fn(*args, **kw)
+            return fn(*args, **kw)
+        return call
+    return wrap
+
+
 def _dtype_code(t):
     if t.dtype == torch.float32:
         return SPEC_F32
@@ -276,6 +295,7 @@ _pinned = {}
 _pin_lock = threading.Lock()
 
 
+@_on_device_of("target")
 def verify(target, draft, draft_tokens, temperature=1.0, top_p=1.0, top_k=0, seed=0, offset=0,
            debug=False, out=None, lenience=1.0):
     """Modified rejection sampling over target [B, gamma+1, V] and draft [B, gamma, V].
@@ -321,6 +341,7 @@ def verify(target, draft, draft_tokens, temperature=1.0, top_p=1.0, top_k=0, see
     return sg.back(o)
 
 
+@_on_device_of("target")
 def verify_tree(target, node_tokens, parent, depth, max_depth):
     """Greedy exact-match verification of BFS-ordered draft trees [B, N, V].
 
@@ -346,6 +367,7 @@ def verify_tree(target, node_tokens, parent, depth, max_depth):
     return sg.back(o)
 
 
+@_on_device_of("candidates")
 def tree_build(candidates, root_token, V, N, counts=None, with_mask=True):
     """REST draft trees from retrieved continuations candidates [B, C, L] (-1 ends one).
 
@@ -370,6 +392,7 @@ def tree_build(candidates, root_token, V, N, counts=None, with_mask=True):
     return sg.back(o)
 
 
+@_on_device_of("target")
 def acceptance_rate(target, draft, temperature=1.0, top_p=1.0, top_k=0):
     """beta [B, gamma] = sum_x min(q_k(x), p_k(x)) per position (temperature > 0),
     and status [B]; the mean of beta estimates the acceptance rate alpha."""
@@ -412,6 +435,7 @@ def best_gamma(alpha, c, gamma_max):
     return load_library().spec_best_gamma(float(alpha), float(c), int(gamma_max))
 
 
+@_on_device_of("target")
 def verify_mentor(target, draft, draft_tokens, temperature=1.0, kl_bound=0.0, bisect_iters=30,
                   seed=0, offset=0, debug=False):
     """Lossy mentor verification; returns the ``verify`` outputs plus alpha and beta [B, gamma]."""
@@ -441,6 +465,7 @@ def verify_mentor(target, draft, draft_tokens, temperature=1.0, kl_bound=0.0, bi
     return sg.back(o)
 
 
+@_on_device_of("logits")
 def sample(logits, temperature=1.0, top_p=1.0, top_k=0, seed=0, offset=0, pos0=0,
            purpose=PURPOSE_DRAFT):
     """One draw per row of logits [B, P, V]; returns tokens [B, P] and status [B]."""
@@ -465,8 +490,9 @@ def philox_uniform(seed, row0, position, purpose, n, device=None):
     device = device or torch.device("cuda", torch.cuda.current_device())
     out = torch.empty(n, dtype=torch.float32, device=device)
     stream = torch.cuda.current_stream(device)
-    _check(lib.spec_philox_uniform(int(seed), int(row0), int(position), int(purpose), int(n), _ptr(out),
-                                   ctypes.c_void_p(stream.cuda_stream)))
+    with torch.cuda.device(device):
+        _check(lib.spec_philox_uniform(int(seed), int(row0), int(position), int(purpose), int(n), _ptr(out),
+                                       ctypes.c_void_p(stream.cuda_stream)))
     return out
 
 
@@ -543,6 +569,7 @@ def _attention_bytes(path, B, N, Hq, Hkv, D, dt):
     return load_library(path).spec_tree_attention_workspace_size(B, N, Hq, Hkv, D, dt)
 
 
+@_on_device_of("k_cache")
 def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_nodes=None, scale=None,
                    with_lse=False, out=None):
     """Attention of the drafted nodes q [B, N, heads, D] over one layer's cache.
@@ -593,6 +620,7 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_node
     return {n: t.cpu() for n, t in o.items()} if host else o
 
 
+@_on_device_of("k_cache")
 def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None):
     """Write k, v [B, N, kv_heads, D] to positions cache_len[b] + i, i < n_nodes[b]
     (None: N), of one layer's cache [pages, page_size, kv_heads, D], in place.
@@ -622,6 +650,7 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None):
     return {"status": status}
 
 
+@_on_device_of("k_cache")
 def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_nodes=None):
     """Keep an accepted path in caches [layers, pages, page_size, kv_heads, D], in
     place: position L + i <- L + path_nodes[b, i], i <= accept_len[b].
@@ -650,6 +679,7 @@ def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_node
     return {"cache_len": new_len, "status": status}
 
 
+@_on_device_of("page_table")
 def cache_resize(page_table, page_refs, seqs, tokens, page_size):
     """Pages for tokens[f] tokens of sequence seqs[f] (None: f), in place: more are
     taken (lowest free number first), surplus ones released; 0 frees a sequence.
@@ -679,6 +709,7 @@ def cache_resize(page_table, page_refs, seqs, tokens, page_size):
     return {"status": status}
 
 
+@_on_device_of("k_cache")
 def cache_fork(k_cache, v_cache, page_table, cache_len, page_refs, src, dst):
     """Sequences dst[f] as copies of src[f], in place: full pages shared, a partly
     filled last page copied (caches [layers, pages, page_size, kv_heads, D]).

@@ -1,0 +1,86 @@
+"""The Python binding's host side, without a GPU: which device a call runs on."""
+
+import contextlib
+
+import pytest
+import torch
+
+import speculative_decoding_verification_05_gb300 as sv
+
+
+class Used(Exception):
+    """A tensor was looked at; .current: the device that was current then."""
+
+
+class OnDevice1:
+    """A stand-in for a tensor on cuda:1 that raises at its first real use."""
+
+    is_cuda = True
+    device = torch.device("cuda", 1)
+
+    def get_device(self):
+        return 1
+
+    def __getattr__(self, name):
+        e = Used(name)
+        e.current = CURRENT[0]
+        raise e
+
+
+CURRENT = [0]
+
+
+@pytest.fixture
+def two_devices(monkeypatch):
+    @contextlib.contextmanager
+    def device(d):
+        before, CURRENT[0] = CURRENT[0], torch.device("cuda", d).index if isinstance(d, int) else d.index
+        try:
+            yield
+        finally:
+            CURRENT[0] = before
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: CURRENT[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(sv, "load_library", lambda path=None: object())
+    monkeypatch.setattr(sv, "_library", lambda: object())
+
+
+T = OnDevice1()
+CALLS = {
+    "verify": lambda: sv.verify(T, T, T),
+    "verify by name": lambda: sv.verify(draft_tokens=T, draft=T, target=T),
+    "verify_tree": lambda: sv.verify_tree(T, T, T, T, 3),
+    "tree_build": lambda: sv.tree_build(T, T, 10, 4),
+    "acceptance_rate": lambda: sv.acceptance_rate(T, T),
+    "verify_mentor": lambda: sv.verify_mentor(T, T, T),
+    "sample": lambda: sv.sample(T),
+    "tree_attention": lambda: sv.tree_attention(torch.zeros(1, 1, 1, 8), T, T, T, T),
+    "tree_attention by name": lambda: sv.tree_attention(torch.zeros(1, 1, 1, 8), v_cache=T, k_cache=T, page_table=T,
+                                                        cache_len=T),
+    "cache_append": lambda: sv.cache_append(T, T, T, T, T, T),
+    "cache_compact": lambda: sv.cache_compact(T, T, T, T, T),
+    "cache_resize": lambda: sv.cache_resize(T, T, None, T, 16),
+    "cache_fork": lambda: sv.cache_fork(T, T, T, T, T, T, T),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_run_on_their_tensors_device(two_devices, name):
+    CURRENT[0] = 0
+    with pytest.raises(Used) as e:
+        CALLS[name]()
+    assert e.value.current == 1
+    assert CURRENT[0] == 0
+    CURRENT[0] = 1
+    with pytest.raises(Used) as e:
+        CALLS[name]()
+    assert e.value.current == 1 and CURRENT[0] == 1
+    CURRENT[0] = 0
+
+
+def test_signatures_and_names_are_kept():
+    import inspect
+
+    assert list(inspect.signature(sv.tree_attention).parameters)[:3] == ["q", "k_cache", "v_cache"]
+    assert sv.cache_fork.__name__ == "cache_fork" and sv.cache_fork.__doc__
