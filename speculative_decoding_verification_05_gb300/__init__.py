@@ -211,6 +211,18 @@ def _on_device_of(name):
     return wrap
 
 
+def _given(out, index, want):
+    """The caller's output tensors as a new dict; each key's must be contiguous and
+    on the call's device, with the shape and dtype that `want` has for it."""
+    o = {} if out is None else dict(out)
+    for key, (shape, dtype) in want.items():
+        t = o.get(key)
+        if t is not None and (t.dtype is not dtype or tuple(t.shape) != tuple(shape) or t.get_device() != index or
+                              not t.is_contiguous()):
+            raise SpecError(f"out[{key!r}] must be a contiguous {dtype} tensor {list(shape)} on the call's device")
+    return o
+
+
 def _dtype_code(t):
     if t.dtype == torch.float32:
         return SPEC_F32
@@ -317,7 +329,9 @@ def verify(target, draft, draft_tokens, temperature=1.0, top_p=1.0, top_k=0, see
         raise SpecError("shape mismatch between target, draft and draft_tokens")
     if draft is not None and draft.dtype != target.dtype:
         raise SpecError("target and draft must share a dtype")
-    o = dict(out or {})
+    i32 = torch.int32
+    o = _given(out, sg.device.index, {"accepted": ((B,), i32), "tokens": ((B, G1), i32), "next_token": ((B,), i32),
+                                      "status": ((B,), i32), "probs": ((B, gamma, 2), torch.float32)})
     o.setdefault("accepted", sg.out((B,)))
     o.setdefault("tokens", sg.out((B, G1)))
     o.setdefault("next_token", sg.out((B,)))
@@ -580,7 +594,8 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_node
     with mask[b, i, j] != 0 (``tree_build``'s mask; None: j <= i, a chain).
     ``scale`` defaults to 1 / sqrt(D). Returns out [B, N, heads, D], status [B]
     and, with ``with_lse``, lse [B, N, heads]; nodes from n_nodes[b] on are
-    zero (lse -inf). ``out`` may pass preallocated outputs under these keys.
+    zero (lse -inf). ``out`` may pass preallocated outputs under these keys
+    (contiguous, of these shapes and types, on the cache's device).
     """
     lib = _library()
     cache, sh, dt = _cache_args(k_cache, v_cache, 0)
@@ -600,7 +615,7 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_node
         n_nodes = _in(n_nodes, dev, index)
     if lens.shape != (B,) or (n_nodes is not None and n_nodes.shape != (B,)):
         raise SpecError("cache_len and n_nodes must be [B]")
-    o = {} if out is None else dict(out)
+    o = _given(out, index, {"out": (q.shape, q.dtype), "lse": ((B, N, Hq), torch.float32), "status": ((B,), torch.int32)})
     if "out" not in o:
         o["out"] = torch.empty_like(q)
     if "status" not in o:

@@ -84,3 +84,22 @@ def test_signatures_and_names_are_kept():
 
     assert list(inspect.signature(sv.tree_attention).parameters)[:3] == ["q", "k_cache", "v_cache"]
     assert sv.cache_fork.__name__ == "cache_fork" and sv.cache_fork.__doc__
+
+
+def test_given_outputs_are_checked():
+    i32, f32 = torch.int32, torch.float32
+    want = dict(out=((2, 3, 4, 8), torch.bfloat16), lse=((2, 3, 4), f32), status=((2,), i32))
+    good = dict(out=torch.zeros(2, 3, 4, 8, dtype=torch.bfloat16), lse=torch.zeros(2, 3, 4), status=torch.zeros(2, dtype=i32))
+    host = -1   # get_device() of a host tensor: the checks are the same
+    assert sv._given(None, host, want) == {}
+    o = sv._given(good, host, want)
+    assert o == good and o is not good
+    assert sv._given({"status": good["status"]}, host, want) == {"status": good["status"]}
+    for key, bad in (("out", good["out"][:1]), ("out", good["out"].float()), ("out", good["out"].flatten()),
+                     ("out", good["out"].transpose(1, 2).contiguous().transpose(1, 2)), ("lse", good["lse"].double()),
+                     ("lse", torch.zeros(2, 3, 8)[..., ::2]), ("lse", torch.zeros(2, 4, 3)), ("status", torch.zeros(2)),
+                     ("status", torch.zeros(2, dtype=torch.int64)), ("status", torch.zeros(3, dtype=i32))):
+        with pytest.raises(sv.SpecError):
+            sv._given({**good, key: bad}, host, want)
+    with pytest.raises(sv.SpecError):
+        sv._given(good, 0, want)   # on the host, for a call on a device
