@@ -943,9 +943,18 @@ bool encode_map(CUtensorMap* map, const void* base, const cuuint64_t (&dims)[4],
     }
     const cuuint32_t box[4] = {64, box1, box2, 1}, step[4] = {1, 1, 1, 1};
     const Encode encode = encoder();
-    return encode && encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, st, box, step,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    auto make = [&] {
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, st, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    };
+    if (!encode) return false;
+    CUresult r = make();
+    // a thread that has not called the runtime yet has no context (without this,
+    // its first call went to the CUDA cores)
+    int dev = 0;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) r = make();
+    return r == CUDA_SUCCESS;
 }
 
 // k or v: boxes of (page_size, at most 128) slots of one head of one page.

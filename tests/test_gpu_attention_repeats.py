@@ -1,6 +1,8 @@
 """Tree attention repeats itself to the bit whatever ran before it: row tiles
 that are partly filled, after calls that leave other queries in shared memory."""
 
+import threading
+
 import pytest
 import torch
 
@@ -25,3 +27,20 @@ def test_absent_rows_have_no_influence(dtype, D, rows):
         again = sv.tree_attention(with_lse=True, **a)
         for k in ("out", "lse"):
             assert torch.equal(again[k], first[k]), (k, q_scale)
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 128)])
+def test_a_thread_s_first_call(dtype, D):
+    """The same bits as in the main thread, and so the same kernel."""
+    a = paged.Case(3, [3000, 40], 5, 2, 4, D, 16, dtype, False).args()
+    want = sv.tree_attention(with_lse=True, **a)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        t = threading.Thread(target=lambda: got.append(sv.tree_attention(with_lse=True, **a)))
+        t.start()
+        t.join()
+    assert len(got) == 3
+    for r in got:
+        for k in ("out", "lse", "status"):
+            assert torch.equal(r[k], want[k]), k
