@@ -49,7 +49,9 @@
  *    *_workspace_size() function returns, 256-byte aligned, owned by the
  *    caller. Its content on entry does not matter: each call clears the small
  *    control region it needs (one cudaMemsetAsync on `stream`) before its
- *    kernels. Calls that share a workspace must not overlap on the GPU.
+ *    kernels. Calls that share a workspace must not overlap on the GPU, nor be
+ *    made at the same time by several threads, also on one stream: a call's
+ *    kernels pass data through it, and another's must not come between them.
  *  - Randomness: Philox-4x32-10 (Salmon et al., SC'11) with
  *    key = (seed lo, seed hi), counter = (row lo, row hi, position, purpose),
  *    row = offset + b; u = ((word0 >> 9) + 0.5) * 2^-23. The acceptance test

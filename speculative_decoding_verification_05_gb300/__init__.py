@@ -236,13 +236,22 @@ def _ptr(t):
 
 
 _ws_cache = {}
+_turns = {}
+
+
+def _turn(index, raw):
+    """The lock of a stream (device index, raw handle) under which a call takes its
+    workspace and enqueues its kernels: they pass data through the workspace, so
+    another thread's call on the stream must not come between them."""
+    return _turns.get((index, raw)) or _turns.setdefault((index, raw), threading.Lock())
 
 
 def workspace(nbytes, device, stream):
     """A workspace of at least nbytes, cached per (device, stream).
 
     The library clears what it needs at the start of every call, so the
-    buffer is reused as is; calls on one stream never overlap on the GPU.
+    buffer is reused as is; calls on one stream never overlap on the GPU, and
+    this module's calls enqueue all their kernels under the stream's lock.
     """
     key = (device.index if device.index is not None else torch.cuda.current_device(), stream.cuda_stream)
     buf = _ws_cache.get(key)
@@ -341,16 +350,17 @@ def verify(target, draft, draft_tokens, temperature=1.0, top_p=1.0, top_k=0, see
     dt = _dtype_code(target)
     stream = torch.cuda.current_stream(sg.device)
     nbytes = lib.spec_verify_workspace_size(B, gamma, V, dt)
-    ws = workspace(nbytes, sg.device, stream)
     smp = SpecSampling(float(temperature), float(top_p), int(top_k))
-    outs = (_ptr(o["accepted"]), _ptr(o["tokens"]), _ptr(o["next_token"]), _ptr(o["status"]),
-            _ptr(o.get("probs")), _ptr(ws), ws.numel(), ctypes.c_void_p(stream.cuda_stream))
-    if lenience == 1.0:
-        rc = lib.spec_verify(_ptr(target), _ptr(draft), dt, _ptr(toks), B, gamma, V, smp, int(seed), int(offset),
-                             *outs)
-    else:
-        rc = lib.spec_verify_lenient(_ptr(target), _ptr(draft), dt, _ptr(toks), B, gamma, V, smp,
-                                     float(lenience), int(seed), int(offset), *outs)
+    with _turn(sg.device.index, stream.cuda_stream):
+        ws = workspace(nbytes, sg.device, stream)
+        outs = (_ptr(o["accepted"]), _ptr(o["tokens"]), _ptr(o["next_token"]), _ptr(o["status"]),
+                _ptr(o.get("probs")), _ptr(ws), ws.numel(), ctypes.c_void_p(stream.cuda_stream))
+        if lenience == 1.0:
+            rc = lib.spec_verify(_ptr(target), _ptr(draft), dt, _ptr(toks), B, gamma, V, smp, int(seed), int(offset),
+                                 *outs)
+        else:
+            rc = lib.spec_verify_lenient(_ptr(target), _ptr(draft), dt, _ptr(toks), B, gamma, V, smp,
+                                         float(lenience), int(seed), int(offset), *outs)
     _check(rc)
     return sg.back(o)
 
@@ -372,11 +382,12 @@ def verify_tree(target, node_tokens, parent, depth, max_depth):
          "bonus": sg.out((B,)), "status": sg.out((B,))}
     dt = _dtype_code(target)
     stream = torch.cuda.current_stream(sg.device)
-    ws = workspace(lib.spec_verify_tree_workspace_size(B, N, V, dt), sg.device, stream)
-    rc = lib.spec_verify_tree(_ptr(target), dt, _ptr(tok), _ptr(par), _ptr(dep), B, N, V, int(max_depth),
-                              _ptr(o["accept_len"]), _ptr(o["path_nodes"]), _ptr(o["tokens"]),
-                              _ptr(o["bonus"]), _ptr(o["status"]), _ptr(ws), ws.numel(),
-                              ctypes.c_void_p(stream.cuda_stream))
+    with _turn(sg.device.index, stream.cuda_stream):
+        ws = workspace(lib.spec_verify_tree_workspace_size(B, N, V, dt), sg.device, stream)
+        rc = lib.spec_verify_tree(_ptr(target), dt, _ptr(tok), _ptr(par), _ptr(dep), B, N, V, int(max_depth),
+                                  _ptr(o["accept_len"]), _ptr(o["path_nodes"]), _ptr(o["tokens"]),
+                                  _ptr(o["bonus"]), _ptr(o["status"]), _ptr(ws), ws.numel(),
+                                  ctypes.c_void_p(stream.cuda_stream))
     _check(rc)
     return sg.back(o)
 
@@ -420,11 +431,12 @@ def acceptance_rate(target, draft, temperature=1.0, top_p=1.0, top_k=0):
     o = {"beta": sg.out((B, gamma), torch.float32), "status": sg.out((B,))}
     dt = _dtype_code(target)
     stream = torch.cuda.current_stream(sg.device)
-    ws = workspace(lib.spec_verify_workspace_size(B, gamma, V, dt), sg.device, stream)
-    rc = lib.spec_acceptance_rate(_ptr(target), _ptr(draft), dt, B, gamma, V,
-                                  SpecSampling(float(temperature), float(top_p), int(top_k)),
-                                  _ptr(o["beta"]), _ptr(o["status"]), _ptr(ws), ws.numel(),
-                                  ctypes.c_void_p(stream.cuda_stream))
+    with _turn(sg.device.index, stream.cuda_stream):
+        ws = workspace(lib.spec_verify_workspace_size(B, gamma, V, dt), sg.device, stream)
+        rc = lib.spec_acceptance_rate(_ptr(target), _ptr(draft), dt, B, gamma, V,
+                                      SpecSampling(float(temperature), float(top_p), int(top_k)),
+                                      _ptr(o["beta"]), _ptr(o["status"]), _ptr(ws), ws.numel(),
+                                      ctypes.c_void_p(stream.cuda_stream))
     _check(rc)
     return sg.back(o)
 
@@ -468,13 +480,14 @@ def verify_mentor(target, draft, draft_tokens, temperature=1.0, kl_bound=0.0, bi
         o["probs"] = sg.out((B, gamma, 2), torch.float32)
     dt = _dtype_code(target)
     stream = torch.cuda.current_stream(sg.device)
-    ws = workspace(lib.spec_verify_mentor_workspace_size(B, gamma, V, dt), sg.device, stream)
-    rc = lib.spec_verify_mentor(_ptr(target), _ptr(draft), dt, _ptr(toks), B, gamma, V,
-                                float(temperature), float(kl_bound), int(bisect_iters), int(seed),
-                                int(offset), _ptr(o["accepted"]), _ptr(o["tokens"]),
-                                _ptr(o["next_token"]), _ptr(o["status"]), _ptr(o["alpha"]),
-                                _ptr(o["beta"]), _ptr(o.get("probs")), _ptr(ws), ws.numel(),
-                                ctypes.c_void_p(stream.cuda_stream))
+    with _turn(sg.device.index, stream.cuda_stream):
+        ws = workspace(lib.spec_verify_mentor_workspace_size(B, gamma, V, dt), sg.device, stream)
+        rc = lib.spec_verify_mentor(_ptr(target), _ptr(draft), dt, _ptr(toks), B, gamma, V,
+                                    float(temperature), float(kl_bound), int(bisect_iters), int(seed),
+                                    int(offset), _ptr(o["accepted"]), _ptr(o["tokens"]),
+                                    _ptr(o["next_token"]), _ptr(o["status"]), _ptr(o["alpha"]),
+                                    _ptr(o["beta"]), _ptr(o.get("probs")), _ptr(ws), ws.numel(),
+                                    ctypes.c_void_p(stream.cuda_stream))
     _check(rc)
     return sg.back(o)
 
@@ -490,10 +503,11 @@ def sample(logits, temperature=1.0, top_p=1.0, top_k=0, seed=0, offset=0, pos0=0
     o = {"tokens": sg.out((B, P)), "status": sg.out((B,))}
     dt = _dtype_code(logits)
     stream = torch.cuda.current_stream(sg.device)
-    ws = workspace(lib.spec_sample_workspace_size(B, P, V, dt), sg.device, stream)
-    rc = lib.spec_sample(_ptr(logits), dt, B, P, V, SpecSampling(float(temperature), float(top_p), int(top_k)),
-                         int(seed), int(offset), int(pos0), int(purpose), _ptr(o["tokens"]),
-                         _ptr(o["status"]), _ptr(ws), ws.numel(), ctypes.c_void_p(stream.cuda_stream))
+    with _turn(sg.device.index, stream.cuda_stream):
+        ws = workspace(lib.spec_sample_workspace_size(B, P, V, dt), sg.device, stream)
+        rc = lib.spec_sample(_ptr(logits), dt, B, P, V, SpecSampling(float(temperature), float(top_p), int(top_k)),
+                             int(seed), int(offset), int(pos0), int(purpose), _ptr(o["tokens"]),
+                             _ptr(o["status"]), _ptr(ws), ws.numel(), ctypes.c_void_p(stream.cuda_stream))
     _check(rc)
     return sg.back(o)
 
@@ -623,13 +637,14 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_node
     if with_lse and "lse" not in o:
         o["lse"] = torch.empty((B, N, Hq), dtype=torch.float32, device=dev)
     raw = _raw_stream(index)
-    ws = _scratch(_attention_bytes(_current[0], B, N, Hq, sh[2], D, dt), dev, index, raw)
-    rc = lib.spec_tree_attention(q.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
-                                 None if mask is None else mask.data_ptr(),
-                                 None if n_nodes is None else n_nodes.data_ptr(), B, N, Hq,
-                                 D ** -0.5 if scale is None else scale, o["out"].data_ptr(),
-                                 o["lse"].data_ptr() if "lse" in o else None, o["status"].data_ptr(),
-                                 ws.data_ptr(), ws.numel(), raw)
+    with _turn(index, raw):
+        ws = _scratch(_attention_bytes(_current[0], B, N, Hq, sh[2], D, dt), dev, index, raw)
+        rc = lib.spec_tree_attention(q.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
+                                     None if mask is None else mask.data_ptr(),
+                                     None if n_nodes is None else n_nodes.data_ptr(), B, N, Hq,
+                                     D ** -0.5 if scale is None else scale, o["out"].data_ptr(),
+                                     o["lse"].data_ptr() if "lse" in o else None, o["status"].data_ptr(),
+                                     ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
     return {n: t.cpu() for n, t in o.items()} if host else o
@@ -745,9 +760,10 @@ def cache_fork(k_cache, v_cache, page_table, cache_len, page_refs, src, dst):
     F = a.shape[0]
     status = torch.empty((F,), dtype=torch.int32, device=dev)
     raw = _raw_stream(index)
-    ws = _scratch(lib.spec_cache_fork_workspace_size(F), dev, index, raw)
-    rc = lib.spec_cache_fork(cache, dt, table, stride, width, S, refs, lens, a.data_ptr(), z.data_ptr(), F,
-                             status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
+    with _turn(index, raw):
+        ws = _scratch(lib.spec_cache_fork_workspace_size(F), dev, index, raw)
+        rc = lib.spec_cache_fork(cache, dt, table, stride, width, S, refs, lens, a.data_ptr(), z.data_ptr(), F,
+                                 status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
     return {"status": status}
