@@ -251,8 +251,14 @@ def workspace(nbytes, device, stream):
 
     The library clears what it needs at the start of every call, so the
     buffer is reused as is; calls on one stream never overlap on the GPU, and
-    this module's calls enqueue all their kernels under the stream's lock.
+    this module's calls enqueue all their kernels under the stream's lock. A
+    call that a graph captures has a buffer of its own, from the graph's memory:
+    a replay may come after the stream's buffer was replaced by a larger one, or
+    beside calls on that stream.
     """
+    if torch.cuda.is_current_stream_capturing():
+        with torch.cuda.stream(stream):
+            return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
     key = (device.index if device.index is not None else torch.cuda.current_device(), stream.cuda_stream)
     buf = _ws_cache.get(key)
     if buf is None or buf.numel() < nbytes:
@@ -544,7 +550,7 @@ def _raw_stream(index):
 def _scratch(nbytes, dev, index, raw):
     """As ``workspace``, by the stream's raw handle (the same buffers)."""
     buf = _ws_cache.get((index, raw))
-    if buf is None or buf.numel() < nbytes:
+    if buf is None or buf.numel() < nbytes or torch.cuda.is_current_stream_capturing():
         buf = workspace(nbytes, dev, torch.cuda.current_stream(dev))
     return buf
 
