@@ -46,7 +46,7 @@ class Model:
         x = self.embed[tokens.long()] + torch.cat([at.sin(), at.cos()], -1).to(self.dtype)
         for l in range(self.layers):
             q, k, v = (self.norm(x) @ self.qkv[l]).view(B, N, -1, self.D).split([self.H, self.Hkv, self.Hkv], 2)
-            sv.cache_append(k, v, cache.k[l], cache.v[l], table, cache_len, n_nodes)
+            sv.cache_append(k, v, cache.k[l], cache.v[l], table, cache_len, n_nodes, cache.refs)
             a = sv.tree_attention(q, cache.k[l], cache.v[l], table, cache_len, mask, n_nodes)["out"]
             x = x + a.reshape(B, N, -1) @ self.proj[l]
             u, g = (self.norm(x) @ self.gate[l]).chunk(2, -1)
@@ -115,7 +115,7 @@ def speculative(model, prompt, branches, steps, drafts, nodes=12):
         # (places that the tree left unused repeat node 1, which comes before them where it is accepted)
         tok, par, dep = (torch.where(unused, t[k][:, 1:2], t[k]) for k in ("node_tokens", "parent", "depth"))
         r = sv.verify_tree(z, tok, par, dep, cand.shape[2])
-        kept = sv.cache_compact(c.k, c.v, table, c.len[1:], r["accept_len"], r["path_nodes"])
+        kept = sv.cache_compact(c.k, c.v, table, c.len[1:], r["accept_len"], r["path_nodes"], c.refs)
         if r["status"].any() or kept["status"].any():
             raise RuntimeError((r["status"].tolist(), kept["status"].tolist()))
         c.len[1:] = kept["cache_len"]

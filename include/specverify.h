@@ -390,6 +390,13 @@ spec_status spec_verify_noalloc(const void* target, const void* draft, spec_dtyp
  * that a sequence does not hold are -1. page_refs[page] counts the table
  * entries that name a page; a page is free iff its count is 0.
  *
+ * Appending and compacting write to the pages of the positions from cache_len
+ * on; these must be the sequence's own (count 1). They are unless a sequence
+ * that shares pages was shortened to inside one of them: what is then written
+ * would be its siblings' too. Such a sequence is forked into an empty one
+ * (spec_cache_fork gives that its own copy of the partly filled page) and
+ * released. With page_refs in spec_cache the two calls check it.
+ *
  * Limits: k and v 16-byte aligned, every stride a multiple of 16 bytes;
  * page_size a power of two in 8 .. SPEC_MAX_PAGE; head_dim a multiple of 8,
  * at most SPEC_MAX_HEAD_DIM; 1 <= B <= 65535. The struct itself is host
@@ -400,6 +407,8 @@ typedef struct {
     void* v;
     int32_t layers, num_pages, page_size, kv_heads, head_dim;
     int64_t layer_stride, page_stride, token_stride, head_stride; /* elements */
+    const int32_t* page_refs; /* [num_pages], or NULL: spec_cache_append and
+                                 spec_cache_compact do not check the counts */
 } spec_cache;
 
 /* ------------------------------------------------------------------------
@@ -447,7 +456,8 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
  * cache_len[b] + i of one layer (layers == 1). cache_len itself is not
  * changed. The pages must be the sequence's already (spec_cache_resize).
  *   status        [B] SPEC_OK, or SPEC_EDATA for a length, node count or page
- *                 out of range (nothing is written); NULL allowed
+ *                 out of range, or a page to be written whose count is not 1
+ *                 (nothing is written); NULL allowed
  * 1 <= N <= 2^20.
  * ---------------------------------------------------------------------- */
 spec_status spec_cache_append(const void* k, const void* v, const spec_cache* cache, spec_dtype dtype,
@@ -468,7 +478,8 @@ spec_status spec_cache_append(const void* k, const void* v, const spec_cache* ca
  *   W             1 .. SPEC_MAX_TREE_N, above every accept_len
  *   new_len       [B] int32 (must not overlap cache_len); -1 on SPEC_EDATA
  *   status        [B] SPEC_OK, or SPEC_EDATA for a length, path or page out of
- *                 range (nothing moves); NULL allowed
+ *                 range, or a page to be written whose count is not 1 (nothing
+ *                 moves); NULL allowed
  * ---------------------------------------------------------------------- */
 spec_status spec_cache_compact(const spec_cache* cache, spec_dtype dtype, const int32_t* page_table,
                                int64_t table_stride, int max_pages, const int32_t* cache_len,

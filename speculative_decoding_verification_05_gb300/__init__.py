@@ -62,7 +62,7 @@ class SpecCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("layers", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("layer_stride", ctypes.c_int64), ("page_stride", ctypes.c_int64),
-                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+                ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("page_refs", ctypes.c_void_p)]
 
 
 class _CacheArg:
@@ -535,7 +535,7 @@ def philox_uniform(seed, row0, position, purpose, n, device=None):
 # These calls run once a layer and step, so the host side is kept short: plain
 # attribute reads, one packed struct, integer pointers, cached workspace sizes.
 
-_pack_cache = struct.Struct("@QQiiiii4xqqqq").pack   # spec_cache
+_pack_cache = struct.Struct("@QQiiiii4xqqqqQ").pack   # spec_cache
 _LIVE = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16}
 
 
@@ -555,7 +555,7 @@ def _scratch(nbytes, dev, index, raw):
     return buf
 
 
-def _cache_args(k_cache, v_cache, layered):
+def _cache_args(k_cache, v_cache, layered, page_refs=None):
     """The packed spec_cache of k / v caches [layers, pages, page_size, heads, head_dim]
     (one layer: no first dimension; any strides with contiguous heads), its
     shape and its dtype code."""
@@ -570,8 +570,9 @@ def _cache_args(k_cache, v_cache, layered):
     dt = _LIVE.get(k_cache.dtype)
     if dt is None:
         raise SpecError(f"caches must be float32 or bfloat16, got {k_cache.dtype}")
+    refs = 0 if page_refs is None else _owned(page_refs, (sh[-4],), k_cache.get_device(), "page_refs")
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), sh[0] if layered else 1, sh[-4], sh[-3], sh[-2], sh[-1],
-                       st[0] if layered else 0, st[-4], st[-3], st[-2]), sh, dt
+                       st[0] if layered else 0, st[-4], st[-3], st[-2], refs), sh, dt
 
 
 def _table_args(page_table, rows, index):
@@ -657,15 +658,17 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_node
 
 
 @_on_device_of("k_cache")
-def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None):
+def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None, page_refs=None):
     """Write k, v [B, N, kv_heads, D] to positions cache_len[b] + i, i < n_nodes[b]
     (None: N), of one layer's cache [pages, page_size, kv_heads, D], in place.
 
-    The pages must be the sequences' already (``cache_resize``); cache_len is
-    not changed. Returns status [B].
+    The pages must be the sequences' already (``cache_resize``) and nobody
+    else's: with ``page_refs`` a sequence whose new rows would go to a shared
+    page (it was shortened to inside one; ``cache_fork`` it instead) is refused,
+    SPEC_EDATA. cache_len is not changed. Returns status [B].
     """
     lib = _library()
-    cache, sh, dt = _cache_args(k_cache, v_cache, 0)
+    cache, sh, dt = _cache_args(k_cache, v_cache, 0, page_refs)
     if k.dim() != 4 or k.shape != v.shape or k.shape[2:] != sh[2:] or k.dtype is not k_cache.dtype or \
             v.dtype is not k_cache.dtype:
         raise SpecError("k and v must be [B, N, kv_heads, head_dim] of the cache's dtype")
@@ -687,16 +690,17 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None):
 
 
 @_on_device_of("k_cache")
-def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_nodes=None):
+def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_nodes=None, page_refs=None):
     """Keep an accepted path in caches [layers, pages, page_size, kv_heads, D], in
     place: position L + i <- L + path_nodes[b, i], i <= accept_len[b].
 
     accept_len [B] and path_nodes [B, W] are ``verify_tree``'s; None: a chain
-    (``verify``'s accepted), whose entries are in place. Returns cache_len [B]
-    = L + accept_len + 1 (-1 on a data error) and status [B].
+    (``verify``'s accepted), whose entries are in place. With ``page_refs`` a
+    sequence whose entries would move into a shared page is refused. Returns
+    cache_len [B] = L + accept_len + 1 (-1 on a data error) and status [B].
     """
     lib = _library()
-    cache, _, dt = _cache_args(k_cache, v_cache, 1)
+    cache, _, dt = _cache_args(k_cache, v_cache, 1, page_refs)
     B = page_table.shape[0]
     dev, index = k_cache.device, k_cache.get_device()
     table, stride, width = _table_args(page_table, B, index)

@@ -21,12 +21,14 @@ constexpr int CT = 256;
 SV_DEV uint4 ldg16(const char* p) { return *reinterpret_cast<const uint4*>(p); }
 SV_DEV void stg16(char* p, uint4 x) { *reinterpret_cast<uint4*>(p) = x; }
 
-// Whether pages [first, last] of a sequence exist (all threads of the block).
-SV_DEV bool pages_ok(const int32_t* table, int first, int last, int num_pages) {
+// Whether pages [first, last] of a sequence exist and, with refs, are its own
+// (all threads of the block).
+SV_DEV bool pages_ok(const int32_t* table, int first, int last, int num_pages, const int32_t* refs) {
     bool bad = false;
     for (int i = first + (int)threadIdx.x; i <= last; i += blockDim.x) {
         const int id = __ldg(table + i);
-        bad |= id < 0 || id >= num_pages;
+        if (id < 0 || id >= num_pages) bad = true;
+        else if (refs) bad |= __ldg(refs + id) != 1;
     }
     return !__syncthreads_or(bad);
 }
@@ -46,7 +48,7 @@ __global__ void __launch_bounds__(CT) append_kernel(const __grid_constant__ Appe
     const int sh = p.c.page_shift;
     const int32_t* table = p.table + b * p.table_stride;
     bool ok = L >= 0 && n >= 0 && n <= p.N && L + n <= ((long long)p.max_pages << sh);
-    if (ok && n > 0) ok = pages_ok(table, (int)(L >> sh), (int)((L + n - 1) >> sh), p.c.num_pages);
+    if (ok && n > 0) ok = pages_ok(table, (int)(L >> sh), (int)((L + n - 1) >> sh), p.c.num_pages, p.c.refs);
     if (blockIdx.x == 0 && tid == 0 && p.status) p.status[b] = ok ? kOk : kEData;
     if (!ok) return;
     const int per_head = p.c.row_bytes / 16, per_token = p.c.heads * per_head;
@@ -88,12 +90,17 @@ __global__ void __launch_bounds__(CT) compact_kernel(const __grid_constant__ Com
     }
     const long long end = ok ? L + (path ? path[a] : a) + 1 : 0;
     if (ok) ok = end <= ((long long)p.max_pages << sh);
-    if (ok) ok = pages_ok(table, (int)(L >> sh), (int)((end - 1) >> sh), p.c.num_pages);
+    if (ok) ok = pages_ok(table, (int)(L >> sh), (int)((end - 1) >> sh), p.c.num_pages, nullptr);
+    int stay = 1;  // the path's first entries may be in place already
+    if (ok && path)
+        while (stay <= a && path[stay] == stay) ++stay;
+    const bool moves = ok && path && stay <= a;
+    if (moves && p.c.refs) ok = pages_ok(table, (int)((L + stay) >> sh), (int)((L + a) >> sh), p.c.num_pages, p.c.refs);
     if (blockIdx.x == 0 && tid == 0) {
         p.new_len[b] = ok ? (int)(L + a + 1) : -1;
         if (p.status) p.status[b] = ok ? kOk : kEData;
     }
-    if (!ok || !path || a == 0) return;
+    if (!ok || !moves) return;
     auto place = [&](long long pos) {
         return (long long)table[pos >> sh] * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride;
     };
@@ -101,8 +108,6 @@ __global__ void __launch_bounds__(CT) compact_kernel(const __grid_constant__ Com
         from[i] = place(L + path[i]);
         to[i] = place(L + i);
     }
-    int stay = 1;  // the path's first entries may be in place already
-    while (stay <= a && path[stay] == stay) ++stay;
     __syncthreads();
     const int per_head = p.c.row_bytes / 16, cols = p.c.heads * per_head;
     const long long units = (long long)p.c.layers * 2 * cols;

@@ -13,6 +13,7 @@ struct CacheView {
     char* v;
     long long layer_stride, page_stride, token_stride, head_stride;  // bytes
     int layers, num_pages, page_shift, heads, row_bytes;
+    const int32_t* refs;  // [num_pages], or null: not checked
 };
 
 struct AppendParams {

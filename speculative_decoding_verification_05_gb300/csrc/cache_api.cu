@@ -42,7 +42,9 @@ int shift_of(int page_size) {
 bool dim_ok(int D) { return D >= 8 && D <= SPEC_MAX_HEAD_DIM && D % 8 == 0; }
 
 bool cache_ok(const spec_cache* c, spec_dtype dtype) {
-    if (!c || !dtype_ok(dtype) || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return false;
+    if (!c || !dtype_ok(dtype) || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16) ||
+        !aligned(c->page_refs, 4))
+        return false;
     if (c->layers < 1 || c->num_pages < 1 || c->num_pages > (1 << 30) || !page_ok(c->page_size) || c->kv_heads < 1 ||
         c->kv_heads > 1024 || !dim_ok(c->head_dim))
         return false;
@@ -70,6 +72,7 @@ sv::CacheView view_of(const spec_cache* c, spec_dtype dtype) {
     v.page_shift = shift_of(c->page_size);
     v.heads = c->kv_heads;
     v.row_bytes = c->head_dim * es;
+    v.refs = c->page_refs;
     return v;
 }
 
