@@ -476,7 +476,8 @@ spec_status spec_cache_append(const void* k, const void* v, const spec_cache* ca
  *   path_nodes    [B, W] int32 (spec_verify_tree's), ascending from 0; NULL
  *                 for a chain, whose accepted entries are in place already
  *   W             1 .. SPEC_MAX_TREE_N, above every accept_len
- *   new_len       [B] int32 (must not overlap cache_len); -1 on SPEC_EDATA
+ *   new_len       [B] int32; -1 on SPEC_EDATA. new_len and status overlap
+ *                 neither each other nor an input
  *   status        [B] SPEC_OK, or SPEC_EDATA for a length, path or page out of
  *                 range, or a page to be written whose count is not 1 (nothing
  *                 moves); NULL allowed

@@ -39,6 +39,12 @@ int shift_of(int page_size) {
     return s;
 }
 
+// Whether n ints from a and m ints from b (null: none) share any.
+bool overlap(const int32_t* a, size_t n, const int32_t* b, size_t m) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && x < y + 4 * m && y < x + 4 * n;
+}
+
 bool dim_ok(int D) { return D >= 8 && D <= SPEC_MAX_HEAD_DIM && D % 8 == 0; }
 
 bool cache_ok(const spec_cache* c, spec_dtype dtype) {
@@ -236,8 +242,13 @@ spec_status spec_cache_compact(const spec_cache* cache, spec_dtype dtype, const 
         !aligned(cache_len, 4) || !aligned(accept_len, 4) || !aligned(path_nodes, 4) || !aligned(new_len, 4) ||
         !aligned(status, 4))
         return SPEC_EINVAL;
-    const uintptr_t a = (uintptr_t)cache_len, z = (uintptr_t)new_len;
-    if (a < z + 4u * B && z < a + 4u * B) return SPEC_EINVAL;
+    // (one block of a sequence writes these while its others still read those)
+    const int32_t* const in[] = {cache_len, accept_len, path_nodes};
+    for (int i = 0; i < 3; ++i) {
+        const size_t n = (size_t)B * (i == 2 ? W : 1);
+        if (overlap(in[i], n, new_len, B) || overlap(in[i], n, status, B)) return SPEC_EINVAL;
+    }
+    if (overlap(new_len, B, status, B)) return SPEC_EINVAL;
     sv::CompactParams p = {};
     p.c = view_of(cache, dtype);
     p.table = page_table;
