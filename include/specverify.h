@@ -555,6 +555,13 @@ int spec_debug_failures(int* line);
  * builds (nothing is changed) or on a CUDA error. */
 int spec_debug_withhold_copy(int j);
 
+/* As spec_debug_withhold_copy, for the attention on the tensor cores: the first
+ * CTA withholds the copies of the j-th tile of keys or values that it takes
+ * (j < 0: none). Its waits give up (within about a second), the
+ * sequences of its part are reported SPEC_ETIMEOUT (their outputs are
+ * incomplete), the others' outputs are as usual. */
+int spec_debug_withhold_tile(int j);
+
 /* Library ABI version (major * 100 + minor). */
 int spec_version(void);
 

@@ -50,7 +50,7 @@ EXPORTED = [
     "spec_tree_attention_workspace_size", "spec_tree_attention", "spec_cache_append", "spec_cache_compact",
     "spec_cache_resize", "spec_cache_fork_workspace_size", "spec_cache_fork",
     "spec_philox_uniform", "spec_verify_noalloc", "spec_status_string", "spec_last_cuda_error",
-    "spec_version", "spec_debug_build", "spec_debug_failures", "spec_debug_withhold_copy",
+    "spec_version", "spec_debug_build", "spec_debug_failures", "spec_debug_withhold_copy", "spec_debug_withhold_tile",
 ]
 
 
@@ -166,6 +166,8 @@ def load_library(path=None):
         lib.spec_debug_failures.restype = _I
         lib.spec_debug_withhold_copy.argtypes = [_I]
         lib.spec_debug_withhold_copy.restype = _I
+        lib.spec_debug_withhold_tile.argtypes = [_I]
+        lib.spec_debug_withhold_tile.restype = _I
         _libs[path] = lib
         return lib
 

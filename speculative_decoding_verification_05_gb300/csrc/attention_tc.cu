@@ -77,6 +77,10 @@
 namespace sv {
 namespace {
 
+#ifdef SPEC_DEBUG
+static __device__ int g_withhold = -1;  // spec_debug_withhold_tile
+#endif
+
 constexpr int NT = 384;
 // Registers: 384 x 168 at launch, handed over as 208 to the softmax groups and
 // 88 to the third (2 x 208 + 88 = 3 x 168).
@@ -117,6 +121,7 @@ struct Ctl {
     uint64_t full[kMaxStages], empty[kMaxStages], clean[kMaxStages];
     uint64_t q_full, q_empty, s_full[2][2], p_full[2][2], pv[2], o_full[2], ask[2], groups, drain;
     uint32_t loads;  // ring entries filled
+    uint32_t asks;   // segments whose queries were asked for
     AttnScan scan;
     uint32_t tmem;
     int abort;
@@ -156,14 +161,15 @@ SV_DEV int halves_of(const Seg& s, int w) {
     return 2 * mine - (mine && has_last && live_of(s, cnt - 1) <= kHalfKv ? 1 : 0);
 }
 
-// Waits give up after some 2^22 polls (a tenth of a second and more), or once
-// `abort` is set. They poll without a suspension of their own: its wake-up costs
-// more than these short waits last.
+// Waits give up after some 2^18 polls (a poll that finds nothing takes up to
+// 2 us: half a second; 2^22 took 8 seconds), or once `abort` is set. They poll
+// without a suspension of their own: its wake-up costs more than these short
+// waits last.
 SV_DEV bool tc_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
     uint32_t n = 0;
 #pragma unroll 1
     while (!mbar_try_wait(bar, parity))
-        if (!(++n & 0xFFu) && (n >> 22 || (abort && *abort))) return false;
+        if (!(++n & 0xFFu) && (n >> 18 || (abort && *abort))) return false;
     return true;
 }
 // By whole warps: every lane gets the same answer.
@@ -206,10 +212,14 @@ SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CU
                 atomicOr(&c->flags[seg & 3], 2);
             }
             const unsigned who = __ballot_sync(0xFFFFFFFFu, there && id >= 0);
+            bool copy = there && id >= 0;
+#ifdef SPEC_DEBUG
+            copy = copy && !(blockIdx.x == 0 && (int)ring == g_withhold);  // the entry is never filled
+#endif
             if (!(ok = warp_wait(&c->empty[st], free_phase, &c->abort))) return;
             if (lane == 0) mbar_expect_tx(&c->full[st], __popc(who) * (uint32_t)ps * 128);
             __syncwarp();
-            if (there && id >= 0)
+            if (copy)
                 tma_load4(stages + st * Shape<D>::kTile + to, map, half * 64, (int)(pos & ps1), h, id, &c->full[st]);
             ++ring;
             if (++st == NS) {
@@ -540,8 +550,9 @@ SV_DEV void help(const AttnParams& p, Ctl* c, const CUtensorMap* mq, uint32_t qs
     constexpr uint32_t NS = Shape<D>::kStages;
     const int lane = threadIdx.x & 31, nodes = 128 / p.G;  // nodes of a half
     const uint32_t box = 128u * min(nodes, p.N) * p.G;     // bytes of 64 columns of them
-    uint32_t seg = 0, ring0 = 0, asked = 0;
+    uint32_t seg = 0, ring0 = 0, asked = 0, asks = 0;
     auto ask_q = [&](const Seg& s) {  // a segment's queries
+        ++asks;
         if (lane == 0) mbar_expect_tx(&c->q_full, box * (D / 64) * (s.dual ? 2 : 1));
         __syncwarp();
         if (lane < D / 64 * (s.dual ? 2 : 1)) {
@@ -595,6 +606,7 @@ SV_DEV void help(const AttnParams& p, Ctl* c, const CUtensorMap* mq, uint32_t qs
         if (ok && (ok = warp_wait(&c->q_empty, (seg - 1) & 1, &c->abort))) ask_q(c->seg[seg & 3]);
         if (!ok) c->abort = 1;
     }
+    if (lane == 0) c->asks = asks;
 }
 
 template <int D>
@@ -907,7 +919,8 @@ __global__ void __launch_bounds__(NT, 1)
         if (tid == 8 * 32)
             for (uint32_t r = c->loads > NS ? c->loads - NS : 0; r < c->loads; ++r)
                 tc_wait(&c->full[r % NS], (r / NS) & 1, nullptr);
-        if (tid == 9 * 32 || tid == 10 * 32) {
+        if (tid == 11 * 32 && c->asks) tc_wait(&c->q_full, (c->asks - 1) & 1, nullptr);
+        if ((warp == 9 || warp == 10) && elected()) {  // (the lane that issued the products)
             mma_commit(&c->drain);
             tc_wait(&c->drain, 0, nullptr);
         }
@@ -1005,3 +1018,12 @@ cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const
 SV_DEBUG_READER(attention_tc)
 
 }  // namespace sv
+
+extern "C" int spec_debug_withhold_tile(int j) {
+#ifdef SPEC_DEBUG
+    return cudaMemcpyToSymbol(sv::g_withhold, &j, sizeof(int)) == cudaSuccess ? 0 : -1;
+#else
+    (void)j;
+    return -1;
+#endif
+}
