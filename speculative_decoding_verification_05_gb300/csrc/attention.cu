@@ -26,6 +26,7 @@
 #include <algorithm>
 
 #include "attention.cuh"
+#include "mbar.cuh"
 #include "per_device.h"
 #include "specverify.h"
 
@@ -48,8 +49,6 @@ size_t simt_smem(int D) {
            (size_t)kRows * KV * 4;
 }
 
-SV_DEV uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 template <typename E>
 SV_DEV float4 lds4(const unsigned char* p);
 template <>
@@ -69,16 +68,6 @@ struct Two {
 };
 SV_DEV float lo2(uint64_t x) { return __uint_as_float((uint32_t)x); }
 SV_DEV float hi2(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
-SV_DEV uint64_t pack2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 SV_DEV uint64_t mul1(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -188,8 +177,8 @@ __global__ void __launch_bounds__(NT, 2) attn_simt_kernel(const __grid_constant_
             next_bad = false;
         }
         if (more) {
-            next_bad |= load_tile<E, KV>(p, next, ahead, smem_addr(ks) + st * KV * kstride,
-                                         smem_addr(vs) + st * KV * D * (int)sizeof(E), lv);
+            next_bad |= load_tile<E, KV>(p, next, ahead, smem_u32(ks) + st * KV * kstride,
+                                         smem_u32(vs) + st * KV * D * (int)sizeof(E), lv);
             if (fresh) {
                 const int vec = D * (int)sizeof(E) / 16;
                 const E* q = static_cast<const E*>(p.q);
@@ -197,7 +186,7 @@ __global__ void __launch_bounds__(NT, 2) attn_simt_kernel(const __grid_constant_
                 for (int i = tid; i < next.rows * vec; i += NT) {
                     const int r = i / vec, c = i - r * vec, node = (next.row0 + r) / p.G, g = (next.row0 + r) - node * p.G;
                     const long long row = ((long long)next.b * p.N + node) * (p.Hkv * p.G) + next.h * p.G + g;
-                    cp16(smem_addr(qs) + ((qb ^ 1) * kRows * vec + i) * 16, q + row * D + c * (16 / (int)sizeof(E)), 16);
+                    cp16(smem_u32(qs) + ((qb ^ 1) * kRows * vec + i) * 16, q + row * D + c * (16 / (int)sizeof(E)), 16);
                 }
             }
         }
@@ -441,8 +430,8 @@ __global__ void __launch_bounds__(NT, NG == 1 ? 2 : 1) attn_many_kernel(const __
             next_bad = false;
         }
         if (more) {
-            next_bad |= load_tile<E, KV>(p, next, ahead, smem_addr(ks) + st * KV * stride,
-                                         smem_addr(vs) + st * KV * D * (int)sizeof(E), lv);
+            next_bad |= load_tile<E, KV>(p, next, ahead, smem_u32(ks) + st * KV * stride,
+                                         smem_u32(vs) + st * KV * D * (int)sizeof(E), lv);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (!have) {  // while the first tile is on its way
@@ -612,7 +601,7 @@ __global__ void __launch_bounds__(NT, NG == 1 ? 2 : 1) attn_many_kernel(const __
                 for (int i = tid; i < sq.rows * vec; i += NT) {
                     const int r = i / vec, c = i - r * vec, node = (sq.row0 + r) / p.G, g = (sq.row0 + r) - node * p.G;
                     const long long row = ((long long)sq.b * p.N + node) * (p.Hkv * p.G) + sq.h * p.G + g;
-                    cp16(smem_addr(qs) + r * stride + c * 16, q + row * D + c * (16 / (int)sizeof(E)), 16);
+                    cp16(smem_u32(qs) + r * stride + c * 16, q + row * D + c * (16 / (int)sizeof(E)), 16);
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             }

@@ -279,6 +279,19 @@ SV_DEV float lse_of(float m2, float l) {
     return l > 0.f ? (m2 + log2f(l)) * 0.6931471805599453f : (l == 0.f ? __uint_as_float(0xFF800000u) : l + m2);
 }
 
+// Two floats as one operand of the packed instructions.
+SV_DEV uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+SV_DEV void unpack2(uint64_t r, float* x, float* y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(r)); }
+SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 template <typename E>
 SV_DEV void store4(E* dst, float4 x);
 template <>

@@ -471,17 +471,6 @@ SV_DEV void add_unclean(const AttnParams& p, const Seg& s, int node, char* out, 
     }
 }
 
-SV_DEV uint64_t pack2(float x, float y) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
-    return r;
-}
-SV_DEV void unpack2(uint64_t r, float* x, float* y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(r)); }
-SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
 SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -597,7 +586,7 @@ SV_DEV void help(const AttnParams& p, Ctl* c, const CUtensorMap* mq, uint32_t qs
             if (!(ok = warp_wait(&c->ask[w], asked >> w & 1, &c->abort))) break;  // (the tile is there)
             asked ^= 1u << w;
             clean_v<D>(c, s, stages + st * Shape<D>::kTile, i, (seg - 1) & 3);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            fence_proxy_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->clean[st]);
         }

@@ -43,11 +43,6 @@ SV_DEV void tmem_st32(uint32_t addr, const uint32_t (&x)[32]) {
                  "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "r"(x[8]), "r"(x[9]), "r"(x[10]), "r"(x[11]), "r"(x[12]), "r"(x[13]), "r"(x[14]), "r"(x[15]), "r"(x[16]), "r"(x[17]), "r"(x[18]), "r"(x[19]), "r"(x[20]), "r"(x[21]), "r"(x[22]), "r"(x[23]), "r"(x[24]), "r"(x[25]), "r"(x[26]), "r"(x[27]), "r"(x[28]), "r"(x[29]), "r"(x[30]), "r"(x[31])
                  : "memory");
 }
-SV_DEV void tmem_st8(uint32_t addr, const uint32_t (&x)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
-                 "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-                 : "memory");
-}
 
 // ---- matrix products: D[128 x N] (+)= A[128 x 16] B[N x 16]^T, bf16 in, fp32 sums.
 // Instruction descriptor: fp32 sums, bf16 operands, N, M = 128, B with its N
