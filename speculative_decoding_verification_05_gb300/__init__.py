@@ -196,6 +196,10 @@ def _check(rc):
         raise SpecError(msg)
 
 
+def _device():
+    return torch._C._cuda_getDevice()
+
+
 def _on_device_of(name):
     """The call runs with the device of its tensor `name` current: a launch goes
     to the current device, and the default stream's handle is the same on all."""
@@ -204,11 +208,14 @@ def _on_device_of(name):
 
         @functools.wraps(fn)
         def call(*args, **kw):
-            t = args[at] if len(args) > at else kw.get(name)
-            if getattr(t, "is_cuda", False) and t.get_device() != torch.cuda.current_device():
-                with torch.cuda.device(t.get_device()):
-                    return fn(*args, **kw)
-            return fn(*args, **kw)
+            try:
+                index = (args[at] if len(args) > at else kw[name]).get_device()   # (a host tensor's is -1)
+            except (AttributeError, KeyError):
+                index = -1   # no tensor: the call says so itself
+            if index < 0 or index == _device():
+                return fn(*args, **kw)
+            with torch.cuda.device(index):
+                return fn(*args, **kw)
         return call
     return wrap
 
@@ -638,7 +645,8 @@ def tree_attention(q, k_cache, v_cache, page_table, cache_len, mask=None, n_node
         n_nodes = _in(n_nodes, dev, index)
     if lens.shape != (B,) or (n_nodes is not None and n_nodes.shape != (B,)):
         raise SpecError("cache_len and n_nodes must be [B]")
-    o = _given(out, index, {"out": (q.shape, q.dtype), "lse": ((B, N, Hq), torch.float32), "status": ((B,), torch.int32)})
+    o = {} if out is None else _given(out, index, {"out": (q.shape, q.dtype), "lse": ((B, N, Hq), torch.float32),
+                                                   "status": ((B,), torch.int32)})
     if "out" not in o:
         o["out"] = torch.empty_like(q)
     if "status" not in o:

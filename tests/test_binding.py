@@ -40,7 +40,7 @@ def two_devices(monkeypatch):
         finally:
             CURRENT[0] = before
 
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: CURRENT[0])
+    monkeypatch.setattr(sv, "_device", lambda: CURRENT[0])
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(sv, "load_library", lambda path=None: object())
     monkeypatch.setattr(sv, "_library", lambda: object())
@@ -77,6 +77,15 @@ def test_calls_run_on_their_tensors_device(two_devices, name):
         CALLS[name]()
     assert e.value.current == 1 and CURRENT[0] == 1
     CURRENT[0] = 0
+
+
+@pytest.mark.parametrize("name", ["verify", "tree_attention", "cache_resize"])
+def test_what_is_no_tensor_raises_as_before(two_devices, name):
+    fn = getattr(sv, name)
+    with pytest.raises((TypeError, AttributeError)):
+        fn()
+    with pytest.raises((TypeError, AttributeError)):
+        fn(*[None] * 5)
 
 
 def test_signatures_and_names_are_kept():
