@@ -621,9 +621,10 @@ __global__ void __launch_bounds__(NT, NG == 1 ? 2 : 1) attn_many_kernel(const __
 // bound by the latency of dependent loads (the pieces come from L2), and a
 // thread's eight loads are a row's pieces; with many (JR = 32) by instructions,
 // and they are two pieces of four rows, so that a block's start is shared by
-// more. Calls with JR = 8 and 32: 16 trees of 512 rows 112.8 and 101.8 us; 16 of
-// 64 rows and 32 heads 83.2 and 81.7; one chain of 20 rows 13.7 and 15.6; one
-// tree of 244 rows in 19 pieces 106.5 and 111.7 (8 units: 64 blocks).
+// more. Calls with JR = 8 and 32: 16 trees of 512 rows 117.7 and 109.3 us; 16 of
+// 64 rows and 32 heads 80.0 and 78.5; 30 of 150 rows 35.1 and 33.0; one of 4000
+// rows 182 and 173; one chain of 20 rows 13.2 and 15.2; five of 28 rows 19.3 and
+// 21.1; one tree of 244 rows in 19 pieces 124 and 131 (8 units: 64 blocks).
 constexpr int kJoinNT = 256;
 constexpr int kJoinFew = 152 * 4;  // blocks of 8 rows that an SM runs side by side
 

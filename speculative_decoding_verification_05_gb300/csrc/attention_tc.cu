@@ -50,12 +50,12 @@
 // that do see them when the results are written.
 
 // What bounds it. One token of 64 sequences, contexts to 8192, 8 key heads of 4
-// query heads, 128 columns: memory (172 us, 6.2 TB/s of K and V). With 64 or
+// query heads, 128 columns: memory (176 us, 6.1 TB/s of K and V). With 64 or
 // more rows the softmax: a warp takes some 400 instructions a half, which at
 // one or two warps a scheduler last 1300 to 1900 cycles, mostly of instruction
 // latency; the tensor pipe is 36 to 50 % busy. 16 trees of 64 nodes, contexts
 // to 1900, 32 heads of one query head (64 rows, half of the product's 128):
-// 79.7 us (3.7 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 110 us (0.61
+// 78.6 us (3.7 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 107 us (0.63
 // PFLOP/s); a tree of 61 nodes over 100003 positions, 8 heads of 4: 124 us
 // (weights of one bf16 number, and a second only where it was heavy: 82.1, 103
 // and 106).
@@ -87,7 +87,7 @@ constexpr int NT = 384;
 constexpr int kGroupRegs = 208, kOtherRegs = 88;
 constexpr int kKv = 128;     // positions of a tile
 constexpr int kMaxStages = 10;
-constexpr int kExtra = 3, kExtraDual = 6;
+constexpr int kExtra = 3, kExtraDual = 4;
 constexpr int kWhole = 4;  // tiles of a unit that is not split
 constexpr float kKeep = 1.f + 0x1p-20f;  // a weight's second part is kKeep of it less its first
 constexpr float kSlack = 8.f;  // octaves of a score above the reference that raise it
@@ -978,10 +978,13 @@ cudaError_t launch_tc(const AttnParams& p, const AttnPlan& plan, const CUtensorM
 }  // namespace
 
 // What a unit's start and end cost, in tiles: more where both streams go over
-// the same tiles. Measured with 2, 3 and 5 (32 heads of 64 rows, alternate
-// tiles): 97.2, 89.4, 91.6 us; with 3, 5, 6 and 8 (same tiles): 118.4, 117.5,
-// 116.8, 118.5 (8 heads of 512 rows) and 114.7, 111.9, 110.4, 109.9 (one tree
-// of 244 rows over 100003 positions).
+// the same tiles. Measured with 2, 3 and 5 (alternate tiles): 16 trees of 64
+// rows, 32 heads 89.0, 78.5, 81.5 us; 48 of 48 rows, 12 heads 70.2, 72.8, 77.8; 8
+// of 100 rows, 16 heads of 64 columns 65.3, 53.2, 43.0; 200 single tokens, 4 x 6
+// heads 112.9, 114.3, 116.9. With 4, 6 and 8 (same tiles): 16 trees of 512 rows
+// 107.0, 109.3, 112.5; 10 of 450 rows 54.5, 55.8, 57.1; 3 of 600 rows, 64 columns
+// 149, 151, 155; one of 4000 rows 168, 173, 175; 30 of 150 rows 31.5, 33.0, 34.6;
+// one of 244 rows over 100003 positions 124 each.
 int attention_tc_extra(int group, int N) { return N * group > attention_tc_rows(group) / 2 ? kExtraDual : kExtra; }
 
 // Two halves of whole nodes, 128 rows at most each.

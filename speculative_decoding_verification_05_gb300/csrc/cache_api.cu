@@ -188,9 +188,11 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
     // Whole units: no more of them than CTAs, of `most` tiles at the most, and not
     // so few that a shared unit's part would be three tiles less (a join costs as
     // much). bf16, units of 8 rows and 128 columns, split and whole: 96 of 2 tiles
-    // 16.1 and 12.8 us, of 4 19.5 and 16.1; 8 of 4 tiles 13.3 and 14.7. float32
-    // tiles take longer than a join: 96 units of 2 tiles (64 columns) 12.0 and
-    // 10.0, of 4 14.0 and 17.8.
+    // 14.2 and 11.1 us, of 4 17.4 and 13.6; 40 of 4 13.9 and 13.1; 8 of 2 11.8 and
+    // 9.7. float32 tiles take longer than a join: 96 units of 2 tiles (64 columns)
+    // 11.8 and 10.0, of 4 14.1 and 17.8. The tiles are those that the page table's
+    // width allows (lengths are known on the device only): a table as wide as the
+    // longest sequence may get has its units split.
     auto whole = [&](sv::AttnPlan plan, int most) {
         const double units = (double)B * p.Hkv * ((N * p.G + plan.rows - 1) / plan.rows);
         const double tiles = std::ceil((double)max_pages * cache->page_size / plan.kv);
