@@ -51,9 +51,10 @@
 
 // What bounds it. One token of 64 sequences, contexts to 8192, 8 key heads of 4
 // query heads, 128 columns: memory (176 us, 6.1 TB/s of K and V). With 64 or
-// more rows the softmax: a warp takes some 400 instructions a half, which at
-// one or two warps a scheduler last 1300 to 1900 cycles, mostly of instruction
-// latency; the tensor pipe is 36 to 50 % busy. 16 trees of 64 nodes, contexts
+// more rows the way of a half from its scores over the softmax and its products
+// to the next scores in its place: a warp takes some 440 instructions, mostly of
+// latency at one or two warps a scheduler (issue 23 to 39 %), and the tensor
+// pipe is 34 to 61 % busy. 16 trees of 64 nodes, contexts
 // to 1900, 32 heads of one query head (64 rows, half of the product's 128):
 // 78.6 us (3.7 TB/s); contexts to 4000, 8 heads of 8 (512 rows): 107 us (0.63
 // PFLOP/s); a tree of 61 nodes over 100003 positions, 8 heads of 4: 124 us

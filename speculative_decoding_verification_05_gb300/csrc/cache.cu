@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(CT) append_kernel(const __grid_constant__ Appe
 // 16-byte column of one layer's K or V and walks the path in such batches:
 // eight rows in flight a thread, no barrier between them. Bound by latency: the
 // path, its pages, the rows (16 sequences, paths to 7, 32 layers, 8 heads of 128
-// columns, bf16: 4.3 us; 61 sequences, paths to 17, 12 layers, float32: 5.7 us).
+// columns, bf16: 4.4 us; 61 sequences, paths to 17, 12 layers, float32: 5.8 us).
 constexpr int kMoves = 8;
 
 __global__ void __launch_bounds__(CT) compact_kernel(const __grid_constant__ CompactParams p) {
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(PT) resize_kernel(const __grid_constant__ Pool
 
 // One CTA: the tables, counts and lengths of the forks, and for each the page
 // copy that is left to do. Its chain of dependent steps (lengths, tables, free
-// pages, tables again) bounds a small fork: 9.8 us of 12 forks with their copies
+// pages, tables again) bounds a small fork: 11.0 us of 12 forks with their copies
 // (8 layers).
 __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PoolParams p) {
     __shared__ int offs[kMaxF + 1];
