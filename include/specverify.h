@@ -116,7 +116,8 @@ enum {
     SPEC_MAX_HEAD_DIM = 256,  /* paged cache: elements of a head */
     SPEC_MAX_PAGE = 256,      /*              tokens of a page */
     SPEC_MAX_GROUP = 128,     /*              query heads on one key / value head */
-    SPEC_MAX_POOL_SEQS = 4096 /*              sequences of one resize or fork */
+    SPEC_MAX_POOL_SEQS = 4096, /*             sequences of one resize or fork */
+    SPEC_MAX_TOP = 32         /* log probabilities: alternatives of a row */
 };
 
 /* ------------------------------------------------------------------------
@@ -328,6 +329,36 @@ spec_status spec_sample(const void* logits, spec_dtype dtype, int B, int P, int 
                         uint32_t pos0, uint32_t purpose,
                         int32_t* tokens_out, int32_t* status,
                         void* workspace, size_t ws_bytes, spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_token_logprobs - log probabilities of given tokens (spec_verify's or
+ * spec_verify_tree's, with the target rows that they came from; or a prompt's),
+ * their ranks, the rows' entropies and their likeliest alternatives, under the
+ * distribution softmax(logits / temperature) of each row.
+ *
+ *   logits        [B, P, V]; B <= 2^24, P <= 65536, B x P <= 2^27
+ *   tokens        [B, P] int32; -1: the row has no token and is not read
+ *   temperature   > 0, finite
+ *   top           alternatives of a row, 0 .. min(V, SPEC_MAX_TOP)
+ * Outputs:
+ *   logprob       [B, P] natural logarithm of the token's probability (-inf
+ *                 for a logit of -inf); 0 for a row without a token
+ *   rank          [B, P] int32 (NULL allowed): how many tokens come before it
+ *                 in the order (logit descending, index ascending); -1 for a
+ *                 row without a token
+ *   entropy       [B, P] (NULL allowed) in nats; 0 for a row without a token
+ *   top_tokens    [B, P, top] int32, the first tokens of that order; -1 for a
+ *                 row without a token. NULL where top is 0
+ *   top_logprobs  [B, P, top]; -inf for a row without a token
+ *   status        [B] (NULL allowed): SPEC_OK, or SPEC_EDATA where a row that
+ *                 is read holds NaN or +inf or only -inf, or a token is neither
+ *                 -1 nor in [0, V). Such a row's outputs are NaN and -1; the
+ *                 sequence's other rows have theirs
+ * No workspace.
+ * ---------------------------------------------------------------------- */
+spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, const int32_t* tokens, int B, int P, int V,
+                                float temperature, int top, float* logprob, int32_t* rank, float* entropy,
+                                int32_t* top_tokens, float* top_logprobs, int32_t* status, spec_stream stream);
 
 /* ------------------------------------------------------------------------
  * spec_philox_uniform - the library's uniforms, for checking a host copy of

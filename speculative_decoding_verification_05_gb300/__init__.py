@@ -11,6 +11,7 @@ Entry points (same names as the C ABI in ``include/specverify.h``):
 * ``verify_tree``    greedy exact-match verification of a REST draft tree
 * ``verify_mentor``  the lossy, KL-bounded mentor variant
 * ``sample``         one draw per row from the transformed distribution
+* ``token_logprobs`` log probabilities, ranks, entropies, likeliest alternatives
 * ``tree_attention`` attention of the drafted nodes over a paged cache
 * ``cache_append``, ``cache_compact``, ``cache_resize``, ``cache_fork``
                      the paged cache itself, changed in place
@@ -39,6 +40,7 @@ DEBUG_LIB_PATH = os.path.join(_HERE, "libspecverify_debug.so")
 SPEC_OK, SPEC_EINVAL, SPEC_ECUDA, SPEC_ETIMEOUT, SPEC_EDATA, SPEC_EBOUNDS, SPEC_ENOPAGES = 0, 1, 2, 3, 4, 5, 6
 SPEC_F32, SPEC_BF16 = 0, 1
 MAX_TREE_N = 1024
+MAX_TOP = 32
 PURPOSE_ACCEPT, PURPOSE_RESAMPLE, PURPOSE_DRAFT = 0, 1, 2
 
 EXPORTED = [
@@ -46,7 +48,7 @@ EXPORTED = [
     "spec_verify_tree_workspace_size", "spec_verify_tree", "spec_tree_build", "spec_acceptance_rate",
     "spec_expected_tokens", "spec_walltime_factor", "spec_ops_factor", "spec_best_gamma",
     "spec_verify_mentor_workspace_size", "spec_verify_mentor",
-    "spec_sample_workspace_size", "spec_sample",
+    "spec_sample_workspace_size", "spec_sample", "spec_token_logprobs",
     "spec_tree_attention_workspace_size", "spec_tree_attention", "spec_cache_append", "spec_cache_compact",
     "spec_cache_resize", "spec_cache_fork_workspace_size", "spec_cache_fork",
     "spec_philox_uniform", "spec_verify_noalloc", "spec_status_string", "spec_last_cuda_error",
@@ -133,6 +135,8 @@ def load_library(path=None):
         lib.spec_sample.argtypes = [_P, _I, _I, _I, _I, SpecSampling, _U64, _U64, ctypes.c_uint32,
                                     ctypes.c_uint32, _P, _P, _P, _SZ, _P]
         lib.spec_sample.restype = _I
+        lib.spec_token_logprobs.argtypes = [_P, _I, _P, _I, _I, _I, ctypes.c_float, _I, _P, _P, _P, _P, _P, _P, _P]
+        lib.spec_token_logprobs.restype = _I
         lib.spec_verify_noalloc.argtypes = [_P, _P, _I, _P, _I, _I, _I, SpecSampling, _U64, _U64,
                                             _P, _P, _P, _P, _P, _P]
         lib.spec_verify_noalloc.restype = _I
@@ -527,6 +531,48 @@ def sample(logits, temperature=1.0, top_p=1.0, top_k=0, seed=0, offset=0, pos0=0
     return sg.back(o)
 
 
+@_on_device_of("logits")
+def token_logprobs(logits, tokens, top=0, temperature=1.0):
+    """Log probabilities of tokens [B, P] under softmax(logits [B, P, V] / temperature).
+
+    Token -1 marks a row that has none and is not read: ``verify``'s tokens go
+    with its target as they are. Returns logprob [B, P] (0 where there is no
+    token), rank [B, P] (tokens before it by logit, then by index; -1), entropy
+    [B, P] in nats (0), status [B] and, with ``top`` <= 32, the likeliest
+    top_tokens and top_logprobs [B, P, top] (-1, -inf). A row with NaN or +inf,
+    or only -inf, or a token outside the vocabulary gives NaN and -1 and its
+    sequence SPEC_EDATA.
+    """
+    lib = _library()
+    host = not logits.is_cuda
+    sg = _Staging(logits) if host else None
+    dev = sg.device if host else logits.device
+    index = dev.index
+    dt = _dtype_code(logits)
+    if logits.dim() != 3:
+        raise SpecError("logits must be [B, P, V]")
+    B, P, V = logits.shape
+    if tokens.shape != (B, P):
+        raise SpecError("tokens must be [B, P]")
+    if not 0 <= top <= min(V, MAX_TOP):
+        raise SpecError(f"top must be in 0 .. min(V, {MAX_TOP})")
+    logits = sg.dev(logits) if host else logits.contiguous()
+    tokens = _in(tokens, dev, index)
+    f32, i32 = dict(dtype=torch.float32, device=dev), dict(dtype=torch.int32, device=dev)
+    o = {"logprob": torch.empty((B, P), **f32), "rank": torch.empty((B, P), **i32),
+         "entropy": torch.empty((B, P), **f32), "status": torch.empty((B,), **i32)}
+    if top:
+        o["top_tokens"], o["top_logprobs"] = torch.empty((B, P, top), **i32), torch.empty((B, P, top), **f32)
+    rc = lib.spec_token_logprobs(logits.data_ptr(), dt, tokens.data_ptr(), B, P, V, temperature, top,
+                                 o["logprob"].data_ptr(), o["rank"].data_ptr(), o["entropy"].data_ptr(),
+                                 o["top_tokens"].data_ptr() if top else None,
+                                 o["top_logprobs"].data_ptr() if top else None, o["status"].data_ptr(),
+                                 _raw_stream(index))
+    if rc:
+        _check(rc)
+    return sg.back(o) if host else o
+
+
 def philox_uniform(seed, row0, position, purpose, n, device=None):
     """The library's uniforms U(seed, row0 + i, position, purpose), i < n (device float32)."""
     lib = load_library()
@@ -790,6 +836,6 @@ def cache_fork(k_cache, v_cache, page_table, cache_len, page_refs, src, dst):
 
 
 __all__ = ["use_library", "DEBUG_LIB_PATH", "philox_uniform", "verify", "verify_tree", "tree_build", "acceptance_rate", "expected_tokens",
-           "walltime_factor", "ops_factor", "best_gamma", "verify_mentor", "sample", "tree_attention", "cache_append", "cache_compact",
+           "walltime_factor", "ops_factor", "best_gamma", "verify_mentor", "sample", "token_logprobs", "tree_attention", "cache_append", "cache_compact",
            "cache_resize", "cache_fork", "load_library", "workspace",
            "SpecError", "SpecSampling", "SpecCache", "EXPORTED", "LIB_PATH"]

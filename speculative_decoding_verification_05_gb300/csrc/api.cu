@@ -11,6 +11,7 @@
 #include "attention.cuh"
 #include "cache.cuh"
 #include "common.cuh"
+#include "logprobs.cuh"
 #include "specverify.h"
 
 namespace sv {
@@ -370,7 +371,8 @@ int spec_debug_failures(int* line) {
     using Reader = cudaError_t (*)(unsigned int*, unsigned int*);
     const Reader readers[] = {sv::debug_read_rows, sv::debug_read_rows_smem, sv::debug_read_argmax,
                               sv::debug_read_mentor, sv::debug_read_beta, sv::debug_read_tree_build,
-                              sv::debug_read_attention, sv::debug_read_attention_tc, sv::debug_read_cache};
+                              sv::debug_read_attention, sv::debug_read_attention_tc, sv::debug_read_cache,
+                              sv::debug_read_logprobs};
     long long total = 0;
     int first = 0;
     for (const Reader rd : readers) {
@@ -639,6 +641,42 @@ spec_status spec_sample(const void* logits, spec_dtype dtype, int B, int P, int 
     p.status = status;
     p.sample_out = tokens_out;
     return run_rows(p, dt, workspace, w, st);
+}
+
+spec_status spec_token_logprobs(const void* logits, spec_dtype dtype, const int32_t* tokens, int B, int P, int V,
+                                float temperature, int top, float* logprob, int32_t* rank, float* entropy,
+                                int32_t* top_tokens, float* top_logprobs, int32_t* status, spec_stream stream) {
+    if (!dtype_ok(dtype) || B < 1 || B > (1 << 24) || P < 1 || P > (1 << 16) || (long long)B * P > (1 << 27) || V < 1 ||
+        V > SPEC_MAX_V || top < 0 || top > SPEC_MAX_TOP || top > V)
+        return SPEC_EINVAL;
+    const float c2 = kLog2e / temperature, inv_t = 1.f / temperature;
+    if (!finite(temperature) || !(temperature > 0.f) || !finite(c2) || !finite(inv_t) || !(inv_t > 0.f)) return SPEC_EINVAL;
+    if (!logits || !tokens || !logprob || (top > 0 && (!top_tokens || !top_logprobs))) return SPEC_EINVAL;
+    if (!aligned(logits, esize(dtype)) || !aligned(tokens, 4) || !aligned(logprob, 4) || !aligned(rank, 4) ||
+        !aligned(entropy, 4) || !aligned(top_tokens, 4) || !aligned(top_logprobs, 4) || !aligned(status, 4))
+        return SPEC_EINVAL;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (status && P > 1) {  // (a sequence's rows only ever raise it)
+        const cudaError_t e = cudaMemsetAsync(status, 0, (size_t)B * sizeof(int32_t), st);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    sv::LogprobParams p = {};
+    p.logits = logits;
+    p.tokens = tokens;
+    p.rows = (long long)B * P;
+    p.P = P;
+    p.V = V;
+    p.top = top;
+    p.c2 = c2;
+    p.inv_t = inv_t;
+    p.logprob = logprob;
+    p.rank = rank;
+    p.entropy = entropy;
+    p.top_tokens = top_tokens;
+    p.top_logprobs = top_logprobs;
+    p.status = status;
+    const cudaError_t e = sv::launch_logprobs(p, dtype == SPEC_F32 ? 0 : 1, st);
+    return e == cudaSuccess ? SPEC_OK : cuda_fail(e);
 }
 
 spec_status spec_philox_uniform(uint64_t seed, uint64_t row0, uint32_t position, uint32_t purpose,
