@@ -497,6 +497,65 @@ spec_status spec_cache_append(const void* k, const void* v, const spec_cache* ca
                               spec_stream stream);
 
 /* ------------------------------------------------------------------------
+ * spec_rotary_turns - rotary frequencies: turns[j], j < dim / 2, is how far pair
+ * j turns a position, in units of 2^-64 of a full turn (modulo whole turns), and
+ * *factor what cosine and sine are multiplied by. Host arithmetic, no GPU; the
+ * table is copied to the device once and given to spec_cache_append_rotary. With
+ * f_j = base^(-2 j / dim) radians a position:
+ *   SPEC_ROTARY_PLAIN   f_j
+ *   SPEC_ROTARY_LINEAR  f_j / scale
+ *   SPEC_ROTARY_NTK     base scale^(dim / (dim - 2)) in the place of base
+ *   SPEC_ROTARY_YARN    f_j k + f_j / scale (1 - k), k falling from 1 to 0 in j
+ *                       between the pairs (rounded outwards) that turn 32 times
+ *                       and once in `original` positions; factor 0.1 ln scale + 1
+ *   SPEC_ROTARY_BANDS   the same mix by wavelength 2 pi / f_j: k = 1 below
+ *                       original / 4, 0 above original, linear in f_j between
+ * dim even, 2 .. SPEC_MAX_HEAD_DIM; base > 1; scale >= 1 (not read for PLAIN);
+ * original > 0 (read for YARN and BANDS). Otherwise SPEC_EINVAL.
+ * ---------------------------------------------------------------------- */
+typedef enum {
+    SPEC_ROTARY_PLAIN = 0,
+    SPEC_ROTARY_LINEAR = 1,
+    SPEC_ROTARY_NTK = 2,
+    SPEC_ROTARY_YARN = 3,
+    SPEC_ROTARY_BANDS = 4
+} spec_rotary_scaling;
+
+spec_status spec_rotary_turns(int dim, double base, spec_rotary_scaling scaling, double scale, double original,
+                              uint64_t* turns, float* factor);
+
+/* ------------------------------------------------------------------------
+ * spec_cache_append_rotary - spec_cache_append with rotary positions: node i of
+ * sequence b is at position p = positions[b] + depth[b][i] of its text, its
+ * queries are rotated to q_out, its keys rotated and written to cache position
+ * cache_len[b] + i, its values written there as they are. The first `dim`
+ * columns of a head are rotated in pairs (j, j + dim / 2) or, interleaved, (2 j,
+ * 2 j + 1), by p turns[j] 2^-64 turns:
+ *   (x, y) -> factor (x cos - y sin, y cos + x sin),
+ * in fp32 (the angle exactly), rounded once to the type.
+ *   q             [B, N, q_heads, head_dim]; k, v [B, N, kv_heads, head_dim]
+ *   turns         [dim / 2] device (spec_rotary_turns), 8-byte aligned; 2 <= dim
+ *                 <= head_dim, even
+ *   positions     [B] int32: the position of node 0; NULL: cache_len (they
+ *                 differ once positions were evicted from the cache)
+ *   depth         [B, N] int32 (spec_tree_build's, read for i < n_nodes[b]);
+ *                 NULL: i, a chain
+ * Outputs:
+ *   q_out         [B, N, q_heads, head_dim], 16-byte aligned, not overlapping q;
+ *                 zero from n_nodes[b] on, NaN for a sequence with bad data
+ *   status        [B] SPEC_OK, or SPEC_EDATA as spec_cache_append's and for a
+ *                 position outside [0, 2^31) (no key or value is written); NULL
+ *                 allowed
+ * Other arguments and limits as spec_cache_append.
+ * ---------------------------------------------------------------------- */
+spec_status spec_cache_append_rotary(const void* q, const void* k, const void* v, const spec_cache* cache,
+                                     spec_dtype dtype, const int32_t* page_table, int64_t table_stride, int max_pages,
+                                     const int32_t* cache_len, const uint64_t* turns, int dim, int interleaved,
+                                     float factor, const int32_t* positions, const int32_t* depth,
+                                     const int32_t* n_nodes, int B, int N, int q_heads, void* q_out, int32_t* status,
+                                     spec_stream stream);
+
+/* ------------------------------------------------------------------------
  * spec_cache_compact - after verification: the entries of the accepted path's
  * nodes moved to the positions after the context, in every layer,
  *   position L + i  <-  position L + path_nodes[b][i],   i <= accept_len[b],
@@ -517,6 +576,63 @@ spec_status spec_cache_compact(const spec_cache* cache, spec_dtype dtype, const 
                                int64_t table_stride, int max_pages, const int32_t* cache_len,
                                const int32_t* accept_len, const int32_t* path_nodes, int B, int W,
                                int32_t* new_len, int32_t* status, spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_cache_weigh - after verification: the attention weights that a step's
+ * accepted rows gave to every position, added up over the rows and over the
+ * query heads of each key / value head (what spec_cache_evict chooses by):
+ *   weights[b, g, t] += sum_r sum_{h of g} exp(scale q_i(r),h . k_t - lse[b, i(r), h]),
+ * over the rows r <= accept_len[b], node i(r) = path_nodes[b][r], with t <= L + r,
+ * L = cache_len[b] (the length before the step). The accepted entries lie at L +
+ * r already (spec_cache_compact).
+ *   q, lse        spec_tree_attention's argument and result, [B, N, q_heads,
+ *                 head_dim] and [B, N, q_heads]; a row whose lse is -inf has no
+ *                 weights
+ *   cache         layers == 1; v is not read
+ *   accept_len    [B] int32, -1 (no row) .. min(N, W) - 1; NULL: N - 1, which
+ *                 needs path_nodes NULL (a chain or one token of plain decoding)
+ *   path_nodes    [B, W] int32; NULL: i(r) = r, a chain
+ *   weights       [B, kv_heads, capacity] float; only t < L + accept_len[b] + 1
+ *                 is touched
+ *   status        [B] SPEC_OK, or SPEC_EDATA for a length, path or page out of
+ *                 range, or positions past the capacity (nothing is added; by a
+ *                 page out of range, nothing at its own positions); NULL allowed
+ * Other arguments and limits as spec_tree_attention. Scores and sums are fp32.
+ * ---------------------------------------------------------------------- */
+spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* cache, spec_dtype dtype,
+                             const int32_t* page_table, int64_t table_stride, int max_pages, const int32_t* cache_len,
+                             const int32_t* accept_len, const int32_t* path_nodes, int B, int N, int W, int q_heads,
+                             float scale, float* weights, int64_t capacity, int32_t* status, spec_stream stream);
+
+/* ------------------------------------------------------------------------
+ * spec_cache_evict - a bounded cache: every sequence with more than budget[b]
+ * positions keeps budget[b] of them, in every layer and for every key / value
+ * head by itself: its first `sink`, its last `recent`, and of those between them
+ * the ones with the largest weights (ties: the lowest position; NaN counts as
+ * larger than all). Kept entries move to positions 0, 1, .. in their order, keys,
+ * values and weights, and the weights of the positions from budget[b] to the old
+ * length are set to zero. Pages are released by spec_cache_resize. Rotary
+ * positions are in the keys already: later tokens keep counting by the text
+ * (spec_cache_append_rotary's positions).
+ *   budget        [B] int32, each at least sink + recent
+ *   weights       [layers, B, kv_heads, capacity] float, changed in place
+ *   capacity      at least every cache_len
+ *   new_len       [B] int32: min(cache_len, budget); -1 on SPEC_EDATA. new_len
+ *                 and status overlap neither each other nor an input
+ *   status        [B] SPEC_OK, or SPEC_EDATA for a length, budget or page out of
+ *                 range, or, with page_refs, a page of the positions sink ..
+ *                 budget - 1 of a sequence to be shortened whose count is not 1
+ *                 (nothing moves); NULL allowed
+ *   workspace     >= spec_cache_evict_workspace_size(layers, B, kv_heads,
+ *                 capacity) bytes
+ * layers x B x kv_heads <= 2^30.
+ * ---------------------------------------------------------------------- */
+size_t spec_cache_evict_workspace_size(int layers, int B, int kv_heads, int64_t capacity);
+
+spec_status spec_cache_evict(const spec_cache* cache, spec_dtype dtype, const int32_t* page_table,
+                             int64_t table_stride, int max_pages, const int32_t* cache_len, const int32_t* budget,
+                             int sink, int recent, float* weights, int64_t capacity, int B, int32_t* new_len,
+                             int32_t* status, void* workspace, size_t ws_bytes, spec_stream stream);
 
 /* ------------------------------------------------------------------------
  * spec_cache_resize - the number of pages that sequences hold: sequence

@@ -13,6 +13,11 @@ Entry points (same names as the C ABI in ``include/specverify.h``):
 * ``sample``         one draw per row from the transformed distribution
 * ``token_logprobs`` log probabilities, ranks, entropies, likeliest alternatives
 * ``tree_attention`` attention of the drafted nodes over a paged cache
+* ``rotary``, ``cache_append_rotary``
+                     the same append with rotary positions, queries rotated
+* ``cache_weigh``, ``cache_evict``
+                     accepted rows' attention weights added up, and the
+                     positions of the least weight evicted
 * ``cache_append``, ``cache_compact``, ``cache_resize``, ``cache_fork``
                      the paged cache itself, changed in place
 
@@ -22,10 +27,12 @@ A paged cache, its page table and its reference counts live on the GPU; a call
 runs on their device, whichever is current.
 """
 
+import collections
 import contextlib
 import ctypes
 import functools
 import inspect
+import math
 import os
 import struct
 import threading
@@ -50,6 +57,8 @@ EXPORTED = [
     "spec_verify_mentor_workspace_size", "spec_verify_mentor",
     "spec_sample_workspace_size", "spec_sample", "spec_token_logprobs",
     "spec_tree_attention_workspace_size", "spec_tree_attention", "spec_cache_append", "spec_cache_compact",
+    "spec_rotary_turns", "spec_cache_append_rotary", "spec_cache_weigh", "spec_cache_evict_workspace_size",
+    "spec_cache_evict",
     "spec_cache_resize", "spec_cache_fork_workspace_size", "spec_cache_fork",
     "spec_philox_uniform", "spec_verify_noalloc", "spec_status_string", "spec_last_cuda_error",
     "spec_version", "spec_debug_build", "spec_debug_failures", "spec_debug_withhold_copy", "spec_debug_withhold_tile",
@@ -150,8 +159,20 @@ def load_library(path=None):
         lib.spec_tree_attention.restype = _I
         lib.spec_cache_append.argtypes = [_P, _P, _C, _I, _P, _I64, _I, _P, _P, _I, _I, _P, _P]
         lib.spec_cache_append.restype = _I
+        lib.spec_rotary_turns.argtypes = [_I, _D, _I, _D, _D, ctypes.POINTER(_U64), ctypes.POINTER(ctypes.c_float)]
+        lib.spec_rotary_turns.restype = _I
+        lib.spec_cache_append_rotary.argtypes = [_P, _P, _P, _C, _I, _P, _I64, _I, _P, _P, _I, _I, ctypes.c_float, _P, _P,
+                                                 _P, _I, _I, _I, _P, _P, _P]
+        lib.spec_cache_append_rotary.restype = _I
         lib.spec_cache_compact.argtypes = [_C, _I, _P, _I64, _I, _P, _P, _P, _I, _I, _P, _P, _P]
         lib.spec_cache_compact.restype = _I
+        lib.spec_cache_weigh.argtypes = [_P, _P, _C, _I, _P, _I64, _I, _P, _P, _P, _I, _I, _I, _I, ctypes.c_float, _P, _I64,
+                                         _P, _P]
+        lib.spec_cache_weigh.restype = _I
+        lib.spec_cache_evict_workspace_size.argtypes = [_I, _I, _I, _I64]
+        lib.spec_cache_evict_workspace_size.restype = _SZ
+        lib.spec_cache_evict.argtypes = [_C, _I, _P, _I64, _I, _P, _P, _I, _I, _P, _I64, _I, _P, _P, _P, _SZ, _P]
+        lib.spec_cache_evict.restype = _I
         lib.spec_cache_resize.argtypes = [_P, _I64, _I, _I, _P, _I, _I, _P, _P, _I, _P, _P]
         lib.spec_cache_resize.restype = _I
         lib.spec_cache_fork_workspace_size.argtypes = [_I]
@@ -745,6 +766,85 @@ def cache_append(k, v, k_cache, v_cache, page_table, cache_len, n_nodes=None, pa
     return {"status": status}
 
 
+Rotary = collections.namedtuple("Rotary", "turns interleaved factor")
+Rotary.__doc__ = """Rotary frequencies on a device: turns [dim / 2] int64 (2^-64 of a turn a position), the pairs'
+layout and the factor of cosine and sine. Made by ``rotary``, kept with the model."""
+_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+def rotary(dim, base=10000.0, interleaved=False, scaling=None, scale=1.0, original=0.0, frequencies=None, device=None):
+    """Rotary frequencies of the first ``dim`` columns of a head, for ``cache_append_rotary``.
+
+    Pairs are columns (j, j + dim / 2) or, ``interleaved``, (2 j, 2 j + 1); pair j
+    turns by base^(-2 j / dim) radians a position. ``scaling`` for long contexts:
+    "linear" (frequencies divided by ``scale``), "ntk" (a larger base), "yarn" and
+    "bands" (slow pairs divided, fast ones kept; ``original``: the length that the
+    model was trained on). Or ``frequencies``: dim / 2 radians a position.
+    """
+    if scaling not in _SCALINGS:
+        raise SpecError(f"scaling must be one of {list(_SCALINGS)}")
+    if dim < 2 or dim % 2:
+        raise SpecError("dim must be even and positive")
+    factor, turns = ctypes.c_float(1.0), (_U64 * (dim // 2))()
+    if frequencies is None:
+        _check(load_library().spec_rotary_turns(dim, base, _SCALINGS[scaling], scale, original, turns, ctypes.byref(factor)))
+    else:
+        f = torch.as_tensor(frequencies, dtype=torch.float64).tolist()
+        if scaling is not None or not isinstance(f, list) or len(f) != dim // 2 or not all(map(math.isfinite, f)):
+            raise SpecError("frequencies must be dim / 2 finite numbers, without a scaling")
+        turns[:] = [int(x / (2.0 * math.pi) % 1.0 * 2.0 ** 64) % 2 ** 64 for x in f]
+    signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return Rotary(torch.tensor(signed, dtype=torch.int64, device=device), bool(interleaved), factor.value)
+
+
+@_on_device_of("k_cache")
+def cache_append_rotary(q, k, v, k_cache, v_cache, page_table, cache_len, rotary, positions=None, depth=None,
+                        n_nodes=None, page_refs=None):
+    """``cache_append`` with rotary positions: queries q [B, N, heads, D] rotated, keys
+    k [B, N, kv_heads, D] rotated into the cache, values as they are.
+
+    Node i is at position positions[b] + depth[b, i] of the text (``positions``
+    [B], None: cache_len, which differs once ``cache_evict`` has shortened the
+    cache; ``depth`` [B, N] ``tree_build``'s, None: i, a chain). ``rotary``: the
+    frequencies (the function of this name). Returns q (rotated; zero from
+    n_nodes[b] on) and status [B] as ``cache_append``.
+    """
+    lib = _library()
+    cache, sh, dt = _cache_args(k_cache, v_cache, 0, page_refs)
+    if k.dim() != 4 or k.shape != v.shape or k.shape[2:] != sh[2:] or k.dtype is not k_cache.dtype or \
+            v.dtype is not k_cache.dtype:
+        raise SpecError("k and v must be [B, N, kv_heads, head_dim] of the cache's dtype")
+    B, N = k.shape[:2]
+    if q.dim() != 4 or q.shape[:2] != (B, N) or q.shape[3] != sh[3] or q.dtype is not k_cache.dtype:
+        raise SpecError("q must be [B, N, heads, head_dim] of the cache's dtype")
+    dev, index = k_cache.device, k_cache.get_device()
+    table, stride, width = _table_args(page_table, B, index)
+    turns = rotary.turns
+    if turns.dtype is not torch.int64 or turns.dim() != 1 or turns.get_device() != index or not turns.is_contiguous():
+        raise SpecError("rotary must be of the cache's device (rotary(..., device=))")
+    q, k, v = _in(q, dev, index, q.dtype), _in(k, dev, index, k.dtype), _in(v, dev, index, v.dtype)
+    ints = [None if t is None else _in(t, dev, index) for t in (cache_len, positions, n_nodes)]
+    if any(t is not None and t.shape != (B,) for t in ints):
+        raise SpecError("cache_len, positions and n_nodes must be [B]")
+    lens, positions, n_nodes = ints
+    if depth is not None:
+        depth = _in(depth, dev, index)
+        if depth.shape != (B, N):
+            raise SpecError("depth must be [B, N]")
+    out = torch.empty_like(q)
+    status = torch.empty((B,), dtype=torch.int32, device=dev)
+    rc = lib.spec_cache_append_rotary(q.data_ptr(), k.data_ptr(), v.data_ptr(), cache, dt, table, stride, width,
+                                      lens.data_ptr(), turns.data_ptr(), 2 * turns.shape[0], rotary.interleaved,
+                                      rotary.factor, None if positions is None else positions.data_ptr(),
+                                      None if depth is None else depth.data_ptr(),
+                                      None if n_nodes is None else n_nodes.data_ptr(), B, N, q.shape[2],
+                                      out.data_ptr(), status.data_ptr(), _raw_stream(index))
+    if rc:
+        _check(rc)
+    return {"q": out, "status": status}
+
+
 @_on_device_of("k_cache")
 def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_nodes=None, page_refs=None):
     """Keep an accepted path in caches [layers, pages, page_size, kv_heads, D], in
@@ -770,6 +870,88 @@ def cache_compact(k_cache, v_cache, page_table, cache_len, accept_len, path_node
                                 None if path is None else path.data_ptr(), B,
                                 MAX_TREE_N if path is None else path.shape[1], new_len.data_ptr(), status.data_ptr(),
                                 _raw_stream(index))
+    if rc:
+        _check(rc)
+    return {"cache_len": new_len, "status": status}
+
+
+def _weights(weights, shape, index):
+    """Pointer and capacity of float32 weights shape + [capacity], changed in place."""
+    sh = tuple(weights.shape)
+    if weights.dtype is not torch.float32 or len(sh) != len(shape) + 1 or sh[:-1] != shape or \
+            weights.get_device() != index or not weights.is_contiguous():
+        raise SpecError(f"weights must be a contiguous float32 tensor {[*shape, 'capacity']} on the cache's device")
+    return weights.data_ptr(), sh[-1]
+
+
+@_on_device_of("k_cache")
+def cache_weigh(q, lse, k_cache, page_table, cache_len, weights, accept_len=None, path_nodes=None, scale=None):
+    """Add the accepted rows' attention weights to weights [B, kv_heads, capacity], in place:
+    weights[b, g, t] += sum over rows r <= accept_len[b] with t <= L + r and the
+    query heads of g of exp(scale q . k_t - lse).
+
+    q [B, N, heads, D] and lse [B, N, heads] are ``tree_attention``'s (with_lse),
+    k_cache one layer's, cache_len the length L before the step. Row r is node
+    path_nodes[b, r] (``verify_tree``'s, after ``cache_compact``; None: r), and
+    accept_len -1 .. the last row's number (None: all N rows of a chain). Returns
+    status [B].
+    """
+    lib = _library()
+    cache, sh, dt = _cache_args(k_cache, k_cache, 0)
+    if q.dim() != 4 or q.shape[3] != sh[3] or q.shape[2] % sh[2] != 0 or q.dtype is not k_cache.dtype:
+        raise SpecError("q must be [B, N, heads, head_dim] of the cache's dtype, heads a multiple of kv_heads")
+    B, N, Hq, D = q.shape
+    dev, index = k_cache.device, k_cache.get_device()
+    table, stride, width = _table_args(page_table, B, index)
+    w, capacity = _weights(weights, (B, sh[2]), index)
+    q, z, lens = _in(q, dev, index, q.dtype), _in(lse, dev, index, torch.float32), _in(cache_len, dev, index)
+    acc = None if accept_len is None else _in(accept_len, dev, index)
+    path = None if path_nodes is None else _in(path_nodes, dev, index)
+    if z.shape != (B, N, Hq):
+        raise SpecError("lse must be [B, N, heads]")
+    if lens.shape != (B,) or (acc is not None and acc.shape != (B,)) or \
+            (path is not None and (acc is None or path.dim() != 2 or path.shape[0] != B)):
+        raise SpecError("cache_len and accept_len must be [B], path_nodes (with accept_len) [B, W]")
+    status = torch.empty((B,), dtype=torch.int32, device=dev)
+    rc = lib.spec_cache_weigh(q.data_ptr(), z.data_ptr(), cache, dt, table, stride, width, lens.data_ptr(),
+                              None if acc is None else acc.data_ptr(), None if path is None else path.data_ptr(), B, N,
+                              N if path is None else path.shape[1], Hq, D ** -0.5 if scale is None else scale, w, capacity,
+                              status.data_ptr(), _raw_stream(index))
+    if rc:
+        _check(rc)
+    return {"status": status}
+
+
+@_on_device_of("k_cache")
+def cache_evict(k_cache, v_cache, page_table, cache_len, weights, budget, sink=0, recent=0, page_refs=None):
+    """Shorten sequences of more than budget[b] positions to budget[b], in place, in
+    caches [layers, pages, page_size, kv_heads, D]: every layer and head keeps its
+    first ``sink``, its last ``recent`` and the heaviest positions between them by
+    weights [layers, B, kv_heads, capacity] (``cache_weigh``'s of every layer), in
+    their order.
+
+    Weights move along, those past the new length become zero. ``budget``: [B], or
+    a number for all. With ``page_refs`` a sequence whose entries would move into a
+    shared page is refused. Returns cache_len [B] (-1 on a data error) and status
+    [B]; ``cache_resize`` then releases the pages.
+    """
+    lib = _library()
+    cache, sh, dt = _cache_args(k_cache, v_cache, 1, page_refs)
+    B = page_table.shape[0]
+    dev, index = k_cache.device, k_cache.get_device()
+    table, stride, width = _table_args(page_table, B, index)
+    w, capacity = _weights(weights, (sh[0], B, sh[3]), index)
+    lens = _in(cache_len, dev, index)
+    most = _in(budget, dev, index) if torch.is_tensor(budget) else torch.full((B,), budget, dtype=torch.int32, device=dev)
+    if lens.shape != (B,) or most.shape != (B,):
+        raise SpecError("cache_len and budget must be [B]")
+    new_len = torch.empty((B,), dtype=torch.int32, device=dev)
+    status = torch.empty((B,), dtype=torch.int32, device=dev)
+    raw = _raw_stream(index)
+    with _turn(index, raw):
+        ws = _scratch(lib.spec_cache_evict_workspace_size(sh[0], B, sh[3], capacity), dev, index, raw)
+        rc = lib.spec_cache_evict(cache, dt, table, stride, width, lens.data_ptr(), most.data_ptr(), sink, recent, w,
+                                  capacity, B, new_len.data_ptr(), status.data_ptr(), ws.data_ptr(), ws.numel(), raw)
     if rc:
         _check(rc)
     return {"cache_len": new_len, "status": status}
@@ -836,6 +1018,7 @@ def cache_fork(k_cache, v_cache, page_table, cache_len, page_refs, src, dst):
 
 
 __all__ = ["use_library", "DEBUG_LIB_PATH", "philox_uniform", "verify", "verify_tree", "tree_build", "acceptance_rate", "expected_tokens",
-           "walltime_factor", "ops_factor", "best_gamma", "verify_mentor", "sample", "token_logprobs", "tree_attention", "cache_append", "cache_compact",
+           "walltime_factor", "ops_factor", "best_gamma", "verify_mentor", "sample", "token_logprobs", "tree_attention", "cache_append", "rotary", "Rotary",
+           "cache_append_rotary", "cache_compact", "cache_weigh", "cache_evict",
            "cache_resize", "cache_fork", "load_library", "workspace",
            "SpecError", "SpecSampling", "SpecCache", "EXPORTED", "LIB_PATH"]

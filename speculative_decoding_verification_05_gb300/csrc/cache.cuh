@@ -28,6 +28,26 @@ struct AppendParams {
     int B, N, max_pages;
 };
 
+struct RotaryParams {
+    CacheView c;
+    const char* q;  // [B, N, q_heads, D]
+    const char* k;  // [B, N, heads, D]
+    const char* v;
+    char* q_out;
+    const unsigned long long* turns;  // [half] 2^-64 of a turn a position
+    float factor;
+    int half, interleaved, q_heads;
+    const int32_t* table;
+    long long table_stride;
+    const int32_t* cache_len;
+    const int32_t* positions;  // [B] or null (cache_len)
+    const int32_t* depth;      // [B, N] or null (the node's number)
+    const int32_t* n_nodes;
+    int32_t* status;
+    int B, N, max_pages;
+    int tokens;  // of a block (set by the launcher)
+};
+
 struct CompactParams {
     CacheView c;
     const int32_t* table;
@@ -38,6 +58,22 @@ struct CompactParams {
     int32_t* new_len;
     int32_t* status;
     int B, W, max_pages;
+};
+
+struct EvictParams {
+    CacheView c;
+    const int32_t* table;
+    long long table_stride;
+    const int32_t* cache_len;  // [B]
+    const int32_t* budget;     // [B]
+    int sink, recent;
+    float* weights;      // [layers, B, heads, capacity]
+    long long capacity;
+    int32_t* new_len;
+    int32_t* status;
+    int32_t* list;  // [layers, B, heads, capacity] kept positions
+    int2* jobs;     // [layers, B, heads] first entry of the list that moves, entries
+    int B, max_pages;
 };
 
 struct PoolParams {
@@ -57,9 +93,12 @@ struct PoolParams {
 };
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t st);
+cudaError_t launch_append_rotary(RotaryParams p, int dtype, cudaStream_t st);
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t st);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
 cudaError_t launch_resize(const PoolParams& p, cudaStream_t st);
 cudaError_t launch_fork(const PoolParams& p, const CacheView& c, cudaStream_t st);
+cudaError_t debug_read_evict(unsigned int* count, unsigned int* line);
 cudaError_t debug_read_cache(unsigned int* count, unsigned int* line);
 
 }  // namespace sv

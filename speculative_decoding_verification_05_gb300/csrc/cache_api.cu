@@ -8,6 +8,7 @@
 #include "attention.cuh"
 #include "cache.cuh"
 #include "specverify.h"
+#include "weigh.cuh"
 
 namespace sv {
 spec_status note_cuda_error(cudaError_t e);
@@ -235,6 +236,49 @@ spec_status spec_cache_append(const void* k, const void* v, const spec_cache* ca
     return done(sv::launch_append(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+spec_status spec_cache_append_rotary(const void* q, const void* k, const void* v, const spec_cache* cache,
+                                     spec_dtype dtype, const int32_t* page_table, int64_t table_stride, int max_pages,
+                                     const int32_t* cache_len, const uint64_t* turns, int dim, int interleaved,
+                                     float factor, const int32_t* positions, const int32_t* depth,
+                                     const int32_t* n_nodes, int B, int N, int q_heads, void* q_out, int32_t* status,
+                                     spec_stream stream) {
+    if (!cache_ok(cache, dtype) || cache->layers != 1 || !table_ok(page_table, table_stride, max_pages))
+        return SPEC_EINVAL;
+    if (B < 1 || B > kMaxB || N < 1 || N > (1 << 20) || q_heads < 1 || q_heads > 1024 * SPEC_MAX_GROUP || dim < 2 ||
+        dim > cache->head_dim || dim % 2 != 0 || !std::isfinite(factor))
+        return SPEC_EINVAL;
+    if (!q || !k || !v || !q_out || !cache_len || !turns || !aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) ||
+        !aligned(q_out, 16) || !aligned(cache_len, 4) || !aligned(turns, 8) || !aligned(positions, 4) ||
+        !aligned(depth, 4) || !aligned(n_nodes, 4) || !aligned(status, 4))
+        return SPEC_EINVAL;
+    // (a column's partner may be another thread's)
+    const size_t bytes = (size_t)B * N * q_heads * cache->head_dim * esize(dtype);
+    const uintptr_t from = (uintptr_t)q, to = (uintptr_t)q_out;
+    if (from < to + bytes && to < from + bytes) return SPEC_EINVAL;
+    sv::RotaryParams p = {};
+    p.c = view_of(cache, dtype);
+    p.q = static_cast<const char*>(q);
+    p.k = static_cast<const char*>(k);
+    p.v = static_cast<const char*>(v);
+    p.q_out = static_cast<char*>(q_out);
+    p.turns = reinterpret_cast<const unsigned long long*>(turns);
+    p.factor = factor;
+    p.half = dim / 2;
+    p.interleaved = interleaved != 0;
+    p.q_heads = q_heads;
+    p.table = page_table;
+    p.table_stride = table_stride;
+    p.cache_len = cache_len;
+    p.positions = positions;
+    p.depth = depth;
+    p.n_nodes = n_nodes;
+    p.status = status;
+    p.B = B;
+    p.N = N;
+    p.max_pages = max_pages;
+    return done(sv::launch_append_rotary(p, dtype == SPEC_F32 ? 0 : 1, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 spec_status spec_cache_compact(const spec_cache* cache, spec_dtype dtype, const int32_t* page_table,
                                int64_t table_stride, int max_pages, const int32_t* cache_len,
                                const int32_t* accept_len, const int32_t* path_nodes, int B, int W,
@@ -264,6 +308,90 @@ spec_status spec_cache_compact(const spec_cache* cache, spec_dtype dtype, const 
     p.W = W;
     p.max_pages = max_pages;
     return done(sv::launch_compact(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* cache, spec_dtype dtype,
+                             const int32_t* page_table, int64_t table_stride, int max_pages, const int32_t* cache_len,
+                             const int32_t* accept_len, const int32_t* path_nodes, int B, int N, int W, int q_heads,
+                             float scale, float* weights, int64_t capacity, int32_t* status, spec_stream stream) {
+    if (!cache_ok(cache, dtype) || cache->layers != 1 || !table_ok(page_table, table_stride, max_pages))
+        return SPEC_EINVAL;
+    if (!attention_shape_ok(B, N, q_heads, cache->kv_heads, cache->head_dim) ||
+        (path_nodes && (!accept_len || W < 1 || W > SPEC_MAX_TREE_N)) || capacity < 1 || capacity > (1LL << 31))
+        return SPEC_EINVAL;
+    if (!q || !lse || !weights || !cache_len || !aligned(q, 16) || !aligned(lse, 4) || !aligned(weights, 4) ||
+        !aligned(cache_len, 4) || !aligned(accept_len, 4) || !aligned(path_nodes, 4) || !aligned(status, 4))
+        return SPEC_EINVAL;
+    const float c2 = scale * 1.4426950408889634f;
+    if (!std::isfinite(scale) || !std::isfinite(c2)) return SPEC_EINVAL;
+    sv::WeighParams p = {};
+    p.q = q;
+    p.lse = lse;
+    p.k = cache->k;
+    p.page_stride = cache->page_stride;
+    p.token_stride = cache->token_stride;
+    p.head_stride = cache->head_stride;
+    p.table = page_table;
+    p.table_stride = table_stride;
+    p.cache_len = cache_len;
+    p.accept = accept_len;
+    p.path = path_nodes;
+    p.B = B;
+    p.N = N;
+    p.W = path_nodes ? W : N;
+    p.Hkv = cache->kv_heads;
+    p.G = q_heads / cache->kv_heads;
+    p.D = cache->head_dim;
+    p.num_pages = cache->num_pages;
+    p.max_pages = max_pages;
+    p.page_shift = shift_of(cache->page_size);
+    p.capacity = capacity;
+    p.c2 = c2;
+    p.weights = weights;
+    p.status = status;
+    return done(sv::launch_weigh_simt(p, dtype == SPEC_F32 ? 0 : 1, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t spec_cache_evict_workspace_size(int layers, int B, int kv_heads, int64_t capacity) {
+    if (layers < 1 || B < 1 || B > kMaxB || kv_heads < 1 || kv_heads > 1024 || capacity < 1 || capacity > (1LL << 31) ||
+        (double)layers * B * kv_heads > (double)(1 << 30))
+        return 0;
+    const size_t units = (size_t)layers * B * kv_heads;
+    return al(units * sizeof(int2)) + al(units * (size_t)capacity * sizeof(int32_t));
+}
+
+spec_status spec_cache_evict(const spec_cache* cache, spec_dtype dtype, const int32_t* page_table,
+                             int64_t table_stride, int max_pages, const int32_t* cache_len, const int32_t* budget,
+                             int sink, int recent, float* weights, int64_t capacity, int B, int32_t* new_len,
+                             int32_t* status, void* workspace, size_t ws_bytes, spec_stream stream) {
+    if (!cache_ok(cache, dtype) || !table_ok(page_table, table_stride, max_pages)) return SPEC_EINVAL;
+    const size_t need = spec_cache_evict_workspace_size(cache->layers, B, cache->kv_heads, capacity);
+    if (need == 0 || sink < 0 || recent < 0 || !cache_len || !budget || !weights || !new_len || !workspace ||
+        !aligned(cache_len, 4) || !aligned(budget, 4) || !aligned(weights, 4) || !aligned(new_len, 4) ||
+        !aligned(status, 4) || !aligned(workspace, kAlign) || ws_bytes < need)
+        return SPEC_EINVAL;
+    // (one block of a sequence writes these while its others still read those)
+    if (overlap(cache_len, B, new_len, B) || overlap(cache_len, B, status, B) || overlap(budget, B, new_len, B) ||
+        overlap(budget, B, status, B) || overlap(new_len, B, status, B))
+        return SPEC_EINVAL;
+    sv::EvictParams p = {};
+    p.c = view_of(cache, dtype);
+    p.table = page_table;
+    p.table_stride = table_stride;
+    p.cache_len = cache_len;
+    p.budget = budget;
+    p.sink = sink;
+    p.recent = recent;
+    p.weights = weights;
+    p.capacity = capacity;
+    p.new_len = new_len;
+    p.status = status;
+    p.jobs = static_cast<int2*>(workspace);
+    p.list = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) +
+                                        al((size_t)cache->layers * B * cache->kv_heads * sizeof(int2)));
+    p.B = B;
+    p.max_pages = max_pages;
+    return done(sv::launch_evict(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 spec_status spec_cache_resize(int32_t* page_table, int64_t table_stride, int max_pages, int num_seqs,

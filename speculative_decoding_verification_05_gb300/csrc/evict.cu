@@ -1,0 +1,245 @@
+// Eviction from the paged cache by accumulated attention weight: a sequence
+// longer than its budget keeps, for every layer and key / value head by itself,
+// its first `sink` positions, its last `recent` ones and of the rest those of the
+// largest weight (ties: the lowest position; NaN counts as larger than all), in
+// their order, and their keys, values and weights move together to the front.
+//
+// Two launches. One block a (layer, sequence, head) finds the weight of rank m
+// among the n middle positions - the largest key that at least m of them reach,
+// by halving the interval of ordered 32-bit keys, a count of the block a step -
+// lists the kept positions by one prefix sum, and moves the weights. Then one
+// block a list and K or V moves the rows: as a kept position's new place is never
+// behind its old one, rows are read a batch at a time and written when the whole
+// block has read its batch, and no later batch's row is overwritten.
+
+#include <algorithm>
+
+#include "cache.cuh"
+#include "specverify.h"
+
+namespace sv {
+namespace {
+
+constexpr int ST = 512;   // threads of a selecting block
+constexpr int kItems = 8;  // positions of a thread: neighbours
+constexpr int CT = 256;
+constexpr int kMoves = 8;
+constexpr int kMostRows = 64;  // rows that a block reads at once, an eighth of a batch
+
+SV_DEV uint4 ldg16(const char* p) { return *reinterpret_cast<const uint4*>(p); }
+SV_DEV void stg16(char* p, uint4 x) { *reinterpret_cast<uint4*>(p) = x; }
+
+// Ordered keys of weights; NaN above everything.
+SV_DEV uint32_t weight_key(float w) { return w != w ? 0xFFFFFFFFu : f32_key(w); }
+
+SV_DEV int block_sum(int v, int* scratch) {
+    v = __reduce_add_sync(0xFFFFFFFFu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < ST / 32; ++w) s += scratch[w];
+    return s;
+}
+
+// Exclusive prefixes of two counts over the block's threads, and their sums.
+SV_DEV void block_prefix2(int a, int b, int* pa, int* pb, int* sa, int* sb, int2* scratch) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = a, y = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xFFFFFFFFu, x, o), v = __shfl_up_sync(0xFFFFFFFFu, y, o);
+        if (lane >= o) x += u, y += v;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = make_int2(x, y);
+    __syncthreads();
+    int bx = 0, by = 0, tx = 0, ty = 0;
+#pragma unroll
+    for (int w = 0; w < ST / 32; ++w) {
+        const int2 u = scratch[w];
+        if (w < warp) bx += u.x, by += u.y;
+        tx += u.x, ty += u.y;
+    }
+    *pa = bx + x - a;
+    *pb = by + y - b;
+    *sa = tx;
+    *sb = ty;
+}
+
+__global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant__ EvictParams p) {
+    __shared__ int scratch[ST / 32];
+    __shared__ int2 scratch2[ST / 32];
+    __shared__ int first_moved;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const long long unit = blockIdx.x;  // (layer, sequence, head)
+    const int h = (int)(unit % p.c.heads), b = (int)(unit / p.c.heads % p.B), tid = threadIdx.x, sh = p.c.page_shift;
+    const long long L = p.cache_len[b], budget = p.budget[b], least = (long long)p.sink + p.recent;
+    const int32_t* table = p.table + b * p.table_stride;
+    bool ok = L >= 0 && L <= ((long long)p.max_pages << sh) && L <= p.capacity && budget >= least;
+    const bool over = ok && L > budget;
+    if (over) {
+        bool bad = false;
+        const int own0 = (int)(p.sink >> sh), own1 = budget > p.sink ? (int)((budget - 1) >> sh) : -1;
+        for (int i = tid; i <= (int)((L - 1) >> sh); i += ST) {
+            const int id = __ldg(table + i);
+            if (id < 0 || id >= p.c.num_pages) bad = true;
+            else if (p.c.refs && i >= own0 && i <= own1) bad |= __ldg(p.c.refs + id) != 1;
+        }
+        ok = !__syncthreads_or(bad);
+    }
+    if (h == 0 && unit < (long long)p.B * p.c.heads && tid == 0) {
+        p.new_len[b] = ok ? (int)min(L, budget) : -1;
+        if (p.status) p.status[b] = ok ? kOk : kEData;
+    }
+    if (!ok || !over) {
+        if (tid == 0) p.jobs[unit] = make_int2(0, 0);
+        return;
+    }
+
+    const int len = (int)L, keep = (int)budget, mid0 = min(p.sink, len), mid1 = len - p.recent, m = keep - p.sink - p.recent;
+    float* w = p.weights + unit * p.capacity;
+    int32_t* list = p.list + unit * p.capacity;
+    const bool fits = len <= ST * kItems;  // the block's registers hold all weights
+    const bool vec = (p.capacity & 3) == 0 && (reinterpret_cast<size_t>(p.weights) & 15) == 0;
+    float x[kItems];
+    auto load = [&](int at) {
+        const int t = at + tid * kItems;
+        if (vec && t + kItems <= len) {
+#pragma unroll
+            for (int j = 0; j < kItems; j += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(w + t + j);
+                x[j] = f.x, x[j + 1] = f.y, x[j + 2] = f.z, x[j + 3] = f.w;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) x[j] = t + j < len ? w[t + j] : 0.f;
+        }
+    };
+    // middle positions whose key is at least k
+    auto count = [&](uint32_t k) {
+        int c = 0;
+        for (int at = 0; at < len; at += ST * kItems) {
+            if (!fits) load(at);
+            const int t = at + tid * kItems;
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) c += t + j >= mid0 && t + j < mid1 && weight_key(x[j]) >= k;
+        }
+        return block_sum(c, scratch);
+    };
+    if (tid == 0) first_moved = keep;
+    if (fits) load(0);
+    // `lo`: reached by m or more; `hi`: by fewer (above all keys at first)
+    unsigned long long lo = 0, hi = 1ull << 32;
+    bool exact = false;  // reached by just m
+    if (m > 0) {
+        while (hi - lo > 1 && !exact) {
+            const unsigned long long mid = (lo + hi) >> 1;
+            const int c = count((uint32_t)mid);
+            if (c >= m) lo = mid;
+            else hi = mid;
+            exact = c == m;
+        }
+    } else {
+        lo = hi;  // none of the middle
+    }
+    const int ties = exact || m == 0 ? 0x7FFFFFFF : m - (hi <= 0xFFFFFFFFull ? count((uint32_t)hi) : 0);
+    // kept so far: those above the bound or always kept, and ties
+    int above0 = 0, tied0 = 0;
+    __syncthreads();
+    for (int at = 0; at < len; at += ST * kItems) {
+        if (!fits) load(at);
+        const int t = at + tid * kItems;
+        uint32_t above = 0, tied = 0;
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const int i = t + j;
+            const unsigned long long k = weight_key(x[j]);
+            const bool in = i < len, always = i < mid0 || i >= mid1;
+            if (in && (always || k > lo)) above |= 1u << j;
+            else if (in && k == lo) tied |= 1u << j;
+        }
+        int a, e, sa, se;
+        block_prefix2(__popc(above), __popc(tied), &a, &e, &sa, &se, scratch2);  // (its barriers: all have read)
+        a += above0;
+        e += tied0;
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) {
+            const bool is = above >> j & 1, tie = tied >> j & 1;
+            const int to = a + min(e, ties);
+            if ((is || (tie && e < ties)) && SV_IN(to, keep)) {
+                list[to] = t + j;
+                w[to] = x[j];
+                if (to != t + j) atomicMin(&first_moved, to);
+            }
+            a += is;
+            e += tie;
+        }
+        above0 += sa;
+        tied0 += se;
+    }
+    __syncthreads();
+    for (int i = keep + tid; i < len; i += ST) w[i] = 0.f;
+    if (tid == 0) p.jobs[unit] = make_int2(first_moved, keep);
+}
+
+__global__ void __launch_bounds__(CT) evict_move_kernel(const __grid_constant__ EvictParams p) {
+    __shared__ longlong2 place[2][kMostRows * kMoves];  // from, to
+    const long long unit = blockIdx.x >> 1;
+    const int h = (int)(unit % p.c.heads), b = (int)(unit / p.c.heads % p.B), tid = threadIdx.x, sh = p.c.page_shift;
+    char* base = (blockIdx.x & 1 ? p.c.v : p.c.k) + unit / p.c.heads / p.B * p.c.layer_stride + h * p.c.head_stride;
+    const int32_t* table = p.table + b * p.table_stride;
+    const int words = p.c.row_bytes / 16, width = min(CT / words, kMostRows), r0 = tid / words, col = tid - r0 * words;
+    const int batch = width * kMoves;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int2 job = __ldcg(p.jobs + unit);
+    const int32_t* list = p.list + unit * p.capacity;
+    auto row = [&](int pos) {
+        return (long long)__ldg(table + (pos >> sh)) * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride;
+    };
+    auto places = [&](int at, int buf) {
+        for (int i = tid; i < batch; i += CT)
+            if (at + i < job.y) place[buf][i] = make_longlong2(row(__ldcg(list + at + i)), row(at + i));
+    };
+    places(job.x, 0);
+    __syncthreads();
+    int buf = 0;
+    for (int at = job.x; at < job.y; at += batch, buf ^= 1) {
+        uint4 x[kMoves];
+        const int n = job.y - at;
+        const bool mine = r0 < width;
+#pragma unroll
+        for (int j = 0; j < kMoves; ++j)
+            if (mine && r0 + j * width < n) x[j] = ldg16(base + place[buf][r0 + j * width].x + col * 16);
+        places(at + batch, buf ^ 1);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kMoves; ++j)
+            if (mine && r0 + j * width < n) stg16(base + place[buf][r0 + j * width].y + col * 16, x[j]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
+    const long long units = (long long)p.c.layers * p.B * p.c.heads;
+    evict_select_kernel<<<(unsigned)units, ST, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // starts while the selection ends (it waits for it before it reads a list)
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * units));
+    cfg.blockDim = dim3(CT);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+}
+
+SV_DEBUG_READER(evict)
+
+}  // namespace sv
