@@ -291,6 +291,11 @@ SV_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 template <typename E>
 SV_DEV void store4(E* dst, float4 x);
@@ -330,6 +335,9 @@ int attention_simt_whole();
 struct alignas(64) AttnMaps {
     unsigned char bytes[384];
 };
+// The map of one layer's keys or values (`base`), tiles of 128 positions in boxes
+// of a page's slots x 64 columns; false where the strides have none.
+bool cache_tc_map(const AttnParams& p, const void* base, AttnMaps* m);
 int attention_tc_rows(int group);
 int attention_tc_kv();
 int attention_tc_extra(int group, int N);

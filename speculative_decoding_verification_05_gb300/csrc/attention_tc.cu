@@ -74,6 +74,7 @@
 
 #include "attention.cuh"
 #include "tcgen.cuh"
+#include "weigh.cuh"
 
 namespace sv {
 namespace {
@@ -162,22 +163,6 @@ SV_DEV int halves_of(const Seg& s, int w) {
     return 2 * mine - (mine && has_last && live_of(s, cnt - 1) <= kHalfKv ? 1 : 0);
 }
 
-// Waits give up after some 2^18 polls (a poll that finds nothing takes up to
-// 2 us: half a second; 2^22 took 8 seconds), or once `abort` is set. They poll
-// without a suspension of their own: its wake-up costs more than these short
-// waits last.
-SV_DEV bool tc_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
-    uint32_t n = 0;
-#pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
-        if (!(++n & 0xFFu) && (n >> 18 || (abort && *abort))) return false;
-    return true;
-}
-// By whole warps: every lane gets the same answer.
-SV_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const int* abort) {
-    return __all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort)) != 0;
-}
-
 // The post of segment number `seg`, null after the last (or a timeout). It
 // stays until segment seg + 3 begins.
 SV_DEV const Seg* next_seg(Ctl* c, uint32_t seg, bool* ok) {
@@ -249,18 +234,6 @@ SV_DEV void produce(const AttnParams& p, Ctl* c, const CUtensorMap* mk, const CU
 }
 
 // ---- products ---------------------------------------------------------------------
-
-// The whole warp goes through the steps and one elected lane issues: operands
-// broadcast from lane 0 are known to be the same in every lane, so that they
-// stay in uniform registers (issued by one thread from its own registers, a
-// product of 16 positions took 80 to 160 cycles to issue and 64 to run).
-SV_DEV uint32_t uni(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
-
-SV_DEV bool elected() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
 
 // A stream's way along the ring. Both issuers wait for every entry in its
 // order and both release it (one's products on it, or its having seen an entry
@@ -472,11 +445,6 @@ SV_DEV void add_unclean(const AttnParams& p, const Seg& s, int node, char* out, 
     }
 }
 
-SV_DEV uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 constexpr float kNegInf = -__builtin_inff();
 
@@ -993,6 +961,10 @@ int attention_tc_rows(int group) { return 2 * (128 / group) * group; }
 int attention_tc_kv() { return kKv; }
 int attention_tc_whole() { return kWhole; }
 
+bool cache_tc_map(const AttnParams& p, const void* base, AttnMaps* m) {
+    return make_map(reinterpret_cast<CUtensorMap*>(m), p, base);
+}
+
 bool attention_tc_maps(const AttnParams& p, AttnMaps* m) {
     static_assert(sizeof(AttnMaps) >= 3 * sizeof(CUtensorMap), "three maps");
     CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(m);
@@ -1014,7 +986,7 @@ SV_DEBUG_READER(attention_tc)
 
 extern "C" int spec_debug_withhold_tile(int j) {
 #ifdef SPEC_DEBUG
-    return cudaMemcpyToSymbol(sv::g_withhold, &j, sizeof(int)) == cudaSuccess ? 0 : -1;
+    return cudaMemcpyToSymbol(sv::g_withhold, &j, sizeof(int)) == cudaSuccess ? sv::debug_withhold_weigh_tile(j) : -1;
 #else
     (void)j;
     return -1;

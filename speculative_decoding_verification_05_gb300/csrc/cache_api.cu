@@ -349,7 +349,13 @@ spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* 
     p.c2 = c2;
     p.weights = weights;
     p.status = status;
-    return done(sv::launch_weigh_simt(p, dtype == SPEC_F32 ? 0 : 1, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (tc_shape(p.D, dtype)) {
+        bool took = false;
+        const cudaError_t e = sv::launch_weigh_tc(p, st, &took);
+        if (took) return done(e);
+    }
+    return done(sv::launch_weigh_simt(p, dtype == SPEC_F32 ? 0 : 1, st));
 }
 
 size_t spec_cache_evict_workspace_size(int layers, int B, int kv_heads, int64_t capacity) {

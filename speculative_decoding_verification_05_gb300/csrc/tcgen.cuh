@@ -1,5 +1,5 @@
 // Tensor-core and tensor-copy instructions of sm_103a, as used by the tree
-// attention: tcgen05 (matrix products with accumulators in tensor memory) and
+// attention and the weighing of its rows: tcgen05 (matrix products with accumulators in tensor memory) and
 // cp.async.bulk.tensor.
 #pragma once
 
@@ -90,6 +90,35 @@ SV_DEV void tma_load4(uint32_t dst, const void* map, int c0, int c1, int c2, int
         "[%6];" ::"r"(dst),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
         : "memory");
+}
+
+// ---- waits and issue.
+// Waits give up after some 2^18 polls (a poll that finds nothing takes up to
+// 2 us: half a second; 2^22 took 8 seconds), or once `abort` is set. They poll
+// without a suspension of their own: its wake-up costs more than these short
+// waits last.
+SV_DEV bool tc_wait(uint64_t* bar, uint32_t parity, const volatile int* abort) {
+    uint32_t n = 0;
+#pragma unroll 1
+    while (!mbar_try_wait(bar, parity))
+        if (!(++n & 0xFFu) && (n >> 18 || (abort && *abort))) return false;
+    return true;
+}
+// By whole warps: every lane gets the same answer.
+SV_DEV bool warp_wait(uint64_t* bar, uint32_t parity, const int* abort) {
+    return __all_sync(0xFFFFFFFFu, tc_wait(bar, parity, abort)) != 0;
+}
+
+// The whole warp goes through the steps and one elected lane issues: operands
+// broadcast from lane 0 are known to be the same in every lane, so that they
+// stay in uniform registers (issued by one thread from its own registers, a
+// product of 16 positions took 80 to 160 cycles to issue and 64 to run).
+SV_DEV uint32_t uni(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+SV_DEV bool elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 }  // namespace sv

@@ -7,7 +7,7 @@
 
 #include <algorithm>
 
-#include "per_device.h"
+#include "attention.cuh"
 #include "weigh.cuh"
 #include "specverify.h"
 
@@ -149,15 +149,8 @@ __global__ void __launch_bounds__(NT) weigh_kernel(const __grid_constant__ Weigh
 
 template <typename E>
 cudaError_t launch(const WeighParams& p, cudaStream_t st) {
-    static OncePerDevice once;
-    const void* fn = reinterpret_cast<const void*>(weigh_kernel<E>);
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(weigh_kernel<E>), smem_bytes(SPEC_MAX_HEAD_DIM));
     if (e != cudaSuccess) return e;
-    const int rc = once.run(fn, dev, [&] {
-        return (int)cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes(SPEC_MAX_HEAD_DIM));
-    });
-    if (rc != 0) return (cudaError_t)rc;
     const size_t bytes = smem_bytes(p.D);
     const int ctas = (int)std::min<size_t>(4, 220 * 1024 / (bytes + 1024));
     weigh_kernel<E><<<152 * ctas, NT, bytes, st>>>(p);

@@ -181,6 +181,11 @@ SV_DEV void weigh_statuses(const WeighParams& p, int gw, int warps) {
     }
 }
 
+// The tensor-core kernel (bf16, D 64 or 128) reads the keys through a tensor map;
+// *took: false where the cache's strides have none (nothing was launched).
+cudaError_t launch_weigh_tc(const WeighParams& p, cudaStream_t st, bool* took);
+int debug_withhold_weigh_tile(int j);
+cudaError_t debug_read_weigh_tc(unsigned int* count, unsigned int* line);
 cudaError_t launch_weigh_simt(const WeighParams& p, int dtype, cudaStream_t st);
 cudaError_t debug_read_weigh(unsigned int* count, unsigned int* line);
 
