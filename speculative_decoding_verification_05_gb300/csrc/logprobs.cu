@@ -21,7 +21,7 @@
 
 #include <algorithm>
 
-#include "common.cuh"
+#include "attention.cuh"
 #include "logprobs.cuh"
 #include "specverify.h"
 
@@ -98,6 +98,73 @@ SV_DEV void rank_keys(const u64* cand, int n, int k, u64* best) {
     }
 }
 
+// Stops the compiler from keeping what it unpacked from a word for the next pass
+// (it needs more registers than the thread has).
+SV_DEV void forget(uint4& x) { asm volatile("" : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w)); }
+
+// The largest of a granule's elements (NaN loses).
+template <typename E>
+SV_DEV float granule_max(const uint4& x) {
+    if constexpr (sizeof(E) == 4) {
+        float r;
+        asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(x.x)), "f"(__uint_as_float(x.y)), "f"(__uint_as_float(x.z)));
+        return fmaxf(r, __uint_as_float(x.w));
+    } else {
+        uint32_t a, b;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(x.x), "r"(x.y));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(x.z), "r"(x.w));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+        return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    }
+}
+
+// A thread's sums, two at a time.
+struct Sums {
+    uint64_t S, U;
+};
+
+// Adds a granule's 2^t and 2^t t, t = (v - ref) c2; NaN in S for a NaN or +inf.
+template <int VN>
+SV_DEV void add_granule(const float (&v)[VN], float ref, float c2, Sums* a) {
+    const uint64_t rr = pack2(-ref, -ref), cc = pack2(c2, c2);
+    uint64_t u = 0ull;
+#pragma unroll
+    for (int e = 0; e < VN; e += 2) {
+        const uint64_t t = mul2(add2(pack2(v[e], v[e + 1]), rr), cc);
+        float t0, t1;
+        unpack2(t, &t0, &t1);
+        const uint64_t w = pack2(ex2(t0), ex2(t1));
+        a->S = add2(a->S, w);
+        u = fma2(w, t, u);
+    }
+    float u0, u1;
+    unpack2(u, &u0, &u1);
+    if (!(u0 + u1 <= 0.f)) {  // a logit of -inf gave 0 times infinity (or the row is bad): again, with an end
+        u0 = u1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < VN; ++e) {
+            const float t = fmaxf((v[e] - ref) * c2, -200.f);  // (2^-200 is 0)
+            u0 = fmaf(ex2(t), t, u0);
+        }
+        u = pack2(u0, u1);
+    }
+    a->U = add2(a->U, u);
+}
+
+// How many of a granule's elements lie above t: the signs of t - v.
+template <int VN>
+SV_DEV int count_above(const float (&v)[VN], float t) {
+    const uint64_t tt = pack2(t, t), minus = pack2(-1.f, -1.f);
+    uint32_t n = 0;
+#pragma unroll
+    for (int e = 0; e < VN; e += 2) {
+        float a, b;
+        unpack2(fma2(pack2(v[e], v[e + 1]), minus, tt), &a, &b);
+        n += (__float_as_uint(a) >> 31) + (__float_as_uint(b) >> 31);
+    }
+    return (int)n;
+}
+
 template <typename E, int NT, int NV>
 __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_constant__ LogprobParams p) {
     constexpr int VN = VecTraits<E>::kN;
@@ -136,7 +203,22 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
     const uint4* g0 = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(z0) - h * sizeof(E));
     const int granules = (p.V + h + VN - 1) / VN;
     const int lo = part * p.part_granules, hi = min(lo + p.part_granules, granules);
-    const float zx = VecTraits<E>::load1(z0 + tok);
+    // a granule; the row's edges element by element, -inf outside of it
+    auto granule = [&](int g) {
+        const int at = g * VN - h;
+        if (at >= 0 && at + VN <= p.V) return ld_stream_v4(g0 + g);
+        constexpr uint32_t fill = sizeof(E) == 4 ? 0xFF800000u : 0xFF80FF80u;
+        uint32_t w[4] = {fill, fill, fill, fill};
+#pragma unroll
+        for (int e = 0; e < VN; ++e)
+            if (at + e >= 0 && at + e < p.V) {
+                const uint32_t bits = __float_as_uint(VecTraits<E>::load1(z0 + at + e));
+                if (sizeof(E) == 4) w[e & 3] = bits;
+                else w[(e >> 1) & 3] = e & 1 ? (w[(e >> 1) & 3] & 0xFFFFu) | bits : (w[(e >> 1) & 3] & 0xFFFF0000u) | bits >> 16;
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    const float zx = VecTraits<E>::load1(z0 + tok) + 0.f;  // (-0 becomes +0: signs of differences are counted)
     // the next value below z_x: z > below where z >= z_x (-inf: none, its ties are counted one by one)
     const float below = zx == -INFINITY ? zx : zx == 0.f ? -0x1p-149f : key_to_f32(f32_key(zx) - 1);
 
@@ -144,35 +226,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
     bool listed = false;
 #pragma unroll 1
     for (int r0 = lo; r0 < hi || r0 == lo; r0 += NT * NV) {
+        const int end = min(hi, r0 + NT * NV);
         uint4 x[NV];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int g = r0 + j * NT + tid, at = g * VN - h;
-            if (g < hi && at >= 0 && at + VN <= p.V) x[j] = ld_stream_v4(g0 + g);
-            else {
-                // the row's edges, element by element; -inf outside of it
-                constexpr uint32_t fill = sizeof(E) == 4 ? 0xFF800000u : 0xFF80FF80u;
-                uint32_t w[4] = {fill, fill, fill, fill};
-                if (g < hi) {
-#pragma unroll
-                    for (int e = 0; e < VN; ++e)
-                        if (at + e >= 0 && at + e < p.V) {
-                            const uint32_t bits = __float_as_uint(VecTraits<E>::load1(z0 + at + e));
-                            if (sizeof(E) == 4) w[e & 3] = bits;
-                            else w[(e >> 1) & 3] = e & 1 ? (w[(e >> 1) & 3] & 0xFFFFu) | bits : (w[(e >> 1) & 3] & 0xFFFF0000u) | bits >> 16;
-                        }
-                }
-                x[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
+        for (int j = 0; j < NV; ++j)
+            if (r0 + j * NT + tid < end) x[j] = granule(r0 + j * NT + tid);
         float mx = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            float v[VN];
-            VecTraits<E>::unpack(x[j], v);
-#pragma unroll
-            for (int e = 0; e < VN; ++e) mx = fmaxf(mx, v[e]);
-        }
+        for (int j = 0; j < NV; ++j)
+            if (r0 + j * NT + tid < end) mx = fmaxf(mx, granule_max<E>(x[j]));
         const float wm = warp_max(mx);
         __syncthreads();
         if (lane == 0) s.red[0][warp] = wm;
@@ -183,40 +245,38 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
 #pragma unroll
         for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, s.red[0][w]);
         const float ref = m == -INFINITY ? 0.f : m;
-        float S = 0.f, U = 0.f;
+        const bool ranked = p.rank && __any_sync(0xFFFFFFFFu, mx >= zx);
+        Sums sums = {0ull, 0ull};
+        int above = 0;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            float v[VN];
-            VecTraits<E>::unpack(x[j], v);
-#pragma unroll
-            for (int e = 0; e < VN; ++e) {
-                const float t = (v[e] - ref) * p.c2, w = ex2(t);
-                S += w;                            // (NaN for a NaN or +inf)
-                U = fmaf(w, fmaxf(t, -200.f), U);  // (2^t is 0 from there on: no 0 times infinity)
-            }
-        }
-        int above = 0;
-        if (p.rank && __any_sync(0xFFFFFFFFu, mx >= zx)) {
-#pragma unroll
-            for (int j = 0; j < NV; ++j) {
+            const int g = r0 + j * NT + tid, at = g * VN - h;
+            if (g < end) {
+                forget(x[j]);
                 float v[VN];
                 VecTraits<E>::unpack(x[j], v);
-                const int g = r0 + j * NT + tid, at = g * VN - h;
-                const float t = at + VN <= tok ? below : zx;
+                add_granule<VN>(v, ref, p.c2, &sums);
+                if (ranked) {
+                    above += count_above<VN>(v, at + VN <= tok ? below : zx);
+                    if (at < tok && (at + VN > tok || zx == -INFINITY)) {  // the token's own granule
 #pragma unroll
-                for (int e = 0; e < VN; ++e) above += v[e] > t;
-                if (g < hi && at < tok && (at + VN > tok || zx == -INFINITY)) {  // the token's own granule
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) above += at + e >= 0 && at + e < tok && v[e] == zx;
+                        for (int e = 0; e < VN; ++e) above += at + e >= 0 && at + e < tok && v[e] == zx;
+                    }
                 }
+                forget(x[j]);
             }
         }
+        float S, U, S1, U1;
+        unpack2(sums.S, &S, &S1);
+        unpack2(sums.U, &U, &U1);
+        S += S1;
+        U += U1;
 
         if (K > 0) {
             // a bound that at least K threads' maxima reach: downwards from the
             // maximum by growing steps, then between the last two
-            const uint32_t key = f32_key(mx), top = f32_key(m);
-            uint32_t hi_k = top + 1, lo_k = top, step = 1u << 19;
+            const uint32_t key = f32_key(mx);
+            uint32_t lo_k = f32_key(m), hi_k = lo_k + 1, step = 1u << 19;
             int n = __syncthreads_count(key >= lo_k);
             while (n < K && lo_k > 0) {
                 hi_k = lo_k;
@@ -234,54 +294,62 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
                     hi_k = mid;
                 }
             }
-            auto each = [&](auto f) {  // f(key, index) of this thread's elements
+            if (key >= lo_k) {
 #pragma unroll
                 for (int j = 0; j < NV; ++j) {
-                    float v[VN];
-                    VecTraits<E>::unpack(x[j], v);
                     const int g = r0 + j * NT + tid, at = g * VN - h;
+                    if (g < end && f32_key(granule_max<E>(x[j])) >= lo_k) {
+                        float v[VN];
+                        VecTraits<E>::unpack(x[j], v);
 #pragma unroll
-                    for (int e = 0; e < VN; ++e)
-                        if (g < hi && at + e >= 0 && at + e < p.V) f(f32_key(v[e]), at + e);
-                }
-            };
-            if (key >= lo_k)
-                each([&](uint32_t k, int i) {
-                    if (k >= lo_k) {
-                        const int to = atomicAdd(&s.found, 1);
-                        if (to < kCap) s.cand[to] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
+                        for (int e = 0; e < VN; ++e)
+                            if (f32_key(v[e]) >= lo_k && at + e >= 0 && at + e < p.V) {
+                                const int to = atomicAdd(&s.found, 1);
+                                if (to < kCap) s.cand[to] = cand_key(v[e], at + e);
+                            }
                     }
-                });
+                }
+            }
             __syncthreads();
             int n_cand = s.found;
             if (n_cand > kCap) {
-                // many equal ones: the K-th key of all elements, then the K-th index among its ties
-                uint32_t a = 0, z = 0xFFFFFFFFu;  // count(>= a) >= want, count(>= z) < want
-                const int before = listed ? K : 0;
-                int have = 0;
-                each([&](uint32_t, int) { ++have; });
-                const int want = min(K, block_sum<NT>(have, s.cnt));
+                // many equal ones: the K-th key of all elements, then the K-th
+                // index among its ties (the elements read again)
+                auto count = [&](auto is) {
+                    int c = 0;
+#pragma unroll 1
+                    for (int g = r0 + tid; g < end; g += NT) {
+                        float v[VN];
+                        VecTraits<E>::unpack(granule(g), v);
+#pragma unroll
+                        for (int e = 0; e < VN; ++e) {
+                            const int i = g * VN - h + e;
+                            c += i >= 0 && i < p.V && is(f32_key(v[e]), i);
+                        }
+                    }
+                    return block_sum<NT>(c, s.cnt);
+                };
+                const int want = min(K, count([](uint32_t, int) { return true; }));
+                uint32_t a = 0, z = 0xFFFFFFFFu;  // reached by `want` or more, and by fewer
                 while (z - a > 1) {
                     const uint32_t mid = a + (z - a) / 2;
-                    int c = 0;
-                    each([&](uint32_t k, int) { c += k >= mid; });
-                    if (block_sum<NT>(c, s.cnt) >= want) a = mid;
+                    if (count([&](uint32_t k, int) { return k >= mid; }) >= want) a = mid;
                     else z = mid;
                 }
-                int ia = -1, iz = p.V - 1;  // count up to iz is enough, up to ia is not
+                int ia = -1, iz = p.V - 1;  // up to iz are enough, up to ia are not
                 while (iz - ia > 1) {
                     const int mid = ia + (iz - ia) / 2;
-                    int c = 0;
-                    each([&](uint32_t k, int i) { c += k > a || (k == a && i <= mid); });
-                    if (block_sum<NT>(c, s.cnt) >= want) iz = mid;
+                    if (count([&](uint32_t k, int i) { return k > a || (k == a && i <= mid); }) >= want) iz = mid;
                     else ia = mid;
                 }
+                const int before = listed ? K : 0;
                 __syncthreads();
                 if (tid == 0) s.found = before;
                 if (tid < before) s.cand[tid] = s.mine[tid];
                 __syncthreads();
-                each([&](uint32_t k, int i) {
+                count([&](uint32_t k, int i) {
                     if (k > a || (k == a && i <= iz)) s.cand[atomicAdd(&s.found, 1)] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
+                    return false;
                 });
                 __syncthreads();
                 n_cand = s.found;
