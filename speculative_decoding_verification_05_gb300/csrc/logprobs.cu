@@ -6,18 +6,22 @@
 //   rank(x) = #{z_i > z_x} + #{i < x: z_i = z_x},
 // and the alternatives are the first K in the order (z descending, i ascending).
 //
-// A row is split over a cluster of CTAs (one to eight); a thread holds its share
-// of the part in registers, so the exponentials follow the maximum without a
-// second read. Parts leave (m, S, sum e^y y, count above z_x) against their own
-// maximum and their K best in the first CTA's shared memory, which joins them
-// in the order of the parts: results depend on the shape alone.
+// A row is split over a cluster of CTAs (one to eight). A thread streams its
+// share in batches of a few 16-byte granules, the next batch on its way, and adds
+// up against its own maximum so far, so no thread waits for another before the
+// part's end. Exponents are t = z c2 - M, c2 = log2(e) / T, with one rounding, M
+// the rounded product of the maximum and c2: whatever M's rounding is, it is the
+// same for all terms and drops out of t_x - log2 S. Parts leave (m, sum 2^t, sum
+// 2^t t, count above z_x) and their K best in the first CTA's shared memory, which
+// joins them in the order of the parts: results depend on the shape alone.
 //
 // The K best of a part: any key that K threads' maxima reach is a bound that no
 // better element lies below, so a search over the threads' maxima (one count of
 // the block a step) ends at a bound that K to 2 K of them reach; only those
-// threads look at their elements, and the few that reach it are ranked by
-// comparing all with all. Where that finds more than fit (rows of equal logits) the
-// bound is taken over the elements themselves, then over the indices of the ties.
+// threads' granules are read again (from L2, shared out over the block), and the
+// few elements that reach the bound are ranked by comparing all with all. Where
+// they are more than fit (rows of equal logits) the bound is taken over the
+// elements themselves, then over the indices of the ties.
 
 #include <algorithm>
 
@@ -32,6 +36,7 @@ typedef unsigned long long u64;
 
 constexpr int kMaxTop = SPEC_MAX_TOP;
 constexpr int kMaxParts = 8;
+constexpr float kLn2 = 0.69314718055994531f;
 constexpr int kCap = 1024;  // elements that are ranked at once
 
 SV_DEV u64 cand_key(float z, int i) { return ((u64)f32_key(z) << 32) | (0xFFFFFFFFu - (uint32_t)i); }
@@ -47,10 +52,11 @@ struct Shared {
     Part parts[kMaxParts];            // (of the cluster: the first CTA's)
     u64 best[kMaxParts * kMaxTop];    // each part's K best, descending
     u64 mine[kMaxTop];                // this part's
-    u64 cand[kCap + kMaxTop];
+    u64 cand[kCap];
     float red[3][NT / 32];
-    int cnt[NT / 32];
-    int found;
+    int cnt[NT / 32], sum[NT / 32];
+    int found, flagged;
+    int who[NT];  // threads whose maximum reaches the bound
 };
 
 SV_DEV uint32_t cluster_rank() {
@@ -82,9 +88,18 @@ SV_DEV int block_sum(int v, int* scratch) {
     return s;
 }
 
-// How far a part's maximum lies below the row's, in octaves (2^-200 is 0; a part
-// of nothing but -inf has no maximum).
-SV_DEV float octaves(float m, float top, float c2) { return m == -INFINITY ? -200.f : fmaxf((m - top) * c2, -200.f); }
+// The exponent of v against the reference m (a maximum), from -200 on (2^-200 is
+// 0). Where m c2 has no place in fp32 the difference is taken first.
+SV_DEV float exponent(float v, float m, float c2) {
+    const float M = m * c2;
+    return fmaxf(fabsf(M) < INFINITY ? fmaf(v, c2, -M) : (v - m) * c2, -200.f);
+}
+// How far one maximum lies below another (a part of nothing but -inf has none).
+SV_DEV float octaves(float m, float top, float c2) {
+    if (m == -INFINITY) return -200.f;
+    const float M = top * c2;
+    return fmaxf(fabsf(M) < INFINITY ? __fmul_rn(m, c2) - M : (m - top) * c2, -200.f);
+}
 
 // The n keys in cand (distinct) ranked against one another; the first k, in
 // descending order, to best.
@@ -102,53 +117,28 @@ SV_DEV void rank_keys(const u64* cand, int n, int k, u64* best) {
 // (it needs more registers than the thread has).
 SV_DEV void forget(uint4& x) { asm volatile("" : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w)); }
 
-// The largest of a granule's elements (NaN loses).
-template <typename E>
-SV_DEV float granule_max(const uint4& x) {
-    if constexpr (sizeof(E) == 4) {
-        float r;
-        asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(x.x)), "f"(__uint_as_float(x.y)), "f"(__uint_as_float(x.z)));
-        return fmaxf(r, __uint_as_float(x.w));
-    } else {
-        uint32_t a, b;
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(x.x), "r"(x.y));
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(x.z), "r"(x.w));
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
-        return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
-    }
+SV_DEV void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+SV_DEV float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+SV_DEV uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// A thread's sums, two at a time.
-struct Sums {
-    uint64_t S, U;
-};
-
-// Adds a granule's 2^t and 2^t t, t = (v - ref) c2; NaN in S for a NaN or +inf.
-template <int VN>
-SV_DEV void add_granule(const float (&v)[VN], float ref, float c2, Sums* a) {
-    const uint64_t rr = pack2(-ref, -ref), cc = pack2(c2, c2);
-    uint64_t u = 0ull;
-#pragma unroll
-    for (int e = 0; e < VN; e += 2) {
-        const uint64_t t = mul2(add2(pack2(v[e], v[e + 1]), rr), cc);
-        float t0, t1;
-        unpack2(t, &t0, &t1);
-        const uint64_t w = pack2(ex2(t0), ex2(t1));
-        a->S = add2(a->S, w);
-        u = fma2(w, t, u);
+// The largest of a granule's elements and of `m` (NaN loses).
+template <typename E>
+SV_DEV float granule_max(const uint4& x, float m) {
+    if constexpr (sizeof(E) == 4) {
+        return max3(max3(m, __uint_as_float(x.x), __uint_as_float(x.y)), __uint_as_float(x.z), __uint_as_float(x.w));
+    } else {
+        const uint32_t a = max_bf16x2(max_bf16x2(x.x, x.y), max_bf16x2(x.z, x.w));
+        return max3(m, __uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
     }
-    float u0, u1;
-    unpack2(u, &u0, &u1);
-    if (!(u0 + u1 <= 0.f)) {  // a logit of -inf gave 0 times infinity (or the row is bad): again, with an end
-        u0 = u1 = 0.f;
-#pragma unroll
-        for (int e = 0; e < VN; ++e) {
-            const float t = fmaxf((v[e] - ref) * c2, -200.f);  // (2^-200 is 0)
-            u0 = fmaf(ex2(t), t, u0);
-        }
-        u = pack2(u0, u1);
-    }
-    a->U = add2(a->U, u);
 }
 
 // How many of a granule's elements lie above t: the signs of t - v.
@@ -165,8 +155,75 @@ SV_DEV int count_above(const float (&v)[VN], float t) {
     return (int)n;
 }
 
-template <typename E, int NT, int NV>
-__global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_constant__ LogprobParams p) {
+// A thread's sums against its maximum so far.
+template <typename E>
+struct Stream {
+    static constexpr int VN = VecTraits<E>::kN;
+    float m = -INFINITY, c2;
+    uint64_t S = 0ull, U = 0ull;  // 2^t, 2^t t, two at a time
+    int above = 0;
+
+    // n granules; z_x is `zx`, `t` what counts as above it in all of them (ranked).
+    template <int n>
+    SV_DEV void add(uint4 (&x)[n], bool rank, float zx, float t) {
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < n; ++j) top = granule_max<E>(x[j], top);
+        if (top > m) {
+            const float d = octaves(m, top, c2), w = ex2(d);
+            const uint64_t dd = pack2(d, d), ww = pack2(w, w);
+            U = mul2(ww, fma2(dd, S, U));
+            S = mul2(ww, S);
+            m = top;
+        }
+        const float M = m * c2;
+        const uint64_t cc = pack2(c2, c2), mm = pack2(-M, -M);
+        const bool count = rank && __any_sync(__activemask(), m >= zx);
+        uint64_t s = 0ull, u = 0ull;
+#pragma unroll
+        for (int j = 0; j < n; ++j) {
+            forget(x[j]);
+            float v[VN];
+            VecTraits<E>::unpack(x[j], v);
+#pragma unroll
+            for (int e = 0; e < VN; e += 2) {
+                const uint64_t tt = fma2(pack2(v[e], v[e + 1]), cc, mm);
+                float t0, t1;
+                unpack2(tt, &t0, &t1);
+                const uint64_t w = pack2(ex2(t0), ex2(t1));
+                s = add2(s, w);
+                u = fma2(w, tt, u);
+            }
+            if (count) above += count_above<VN>(v, t);
+        }
+        float u0, u1;
+        unpack2(u, &u0, &u1);
+        u0 += u1;
+        if (!(fabsf(u0) < INFINITY)) {  // a logit of -inf gave 0 times infinity, or M is infinite, or the row is bad: one by one
+            float s0 = 0.f;
+            u0 = 0.f;
+            const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int j = 0; j < n; ++j) {
+                float v[VN];
+                VecTraits<E>::unpack(x[j], v);
+#pragma unroll
+                for (int e = 0; e < VN; ++e) {
+                    const float e2 = exponent(v[e], ref, c2), w = v[e] != v[e] || v[e] == INFINITY ? v[e] - v[e] : ex2(e2);
+                    s0 += w;
+                    u0 = fmaf(w, e2, u0);
+                }
+            }
+            s = pack2(s0, 0.f);
+            u = pack2(u0, 0.f);
+        }
+        S = add2(S, s);
+        U = add2(U, u);
+    }
+};
+
+template <typename E, int NT, int U>
+__global__ void __launch_bounds__(NT, 4) logprob_kernel(const __grid_constant__ LogprobParams p) {
     constexpr int VN = VecTraits<E>::kN;
     __shared__ Shared<NT> s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -222,173 +279,221 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
     // the next value below z_x: z > below where z >= z_x (-inf: none, its ties are counted one by one)
     const float below = zx == -INFINITY ? zx : zx == 0.f ? -0x1p-149f : key_to_f32(f32_key(zx) - 1);
 
-    Part acc = {-INFINITY, 0.f, 0.f, 0};
-    bool listed = false;
+    // Whole granules [in, out) of the part lie inside the row; the row's first and
+    // last may not.
+    const int in = lo + (lo == 0 && h > 0), out = min(hi, (p.V + h) / VN), mine = (tok + h) / VN;  // (the token's granule)
+    // (a row inside one granule has one edge: the first)
+    const bool head = in > lo, tail = out < hi && out >= in, rank = p.rank != nullptr;
+    Stream<E> a;
+    a.c2 = p.c2;
+    // granules from g on, NT apart: added, those before the token's counted as
+    // above it with ties. `base`: the block's first, `n` of them a thread
+    auto add = [&](auto& x, int base, int n) {
+        const int g = base + tid;
+        if (base > mine || base + n * NT <= mine) {
+            a.add(x, rank, zx, base > mine ? zx : below);
+            return;
+        }
+        // (the batch that holds the token's granule)
+        a.add(x, false, zx, zx);
+        for (int j = 0; rank && j < n; ++j) {
+            float v[VN];
+            uint4 y = x[0];
+#pragma unroll
+            for (int k = 1; k < n; ++k)
+                if (k == j) y = x[k];
+            VecTraits<E>::unpack(y, v);
+            a.above += count_above<VN>(v, g + j * NT < mine ? below : zx);
+            const int at = (g + j * NT) * VN - h;
+            if (g + j * NT == mine)
+#pragma unroll
+                for (int e = 0; e < VN; ++e) a.above += at + e >= 0 && at + e < tok && v[e] == zx;
+        }
+    };
+    {
+        const uint4* z = g0 + in + tid;
+        const int full = max(0, (out - in) / (NT * U)), base = in + full * (NT * U);
+        // (what comes last, less than a batch and the edges, is called for now)
+        for (int g = base + tid; g < out; g += NT) prefetch_l2(g0 + g);
+        uint4 x[U], y[U];
+        auto fetch = [&](uint4 (&to)[U], int i) {
+#pragma unroll
+            for (int j = 0; j < U; ++j) to[j] = ld_stream_v4(z + (long long)i * (NT * U) + j * NT);
+        };
+        if (full > 0) fetch(x, 0);
 #pragma unroll 1
-    for (int r0 = lo; r0 < hi || r0 == lo; r0 += NT * NV) {
-        const int end = min(hi, r0 + NT * NV);
-        uint4 x[NV];
+        for (int i = 0; i < full; i += 2) {
+            if (i + 1 < full) fetch(y, i + 1);
+            add(x, in + i * (NT * U), U);
+            if (i + 1 < full) {
+                if (i + 2 < full) fetch(x, i + 2);
+                add(y, in + (i + 1) * (NT * U), U);
+            }
+        }
+#pragma unroll 1
+        for (int j = base < out ? 0 : U; j < U + 2; ++j) {
+            // the row's edges: one thread each
+            const int g = j < U ? base + j * NT + tid : j == U ? (tid == 0 && head ? lo : hi) : (tid == 0 && tail ? out : hi);
+            if (g < (j < U ? out : hi)) {
+                uint4 one[1] = {granule(g)};
+                add(one, g - tid, 1);
+            }
+        }
+    }
+    __syncwarp();
+    if (rank && zx == -INFINITY) {  // a token without probability: its ties before it
+#pragma unroll 1
+        for (int g = lo + tid; g < min(hi, mine + 1); g += NT) {
+            float v[VN];
+            VecTraits<E>::unpack(granule(g), v);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (r0 + j * NT + tid < end) x[j] = granule(r0 + j * NT + tid);
-        float mx = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (r0 + j * NT + tid < end) mx = fmaxf(mx, granule_max<E>(x[j]));
-        const float wm = warp_max(mx);
-        __syncthreads();
+            for (int e = 0; e < VN; ++e) {
+                const int i = g * VN - h + e;
+                // (the token's own granule has counted its ties already)
+                a.above += g != mine && i >= 0 && v[e] == zx;
+            }
+        }
+        __syncwarp();
+    }
+    float m = a.m;
+    int above = a.above;
+
+    // The part's maximum, and the sums against it.
+    Part acc;
+    {
+        const float wm = warp_max(m);
         if (lane == 0) s.red[0][warp] = wm;
-        if (tid == 0) s.found = listed ? K : 0;
-        if (listed && tid < K) s.cand[tid] = s.mine[tid];
+        if (tid == 0) s.found = s.flagged = 0;
         __syncthreads();
-        float m = s.red[0][0];
+        acc.m = s.red[0][0];
 #pragma unroll
-        for (int w = 1; w < NT / 32; ++w) m = fmaxf(m, s.red[0][w]);
-        const float ref = m == -INFINITY ? 0.f : m;
-        const bool ranked = p.rank && __any_sync(0xFFFFFFFFu, mx >= zx);
-        Sums sums = {0ull, 0ull};
-        int above = 0;
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int g = r0 + j * NT + tid, at = g * VN - h;
-            if (g < end) {
-                forget(x[j]);
-                float v[VN];
-                VecTraits<E>::unpack(x[j], v);
-                add_granule<VN>(v, ref, p.c2, &sums);
-                if (ranked) {
-                    above += count_above<VN>(v, at + VN <= tok ? below : zx);
-                    if (at < tok && (at + VN > tok || zx == -INFINITY)) {  // the token's own granule
-#pragma unroll
-                        for (int e = 0; e < VN; ++e) above += at + e >= 0 && at + e < tok && v[e] == zx;
-                    }
-                }
-                forget(x[j]);
-            }
-        }
-        float S, U, S1, U1;
-        unpack2(sums.S, &S, &S1);
-        unpack2(sums.U, &U, &U1);
+        for (int w = 1; w < NT / 32; ++w) acc.m = fmaxf(acc.m, s.red[0][w]);
+        float S, T, S1, T1;
+        unpack2(a.S, &S, &S1);
+        unpack2(a.U, &T, &T1);
+        const float d = octaves(m, acc.m, p.c2), w = ex2(d);
         S += S1;
-        U += U1;
-
-        if (K > 0) {
-            // a bound that at least K threads' maxima reach: downwards from the
-            // maximum by growing steps, then between the last two
-            const uint32_t key = f32_key(mx);
-            uint32_t lo_k = f32_key(m), hi_k = lo_k + 1, step = 1u << 19;
-            int n = __syncthreads_count(key >= lo_k);
-            while (n < K && lo_k > 0) {
-                hi_k = lo_k;
-                lo_k = lo_k > step ? lo_k - step : 0;
-                step <<= 1;
-                n = __syncthreads_count(key >= lo_k);
-            }
-            while (n > 2 * K && hi_k - lo_k > 1) {
-                const uint32_t mid = lo_k + (hi_k - lo_k) / 2;
-                const int c = __syncthreads_count(key >= mid);
-                if (c >= K) {
-                    lo_k = mid;
-                    n = c;
-                } else {
-                    hi_k = mid;
-                }
-            }
-            if (key >= lo_k) {
-#pragma unroll
-                for (int j = 0; j < NV; ++j) {
-                    const int g = r0 + j * NT + tid, at = g * VN - h;
-                    if (g < end && f32_key(granule_max<E>(x[j])) >= lo_k) {
-                        float v[VN];
-                        VecTraits<E>::unpack(x[j], v);
-#pragma unroll
-                        for (int e = 0; e < VN; ++e)
-                            if (f32_key(v[e]) >= lo_k && at + e >= 0 && at + e < p.V) {
-                                const int to = atomicAdd(&s.found, 1);
-                                if (to < kCap) s.cand[to] = cand_key(v[e], at + e);
-                            }
-                    }
-                }
-            }
-            __syncthreads();
-            int n_cand = s.found;
-            if (n_cand > kCap) {
-                // many equal ones: the K-th key of all elements, then the K-th
-                // index among its ties (the elements read again)
-                auto count = [&](auto is) {
-                    int c = 0;
-#pragma unroll 1
-                    for (int g = r0 + tid; g < end; g += NT) {
-                        float v[VN];
-                        VecTraits<E>::unpack(granule(g), v);
-#pragma unroll
-                        for (int e = 0; e < VN; ++e) {
-                            const int i = g * VN - h + e;
-                            c += i >= 0 && i < p.V && is(f32_key(v[e]), i);
-                        }
-                    }
-                    return block_sum<NT>(c, s.cnt);
-                };
-                const int want = min(K, count([](uint32_t, int) { return true; }));
-                uint32_t a = 0, z = 0xFFFFFFFFu;  // reached by `want` or more, and by fewer
-                while (z - a > 1) {
-                    const uint32_t mid = a + (z - a) / 2;
-                    if (count([&](uint32_t k, int) { return k >= mid; }) >= want) a = mid;
-                    else z = mid;
-                }
-                int ia = -1, iz = p.V - 1;  // up to iz are enough, up to ia are not
-                while (iz - ia > 1) {
-                    const int mid = ia + (iz - ia) / 2;
-                    if (count([&](uint32_t k, int i) { return k > a || (k == a && i <= mid); }) >= want) iz = mid;
-                    else ia = mid;
-                }
-                const int before = listed ? K : 0;
-                __syncthreads();
-                if (tid == 0) s.found = before;
-                if (tid < before) s.cand[tid] = s.mine[tid];
-                __syncthreads();
-                count([&](uint32_t k, int i) {
-                    if (k > a || (k == a && i <= iz)) s.cand[atomicAdd(&s.found, 1)] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
-                    return false;
-                });
-                __syncthreads();
-                n_cand = s.found;
-            }
-            if (tid < K && n_cand < K) s.mine[tid] = 0;  // (a part of fewer elements)
-            if (n_cand < K) __syncthreads();
-            rank_keys<NT>(s.cand, n_cand, K, s.mine);
-            listed = true;
-        }
-
-        // this round joined to the ones before it
+        T = w * fmaf(d, S, T + T1);
+        S *= w;
         S = warp_sum(S);
-        U = warp_sum(U);
+        T = warp_sum(T);
         above = __reduce_add_sync(0xFFFFFFFFu, above);
-        __syncthreads();
         if (lane == 0) {
             s.red[1][warp] = S;
-            s.red[2][warp] = U;
+            s.red[2][warp] = T;
             s.cnt[warp] = above;
         }
-        __syncthreads();
-        S = U = 0.f;
+    }
+
+    if (K > 0) {
+        // a bound that at least K threads' maxima reach: downwards from the
+        // maximum by growing steps, then between the last two
+        const uint32_t key = f32_key(m);
+        uint32_t lo_k = f32_key(acc.m), hi_k = lo_k + 1, step = 1u << 19;
+        int n = __syncthreads_count(key >= lo_k);
+        while (n < K && lo_k > 0) {
+            hi_k = lo_k;
+            lo_k = lo_k > step ? lo_k - step : 0;
+            step <<= 1;
+            n = __syncthreads_count(key >= lo_k);
+        }
+        while (n > 2 * K && hi_k - lo_k > 1) {
+            const uint32_t mid = lo_k + (hi_k - lo_k) / 2;
+            const int c = __syncthreads_count(key >= mid);
+            if (c >= K) {
+                lo_k = mid;
+                n = c;
+            } else {
+                hi_k = mid;
+            }
+        }
+        auto gather = [&](const uint4& x, int g) {
+            if (f32_key(granule_max<E>(x, -INFINITY)) < lo_k) return;
+            float v[VN];
+            VecTraits<E>::unpack(x, v);
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
-            S += s.red[1][w];
-            U += s.red[2][w];
-            acc.above += s.cnt[w];
+            for (int e = 0; e < VN; ++e) {
+                const int i = g * VN - h + e;
+                if (f32_key(v[e]) >= lo_k && i >= 0 && i < p.V) {
+                    const int to = atomicAdd(&s.found, 1);
+                    if (to < kCap) s.cand[to] = cand_key(v[e], i);
+                }
+            }
+        };
+        if (tid == 0 && head) gather(granule(lo), lo);
+        if (tid == 0 && tail) gather(granule(out), out);
+        if (key >= lo_k) s.who[atomicAdd(&s.flagged, 1)] = tid;
+        __syncthreads();
+        const int who = s.flagged, jobs = who * max(0, (out - in + NT - 1) / NT);
+#pragma unroll 1
+        for (int i0 = tid; i0 < jobs; i0 += NT * U) {
+            uint4 x[U];
+            int g[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const int i = i0 + j * NT, k = i / who;
+                g[j] = i < jobs ? in + k * NT + s.who[i - k * who] : out;
+                if (g[j] < out) x[j] = ld_stream_v4(g0 + g[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (g[j] < out) gather(x[j], g[j]);
         }
-        if (r0 == lo) {
-            acc.m = m;
-            acc.S = S;
-            acc.U = U;
-        } else {
-            const float top = fmaxf(acc.m, m), at = top == -INFINITY ? 0.f : top;
-            const float da = octaves(acc.m, at, p.c2), db = octaves(m, at, p.c2), wa = ex2(da), wb = ex2(db);
-            acc.U = wa * fmaf(acc.S, da, acc.U) + wb * fmaf(S, db, U);
-            acc.S = wa * acc.S + wb * S;
-            acc.m = top;
+        __syncthreads();
+        int n_cand = s.found;
+        if (n_cand > kCap) {
+            // many equal ones: the K-th key of all elements, then the K-th index
+            // among its ties
+            auto count = [&](auto is) {
+                int c = 0;
+#pragma unroll 1
+                for (int g = lo + tid; g < hi; g += NT) {
+                    float v[VN];
+                    VecTraits<E>::unpack(granule(g), v);
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) {
+                        const int i = g * VN - h + e;
+                        c += i >= 0 && i < p.V && is(f32_key(v[e]), i);
+                    }
+                }
+                return block_sum<NT>(c, s.sum);
+            };
+            const int want = min(K, count([](uint32_t, int) { return true; }));
+            uint32_t k0 = 0, k1 = 0xFFFFFFFFu;  // reached by `want` or more, and by fewer
+            while (k1 - k0 > 1) {
+                const uint32_t mid = k0 + (k1 - k0) / 2;
+                if (count([&](uint32_t k, int) { return k >= mid; }) >= want) k0 = mid;
+                else k1 = mid;
+            }
+            int i0 = -1, i1 = p.V - 1;  // up to i1 are enough, up to i0 are not
+            while (i1 - i0 > 1) {
+                const int mid = i0 + (i1 - i0) / 2;
+                if (count([&](uint32_t k, int i) { return k > k0 || (k == k0 && i <= mid); }) >= want) i1 = mid;
+                else i0 = mid;
+            }
+            if (tid == 0) s.found = 0;
+            __syncthreads();
+            count([&](uint32_t k, int i) {
+                if (k > k0 || (k == k0 && i <= i1)) s.cand[atomicAdd(&s.found, 1)] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
+                return false;
+            });
+            __syncthreads();
+            n_cand = s.found;
         }
+        if (n_cand < K) {  // (a part of fewer elements)
+            if (tid < K) s.mine[tid] = 0;
+            __syncthreads();
+        }
+        rank_keys<NT>(s.cand, n_cand, K, s.mine);
+    }
+    __syncthreads();
+    acc.S = acc.U = 0.f;
+    acc.above = 0;
+#pragma unroll
+    for (int w = 0; w < NT / 32; ++w) {
+        acc.S += s.red[1][w];
+        acc.U += s.red[2][w];
+        acc.above += s.cnt[w];
     }
 
     if (p.parts > 1) {
@@ -408,23 +513,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
         __syncthreads();
     }
 
-    float m = -INFINITY;
+    m = -INFINITY;
     for (int c = 0; c < p.parts; ++c) m = fmaxf(m, s.parts[c].m);
-    float S = 0.f, U = 0.f;
-    int above = 0;
+    float S = 0.f, T = 0.f;
+    above = 0;
     for (int c = 0; c < p.parts; ++c) {
         const Part q = s.parts[c];
         const float d = octaves(q.m, m, p.c2), w = ex2(d);
         S = fmaf(w, q.S, S);
-        U += w * fmaf(q.S, d, q.U);
+        T += w * fmaf(q.S, d, q.U);
         above += q.above;
     }
     // (S is 0 where all are -inf, NaN with a NaN or +inf among them)
     const bool bad = !(S > 0.f) || m == INFINITY;
     const float log_s = logf(S), nan = __int_as_float(0x7FC00000);
+    const float M = m * p.c2;
+    // (not above 0 by a rounding)
+    auto log_of = [&](float z) {
+        const float t = fmaf(z, p.c2, -M);
+        return fminf(0.f, (fabsf(t) < INFINITY ? t * kLn2 : (z - m) * p.inv_t) - log_s);
+    };
     if (tid == 0) {
-        p.logprob[row] = bad ? nan : (zx - m) * p.inv_t - log_s;
-        if (p.entropy) p.entropy[row] = bad ? nan : fmaxf(0.f, log_s - U / S * 0.69314718055994531f);
+        p.logprob[row] = bad ? nan : log_of(zx);
+        if (p.entropy) p.entropy[row] = bad ? nan : fmaxf(0.f, log_s - T / S * kLn2);
         if (p.rank) p.rank[row] = bad ? -1 : above;
         if (p.status) {
             if (p.P == 1) p.status[b] = bad ? kEData : kOk;
@@ -446,21 +557,24 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
             if (key != 0 && r < K && SV_IN(row * K + r, p.rows * K)) {
                 const float z = key_to_f32((uint32_t)(key >> 32));
                 p.top_tokens[row * K + r] = (int32_t)(0xFFFFFFFFu - (uint32_t)key);
-                p.top_logprobs[row * K + r] = (z - m) * p.inv_t - log_s;
+                p.top_logprobs[row * K + r] = log_of(z);
             }
         }
     }
 }
 
-template <typename E, int NT, int NV>
+template <typename E, int NT, int U>
 cudaError_t launch(LogprobParams p, cudaStream_t st) {
     constexpr int VN = VecTraits<E>::kN;
     const long long granules = ((long long)p.V + VN - 1) / VN + 1;  // (one more where the row starts inside one)
-    // as few CTAs a row as hold it in their registers; more where there are few
-    // rows, down to parts of four granules a thread
+    // Few rows are split, until there are four CTAs an SM, down to parts of two
+    // granules a thread: a part's end costs as much as 30 KB of it. 288 rows of
+    // 128256 float32 logits, no alternatives (and 20): 33.2 (47.0) us whole, 30.8
+    // (42.3) in two parts, 36.5 (47.2) in four. Half of a step's rows have no token
+    // as a rule (512 rows, 288 with one, 20 alternatives: 53.5 us whole, 43.2 in two
+    // parts), hence four and not two.
     int parts = 1;
-    while (parts < kMaxParts && granules > (long long)parts * NT * NV) parts *= 2;
-    while (parts < kMaxParts && p.rows * parts < 152 * 2 && granules / parts > NT * 2) parts *= 2;
+    while (parts < kMaxParts && p.rows * parts < 152 * 4 && granules / parts > NT * 2) parts *= 2;
     p.parts = parts;
     p.part_granules = (int)((granules + parts - 1) / parts);
     cudaLaunchAttribute attr = {};
@@ -473,13 +587,13 @@ cudaError_t launch(LogprobParams p, cudaStream_t st) {
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, logprob_kernel<E, NT, NV>, p);
+    return cudaLaunchKernelEx(&cfg, logprob_kernel<E, NT, U>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams& p, int dtype, cudaStream_t st) {
-    return dtype == 0 ? launch<float, 512, 8>(p, st) : launch<bf16_t, 256, 8>(p, st);
+    return dtype == 0 ? launch<float, 256, 4>(p, st) : launch<bf16_t, 256, 2>(p, st);
 }
 
 SV_DEBUG_READER(logprobs)
