@@ -343,6 +343,9 @@ struct alignas(64) AttnMaps {
 // The map of one layer's keys or values (`base`), tiles of 128 positions in boxes
 // of a page's slots x 64 columns; false where the strides have none.
 bool cache_tc_map(const AttnParams& p, const void* base, AttnMaps* m);
+// The map of the queries: boxes of the heads of one group, as many nodes as have 128
+// rows together (at most N), 64 columns.
+bool query_tc_map(const AttnParams& p, AttnMaps* m);
 int attention_tc_rows(int group);
 int attention_tc_kv();
 int attention_tc_extra(int group, int N);

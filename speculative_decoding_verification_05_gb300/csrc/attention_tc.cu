@@ -965,14 +965,16 @@ bool cache_tc_map(const AttnParams& p, const void* base, AttnMaps* m) {
     return make_map(reinterpret_cast<CUtensorMap*>(m), p, base);
 }
 
+bool query_tc_map(const AttnParams& p, AttnMaps* m) {
+    const long long Hq = (long long)p.Hkv * p.G;
+    return encode_map(reinterpret_cast<CUtensorMap*>(m), p.q, {(cuuint64_t)p.D, (cuuint64_t)Hq, (cuuint64_t)p.N, (cuuint64_t)p.B},
+                      {p.D, Hq * p.D, p.N * Hq * p.D}, (cuuint32_t)p.G, (cuuint32_t)std::min(128 / p.G, p.N));
+}
+
 bool attention_tc_maps(const AttnParams& p, AttnMaps* m) {
     static_assert(sizeof(AttnMaps) >= 3 * sizeof(CUtensorMap), "three maps");
     CUtensorMap* maps = reinterpret_cast<CUtensorMap*>(m);
-    const long long Hq = (long long)p.Hkv * p.G;
-    // queries: boxes of the nodes of a half, the heads of one group
-    return make_map(maps, p, p.k) && make_map(maps + 1, p, p.v) &&
-           encode_map(maps + 2, p.q, {(cuuint64_t)p.D, (cuuint64_t)Hq, (cuuint64_t)p.N, (cuuint64_t)p.B},
-                      {p.D, Hq * p.D, p.N * Hq * p.D}, (cuuint32_t)p.G, (cuuint32_t)std::min(128 / p.G, p.N));
+    return make_map(maps, p, p.k) && make_map(maps + 1, p, p.v) && query_tc_map(p, reinterpret_cast<AttnMaps*>(maps + 2));
 }
 
 cudaError_t launch_attention_tc(const AttnParams& p, const AttnPlan& plan, const AttnMaps& m, cudaStream_t st) {

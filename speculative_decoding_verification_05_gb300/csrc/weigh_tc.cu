@@ -9,8 +9,8 @@
 //             the 128-byte swizzle) into a ring of stages;
 //   issuer    (warp 9) issues the products of up to two tiles with a chunk of up
 //             to 128 rows (whole nodes);
-//   loaders   (warps 10, 11) bring the chunks (copies of 16 bytes: a path's nodes
-//             lie anywhere) and their log-sums, three chunks ahead;
+//   loaders   (warps 10, 11) bring the chunks (a chain's by tensor copies; a path's
+//             nodes lie anywhere: copies of 16 bytes) and their log-sums, two ahead;
 //   two groups (warps 0-3, 4-7) of 128 threads, a key each: one of the two tiles;
 //   a warp that checks the sequences' data.
 // A stay's only chunk is brought once. Where there are more, they go by for every
@@ -34,14 +34,14 @@ static __device__ int g_withhold = -1;  // spec_debug_withhold_tile
 constexpr int NT = 416;
 constexpr int kKv = 128;    // keys of a tile
 constexpr int kRows = 128;  // rows of a chunk, at most
-constexpr int kChunks = 3;  // chunks in shared memory
-constexpr int kMaxStages = 8;
+constexpr int kChunks = 2;  // chunks in shared memory
+constexpr int kMaxStages = 10;
 constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile or a chunk
 
 template <int D>
 struct Shape {
     static constexpr uint32_t kTile = kKv * D * 2;
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = D == 128 ? 5 : 10;
     static constexpr size_t kSmem = 1024 + 2048 + (size_t)(kChunks + kStages) * kTile;
 };
 
@@ -50,15 +50,15 @@ struct Ctl {
     uint64_t q_full[kChunks], q_empty[kChunks];
     uint64_t s_full[2][2], s_free[2][2];  // of a group's two places
     uint64_t drain;
-    uint32_t tmem, loads;
+    uint32_t tmem, loads, asked;  // ring entries and chunks that copies were issued for
     int abort;
     int odd[kChunks][2];  // a log-sum of -inf among a loader's rows
     union {
         WeighScan scan;  // (before the loop)
-        float lse[kChunks][kRows];  // less the log-sums, in octaves; -inf: no weight
+        alignas(16) float lse[kChunks][kRows];  // less the log-sums, in octaves; -inf: no weight
     };
 };
-static_assert(sizeof(Ctl) <= 2048, "control region");
+static_assert(sizeof(Ctl) <= 2048 && offsetof(Ctl, lse) % 16 == 0, "control region");
 
 // The way through the part that all warps go: stays, their tiles two at a time,
 // and for each two the chunks. Everything in it is a function of the inputs.
@@ -157,9 +157,10 @@ struct Loader {
     static constexpr int kWords = D / 8, kPer = 32 / kWords;  // 16-byte words of a row, rows of a warp at a time
     const WeighParams& p;
     Ctl* c;
+    const CUtensorMap* map;
     uint32_t qs;
     int w;  // 0, 1
-    uint32_t buf = 0, phase = 1;
+    uint32_t buf = 0, phase = 1, count = 0;
 
     SV_DEV bool chunk(const Way& way, int k) {
         const int lane = threadIdx.x & 31, cols = way.cols(k), whole = (cols + 15) & ~15, Hq = p.Hkv * p.G;
@@ -187,30 +188,42 @@ struct Loader {
         }
         if (!warp_wait(&c->q_empty[buf], phase, &c->abort)) return false;
         const uint32_t base = qs + buf * Shape<D>::kTile;
-        const int word = lane % kWords;
-        const uint32_t col = (word >> 3) * kHalf;
+        if (!p.path) {
+            if (w == 0 && lane == 0) {
+                const int box = min(way.nodes, p.N);  // (nodes past the last one are zeros)
+                mbar_expect_tx(&c->q_full[buf], (uint32_t)(box * p.G) * (D * 2));
 #pragma unroll
-        for (int i = 0; i < kRows / 32; ++i) {
-            if (32 * i >= whole) break;
+                for (int i = 0; i < D / 64; ++i)
+                    tma_load4(base + i * kHalf, map, i * 64, s.h * p.G, k * way.nodes, s.b, &c->q_full[buf]);
+            }
+            __syncwarp();
+        } else {
+            const int word = lane % kWords;
+            const uint32_t col = (word >> 3) * kHalf;
 #pragma unroll
-            for (int j = 0; j < 32 / kPer / 2; ++j) {
-                const int lr = (2 * j + w) * kPer + lane / kWords, row = 32 * i + lr;
-                const long long from = __shfl_sync(0xFFFFFFFFu, at[i], lr);
-                if (row < whole) {
-                    const uint32_t dst = base + col + row * 128 + (((word & 7) ^ (row & 7)) << 4);
-                    const char* src = reinterpret_cast<const char*>(p.q) + (from < 0 ? 0 : from * (D * 2) + word * 16);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(from < 0 ? 0 : 16)
-                                 : "memory");
+            for (int i = 0; i < kRows / 32; ++i) {
+                if (32 * i >= whole) break;
+#pragma unroll
+                for (int j = 0; j < 32 / kPer / 2; ++j) {
+                    const int lr = (2 * j + w) * kPer + lane / kWords, row = 32 * i + lr;
+                    const long long from = __shfl_sync(0xFFFFFFFFu, at[i], lr);
+                    if (row < whole) {
+                        const uint32_t dst = base + col + row * 128 + (((word & 7) ^ (row & 7)) << 4);
+                        const char* src = reinterpret_cast<const char*>(p.q) + (from < 0 ? 0 : from * (D * 2) + word * 16);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(from < 0 ? 0 : 16)
+                                     : "memory");
+                    }
                 }
             }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&c->q_full[buf])) : "memory");
         }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&c->q_full[buf])) : "memory");
 #pragma unroll
         for (int i = 0; i < kRows / 32; ++i)
             if (i / 2 == w) c->lse[buf][32 * i + lane] = z[i];
         odd = __any_sync(0xFFFFFFFFu, odd);
         if (lane == 0) c->odd[buf][w] = odd;
         mbar_arrive(&c->q_full[buf]);
+        ++count;
         if (++buf == kChunks) {
             buf = 0;
             phase ^= 1;
@@ -231,6 +244,7 @@ struct Loader {
                 for (int k = way.first_chunk(tile); ok && k < way.chunks; ++k) ok = chunk(way, k);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
+        if (w == 0 && (threadIdx.x & 31) == 0) c->asked = count;
         if (!ok) c->abort = 1;
     }
 };
@@ -415,7 +429,8 @@ struct Group {
 
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
-    weigh_tc_kernel(const __grid_constant__ WeighParams p, const __grid_constant__ CUtensorMap map) {
+    weigh_tc_kernel(const __grid_constant__ WeighParams p, const __grid_constant__ CUtensorMap map,
+                    const __grid_constant__ CUtensorMap mq) {
     extern __shared__ unsigned char dyn[];
     unsigned char* mem = dyn + ((1024 - (smem_u32(dyn) & 1023)) & 1023);
     Ctl* c = reinterpret_cast<Ctl*>(mem);
@@ -429,7 +444,7 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&c->empty[i], 1);
         }
         for (int i = 0; i < kChunks; ++i) {
-            mbar_init(&c->q_full[i], 2 * 64);  // the loaders' copies and their stores
+            mbar_init(&c->q_full[i], p.path ? 2 * 64 : 1 + 64);  // the loaders' copies and their stores
             mbar_init(&c->q_empty[i], 1 + 8);  // the products and the groups' warps
         }
         for (int i = 0; i < 4; ++i) {
@@ -437,11 +452,12 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&c->s_free[i >> 1][i & 1], 4);
         }
         mbar_init(&c->drain, 1);
-        c->loads = 0;
+        c->loads = c->asked = 0;
         c->abort = 0;
         mbar_init_fence();
     }
     if (tid == 8 * 32) tma_prefetch(&map);
+    if (tid == 10 * 32 && !p.path) tma_prefetch(&mq);
     if (warp == 9) tmem_alloc512(&c->tmem);
     tc_fence_before();
     __syncthreads();
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(NT, 1)
         Issuer<D> is{c, uni(tmem), qs, stages};
         is.run(way);
     } else if (warp < 12) {
-        Loader<D> l{p, c, qs, warp - 10};
+        Loader<D> l{p, c, &mq, qs, warp - 10};
         l.run(way);
     } else {
         weigh_statuses(p, blockIdx.x, gridDim.x);
@@ -469,6 +485,9 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_after();
     if (c->abort) {  // copies and products in flight end before the CTA does
         constexpr uint32_t NS = Shape<D>::kStages;
+        if (tid == 10 * 32 && !p.path)
+            for (uint32_t r = c->asked > kChunks ? c->asked - kChunks : 0; r < c->asked; ++r)
+                tc_wait(&c->q_full[r % kChunks], (r / kChunks) & 1, nullptr);
         if (tid == 8 * 32)
             for (uint32_t r = c->loads > NS ? c->loads - NS : 0; r < c->loads; ++r)
                 tc_wait(&c->full[r % NS], (r / NS) & 1, nullptr);
@@ -487,10 +506,10 @@ __global__ void __launch_bounds__(NT, 1)
 }
 
 template <int D>
-cudaError_t launch(const WeighParams& p, const CUtensorMap& map, cudaStream_t st) {
+cudaError_t launch(const WeighParams& p, const CUtensorMap& map, const CUtensorMap& mq, cudaStream_t st) {
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(weigh_tc_kernel<D>), Shape<D>::kSmem);
     if (e != cudaSuccess) return e;
-    weigh_tc_kernel<D><<<152, NT, Shape<D>::kSmem, st>>>(p, map);
+    weigh_tc_kernel<D><<<152, NT, Shape<D>::kSmem, st>>>(p, map, mq);
     return cudaGetLastError();
 }
 
@@ -505,11 +524,15 @@ cudaError_t launch_weigh_tc(const WeighParams& p, cudaStream_t st, bool* took) {
     a.page_stride = p.page_stride;
     a.token_stride = p.token_stride;
     a.head_stride = p.head_stride;
-    AttnMaps m;
-    *took = cache_tc_map(a, p.k, &m);
+    a.q = p.q;
+    a.B = p.B;
+    a.N = p.N;
+    a.G = p.G;
+    AttnMaps k, q;
+    *took = cache_tc_map(a, p.k, &k) && query_tc_map(a, &q);
     if (!*took) return cudaSuccess;
-    const CUtensorMap& map = *reinterpret_cast<const CUtensorMap*>(&m);
-    return p.D == 128 ? launch<128>(p, map, st) : launch<64>(p, map, st);
+    const CUtensorMap &mk = *reinterpret_cast<const CUtensorMap*>(&k), &mq = *reinterpret_cast<const CUtensorMap*>(&q);
+    return p.D == 128 ? launch<128>(p, mk, mq, st) : launch<64>(p, mk, mq, st);
 }
 
 int debug_withhold_weigh_tile(int j) {
