@@ -6,8 +6,9 @@
 //
 // Two launches. One block a (layer, sequence, head) finds the weight of rank m
 // among the n middle positions - the largest key that at least m of them reach,
-// by halving the interval of ordered 32-bit keys, a count of the block a step -
-// lists the kept positions by one prefix sum, and moves the weights. Then one
+// digit by digit of the ordered 32-bit keys (11, 11 and 10 bits), each by a
+// histogram of the positions that share the digits before it -, lists the kept
+// positions by one prefix sum, and moves the weights. Then one
 // block a list and K or V moves the rows: as a kept position's new place is never
 // behind its old one, rows are read a batch at a time and written when the whole
 // block has read its batch, and no later batch's row is overwritten.
@@ -22,6 +23,7 @@ namespace {
 
 constexpr int ST = 512;   // threads of a selecting block
 constexpr int kItems = 8;  // positions of a thread: neighbours
+constexpr int kBins = 2048;  // values of a digit of a key
 constexpr int CT = 256;
 constexpr int kMoves = 8;
 constexpr int kMostRows = 64;  // rows that a block reads at once, an eighth of a batch
@@ -31,17 +33,6 @@ SV_DEV void stg16(char* p, uint4 x) { *reinterpret_cast<uint4*>(p) = x; }
 
 // Ordered keys of weights; NaN above everything.
 SV_DEV uint32_t weight_key(float w) { return w != w ? 0xFFFFFFFFu : f32_key(w); }
-
-SV_DEV int block_sum(int v, int* scratch) {
-    v = __reduce_add_sync(0xFFFFFFFFu, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < ST / 32; ++w) s += scratch[w];
-    return s;
-}
 
 // Exclusive prefixes of two counts over the block's threads, and their sums.
 SV_DEV void block_prefix2(int a, int b, int* pa, int* pb, int* sa, int* sb, int2* scratch) {
@@ -69,9 +60,12 @@ SV_DEV void block_prefix2(int a, int b, int* pa, int* pb, int* sa, int* sb, int2
 }
 
 __global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant__ EvictParams p) {
-    __shared__ int scratch[ST / 32];
-    __shared__ int2 scratch2[ST / 32];
-    __shared__ int first_moved;
+    __shared__ union {
+        int hist[kBins];
+        int2 kept[ST * kItems];  // positions and weights that one round keeps
+    } u;
+    __shared__ int2 scratch[ST / 32];
+    __shared__ int first_moved, found, rest;
     asm volatile("griddepcontrol.launch_dependents;");
     const long long unit = blockIdx.x;  // (layer, sequence, head)
     const int h = (int)(unit % p.c.heads), b = (int)(unit / p.c.heads % p.B), tid = threadIdx.x, sh = p.c.page_shift;
@@ -117,36 +111,56 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant_
             for (int j = 0; j < kItems; ++j) x[j] = t + j < len ? w[t + j] : 0.f;
         }
     };
-    // middle positions whose key is at least k
-    auto count = [&](uint32_t k) {
-        int c = 0;
-        for (int at = 0; at < len; at += ST * kItems) {
-            if (!fits) load(at);
-            const int t = at + tid * kItems;
-#pragma unroll
-            for (int j = 0; j < kItems; ++j) c += t + j >= mid0 && t + j < mid1 && weight_key(x[j]) >= k;
-        }
-        return block_sum(c, scratch);
-    };
     if (tid == 0) first_moved = keep;
     if (fits) load(0);
-    // `lo`: reached by m or more; `hi`: by fewer (above all keys at first)
-    unsigned long long lo = 0, hi = 1ull << 32;
-    bool exact = false;  // reached by just m
+    // The m-th key from above, and how many of its ties are kept (m = 0: a bound
+    // above all keys).
+    unsigned long long bound = 1ull << 32;
+    int ties = m;
     if (m > 0) {
-        while (hi - lo > 1 && !exact) {
-            const unsigned long long mid = (lo + hi) >> 1;
-            const int c = count((uint32_t)mid);
-            if (c >= m) lo = mid;
-            else hi = mid;
-            exact = c == m;
+        uint32_t prefix = 0;  // the digits so far
+#pragma unroll 1
+        for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {
+            const uint32_t mask = shift ? kBins - 1 : 1023;
+            const int before = shift == 21 ? 32 : shift + (shift ? 11 : 10);  // bits that the prefix leaves
+            for (int i = tid; i < kBins; i += ST) u.hist[i] = 0;
+            __syncthreads();
+            for (int at = 0; at < len; at += ST * kItems) {
+                if (!fits) load(at);
+                const int t = at + tid * kItems;
+#pragma unroll
+                for (int j = 0; j < kItems; ++j) {
+                    const uint32_t k = weight_key(x[j]);
+                    if (t + j >= mid0 && t + j < mid1 && (before == 32 || k >> before == prefix))
+                        atomicAdd(&u.hist[k >> shift & mask], 1);
+                }
+            }
+            __syncthreads();
+            // from the largest digit down, kBins / ST a thread
+            const int top = kBins - 1 - tid * (kBins / ST);
+            int n[kBins / ST], sum = 0;
+#pragma unroll
+            for (int j = 0; j < kBins / ST; ++j) sum += n[j] = u.hist[top - j];
+            int above, unused, s0, s1;
+            block_prefix2(sum, 0, &above, &unused, &s0, &s1, scratch);
+            if (above < ties && ties <= above + sum) {
+#pragma unroll
+                for (int j = 0; j < kBins / ST; ++j) {
+                    if (above < ties && ties <= above + n[j]) {
+                        found = top - j;
+                        rest = ties - above;
+                    }
+                    above += n[j];
+                }
+            }
+            __syncthreads();
+            prefix = prefix << (shift ? 11 : 10) | (uint32_t)found;
+            ties = rest;
         }
-    } else {
-        lo = hi;  // none of the middle
+        bound = prefix;
     }
-    const int ties = exact || m == 0 ? 0x7FFFFFFF : m - (hi <= 0xFFFFFFFFull ? count((uint32_t)hi) : 0);
     // kept so far: those above the bound or always kept, and ties
-    int above0 = 0, tied0 = 0;
+    int above0 = 0, tied0 = 0, moved = keep;  // (moved: the first entry that changes its place)
     __syncthreads();
     for (int at = 0; at < len; at += ST * kItems) {
         if (!fits) load(at);
@@ -157,28 +171,40 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant_
             const int i = t + j;
             const unsigned long long k = weight_key(x[j]);
             const bool in = i < len, always = i < mid0 || i >= mid1;
-            if (in && (always || k > lo)) above |= 1u << j;
-            else if (in && k == lo) tied |= 1u << j;
+            if (in && (always || k > bound)) above |= 1u << j;
+            else if (in && k == bound) tied |= 1u << j;
         }
         int a, e, sa, se;
-        block_prefix2(__popc(above), __popc(tied), &a, &e, &sa, &se, scratch2);  // (its barriers: all have read)
+        block_prefix2(__popc(above), __popc(tied), &a, &e, &sa, &se, scratch);  // (its barriers: all have read)
+        // (in shared memory first: the threads' places lie apart, and each is one word)
+        const int start = above0 + min(tied0, ties);
         a += above0;
         e += tied0;
 #pragma unroll
         for (int j = 0; j < kItems; ++j) {
             const bool is = above >> j & 1, tie = tied >> j & 1;
             const int to = a + min(e, ties);
-            if ((is || (tie && e < ties)) && SV_IN(to, keep)) {
-                list[to] = t + j;
-                w[to] = x[j];
-                if (to != t + j) atomicMin(&first_moved, to);
+            if (is || (tie && e < ties)) {
+                u.kept[to - start] = make_int2(t + j, __float_as_int(x[j]));
+                if (to != t + j) moved = min(moved, to);
             }
             a += is;
             e += tie;
         }
         above0 += sa;
         tied0 += se;
+        __syncthreads();
+        const int n = above0 + min(tied0, ties) - start;
+        for (int i = tid; i < n; i += ST) {
+            const int2 k = u.kept[i];
+            if (SV_IN(start + i, keep)) {
+                list[start + i] = k.x;
+                w[start + i] = __int_as_float(k.y);
+            }
+        }
     }
+    moved = __reduce_min_sync(0xFFFFFFFFu, moved);
+    if ((tid & 31) == 0 && moved < keep) atomicMin(&first_moved, moved);
     __syncthreads();
     for (int i = keep + tid; i < len; i += ST) w[i] = 0.f;
     if (tid == 0) p.jobs[unit] = make_int2(first_moved, keep);
@@ -190,7 +216,8 @@ __global__ void __launch_bounds__(CT) evict_move_kernel(const __grid_constant__ 
     const int h = (int)(unit % p.c.heads), b = (int)(unit / p.c.heads % p.B), tid = threadIdx.x, sh = p.c.page_shift;
     char* base = (blockIdx.x & 1 ? p.c.v : p.c.k) + unit / p.c.heads / p.B * p.c.layer_stride + h * p.c.head_stride;
     const int32_t* table = p.table + b * p.table_stride;
-    const int words = p.c.row_bytes / 16, width = min(CT / words, kMostRows), r0 = tid / words, col = tid - r0 * words;
+    const int words = p.c.row_bytes / 16 / gridDim.y, width = min(CT / words, kMostRows), r0 = tid / words;
+    const int col = blockIdx.y * words + tid - r0 * words;
     const int batch = width * kMoves;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int2 job = __ldcg(p.jobs + unit);
@@ -232,7 +259,10 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t st) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * units));
+    // few lists: a row's columns are shared out too, down to 64 bytes
+    int split = 1;
+    while (split < 4 && p.c.row_bytes % (128 * split) == 0 && 2 * units * split < 152 * 4) split *= 2;
+    cfg.gridDim = dim3((unsigned)(2 * units), split);
     cfg.blockDim = dim3(CT);
     cfg.stream = st;
     cfg.attrs = &attr;
