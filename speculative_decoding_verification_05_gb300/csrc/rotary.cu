@@ -66,20 +66,29 @@ enum Layout : int {
 // where c < half): the result's one or two words. cs: the token's pairs.
 template <typename E, int LAYOUT>
 struct Row {
-    static constexpr int VN = VecTraits<E>::kN;
+    static constexpr int VN = VecTraits<E>::kN, kPairs = LAYOUT == kNeighbours ? VN / 2 : VN;
     uint4 x, y;
+    // The word's pairs of a token's (cs).
+    SV_DEV static void pairs(const RotaryParams& p, const float2* cs, int c, float2 (&z)[kPairs]) {
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+            int j = c * kPairs + e;
+            if (LAYOUT == kSplit && j >= p.half) j -= p.half;
+            if (j < p.half) z[e] = cs[j];
+        }
+    }
     SV_DEV void load(const RotaryParams& p, const char* from, int c) {
         x = ldg16(from + c * 16);
         if (LAYOUT == kHalves && c * VN < p.half) y = ldg16(from + c * 16 + p.half * (int)sizeof(E));
     }
-    SV_DEV void store(const RotaryParams& p, const char* from, char* to, int c, const float2* cs) {
+    SV_DEV void store(const RotaryParams& p, const char* from, char* to, int c, const float2 (&cs)[kPairs]) {
         float a[VN], b[VN], u[VN], v[VN];
         VecTraits<E>::unpack(x, a);
         if (LAYOUT == kHalves) {
             if (c * VN >= p.half) return stg16(to + c * 16, x);
             VecTraits<E>::unpack(y, b);
 #pragma unroll
-            for (int e = 0; e < VN; ++e) rotate(a[e], b[e], cs[c * VN + e], &u[e], &v[e]);
+            for (int e = 0; e < VN; ++e) rotate(a[e], b[e], cs[e], &u[e], &v[e]);
             stg16(to + c * 16, pack<E>(u));
             stg16(to + c * 16 + p.half * (int)sizeof(E), pack<E>(v));
         } else if (LAYOUT == kNeighbours) {
@@ -88,7 +97,7 @@ struct Row {
                 const int j = (c * VN + e) >> 1;
                 u[e] = a[e];
                 u[e + 1] = a[e + 1];
-                if (j < p.half) rotate(a[e], a[e + 1], cs[j], &u[e], &u[e + 1]);
+                if (j < p.half) rotate(a[e], a[e + 1], cs[e >> 1], &u[e], &u[e + 1]);
             }
             stg16(to + c * 16, pack<E>(u));
         } else {
@@ -99,8 +108,8 @@ struct Row {
                 if (j < p.half) {
                     const float other = VecTraits<E>::load1(from + (i < p.half ? i + p.half : j) * (int)sizeof(E));
                     float w;
-                    if (i < p.half) rotate(a[e], other, cs[j], &u[e], &w);
-                    else rotate(other, a[e], cs[j], &w, &u[e]);
+                    if (i < p.half) rotate(a[e], other, cs[e], &u[e], &w);
+                    else rotate(other, a[e], cs[e], &w, &u[e]);
                 }
             }
             stg16(to + c * 16, pack<E>(u));
@@ -109,7 +118,7 @@ struct Row {
 };
 
 template <typename E, int LAYOUT>
-__global__ void __launch_bounds__(CT) append_rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(CT, 4) append_rotary_kernel(const __grid_constant__ RotaryParams p) {
     constexpr int VN = VecTraits<E>::kN;
     __shared__ float2 cs[kMostTokens * SPEC_MAX_HEAD_DIM / 2];
     __shared__ long long place[kMostTokens];
@@ -144,6 +153,35 @@ __global__ void __launch_bounds__(CT) append_rotary_kernel(const __grid_constant
         for (long long i = tid; i < words; i += CT) stg16(o + i * 16, make_uint4(fill, fill, fill, fill));
     }
     if (used == t0) return;  // (the same for the whole block)
+    // rotated rows, the queries' heads, then the keys': a thread has one column of
+    // one token (its cosines stay in registers) and every `slots`-th head
+    const int heads = p.q_heads + p.c.heads;
+    const int cols = LAYOUT == kHalves ? (D - p.half) / VN : D / VN, slots = CT / cols / p.tokens;
+    const int r0 = tid / cols, c0 = tid - r0 * cols, t = r0 / slots, h0 = r0 - t * slots;
+    // (kHalves: columns from half on are the ones that are not rotated)
+    const int c = LAYOUT == kHalves && c0 * VN >= p.half ? c0 + p.half / VN : c0;
+    const bool mine = t < used - t0;
+    const long long token = (long long)b * p.N + t0 + t;
+    auto from = [&](int h) {
+        return h < p.q_heads ? p.q + (token * p.q_heads + h) * p.c.row_bytes : p.k + (token * p.c.heads + h - p.q_heads) * p.c.row_bytes;
+    };
+    constexpr int U = LAYOUT == kHalves ? 2 : 4;  // rows in flight
+    Row<E, LAYOUT> row[U];
+    auto load = [&](int h) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (h + u * slots < heads) row[u].load(p, from(h + u * slots), c);
+    };
+    // the values, as they are: the first ones, and the first rows, are on their way
+    // while the cosines are computed
+    const int per_head = D / VN, per_token = p.c.heads * per_head, words = (used - t0) * per_token;
+    const char* v = p.v + ((long long)b * p.N + t0) * per_token * 16;
+    constexpr int VU = 2;
+    uint4 x[VU];
+#pragma unroll
+    for (int u = 0; u < VU; ++u)
+        if (tid + u * CT < words) x[u] = ldg16(v + (long long)(tid + u * CT) * 16);
+    if (mine) load(h0);
     for (int i = tid; i < (used - t0) * p.half; i += CT) {
         const int t = i / p.half, j = i - t * p.half;
         cs[i] = turn(__ldg(p.turns + j), pos0 + (depth ? depth[t0 + t] : t0 + t), p.factor);
@@ -153,48 +191,30 @@ __global__ void __launch_bounds__(CT) append_rotary_kernel(const __grid_constant
         place[tid] = (long long)table[pos >> sh] * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride;
     }
     __syncthreads();
-
-    // rotated rows: the queries' heads, then the keys'
-    const int heads = p.q_heads + p.c.heads, rows = (used - t0) * heads;
-    const int cols = LAYOUT == kHalves ? (D - p.half) / VN : D / VN, width = CT / cols;
-    const int r0 = tid / cols, c0 = tid - r0 * cols;
-    // (kHalves: columns from half on are the ones that are not rotated)
-    const int c = LAYOUT == kHalves && c0 * VN >= p.half ? c0 + p.half / VN : c0;
-    auto from = [&](int r, int* t, int* h) {
-        *t = r / heads;
-        *h = r - *t * heads;
-        const long long token = (long long)b * p.N + t0 + *t;
-        return *h < p.q_heads ? p.q + (token * p.q_heads + *h) * p.c.row_bytes
-                              : p.k + (token * p.c.heads + *h - p.q_heads) * p.c.row_bytes;
+    auto put = [&](int i, uint4 y) {
+        const int t = i / per_token, e = i - t * per_token, h = e / per_head;
+        stg16(p.c.v + place[t] + h * p.c.head_stride + (e - h * per_head) * 16, y);
     };
-    auto to = [&](int t, int h) {
-        return h < p.q_heads ? p.q_out + (((long long)b * p.N + t0 + t) * p.q_heads + h) * p.c.row_bytes
-                             : p.c.k + place[t] + (h - p.q_heads) * p.c.head_stride;
-    };
-    if (r0 < width) {
-        constexpr int U = 2;
-        for (int r = r0; r < rows; r += U * width) {
-            Row<E, LAYOUT> row[U];
-            int t[U], h[U];
-            const char* f[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + u * width < rows) {
-                    f[u] = from(r + u * width, &t[u], &h[u]);
-                    row[u].load(p, f[u], c);
-                }
+    for (int u = 0; u < VU; ++u)
+        if (tid + u * CT < words) put(tid + u * CT, x[u]);
+    if (mine) {
+        float2 z[Row<E, LAYOUT>::kPairs];
+        Row<E, LAYOUT>::pairs(p, cs + t * p.half, c, z);
+        char* const k = p.c.k + place[t];
+        for (int h = h0; h < heads; h += U * slots) {
+            if (h != h0) load(h);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + u * width < rows) row[u].store(p, f[u], to(t[u], h[u]), c, cs + t[u] * p.half);
+            for (int u = 0; u < U; ++u) {
+                const int i = h + u * slots;
+                if (i < heads)
+                    row[u].store(p, from(i),
+                                 i < p.q_heads ? p.q_out + (token * p.q_heads + i) * p.c.row_bytes : k + (i - p.q_heads) * p.c.head_stride,
+                                 c, z);
+            }
         }
     }
-    // values, as they are
-    const int per_head = D / VN, per_token = p.c.heads * per_head;
-    const char* v = p.v + ((long long)b * p.N + t0) * per_token * 16;
-    for (int i = tid; i < (used - t0) * per_token; i += CT) {
-        const int t = i / per_token, e = i - t * per_token, h = e / per_head;
-        stg16(p.c.v + place[t] + h * p.c.head_stride + (e - h * per_head) * 16, ldg16(v + (long long)i * 16));
-    }
+    for (int i = tid + VU * CT; i < words; i += CT) put(i, ldg16(v + (long long)i * 16));
 }
 
 template <typename E>
