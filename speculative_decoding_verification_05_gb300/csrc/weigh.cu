@@ -29,7 +29,7 @@ struct alignas(16) Ctl {
 size_t smem_bytes(int D) { return sizeof(Ctl) + (size_t)(KV + R) * (D + 4) * sizeof(float); }
 
 template <typename E>
-__global__ void __launch_bounds__(NT) weigh_kernel(const __grid_constant__ WeighParams p) {
+__global__ void __launch_bounds__(NT, 4) weigh_kernel(const __grid_constant__ WeighParams p) {
     constexpr int VN = VecTraits<E>::kN;
     extern __shared__ __align__(16) unsigned char smem[];
     Ctl* c = reinterpret_cast<Ctl*>(smem);
