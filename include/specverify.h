@@ -40,11 +40,12 @@
  *    an ordinary zero-probability logit. SPEC_ETIMEOUT: a bounded device
  *    wait gave up. Kernels never wait on other CTAs (every hand-off between
  *    CTAs is a last-arriver counter or the end of a kernel); only the warps
- *    of one CTA of the shared-memory row path and of the attention on the
- *    tensor cores wait on one another (bounded, about a second at the most),
- *    and when one such wait gives up, what that CTA had left is reported with
- *    SPEC_ETIMEOUT (rows: outputs -1; attention: the sequences whose outputs
- *    are incomplete).
+ *    of one CTA of the shared-memory row path and of the attention and the
+ *    weighing on the tensor cores wait on one another (bounded, about a second
+ *    at the most), and when one such wait gives up, what that CTA had left is
+ *    reported with SPEC_ETIMEOUT (rows: outputs -1; attention and weighing: the
+ *    sequences whose outputs are incomplete). The CTAs of a thread-block cluster
+ *    meet at the hardware's cluster barriers.
  *  - Workspace: a device buffer of at least the size the matching
  *    *_workspace_size() function returns, 256-byte aligned, owned by the
  *    caller. Its content on entry does not matter: each call clears the small
@@ -593,7 +594,7 @@ spec_status spec_cache_compact(const spec_cache* cache, spec_dtype dtype, const 
  *                 needs path_nodes NULL (a chain or one token of plain decoding)
  *   path_nodes    [B, W] int32; NULL: i(r) = r, a chain
  *   weights       [B, kv_heads, capacity] float; only t < L + accept_len[b] + 1
- *                 is touched
+ *                 is touched; capacity <= 2^30
  *   status        [B] SPEC_OK, or SPEC_EDATA for a length, path or page out of
  *                 range, or positions past the capacity (nothing is added; by a
  *                 page out of range, nothing at its own positions); NULL allowed
@@ -616,7 +617,7 @@ spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* 
  * (spec_cache_append_rotary's positions).
  *   budget        [B] int32, each at least sink + recent
  *   weights       [layers, B, kv_heads, capacity] float, changed in place
- *   capacity      at least every cache_len
+ *   capacity      at least every cache_len, at most 2^30
  *   new_len       [B] int32: min(cache_len, budget); -1 on SPEC_EDATA. new_len
  *                 and status overlap neither each other nor an input
  *   status        [B] SPEC_OK, or SPEC_EDATA for a length, budget or page out of
@@ -625,7 +626,7 @@ spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* 
  *                 (nothing moves); NULL allowed
  *   workspace     >= spec_cache_evict_workspace_size(layers, B, kv_heads,
  *                 capacity) bytes
- * layers x B x kv_heads <= 2^30.
+ * layers x B x kv_heads < 2^30.
  * ---------------------------------------------------------------------- */
 size_t spec_cache_evict_workspace_size(int layers, int B, int kv_heads, int64_t capacity);
 
@@ -702,8 +703,8 @@ int spec_debug_failures(int* line);
  * builds (nothing is changed) or on a CUDA error. */
 int spec_debug_withhold_copy(int j);
 
-/* As spec_debug_withhold_copy, for the attention on the tensor cores: the first
- * CTA withholds the copies of the j-th tile of keys or values that it takes
+/* As spec_debug_withhold_copy, for the attention and the weighing on the tensor
+ * cores: the first CTA withholds the copies of the j-th tile of keys or values that it takes
  * (j < 0: none). Its waits give up (within about a second), the
  * sequences of its part are reported SPEC_ETIMEOUT (their outputs are
  * incomplete), the others' outputs are as usual. */

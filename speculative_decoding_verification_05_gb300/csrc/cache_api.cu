@@ -317,7 +317,7 @@ spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* 
     if (!cache_ok(cache, dtype) || cache->layers != 1 || !table_ok(page_table, table_stride, max_pages))
         return SPEC_EINVAL;
     if (!attention_shape_ok(B, N, q_heads, cache->kv_heads, cache->head_dim) ||
-        (path_nodes && (!accept_len || W < 1 || W > SPEC_MAX_TREE_N)) || capacity < 1 || capacity > (1LL << 31))
+        (path_nodes && (!accept_len || W < 1 || W > SPEC_MAX_TREE_N)) || capacity < 1 || capacity > (1LL << 30))
         return SPEC_EINVAL;
     if (!q || !lse || !weights || !cache_len || !aligned(q, 16) || !aligned(lse, 4) || !aligned(weights, 4) ||
         !aligned(cache_len, 4) || !aligned(accept_len, 4) || !aligned(path_nodes, 4) || !aligned(status, 4))
@@ -359,8 +359,8 @@ spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* 
 }
 
 size_t spec_cache_evict_workspace_size(int layers, int B, int kv_heads, int64_t capacity) {
-    if (layers < 1 || B < 1 || B > kMaxB || kv_heads < 1 || kv_heads > 1024 || capacity < 1 || capacity > (1LL << 31) ||
-        (double)layers * B * kv_heads > (double)(1 << 30))
+    if (layers < 1 || B < 1 || B > kMaxB || kv_heads < 1 || kv_heads > 1024 || capacity < 1 || capacity > (1LL << 30) ||
+        (double)layers * B * kv_heads >= (double)(1 << 30))
         return 0;
     const size_t units = (size_t)layers * B * kv_heads;
     return al(units * sizeof(int2)) + al(units * (size_t)capacity * sizeof(int32_t));
