@@ -10,8 +10,16 @@
 // quarter turn goes through sinpi and cospi. Products are fp32, rounded once.
 //
 // A block takes a few tokens: their cosines and sines once in shared memory for
-// all heads, then a thread a 16-byte column (or a pair of them) of a head's row,
-// two rows in flight.
+// all heads, then a thread a 16-byte column (or a pair of them) of one token, its
+// cosines in registers, and every few heads of it, two to four rows in flight; the
+// first rows and values are under way before the cosines are computed. Neighbouring
+// threads have neighbouring heads (neighbouring tokens: 36.2 us for 32.4).
+//
+// Bound by memory where there is enough of it: 8 x 1000 tokens, 32 query and 8 key
+// heads of 128 columns, bf16: 32.4 us, 5.6 TB/s read and written (the append alone,
+// which has no queries to write, 6.0). Below that by the chain of lengths, table,
+// cosines and rows: 16 trees of 61 nodes, 12 heads of 64, float32: 7.4 us, one chain
+// of 5: 3.6 us.
 
 #include <algorithm>
 
@@ -228,6 +236,8 @@ cudaError_t launch(const RotaryParams& p, dim3 grid, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_append_rotary(RotaryParams p, int dtype, cudaStream_t st) {
+    // four tokens a block where that leaves every SM four blocks (one: the first
+    // steps of a block, its lengths and page, would be taken four times)
     p.tokens = (long long)p.B * p.N >= 152 * 4 * kMostTokens ? kMostTokens : 1;
     const dim3 grid((p.N + p.tokens - 1) / p.tokens, p.B);
     return dtype == 0 ? launch<float>(p, grid, st) : launch<bf16_t>(p, grid, st);

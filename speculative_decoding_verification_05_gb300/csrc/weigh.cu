@@ -4,6 +4,11 @@
 // A block holds a tile of 64 keys in shared memory (fp32, whatever the type) and
 // brings its rows 32 at a time; a thread has 4 keys and 2 rows of the products.
 // The sums over rows stay in registers until the tile's end.
+//
+// Bound by latency where there are few tiles (keys, rows, products and sums follow
+// one another; four blocks an SM overlap them: 8 chains of 8, 12 heads of 64,
+// float32, 20-1500 positions 21.9 us, 26.5 with two), else by the products' reads of
+// shared memory, 10 wavefronts for 32 multiplications of a warp.
 
 #include <algorithm>
 

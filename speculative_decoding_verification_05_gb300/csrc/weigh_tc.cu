@@ -10,11 +10,20 @@
 //   issuer    (warp 9) issues the products of up to two tiles with a chunk of up
 //             to 128 rows (whole nodes);
 //   loaders   (warps 10, 11) bring the chunks (a chain's by tensor copies; a path's
-//             nodes lie anywhere: copies of 16 bytes) and their log-sums, two ahead;
+//             nodes lie anywhere: copies of 16 bytes) and their log-sums, three ahead;
 //   two groups (warps 0-3, 4-7) of 128 threads, a key each: one of the two tiles;
 //   a warp that checks the sequences' data.
 // A stay's only chunk is brought once. Where there are more, they go by for every
 // two tiles, from L2.
+//
+// What bounds it. Few rows: memory (one token of 64 sequences, contexts to 8192, 8
+// key heads of 4 query heads: 100 us, 5.5 TB/s of keys and weights). Accepted paths
+// of 1 to 7 nodes, 16 sequences, 300-4000 positions, 8 x 8 heads: 22.7 us, of which
+// the keys at that rate would take 13; the rest are the first lookups of a launch
+// and of each stay. Many rows: the exponentials, 16 a cycle and SM (a chunk of 500
+// nodes at 4000 positions, 8 x 4 heads: 33.4 us, 0.52 PFLOP/s; with the chunks
+// brought by 16-byte copies, whose addresses took two warps longer than the
+// products, 44.9).
 
 #include <cuda.h>
 
@@ -34,14 +43,14 @@ static __device__ int g_withhold = -1;  // spec_debug_withhold_tile
 constexpr int NT = 416;
 constexpr int kKv = 128;    // keys of a tile
 constexpr int kRows = 128;  // rows of a chunk, at most
-constexpr int kChunks = 2;  // chunks in shared memory
+constexpr int kChunks = 3;  // chunks in shared memory
 constexpr int kMaxStages = 10;
 constexpr uint32_t kHalf = kKv * 128;  // bytes of 64 columns of a tile or a chunk
 
 template <int D>
 struct Shape {
     static constexpr uint32_t kTile = kKv * D * 2;
-    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr int kStages = D == 128 ? 4 : 10;
     static constexpr size_t kSmem = 1024 + 2048 + (size_t)(kChunks + kStages) * kTile;
 };
 

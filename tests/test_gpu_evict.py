@@ -193,3 +193,34 @@ def test_debug_build_agrees():
     with sv.use_library(sv.DEBUG_LIB_PATH):
         d.check(50, 2, 8)
         assert sv.load_library().spec_debug_failures(None) == 0
+
+
+@pytest.mark.parametrize("dtype,D,page_size", [("bf16", 128, 32), ("f32", 64, 16), ("bf16", 64, 128), ("bf16", 8, 256)])
+def test_many_long_lists(dtype, D, page_size):
+    """Lists of many batches in all blocks at once, several times: warps that are behind
+    must find their batch's places as they were."""
+    layers, H, keep, sink, recent = 6, 8, 1300, 4, 300
+    lens = [3000 - 37 * b for b in range(8)]
+    for seed in range(4):
+        c = Cache(seed, lens, layers, H, D, page_size, dtype)
+        B, T = len(lens), c.T
+        place = torch.arange(T, device="cuda")
+        order = c.w.clone()
+        order[..., :sink] = math.inf
+        for b, L in enumerate(lens):
+            order[:, b, :, L - recent:L] = math.inf
+            order[:, b, :, L:] = -math.inf
+        kept = torch.sort(order, dim=-1, descending=True, stable=True).indices[..., :keep].sort(-1).values   # [y, b, h, keep]
+        page = c.table.long()[None, :, None].expand(layers, B, H, -1)
+        y, h = torch.arange(layers, device="cuda")[:, None, None, None], torch.arange(H, device="cuda")[None, None, :, None]
+        frm = page.gather(-1, kept // page_size) * page_size + kept % page_size
+        to = page.gather(-1, (place[:keep] // page_size).expand_as(kept)) * page_size + place[:keep] % page_size
+        want = []
+        for cache in (c.k, c.v):
+            flat = cache.clone().view(layers, -1, H, D)
+            flat[y, to, h] = flat[y, frm, h]
+            want.append(flat.view_as(cache))
+        w = c.w.gather(-1, kept)
+        r = sv.cache_evict(c.k, c.v, c.table, c.len, c.w, keep, sink, recent)
+        assert r["cache_len"].tolist() == [keep] * B
+        assert torch.equal(c.k, want[0]) and torch.equal(c.v, want[1]) and torch.equal(c.w[..., :keep], w)

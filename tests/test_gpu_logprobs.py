@@ -2,10 +2,11 @@
 
 Tolerances. A log probability is (z - m) / T - ln S: three roundings of y = (z -
 m) / T, 2^-24 |y| each, and S, whose terms are off by 2^-22 (the exponential, 2
-units) and 2^-24 |t| of their exponent t, and which a thread sums 64 at a time,
-4 rounds at the most, before trees of under 20 additions: (256 + 20) 2^-24 of it
-if every rounding went the same way, below 2^-15. Entropies add sum w t / S, off by
-that share of itself, at most ln V + |ln S| each.
+units) and 2^-24 |t| of their exponent t, and which a thread sums by batches of 16
+before it adds the batches (64 of them at the most), threads and parts in trees of
+under 20 additions: far fewer than 276 roundings of 2^-24 on any way, below 2^-15 if
+all went the same way. Entropies add sum w t / S, off by that share of itself, at most
+ln V + |ln S| each.
 """
 
 import math
