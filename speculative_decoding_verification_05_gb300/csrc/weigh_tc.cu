@@ -17,13 +17,15 @@
 // two tiles, from L2.
 //
 // What bounds it. Few rows: memory (one token of 64 sequences, contexts to 8192, 8
-// key heads of 4 query heads: 100 us, 5.5 TB/s of keys and weights). Accepted paths
-// of 1 to 7 nodes, 16 sequences, 300-4000 positions, 8 x 8 heads: 22.7 us, of which
-// the keys at that rate would take 13; the rest are the first lookups of a launch
-// and of each stay. Many rows: the exponentials, 16 a cycle and SM (a chunk of 500
-// nodes at 4000 positions, 8 x 4 heads: 33.4 us, 0.52 PFLOP/s; with the chunks
-// brought by 16-byte copies, whose addresses took two warps longer than the
-// products, 44.9).
+// key heads of 4 query heads: 102 us, 5.4 TB/s of keys and weights; 100 with five
+// stages and two chunks). Accepted paths of 1 to 7 nodes, 16 sequences, 300-4000
+// positions, 8 x 8 heads: 22.7 us, of which the keys at that rate would take 13; the
+// rest are the first lookups of a launch and of each stay. Many rows: the latency
+// of a chunk's way (wait, tensor memory, exponentials, release; tensor pipe and
+// exponential unit are a quarter busy, the schedulers a third): a chunk of 500 nodes
+// at 4000 positions, 8 x 4 heads 32.2 us, 0.54 PFLOP/s (33.3 with two chunks of rows
+// in shared memory; 44.9 with the chunks brought by 16-byte copies, whose addresses
+// took two warps longer than the products).
 
 #include <cuda.h>
 
