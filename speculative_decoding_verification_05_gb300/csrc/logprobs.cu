@@ -28,7 +28,7 @@
 // rank, the rest loads and batches' ends), bf16 15; the scheduler issues in half
 // to two thirds of the cycles. 288 rows of 128256 float32 logits: 36.9 us without
 // alternatives (4.0 TB/s; 30.8 in parts of half a row), 48.3 with 20; 2000 rows of
-// 32016 bf16: 41.1 us (3.1 TB/s); five rows of 32000 bf16, five alternatives: 10.3
+// 32016 bf16: 37.0 us (3.5 TB/s); five rows of 32000 bf16, five alternatives: 10.3
 // us. Tried: a part held in registers whole, the maximum first (a barrier between
 // every two passes; 59 us for the 288 rows), the parts' granules through shared
 // memory by asynchronous copies, 6 to 12 a thread in flight (33 to 41 us), four
@@ -234,7 +234,7 @@ struct Stream {
 };
 
 template <typename E, int NT, int U>
-__global__ void __launch_bounds__(NT, 4) logprob_kernel(const __grid_constant__ LogprobParams p) {
+__global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_constant__ LogprobParams p) {
     constexpr int VN = VecTraits<E>::kN;
     __shared__ Shared<NT> s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -604,7 +604,10 @@ cudaError_t launch(LogprobParams p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams& p, int dtype, cudaStream_t st) {
-    return dtype == 0 ? launch<float, 256, 4>(p, st) : launch<bf16_t, 256, 2>(p, st);
+    // bf16 rows, half as long, by blocks of 128 threads (of 256): 2000 rows of 32016
+    // 37.0 us (42.1), with five alternatives 47.1 (51.4); float32 rows of 128256 with 20
+    // alternatives, 288 of 512 with a token, 57.4 (41.2).
+    return dtype == 0 ? launch<float, 256, 4>(p, st) : launch<bf16_t, 128, 2>(p, st);
 }
 
 SV_DEBUG_READER(logprobs)
