@@ -14,10 +14,10 @@
 // block has read its batch, and no later batch's row is overwritten.
 //
 // Bound by memory where there is enough of it: 16 sequences of 1500-4000 positions,
-// 32 layers, 8 heads of 128 columns, bf16, to 1600: 1054 us, 6.0 TB/s over both
-// launches (the moves alone 895 us, 7.0 TB/s of what has to move; the selection 137:
-// digits, the prefix sum and the way of its few bytes). One sequence, 12 layers, 4
-// heads of 64, float32, 1501 to 1003: 17.5 us, the chain of dependent steps (with
+// 32 layers, 8 heads of 128 columns, bf16, to 1600: 1042 us, 6.1 TB/s over both
+// launches (the moves alone 895 us, 7.0 TB/s of what has to move; the selection 122,
+// 137 with the keys formed anew for every digit: its instructions, two blocks an
+// SM). One sequence, 12 layers, 4 heads of 64, float32, 1501 to 1003: 17.1 us, the chain of dependent steps (with
 // the bound found bit by bit, a count of the block each, 34).
 
 #include <algorithm>
@@ -66,7 +66,7 @@ SV_DEV void block_prefix2(int a, int b, int* pa, int* pb, int* sa, int* sb, int2
     *sb = ty;
 }
 
-__global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(ST, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
     __shared__ union {
         int hist[kBins];
         int2 kept[ST * kItems];  // positions and weights that one round keeps
@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant_
     const bool fits = len <= ST * kItems;  // the block's registers hold all weights
     const bool vec = (p.capacity & 3) == 0 && (reinterpret_cast<size_t>(p.weights) & 15) == 0;
     float x[kItems];
+    uint32_t key[kItems];
     auto load = [&](int at) {
         const int t = at + tid * kItems;
         if (vec && t + kItems <= len) {
@@ -117,6 +118,8 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant_
 #pragma unroll
             for (int j = 0; j < kItems; ++j) x[j] = t + j < len ? w[t + j] : 0.f;
         }
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) key[j] = weight_key(x[j]);
     };
     if (tid == 0) first_moved = keep;
     if (fits) load(0);
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant_
                 const int t = at + tid * kItems;
 #pragma unroll
                 for (int j = 0; j < kItems; ++j) {
-                    const uint32_t k = weight_key(x[j]);
+                    const uint32_t k = key[j];
                     if (t + j >= mid0 && t + j < mid1 && (before == 32 || k >> before == prefix))
                         atomicAdd(&u.hist[k >> shift & mask], 1);
                 }
@@ -176,7 +179,7 @@ __global__ void __launch_bounds__(ST) evict_select_kernel(const __grid_constant_
 #pragma unroll
         for (int j = 0; j < kItems; ++j) {
             const int i = t + j;
-            const unsigned long long k = weight_key(x[j]);
+            const unsigned long long k = key[j];
             const bool in = i < len, always = i < mid0 || i >= mid1;
             if (in && (always || k > bound)) above |= 1u << j;
             else if (in && k == bound) tied |= 1u << j;

@@ -17,7 +17,7 @@
 //
 // The K best of a part: any key that K threads' maxima reach is a bound that no
 // better element lies below, so a search over the threads' maxima (one count of
-// the block a step) ends at a bound that K to 2 K of them reach; only those
+// the block a step) ends at a bound that K to 5 K / 4 of them reach; only those
 // threads' granules are read again (from L2, shared out over the block), and the
 // few elements that reach the bound are ranked by comparing all with all. Where
 // they are more than fit (rows of equal logits) the bound is taken over the
@@ -26,8 +26,8 @@
 // What bounds it: latency and issue, no longer memory. float32 takes 14 warp
 // instructions for 32 elements (an exponential, 2.5 for the sums, 1.5 for the
 // rank, the rest loads and batches' ends), bf16 15; the scheduler issues in half
-// to two thirds of the cycles. 288 rows of 128256 float32 logits: 36.9 us without
-// alternatives (4.0 TB/s; 30.8 in parts of half a row), 48.3 with 20; 2000 rows of
+// to two thirds of the cycles. 288 rows of 128256 float32 logits: 36.5 us without
+// alternatives (4.0 TB/s; 30.8 in parts of half a row), 45.4 with 20; 2000 rows of
 // 32016 bf16: 37.0 us (3.5 TB/s); five rows of 32000 bf16, five alternatives: 10.3
 // us. Tried: a part held in registers whole, the maximum first (a barrier between
 // every two passes; 59 us for the 288 rows), the parts' granules through shared
@@ -408,7 +408,9 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
             step <<= 1;
             n = __syncthreads_count(key >= lo_k);
         }
-        while (n > 2 * K && hi_k - lo_k > 1) {
+        // (up to 2 K of them: 41.4 us for 38.7 where the granules that are read again come
+        // from DRAM, 512 rows of 128256 float32 logits, 288 with a token, 20 alternatives)
+        while (n > K + K / 4 && hi_k - lo_k > 1) {
             const uint32_t mid = lo_k + (hi_k - lo_k) / 2;
             const int c = __syncthreads_count(key >= mid);
             if (c >= K) {
