@@ -4,15 +4,15 @@
 // The products are S^T = K Q^T: 128 keys are the lanes of tensor memory and the
 // rows (nodes' query heads) its columns, so that a position's sum over the rows is
 // a sum over one thread's columns and no thread needs another's. One CTA an SM,
-// thirteen warps:
+// twelve warps:
 //   producer  (warp 8) copies tiles of 128 keys page by page (tensor copies with
 //             the 128-byte swizzle) into a ring of stages;
 //   issuer    (warp 9) issues the products of up to two tiles with a chunk of up
 //             to 128 rows (whole nodes);
 //   loaders   (warps 10, 11) bring the chunks (a chain's by tensor copies; a path's
 //             nodes lie anywhere: copies of 16 bytes) and their log-sums, three ahead;
-//   two groups (warps 0-3, 4-7) of 128 threads, a key each: one of the two tiles;
-//   a warp that checks the sequences' data.
+//   two groups (warps 0-3, 4-7) of 128 threads, a key each: one of the two tiles.
+// The second loader also checks the sequences' data, when its chunks are on their way.
 // A stay's only chunk is brought once. Where there are more, they go by for every
 // two tiles, from L2.
 //
@@ -42,7 +42,7 @@ namespace {
 static __device__ int g_withhold = -1;  // spec_debug_withhold_tile
 #endif
 
-constexpr int NT = 416;
+constexpr int NT = 384;
 constexpr int kKv = 128;    // keys of a tile
 constexpr int kRows = 128;  // rows of a chunk, at most
 constexpr int kChunks = 3;  // chunks in shared memory
@@ -416,12 +416,22 @@ struct Group {
                         const volatile int* odd = c->odd[qb];
                         const long long hidden = ((long long)t - s.L - row0) * p.G;  // columns that do not see this key
                         const bool all = (long long)mine * kKv + kKv - 1 <= (long long)s.L + row0 && !odd[0] && !odd[1];
-#pragma unroll 1
-                        for (int j = 0; j < cols; j += 32) {
-                            float x[32];
-                            tmem_ld32(tmem + 128 * place + j, x);
+const uint32_t from = tmem + 128 * place;
+                        auto sum = [&](const float (&x)[32], int j) {
                             acc += all && j + 32 <= cols ? weigh32<false>(x, z + j, p.c2, 0)
                                                          : weigh32<true>(x, z + j, p.c2, (int)max(0LL, min(hidden - j, 32LL)));
+                        };
+                        // (the second 32 columns are on their way while the first are added
+                        // up; a place has 128, what lies past the chunk's is not used)
+#pragma unroll 1
+                        for (int j = 0; j < cols; j += 64) {
+                            float x[32], y[32];
+                            tmem_ld32_start(from + j, x);
+                            tmem_ld32_wait(x);
+                            tmem_ld32_start(from + j + 32, y);
+                            sum(x, j);
+                            tmem_ld32_wait(y);
+                            if (j + 32 < cols) sum(y, j + 32);
                         }
                         tc_fence_before();
                         __syncwarp();
@@ -484,11 +494,10 @@ __global__ void __launch_bounds__(NT, 1)
     } else if (warp == 9) {
         Issuer<D> is{c, uni(tmem), qs, stages};
         is.run(way);
-    } else if (warp < 12) {
+    } else {
         Loader<D> l{p, c, &mq, qs, warp - 10};
         l.run(way);
-    } else {
-        weigh_statuses(p, blockIdx.x, gridDim.x);
+        if (warp == 11) weigh_statuses(p, blockIdx.x, gridDim.x);
     }
     __syncwarp();
     tc_fence_before();
