@@ -23,9 +23,10 @@
 // rest are the first lookups of a launch and of each stay. Many rows: the latency
 // of a chunk's way (wait, tensor memory, exponentials, release; tensor pipe and
 // exponential unit are a quarter busy, the schedulers a third): a chunk of 500 nodes
-// at 4000 positions, 8 x 4 heads 32.2 us, 0.54 PFLOP/s (33.3 with two chunks of rows
+// at 4000 positions, 8 x 4 heads 32.5 us, 0.54 PFLOP/s (33.3 with two chunks of rows
 // in shared memory; 44.9 with the chunks brought by 16-byte copies, whose addresses
-// took two warps longer than the products).
+// took two warps longer than the products; scalar in the place of packed arithmetic
+// 33.2, as is the second 32 columns' fetch beside the first one's sums or after them).
 
 #include <cuda.h>
 
