@@ -28,7 +28,7 @@
 // rank, the rest loads and batches' ends), bf16 15; the scheduler issues in half
 // to two thirds of the cycles. 288 rows of 128256 float32 logits: 36.5 us without
 // alternatives (4.0 TB/s; 30.8 in parts of half a row), 45.4 with 20; 2000 rows of
-// 32016 bf16: 37.0 us (3.5 TB/s); five rows of 32000 bf16, five alternatives: 10.3
+// 32016 bf16: 37.4 us (3.4 TB/s); five rows of 32000 bf16, five alternatives: 10.3
 // us. Tried: a part held in registers whole, the maximum first (a barrier between
 // every two passes; 59 us for the 288 rows), the parts' granules through shared
 // memory by asynchronous copies, 6 to 12 a thread in flight (33 to 41 us), four
@@ -99,17 +99,22 @@ SV_DEV int block_sum(int v, int* scratch) {
     return s;
 }
 
-// The exponent of v against the reference m (a maximum), from -200 on (2^-200 is
-// 0). Where m c2 has no place in fp32 the difference is taken first.
+// Whether exponents against the maximum m are taken from its rounded product M = m
+// c2. Its rounding, which all terms of a sum share, is then below 2^-4; past that (low
+// temperatures, masks of the type's lowest value) the difference v - m comes first.
+SV_DEV bool by_product(float m, float c2) { return fabsf(m * c2) < 0x1p20f; }
+
+// The exponent of v against the reference m, from -200 on (2^-200 is 0).
 SV_DEV float exponent(float v, float m, float c2) {
-    const float M = m * c2;
-    return fmaxf(fabsf(M) < INFINITY ? fmaf(v, c2, -M) : (v - m) * c2, -200.f);
+    return fmaxf(by_product(m, c2) ? fmaf(v, c2, -__fmul_rn(m, c2)) : (v - m) * c2, -200.f);
 }
-// How far one maximum lies below another (a part of nothing but -inf has none).
+// How far one reference lies below another (a part of nothing but -inf has none).
 SV_DEV float octaves(float m, float top, float c2) {
     if (m == -INFINITY) return -200.f;
-    const float M = top * c2;
-    return fmaxf(fabsf(M) < INFINITY ? __fmul_rn(m, c2) - M : (m - top) * c2, -200.f);
+    const float a = __fmul_rn(m, c2), b = __fmul_rn(top, c2);
+    const float d = by_product(m, c2) ? (by_product(top, c2) ? a - b : fmaf(-top, c2, a))
+                                      : (by_product(top, c2) ? fmaf(m, c2, -b) : (m - top) * c2);
+    return fmaxf(d, -200.f);
 }
 
 // The n keys in cand (distinct) ranked against one another; the first k, in
@@ -171,6 +176,7 @@ template <typename E>
 struct Stream {
     static constexpr int VN = VecTraits<E>::kN;
     float m = -INFINITY, c2;
+    float M = __builtin_nanf("");  // of m; NaN where exponents are not taken from it
     uint64_t S = 0ull, U = 0ull;  // 2^t, 2^t t, two at a time
     int above = 0;
 
@@ -181,13 +187,17 @@ struct Stream {
 #pragma unroll
         for (int j = 0; j < n; ++j) top = granule_max<E>(x[j], top);
         if (top > m) {
-            const float d = octaves(m, top, c2), w = ex2(d);
+            float to = __fmul_rn(top, c2);
+            to = fabsf(to) < 0x1p20f ? to : __builtin_nanf("");
+            float d = M - to;
+            d = d == d ? fmaxf(d, -200.f) : octaves(m, top, c2);
+            const float w = ex2(d);
             const uint64_t dd = pack2(d, d), ww = pack2(w, w);
             U = mul2(ww, fma2(dd, S, U));
             S = mul2(ww, S);
             m = top;
+            M = to;
         }
-        const float M = m * c2;
         const uint64_t cc = pack2(c2, c2), mm = pack2(-M, -M);
         const bool count = rank && __any_sync(__activemask(), m >= zx);
         uint64_t s = 0ull, u = 0ull;
@@ -210,7 +220,7 @@ struct Stream {
         float u0, u1;
         unpack2(u, &u0, &u1);
         u0 += u1;
-        if (!(fabsf(u0) < INFINITY)) {  // a logit of -inf gave 0 times infinity, or M is infinite, or the row is bad: one by one
+        if (!(fabsf(u0) < INFINITY)) {  // a logit of -inf gave 0 times infinity, or M is NaN, or the row is bad: one by one
             float s0 = 0.f;
             u0 = 0.f;
             const float ref = m == -INFINITY ? 0.f : m;
@@ -544,7 +554,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
     // (not above 0 by a rounding)
     auto log_of = [&](float z) {
         const float t = fmaf(z, p.c2, -M);
-        return fminf(0.f, (fabsf(t) < INFINITY ? t * kLn2 : (z - m) * p.inv_t) - log_s);
+        return fminf(0.f, (by_product(m, p.c2) && fabsf(t) < INFINITY ? t * kLn2 : (z - m) * p.inv_t) - log_s);
     };
     if (tid == 0) {
         p.logprob[row] = bad ? nan : log_of(zx);
