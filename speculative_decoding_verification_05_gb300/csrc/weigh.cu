@@ -7,8 +7,10 @@
 //
 // Bound by latency where there are few tiles (keys, rows, products and sums follow
 // one another; four blocks an SM overlap them: 8 chains of 8, 12 heads of 64,
-// float32, 20-1500 positions 21.9 us, 26.5 with two), else by the products' reads of
-// shared memory, 10 wavefronts for 32 multiplications of a warp.
+// float32, 20-1500 positions 20.6 us, 26.5 with two; one token of 16 sequences, to
+// 8000 positions, 8 x 4 heads of 128: 197 us, 1.3 TB/s), else by the products' reads
+// of shared memory, 10 wavefronts for 32 multiplications of a warp (trees' paths of 1
+// to 17 of 61 nodes, 16 sequences, 300-4000 positions, 8 x 4 heads of 96, bf16: 118).
 
 #include <algorithm>
 
@@ -32,6 +34,13 @@ struct alignas(16) Ctl {
 };
 
 size_t smem_bytes(int D) { return sizeof(Ctl) + (size_t)(KV + R) * (D + 4) * sizeof(float); }
+
+// A word's elements, as 16-byte words of floats.
+template <int VN>
+SV_DEV void put(float* to, const float (&v)[VN]) {
+#pragma unroll
+    for (int e = 0; e < VN; e += 4) *reinterpret_cast<float4*>(to + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+}
 
 template <typename E>
 __global__ void __launch_bounds__(NT, 4) weigh_kernel(const __grid_constant__ WeighParams p) {
@@ -63,26 +72,43 @@ __global__ void __launch_bounds__(NT, 4) weigh_kernel(const __grid_constant__ We
             const long long t0 = (long long)tile * KV;
             const int live = (int)min((long long)KV, len - t0);
             __syncthreads();  // (the last tile's keys and sums are done with)
-            for (int i = tid; i < KV * words; i += NT) {
-                const int t = i / words, w = i - t * words;
-                float v[VN];
-                int id = -1;
-                if (t < live) id = __ldg(table + ((t0 + t) >> p.page_shift));
-                if (id >= 0 && id < p.num_pages) {
-                    const long long at = id * p.page_stride + ((t0 + t) & ((1 << p.page_shift) - 1)) * p.token_stride +
-                                         s.h * p.head_stride + w * VN;
-                    VecTraits<E>::unpack(*reinterpret_cast<const uint4*>(k + at), v);
-                } else {
+            // four words of keys a thread on their way at a time (one after the other: 220
+            // us for 16 float32 contexts to 8000, 8 heads of 128)
+            constexpr int U = 4;
+#pragma unroll 1
+            for (int i0 = tid; i0 < KV * words; i0 += NT * U) {
+                int id[U];
+                uint4 x[U];
 #pragma unroll
-                    for (int e = 0; e < VN; ++e) v[e] = 0.f;
+                for (int j = 0; j < U; ++j) {
+                    const int t = (i0 + j * NT) / words;
+                    id[j] = t < live ? __ldg(table + ((t0 + t) >> p.page_shift)) : -1;
                 }
 #pragma unroll
-                for (int e = 0; e < VN; ++e) ks[t * stride + w * VN + e] = v[e];
+                for (int j = 0; j < U; ++j) {
+                    const int i = i0 + j * NT, t = i / words, w = i - t * words;
+                    x[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (id[j] >= 0 && id[j] < p.num_pages)
+                        x[j] = *reinterpret_cast<const uint4*>(k + id[j] * p.page_stride +
+                                                               ((t0 + t) & ((1 << p.page_shift) - 1)) * p.token_stride +
+                                                               s.h * p.head_stride + w * VN);
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int i = i0 + j * NT, t = i / words, w = i - t * words;
+                    if (t < KV) {
+                        float v[VN];
+                        VecTraits<E>::unpack(x[j], v);
+                        put<VN>(ks + t * stride + w * VN, v);
+                    }
+                }
             }
             float acc[4] = {0.f, 0.f, 0.f, 0.f};
             for (int r0 = 0; r0 < rows; r0 += R) {
                 __syncthreads();
-                for (int i = tid; i < R * words; i += NT) {
+                // (rows that are one chunk stay for the stay's other tiles)
+                const bool fresh = rows > R || tile == s.first;
+                for (int i = tid; fresh && i < R * words; i += NT) {
                     const int r = i / words, w = i - r * words;
                     float v[VN];
 #pragma unroll
@@ -92,15 +118,19 @@ __global__ void __launch_bounds__(NT, 4) weigh_kernel(const __grid_constant__ We
                         const long long at = (((long long)s.b * p.N + node) * Hq + s.h * p.G + g) * p.D + w * VN;
                         VecTraits<E>::unpack(*reinterpret_cast<const uint4*>(q + at), v);
                     }
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) qs[r * stride + w * VN + e] = v[e];
+                    put<VN>(qs + r * stride + w * VN, v);
                 }
                 if (tid < R) {
                     float z = INFINITY;
                     int see = 0;
                     if (r0 + tid < rows) {
-                        const int row = (r0 + tid) / p.G, g = r0 + tid - row * p.G, node = path ? path[row] : row;
-                        z = __ldg(p.lse + ((long long)s.b * p.N + node) * Hq + s.h * p.G + g) * 1.4426950408889634f;
+                        const int row = (r0 + tid) / p.G, g = r0 + tid - row * p.G;
+                        if (fresh) {
+                            const int node = path ? path[row] : row;
+                            z = __ldg(p.lse + ((long long)s.b * p.N + node) * Hq + s.h * p.G + g) * 1.4426950408889634f;
+                        } else {
+                            z = c->lse[tid];
+                        }
                         // (a row that sees nothing has no weights)
                         see = z == -INFINITY ? 0 : (int)min((long long)KV, max(0LL, (long long)s.L + row + 1 - t0));
                     }
