@@ -482,9 +482,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
                 return block_sum<NT>(c, s.sum);
             };
             const int want = min(K, count([](uint32_t, int) { return true; }));
-            uint32_t k0 = 0, k1 = 0xFFFFFFFFu;  // reached by `want` or more, and by fewer
+            // reached by `want` or more, and by fewer (by none: the key of the NaN 0x7FFFFFFF is
+            // 2^32 - 1)
+            u64 k0 = 0, k1 = 1ull << 32;
             while (k1 - k0 > 1) {
-                const uint32_t mid = k0 + (k1 - k0) / 2;
+                const u64 mid = k0 + (k1 - k0) / 2;
                 if (count([&](uint32_t k, int) { return k >= mid; }) >= want) k0 = mid;
                 else k1 = mid;
             }
@@ -497,11 +499,14 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
             if (tid == 0) s.found = 0;
             __syncthreads();
             count([&](uint32_t k, int i) {
-                if (k > k0 || (k == k0 && i <= i1)) s.cand[atomicAdd(&s.found, 1)] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
+                if (k > k0 || (k == k0 && i <= i1)) {
+                    const int to = atomicAdd(&s.found, 1);  // (`want` of them in all)
+                    if (to < kCap) s.cand[to] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
+                }
                 return false;
             });
             __syncthreads();
-            n_cand = s.found;
+            n_cand = min(s.found, kCap);
         }
         if (n_cand < K) {  // (a part of fewer elements)
             if (tid < K) s.mine[tid] = 0;
