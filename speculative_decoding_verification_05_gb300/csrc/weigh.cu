@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(NT, 4) weigh_kernel(const __grid_constant__ We
     const int stride = p.D + 4, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float* qs = ks + KV * stride;
     const int words = p.D / VN, kx = tid & 15, ry = tid >> 4;
-    weigh_statuses(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
+    weigh_statuses<false>(p, blockIdx.x * (NT / 32) + warp, gridDim.x * (NT / 32));
     WeighPart part = weigh_locate<KV, R, NT>(p, &c->scan);
     const E* q = reinterpret_cast<const E*>(p.q);
     const E* k = reinterpret_cast<const E*>(p.k);

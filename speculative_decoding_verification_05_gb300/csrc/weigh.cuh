@@ -171,13 +171,17 @@ SV_DEV bool weigh_check(const WeighParams& p, int b) {
     return !__any_sync(0xFFFFFFFFu, bad);
 }
 
-// Statuses of all sequences, shared out over the grid's warps.
+// Statuses of all sequences, shared out over the grid's warps. RAISE: they are zero
+// before, and are only ever raised, as those of a part that gave up are.
+template <bool RAISE>
 SV_DEV void weigh_statuses(const WeighParams& p, int gw, int warps) {
     if (!p.status) return;
 #pragma unroll 1
     for (int b = gw; b < p.B; b += warps) {
         const bool ok = weigh_check(p, b);
-        if ((threadIdx.x & 31) == 0) p.status[b] = ok ? kOk : kEData;
+        if ((threadIdx.x & 31) != 0) continue;
+        if (!RAISE) p.status[b] = ok ? kOk : kEData;
+        else if (!ok) atomicMax(p.status + b, kEData);
     }
 }
 

@@ -12,18 +12,18 @@
 //   loaders   (warps 10, 11) bring the chunks (a chain's by tensor copies; a path's
 //             nodes lie anywhere: copies of 16 bytes) and their log-sums, three ahead;
 //   two groups (warps 0-3, 4-7) of 128 threads, a key each: one of the two tiles.
-// The sequences' data are checked by a kernel before, which this one starts beside.
+// The second loader also checks the sequences' data, when its chunks are on their way.
 // A stay's only chunk is brought once. Where there are more, they go by for every
 // two tiles, from L2.
 //
 // What bounds it. Few rows: memory (one token of 64 sequences, contexts to 8192, 8
 // key heads of 4 query heads: 102 us, 5.4 TB/s of keys and weights; 100 with five
 // stages and two chunks). Accepted paths of 1 to 7 nodes, 16 sequences, 300-4000
-// positions, 8 x 8 heads: 23.6 us, of which the keys at that rate would take 13; the
+// positions, 8 x 8 heads: 23.4 us, of which the keys at that rate would take 13; the
 // rest are the first lookups of a launch and of each stay. Many rows: the latency
 // of a chunk's way (wait, tensor memory, exponentials, release; tensor pipe and
 // exponential unit are a quarter busy, the schedulers a third): a chunk of 500 nodes
-// at 4000 positions, 8 x 4 heads 33.4 us, 0.52 PFLOP/s (0.8 more with two chunks of rows
+// at 4000 positions, 8 x 4 heads 33.2 us, 0.52 PFLOP/s (0.8 more with two chunks of rows
 // in shared memory; 44.9 with the chunks brought by 16-byte copies, whose addresses
 // took two warps longer than the products; 0.7 more with scalar in the place of packed
 // arithmetic; the second 32 columns fetched beside the first ones' sums or after them, the same).
@@ -449,13 +449,16 @@ const uint32_t from = tmem + 128 * place;
     }
 };
 
-// The statuses by what the data are, before the weighing, which starts beside it: a CTA
-// that gives up raises them, and a plain store by one of the same grid that began later
-// would take that back. (Paths of 16 sequences: 23.6 us; 26.6 with a memset and statuses
-// that are only raised, 22.8 with the stores among the weighing.)
-__global__ void __launch_bounds__(256) weigh_status_kernel(const __grid_constant__ WeighParams p) {
+// Clears the statuses, which the weighing's CTAs only raise: a plain store of a good one by a
+// CTA that began late, behind another stream's work, would take back what one that gave up
+// reported. The weighing starts beside it and waits for it before it raises any. (Paths of
+// 16 sequences: 23.4 us, 22.6 with the plain stores, 26.6 with a memset. With the checks in
+// this kernel too, 23.5, but one token over 100003 positions in pages of 8 63.6 for 60.7, as
+// its blocks keep the weighing's from their SMs, and of 4000 sequences 668 for 580.)
+__global__ void __launch_bounds__(256) weigh_clear_kernel(int32_t* status, int B) {
     asm volatile("griddepcontrol.launch_dependents;");
-    weigh_statuses(p, blockIdx.x * 8 + (threadIdx.x >> 5), gridDim.x * 8);
+    const int b = blockIdx.x * 256 + threadIdx.x;
+    if (b < B) status[b] = kOk;
 }
 
 template <int D>
@@ -507,6 +510,10 @@ __global__ void __launch_bounds__(NT, 1)
     } else {
         Loader<D> l{p, c, &mq, qs, warp - 10};
         l.run(way);
+        if (warp == 11) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // (the statuses are cleared; the block's end follows)
+            weigh_statuses<true>(p, blockIdx.x, gridDim.x);
+        }
     }
     __syncwarp();
     tc_fence_before();
@@ -527,8 +534,6 @@ __global__ void __launch_bounds__(NT, 1)
         __syncthreads();
     }
     if (warp == 9) tmem_free512(tmem);
-    // (the statuses are written by the kernel before this one: raised after them)
-    if (warp == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     if (warp == 0 && c->abort && p.status) {  // a wait gave up: the sequences of this part are not whole
         Way again(p, part);
         while (again.next())
@@ -549,7 +554,7 @@ cudaError_t launch(const WeighParams& p, const CUtensorMap& map, const CUtensorM
     cfg.dynamicSmemBytes = Shape<D>::kSmem;
     cfg.stream = st;
     if (p.status) {
-        weigh_status_kernel<<<std::min((p.B + 7) / 8, 152 * 4), 256, 0, st>>>(p);
+        weigh_clear_kernel<<<(p.B + 255) / 256, 256, 0, st>>>(p.status, p.B);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         cfg.attrs = &attr;
