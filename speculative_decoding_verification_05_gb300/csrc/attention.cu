@@ -637,7 +637,13 @@ __global__ void __launch_bounds__(kJoinNT) attn_join_kernel(const __grid_constan
     const int tid = threadIdx.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4* src = reinterpret_cast<const int4*>(p.joins + blockIdx.x + 1);
-    const int4 u = __ldcg(src), v = __ldcg(src + 1);  // b, h, row0, rows; slot0, first, last
+    const int4 u = __ldcg(src), v = __ldcg(src + 1);  // b, h, row0, rows; slot0, first, last, lost
+    // parts that gave up (the first one's entry, which joins nothing, by the first block)
+    const uint32_t lost0 = blockIdx.x == 0 ? __ldcg(&p.joins->lost) : 0u;
+    if ((lost0 | (uint32_t)v.w) && tid == 0 && blockIdx.y == 0 && p.status) {
+        if (lost0) attn_lost(p, (int)(lost0 & 0xFFFF) - 1, (int)(lost0 >> 16));
+        if (v.w) attn_lost(p, (v.w & 0xFFFF) - 1, (int)((uint32_t)v.w >> 16));
+    }
     const int r0 = blockIdx.y * JR, rows = min(JR, u.w - r0);
     if (rows <= 0) return;
     const int pieces = v.z - v.y + 2, D4 = p.D / 4, lw = D4 <= 1 ? 0 : 32 - __clz(D4 - 1);

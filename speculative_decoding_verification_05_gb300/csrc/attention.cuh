@@ -32,7 +32,7 @@ struct AttnJoin {
     int b, h, row0, rows;  // rows = 0: nothing to join here
     int slot0;             // the first piece's slot; the others' are 2 * part
     int first, last;       // parts of the other pieces
-    int pad;
+    uint32_t lost;         // sequences that this part, which gave up, left: the first + 1, the last << 16; 0: none
 };
 
 struct AttnParams {
@@ -241,8 +241,9 @@ SV_DEV void attn_join(const AttnParams& p, const AttnScan& sc, const AttnCut& cu
 // grid (this is warp `gw`; as many warps a sequence as there are): status, and
 // the rows that no unit writes, zeros (lse -inf) from the node count on and NaN
 // everywhere for a sequence with bad data. A bad page id is reported here; the
-// units that meet it make their rows NaN.
-template <typename E>
+// units that meet it make their rows NaN. RAISE: where units are whole the statuses
+// were cleared by the kernel before, and a part that gave up may have raised some.
+template <typename E, bool RAISE = false>
 SV_DEV void attn_edges(const AttnParams& p, int gw, int warps) {
     const int lane = threadIdx.x & 31, team = max(1, warps / p.B), member = gw % team;
 #pragma unroll 1
@@ -259,7 +260,12 @@ SV_DEV void attn_edges(const AttnParams& p, int gw, int warps) {
                 }
             }
             bad = __any_sync(0xFFFFFFFFu, bad) != 0;
-            if (lane == 0) p.status[b] = bad ? kEData : kOk;
+            if (!RAISE || !p.whole) {
+                if (lane == 0) p.status[b] = bad ? kEData : kOk;
+            } else if (bad) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                if (lane == 0) atomicMax(p.status + b, kEData);
+            }
         }
         const int Hq = p.Hkv * p.G, n = max(s.n, 0);
         const long long row0 = ((long long)b * p.N + n) * Hq, rows = (long long)(p.N - n) * Hq;
@@ -273,6 +279,14 @@ SV_DEV void attn_edges(const AttnParams& p, int gw, int warps) {
             for (long long i = member * 32 + lane; i < rows; i += team * 32)
                 p.lse[row0 + i] = __uint_as_float(s.n < 0 ? 0x7FC00000u : 0xFF800000u);
     }
+}
+
+// Reports the sequences from `first` to `last` that have nodes (all have units of the
+// part that gave up), after the statuses' own stores.
+SV_DEV void attn_lost(const AttnParams& p, int first, int last) {
+#pragma unroll 1
+    for (int b = first; b <= last; ++b)
+        if (attn_seq(p, b).n > 0) atomicMax(p.status + b, kETimeout);
 }
 
 SV_DEV float lse_of(float m2, float l) {

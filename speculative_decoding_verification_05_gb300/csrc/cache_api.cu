@@ -191,7 +191,8 @@ spec_status spec_tree_attention(const void* q, const spec_cache* cache, spec_dty
     // much). bf16, units of 8 rows and 128 columns, split and whole: 96 of 2 tiles
     // 14.2 and 11.1 us, of 4 17.4 and 13.6; 40 of 4 13.9 and 13.1; 8 of 2 11.8 and
     // 9.7. float32 tiles take longer than a join: 96 units of 2 tiles (64 columns)
-    // 11.8 and 10.0, of 4 14.1 and 17.8. The tiles are those that the page table's
+    // 11.8 and 10.0, of 4 14.1 and 17.8 (bf16 before the kernel that clears the statuses of
+    // whole units, half a us to one). The tiles are those that the page table's
     // width allows (lengths are known on the device only): a table as wide as the
     // longest sequence may get has its units split.
     auto whole = [&](sv::AttnPlan plan, int most) {
