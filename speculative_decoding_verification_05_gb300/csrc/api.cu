@@ -374,7 +374,8 @@ int spec_debug_failures(int* line) {
                               sv::debug_read_mentor, sv::debug_read_beta, sv::debug_read_tree_build,
                               sv::debug_read_attention, sv::debug_read_attention_tc, sv::debug_read_cache,
                               sv::debug_read_logprobs, sv::debug_read_weigh,
-                              sv::debug_read_weigh_tc, sv::debug_read_evict};
+                              sv::debug_read_weigh_tc, sv::debug_read_evict,
+                              sv::debug_read_rotary};
     long long total = 0;
     int first = 0;
     for (const Reader rd : readers) {

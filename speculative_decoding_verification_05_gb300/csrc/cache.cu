@@ -56,7 +56,9 @@ __global__ void __launch_bounds__(CT) append_kernel(const __grid_constant__ Appe
     for (int i = tid; i < (t1 - t0) * per_token; i += CT) {
         const int t = t0 + i / per_token, c = i % per_token, h = c / per_head;
         const long long pos = L + t;
-        const long long to = (long long)table[pos >> sh] * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride +
+        const int id = table[pos >> sh];
+        if (!SV_IN(id, p.c.num_pages) || !SV_IN(h, p.c.heads)) continue;
+        const long long to = (long long)id * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride +
                              h * p.c.head_stride + (c - h * per_head) * 16;
         const long long from = (((long long)b * p.N + t) * per_token + c) * 16;
         const uint4 x = ldg16(p.k + from), y = ldg16(p.v + from);
@@ -102,9 +104,10 @@ __global__ void __launch_bounds__(CT) compact_kernel(const __grid_constant__ Com
     }
     if (!ok || !moves) return;
     auto place = [&](long long pos) {
-        return (long long)table[pos >> sh] * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride;
+        const int id = SV_IN(pos, (long long)p.max_pages << sh) ? table[pos >> sh] : -1;
+        return SV_IN(id, p.c.num_pages) ? (long long)id * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride : -1LL;
     };
-    for (int i = tid; i <= a; i += CT) {
+    for (int i = tid; i <= a && SV_IN(i, SPEC_MAX_TREE_N); i += CT) {
         from[i] = place(L + path[i]);
         to[i] = place(L + i);
     }
@@ -119,10 +122,10 @@ __global__ void __launch_bounds__(CT) compact_kernel(const __grid_constant__ Com
             uint4 x[kMoves];
 #pragma unroll
             for (int j = 0; j < kMoves; ++j)
-                if (i + j <= a) x[j] = ldg16(base + from[i + j]);
+                if (i + j <= a && SV_PLACE(from[i + j])) x[j] = ldg16(base + from[i + j]);
 #pragma unroll
             for (int j = 0; j < kMoves; ++j)
-                if (i + j <= a) stg16(base + to[i + j], x[j]);
+                if (i + j <= a && SV_PLACE(from[i + j]) && SV_PLACE(to[i + j])) stg16(base + to[i + j], x[j]);
         }
     }
 }
@@ -292,8 +295,10 @@ __global__ void __launch_bounds__(PT) resize_kernel(const __grid_constant__ Pool
     };
     const int got = take_free(p.refs, p.num_pages, need, scratch, [&](int rank, int pg) {
         const int f = owner_of(offs, p.F, rank);
-        *entry(f, rank - offs[f]) = pg;
-        p.refs[pg] = 1;
+        if (SV_IN(entry(f, rank - offs[f]) - p.table, p.S * p.table_stride) && SV_IN(pg, p.num_pages)) {
+            *entry(f, rank - offs[f]) = pg;
+            p.refs[pg] = 1;
+        }
     });
     if (got == need) return;
     // too few: the sequences that were not served whole give theirs back
@@ -301,6 +306,7 @@ __global__ void __launch_bounds__(PT) resize_kernel(const __grid_constant__ Pool
         if (offs[f + 1] == offs[f] || offs[f + 1] <= got) continue;
         for (int r = offs[f] + lane; r < got; r += 32) {
             int32_t* e = entry(f, r - offs[f]);
+            if (!SV_IN(e - p.table, p.S * p.table_stride) || !SV_IN(*e, p.num_pages)) continue;
             p.refs[*e] = 0;
             *e = -1;
         }
@@ -343,7 +349,10 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PoolPa
     }
     __syncthreads();
     const int need = prefix_needs(offs, p.F, scratch);
-    take_free(p.refs, p.num_pages, need, scratch, [&](int rank, int pg) { p.copies[owner_of(offs, p.F, rank)].y = pg; });
+    take_free(p.refs, p.num_pages, need, scratch, [&](int rank, int pg) { 
+        const int f = owner_of(offs, p.F, rank);
+        if (SV_IN(f, p.F)) p.copies[f].y = pg;
+    });
     __syncthreads();
     for (int f = warp; f < p.F; f += PT / 32) {
         const int4 c = p.copies[f];
@@ -357,11 +366,12 @@ __global__ void __launch_bounds__(PT) fork_kernel(const __grid_constant__ PoolPa
         int32_t* to = p.table + (long long)d * p.table_stride;
         for (int i = lane; i < full; i += 32) {
             const int id = from[i];
+            if (!SV_IN(id, p.num_pages) || !SV_IN(i, p.max_pages)) continue;
             to[i] = id;
             atomicAdd(p.refs + id, 1);
         }
         if (lane == 0) {
-            if (c.z > 0) {
+            if (c.z > 0 && SV_IN(full, p.max_pages) && SV_IN(c.y, p.num_pages)) {
                 to[full] = c.y;
                 p.refs[c.y] = 1;
             }
@@ -382,6 +392,7 @@ __global__ void __launch_bounds__(CT) fork_copy_kernel(const __grid_constant__ C
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 job = __ldcg(copies + blockIdx.y);
     if (job.z <= 0 || job.y < 0) return;
+    if (!SV_IN(job.x, c.num_pages) || !SV_IN(job.y, c.num_pages) || !SV_IN(job.z, 1 << c.page_shift)) return;
     const char* from = base + job.x * c.page_stride;
     char* to = base + job.y * c.page_stride;
     const int words = job.z * per_token;

@@ -98,6 +98,7 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t st);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t st);
 cudaError_t launch_resize(const PoolParams& p, cudaStream_t st);
 cudaError_t launch_fork(const PoolParams& p, const CacheView& c, cudaStream_t st);
+cudaError_t debug_read_rotary(unsigned int* count, unsigned int* line);
 cudaError_t debug_read_evict(unsigned int* count, unsigned int* line);
 cudaError_t debug_read_cache(unsigned int* count, unsigned int* line);
 

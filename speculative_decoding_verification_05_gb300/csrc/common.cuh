@@ -67,6 +67,10 @@ SV_DEV bool sv_in_seq(long long i, long long n, int line, int32_t* status, long 
     }
 #endif
 
+// An offset that was computed for a write (debug builds: -1 where a check of its
+// parts failed).
+#define SV_PLACE(x) SV_IN((x), 1LL << 62)
+
 // The debug readers of the kernel translation units.
 cudaError_t debug_read_rows(unsigned int* count, unsigned int* line);
 cudaError_t debug_read_rows_smem(unsigned int* count, unsigned int* line);

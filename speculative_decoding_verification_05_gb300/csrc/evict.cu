@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(ST, 2) evict_select_kernel(const __grid_consta
     __shared__ int first_moved, found, rest;
     asm volatile("griddepcontrol.launch_dependents;");
     const long long unit = blockIdx.x;  // (layer, sequence, head)
+    [[maybe_unused]] const long long units = (long long)p.c.layers * p.B * p.c.heads;
     const int h = (int)(unit % p.c.heads), b = (int)(unit / p.c.heads % p.B), tid = threadIdx.x, sh = p.c.page_shift;
     const long long L = p.cache_len[b], budget = p.budget[b], least = (long long)p.sink + p.recent;
     const int32_t* table = p.table + b * p.table_stride;
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(ST, 2) evict_select_kernel(const __grid_consta
         if (p.status) p.status[b] = ok ? kOk : kEData;
     }
     if (!ok || !over) {
-        if (tid == 0) p.jobs[unit] = make_int2(0, 0);
+        if (tid == 0 && SV_IN(unit, units)) p.jobs[unit] = make_int2(0, 0);
         return;
     }
 
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(ST, 2) evict_select_kernel(const __grid_consta
             const bool is = above >> j & 1, tie = tied >> j & 1;
             const int to = a + min(e, ties);
             if (is || (tie && e < ties)) {
-                u.kept[to - start] = make_int2(t + j, __float_as_int(x[j]));
+                if (SV_IN(to - start, ST * kItems)) u.kept[to - start] = make_int2(t + j, __float_as_int(x[j]));
                 if (to != t + j) moved = min(moved, to);
             }
             a += is;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(ST, 2) evict_select_kernel(const __grid_consta
         const int n = above0 + min(tied0, ties) - start;
         for (int i = tid; i < n; i += ST) {
             const int2 k = u.kept[i];
-            if (SV_IN(start + i, keep)) {
+            if (SV_IN(start + i, keep) && SV_IN(start + i, p.capacity)) {
                 list[start + i] = k.x;
                 w[start + i] = __int_as_float(k.y);
             }
@@ -216,8 +217,9 @@ __global__ void __launch_bounds__(ST, 2) evict_select_kernel(const __grid_consta
     moved = __reduce_min_sync(0xFFFFFFFFu, moved);
     if ((tid & 31) == 0 && moved < keep) atomicMin(&first_moved, moved);
     __syncthreads();
-    for (int i = keep + tid; i < len; i += ST) w[i] = 0.f;
-    if (tid == 0) p.jobs[unit] = make_int2(first_moved, keep);
+    for (int i = keep + tid; i < len; i += ST)
+        if (SV_IN(i, p.capacity)) w[i] = 0.f;
+    if (tid == 0 && SV_IN(unit, units)) p.jobs[unit] = make_int2(first_moved, keep);
 }
 
 __global__ void __launch_bounds__(CT) evict_move_kernel(const __grid_constant__ EvictParams p) {
@@ -235,7 +237,9 @@ __global__ void __launch_bounds__(CT) evict_move_kernel(const __grid_constant__ 
     const int2 job = __ldcg(p.jobs + unit);
     const int32_t* list = p.list + unit * p.capacity;
     auto row = [&](int pos) {
-        return (long long)__ldg(table + (pos >> sh)) * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride;
+        if (!SV_IN(pos, (long long)p.max_pages << sh)) return -1LL;
+        const int id = __ldg(table + (pos >> sh));
+        return SV_IN(id, p.c.num_pages) ? (long long)id * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride : -1LL;
     };
     auto places = [&](int at, int buf) {
         for (int i = tid; i < batch; i += CT)
@@ -251,12 +255,13 @@ __global__ void __launch_bounds__(CT) evict_move_kernel(const __grid_constant__ 
         const bool mine = r0 < width;
 #pragma unroll
         for (int j = 0; j < kMoves; ++j)
-            if (mine && r0 + j * width < n) x[j] = ldg16(base + place[buf][r0 + j * width].x + col * 16);
+            if (mine && r0 + j * width < n && SV_PLACE(place[buf][r0 + j * width].x)) x[j] = ldg16(base + place[buf][r0 + j * width].x + col * 16);
         places(at + batch, next);
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kMoves; ++j)
-            if (mine && r0 + j * width < n) stg16(base + place[buf][r0 + j * width].y + col * 16, x[j]);
+            if (mine && r0 + j * width < n && SV_PLACE(place[buf][r0 + j * width].x) && SV_PLACE(place[buf][r0 + j * width].y))
+                stg16(base + place[buf][r0 + j * width].y + col * 16, x[j]);
         buf = next;
     }
 }

@@ -126,7 +126,7 @@ SV_DEV void rank_keys(const u64* cand, int n, int k, u64* best) {
         const u64 key = cand[i];
         int r = 0;
         for (int j = 0; j < n; ++j) r += cand[j] > key;
-        if (r < k) best[r] = key;
+        if (r < k && SV_IN(r, kMaxTop)) best[r] = key;
     }
 }
 
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
         const bool bad = tok != -1;
         if (!first) return;
         const float nan = __int_as_float(0x7FC00000);
-        if (tid == 0) {
+        if (tid == 0 && SV_IN(row, p.rows)) {
             p.logprob[row] = bad ? nan : 0.f;
             if (p.entropy) p.entropy[row] = bad ? nan : 0.f;
             if (p.rank) p.rank[row] = -1;
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
                 else atomicMax(p.status + b, kEData);
             }
         }
-        if (tid < K) {
+        if (tid < K && SV_IN(row * K + tid, p.rows * K)) {
             p.top_tokens[row * K + tid] = -1;
             p.top_logprobs[row * K + tid] = bad ? nan : -INFINITY;
         }
@@ -446,7 +446,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
         };
         if (tid == 0 && head) gather(granule(lo), lo);
         if (tid == 0 && tail) gather(granule(out), out);
-        if (key >= lo_k) s.who[atomicAdd(&s.flagged, 1)] = tid;
+        if (key >= lo_k) {
+            const int to = atomicAdd(&s.flagged, 1);
+            if (SV_IN(to, NT)) s.who[to] = tid;
+        }
         __syncthreads();
         const int who = s.flagged, jobs = who * max(0, (out - in + NT - 1) / NT);
 #pragma unroll 1
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
             count([&](uint32_t k, int i) {
                 if (k > k0 || (k == k0 && i <= i1)) {
                     const int to = atomicAdd(&s.found, 1);  // (`want` of them in all)
-                    if (to < kCap) s.cand[to] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
+                    if (to < kCap && SV_IN(to, kMaxTop)) s.cand[to] = ((u64)k << 32) | (0xFFFFFFFFu - (uint32_t)i);
                 }
                 return false;
             });
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
         const float t = fmaf(z, p.c2, -M);
         return fminf(0.f, (by_product(m, p.c2) && fabsf(t) < INFINITY ? t * kLn2 : (z - m) * p.inv_t) - log_s);
     };
-    if (tid == 0) {
+    if (tid == 0 && SV_IN(row, p.rows)) {
         p.logprob[row] = bad ? nan : log_of(zx);
         if (p.entropy) p.entropy[row] = bad ? nan : fmaxf(0.f, log_s - T / S * kLn2);
         if (p.rank) p.rank[row] = bad ? -1 : above;
@@ -572,7 +575,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprob_kernel(const __grid_con
         }
     }
     if (bad) {
-        if (tid < K) {
+        if (tid < K && SV_IN(row * K + tid, p.rows * K)) {
             p.top_tokens[row * K + tid] = -1;
             p.top_logprobs[row * K + tid] = nan;
         }

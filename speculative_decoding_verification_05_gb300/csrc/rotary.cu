@@ -158,7 +158,9 @@ __global__ void __launch_bounds__(CT, 4) append_rotary_kernel(const __grid_const
         const uint32_t fill = ok ? 0u : (sizeof(E) == 4 ? 0x7FC00000u : 0x7FC07FC0u);
         const long long words = (long long)(t1 - used) * p.q_heads * (D / VN);
         char* o = p.q_out + ((long long)b * p.N + used) * p.q_heads * p.c.row_bytes;
-        for (long long i = tid; i < words; i += CT) stg16(o + i * 16, make_uint4(fill, fill, fill, fill));
+        const long long at = ((long long)b * p.N + used) * p.q_heads * (D / VN), all = (long long)p.B * p.N * p.q_heads * (D / VN);
+        for (long long i = tid; i < words; i += CT)
+            if (SV_IN(at + i, all)) stg16(o + i * 16, make_uint4(fill, fill, fill, fill));
     }
     if (used == t0) return;  // (the same for the whole block)
     // rotated rows, the queries' heads, then the keys': a thread has one column of
@@ -196,12 +198,14 @@ __global__ void __launch_bounds__(CT, 4) append_rotary_kernel(const __grid_const
     }
     if (tid < used - t0) {
         const long long pos = L + t0 + tid;
-        place[tid] = (long long)table[pos >> sh] * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride;
+        const int id = table[pos >> sh];
+        place[tid] = SV_IN(id, p.c.num_pages) ? (long long)id * p.c.page_stride + (pos & ((1 << sh) - 1)) * p.c.token_stride : -1;
     }
     __syncthreads();
     auto put = [&](int i, uint4 y) {
         const int t = i / per_token, e = i - t * per_token, h = e / per_head;
-        stg16(p.c.v + place[t] + h * p.c.head_stride + (e - h * per_head) * 16, y);
+        if (SV_IN(h, p.c.heads) && SV_PLACE(place[t]))
+            stg16(p.c.v + place[t] + h * p.c.head_stride + (e - h * per_head) * 16, y);
     };
 #pragma unroll
     for (int u = 0; u < VU; ++u)
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(CT, 4) append_rotary_kernel(const __grid_const
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int i = h + u * slots;
-                if (i < heads)
+                if (i < heads && SV_PLACE(place[t]) && SV_IN(token * p.q_heads, (long long)p.B * p.N * p.q_heads) && SV_IN(c, D / VN))
                     row[u].store(p, from(i),
                                  i < p.q_heads ? p.q_out + (token * p.q_heads + i) * p.c.row_bytes : k + (i - p.q_heads) * p.c.head_stride,
                                  c, z);
@@ -242,5 +246,7 @@ cudaError_t launch_append_rotary(RotaryParams p, int dtype, cudaStream_t st) {
     const dim3 grid((p.N + p.tokens - 1) / p.tokens, p.B);
     return dtype == 0 ? launch<float>(p, grid, st) : launch<bf16_t>(p, grid, st);
 }
+
+SV_DEBUG_READER(rotary)
 
 }  // namespace sv

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(NT, 4) weigh_kernel(const __grid_constant__ We
                 float sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < NT / 32; ++w) sum += c->sums[w][tid];
-                if (id >= 0 && id < p.num_pages)
+                if (id >= 0 && id < p.num_pages && SV_IN(t0 + tid, p.capacity))
                     p.weights[((long long)s.b * p.Hkv + s.h) * p.capacity + t0 + tid] += sum;
             }
         }

@@ -417,7 +417,7 @@ struct Group {
                         const volatile int* odd = c->odd[qb];
                         const long long hidden = ((long long)t - s.L - row0) * p.G;  // columns that do not see this key
                         const bool all = (long long)mine * kKv + kKv - 1 <= (long long)s.L + row0 && !odd[0] && !odd[1];
-const uint32_t from = tmem + 128 * place;
+                        const uint32_t from = tmem + 128 * place;
                         auto sum = [&](const float (&x)[32], int j) {
                             acc += all && j + 32 <= cols ? weigh32<false>(x, z + j, p.c2, 0)
                                                          : weigh32<true>(x, z + j, p.c2, (int)max(0LL, min(hidden - j, 32LL)));
@@ -441,7 +441,7 @@ const uint32_t from = tmem + 128 * place;
                     }
                     if (way.chunks > 1) chunk_done();
                 }
-                if (ok && store) weights[t] = before + acc;
+                if (ok && store && SV_IN(t, p.capacity)) weights[t] = before + acc;
             }
             if (ok && way.chunks == 1) chunk_done();
         }
