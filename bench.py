@@ -115,14 +115,36 @@ def measured_peaks():
     return 6800.0, "fallback"
 
 
-def kernel_sources_sha():
-    """Hash of the library's CUDA sources: a recorded ncu traffic figure holds
-    only for the kernels it was taken on."""
+# The CUDA sources that hold the kernels of a workload with recorded traffic.
+SOURCES_OF = {"large_vocab": ("rows.cu",), "large_vocab_t0": ("argmax.cu",), "nucleus": ("rows_smem.cu",),
+              "tree": ("argmax.cu",), "mentor": ("rows.cu", "mentor.cu")}
+
+
+def kernel_sources(workload):
+    """The sources of a workload's kernels and the headers that they are built
+    from (of the library's own), sorted."""
+    import re
+
+    src = os.path.join(ROOT, "speculative_decoding_verification_05_gb300", "csrc")
+    found, todo = set(), list(SOURCES_OF[workload])
+    while todo:
+        f = todo.pop()
+        if f in found or not os.path.exists(os.path.join(src, f)):
+            continue
+        found.add(f)
+        with open(os.path.join(src, f)) as fh:
+            todo += re.findall(r'^\s*#include "([^"]+)"', fh.read(), flags=re.M)
+    return sorted(found)
+
+
+def kernel_sources_sha(workload):
+    """Hash of those files: a recorded ncu traffic figure holds only for the
+    kernels it was taken on, and is taken anew when one of them changes."""
     import hashlib
 
     h = hashlib.sha256()
     src = os.path.join(ROOT, "speculative_decoding_verification_05_gb300", "csrc")
-    for f in sorted(os.listdir(src)):
+    for f in kernel_sources(workload):
         with open(os.path.join(src, f), "rb") as fh:
             h.update(f.encode() + b"\0" + fh.read())
     return h.hexdigest()[:16]
@@ -138,7 +160,7 @@ def recorded_traffic(workload, stacked):
     with open(path) as f:
         d = json.load(f)
     e = d.get(workload)
-    if e is None or e.get("stacked") != stacked or e.get("csrc_sha16") != kernel_sources_sha():
+    if e is None or e.get("stacked") != stacked or e.get("sources_sha16") != kernel_sources_sha(workload):
         return None
     return e.get("bytes_per_launch")
 
