@@ -14,10 +14,10 @@
 // block has read its batch, and no later batch's row is overwritten.
 //
 // Bound by memory where there is enough of it: 16 sequences of 1500-4000 positions,
-// 32 layers, 8 heads of 128 columns, bf16, to 1600: 1042 us, 6.1 TB/s over both
+// 32 layers, 8 heads of 128 columns, bf16, to 1600: 1044 us, 6.1 TB/s over both
 // launches (the moves alone 895 us, 7.0 TB/s of what has to move; the selection 122,
 // 137 with the keys formed anew for every digit: its instructions, two blocks an
-// SM). One sequence, 12 layers, 4 heads of 64, float32, 1501 to 1003: 17.1 us, the chain of dependent steps (with
+// SM). One sequence, 12 layers, 4 heads of 64, float32, 1501 to 1003: 17.2 us, the chain of dependent steps (with
 // the bound found bit by bit, a count of the block each, 34).
 
 #include <algorithm>

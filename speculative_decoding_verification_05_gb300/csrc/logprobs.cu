@@ -26,9 +26,9 @@
 // What bounds it: latency and issue, no longer memory. float32 takes 14 warp
 // instructions for 32 elements (an exponential, 2.5 for the sums, 1.5 for the
 // rank, the rest loads and batches' ends), bf16 15; the scheduler issues in half
-// to two thirds of the cycles. 288 rows of 128256 float32 logits: 36.5 us without
-// alternatives (4.0 TB/s; 30.8 in parts of half a row), 45.4 with 20; 2000 rows of
-// 32016 bf16: 37.4 us (3.4 TB/s); five rows of 32000 bf16, five alternatives: 10.3
+// to two thirds of the cycles. 288 rows of 128256 float32 logits: 37.0 us without
+// alternatives (4.0 TB/s; 28.8 in parts of half a row), 45.7 with 20; 2000 rows of
+// 32016 bf16: 37.4 us (3.4 TB/s); five rows of 32000 bf16, five alternatives: 10.4
 // us. Tried: a part held in registers whole, the maximum first (a barrier between
 // every two passes; 59 us for the 288 rows), the parts' granules through shared
 // memory by asynchronous copies, 6 to 12 a thread in flight (33 to 41 us), four
@@ -601,10 +601,11 @@ cudaError_t launch(LogprobParams p, cudaStream_t st) {
     const long long granules = ((long long)p.V + VN - 1) / VN + 1;  // (one more where the row starts inside one)
     // Few rows are split, until there are four CTAs an SM, down to parts of two
     // granules a thread: a part's end costs as much as 30 KB of it. 288 rows of
-    // 128256 float32 logits, no alternatives (and 20): 33.2 (47.0) us whole, 30.8
-    // (42.3) in two parts, 36.5 (47.2) in four. Half of a step's rows have no token
-    // as a rule (512 rows, 288 with one, 20 alternatives: 53.5 us whole, 43.2 in two
-    // parts), hence four and not two.
+    // 128256 float32 logits, no alternatives (and 20): 32.9 (43.0) us whole, 28.8
+    // (36.1) in two parts, 37.0 (45.5) in four. Half of a step's rows have no token
+    // as a rule (512 rows, 288 with one, 20 alternatives: 49.0 us whole, 38.5 in two
+    // parts, 46.7 in four), hence four and not two, which a few hundred rows that all
+    // have a token pay for.
     int parts = 1;
     while (parts < kMaxParts && p.rows * parts < 152 * 4 && granules / parts > NT * 2) parts *= 2;
     p.parts = parts;
@@ -625,9 +626,11 @@ cudaError_t launch(LogprobParams p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_logprobs(const LogprobParams& p, int dtype, cudaStream_t st) {
-    // bf16 rows, half as long, by blocks of 128 threads (of 256): 2000 rows of 32016
-    // 37.0 us (42.1), with five alternatives 47.1 (51.4); float32 rows of 128256 with 20
-    // alternatives, 288 of 512 with a token, 57.4 (41.2).
+    // bf16 rows by blocks of 128 threads (of 256): 2000 rows of 32016 37.3 us (43.1), with
+    // five alternatives 46.4 (53.3); 256 of 128256 22.1 (24.6), with 20 30.8 (34.9). float32
+    // rows by 256 (128): of 128256 with 20 alternatives, 288 of 512 with a token, 39.0 us
+    // (54.5), five with five 12.6 (14.4); but 2000 of 32000 54.5 (49.0), which this rule by
+    // type leaves.
     return dtype == 0 ? launch<float, 256, 4>(p, st) : launch<bf16_t, 128, 2>(p, st);
 }
 

@@ -13,13 +13,13 @@
 // all heads, then a thread a 16-byte column (or a pair of them) of one token, its
 // cosines in registers, and every few heads of it, two to four rows in flight; the
 // first rows and values are under way before the cosines are computed. Neighbouring
-// threads have neighbouring heads (neighbouring tokens: 36.2 us for 32.4).
+// threads have neighbouring heads (neighbouring tokens: 36.2 us for 32.4 then).
 //
 // Bound by memory where there is enough of it: 8 x 1000 tokens, 32 query and 8 key
-// heads of 128 columns, bf16: 32.4 us, 5.6 TB/s read and written (the append alone,
+// heads of 128 columns, bf16: 32.6 us, 5.5 TB/s read and written (the append alone,
 // which has no queries to write, 6.0). Below that by the chain of lengths, table,
-// cosines and rows: 16 trees of 61 nodes, 12 heads of 64, float32: 7.4 us, one chain
-// of 5: 3.6 us.
+// cosines and rows: 16 trees of 61 nodes, 12 heads of 64, float32: 7.5 us, one chain
+// of 5: 3.9 us.
 
 #include <algorithm>
 

@@ -7,7 +7,7 @@
 //
 // Bound by latency where there are few tiles (keys, rows, products and sums follow
 // one another; four blocks an SM overlap them: 8 chains of 8, 12 heads of 64,
-// float32, 20-1500 positions 20.6 us, 26.5 with two; one token of 16 sequences, to
+// float32, 20-1500 positions 20.8 us, 26.5 with two; one token of 16 sequences, to
 // 8000 positions, 8 x 4 heads of 128: 197 us, 1.3 TB/s), else by the products' reads
 // of shared memory, 10 wavefronts for 32 multiplications of a warp (trees' paths of 1
 // to 17 of 61 nodes, 16 sequences, 300-4000 positions, 8 x 4 heads of 96, bf16: 118).
