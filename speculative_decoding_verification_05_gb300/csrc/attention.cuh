@@ -262,9 +262,8 @@ SV_DEV void attn_edges(const AttnParams& p, int gw, int warps) {
             bad = __any_sync(0xFFFFFFFFu, bad) != 0;
             if (!RAISE || !p.whole) {
                 if (lane == 0) p.status[b] = bad ? kEData : kOk;
-            } else if (bad) {
-                asm volatile("griddepcontrol.wait;" ::: "memory");
-                if (lane == 0) atomicMax(p.status + b, kEData);
+            } else if (bad && lane == 0) {
+                atomicMax(p.status + b, kEData);
             }
         }
         const int Hq = p.Hkv * p.G, n = max(s.n, 0);

@@ -808,6 +808,8 @@ __global__ void __launch_bounds__(NT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     asm volatile("griddepcontrol.launch_dependents;");
+    // (whole units: nothing is read before the kernel that clears the statuses is done)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const AttnCut cut = attn_locate<kKv, NT>(p, &c->scan);
     Walk walk(c->scan, cut);
 
@@ -867,7 +869,6 @@ __global__ void __launch_bounds__(NT, 1)
         if (warp == 9 || warp == 10) {
             Issuer<D> is{c, uni(warp - 9), uni(tmem), qs, stages};
             is.run();
-            if (p.whole) asm volatile("griddepcontrol.wait;" ::: "memory");  // (the statuses are cleared; the block's end follows)
         }
         if (warp == 11) help<D>(p, c, &mq, qs, stages, walk);
     }
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(NT, 1)
 
 // Clears the statuses that the attention of whole units, which starts beside it, raises
 // (8 chains of 5, contexts of 120, one head: 9.8 us, 9.3 with statuses stored among the
-// grid; of 200, 8 heads: 12.6 and 11.4; 40 tokens at 500, 2 heads: 16.7 and 15.7. Shared
+// grid; of 200, 8 heads: 12.4 and 11.5; 40 tokens at 500, 2 heads: 16.7 and 15.9. Shared
 // units' statuses cost nothing: the join raises them).
 __global__ void __launch_bounds__(256) attn_clear_kernel(int32_t* status, int B) {
     asm volatile("griddepcontrol.launch_dependents;");

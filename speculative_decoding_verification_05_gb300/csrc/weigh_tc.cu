@@ -17,13 +17,13 @@
 // two tiles, from L2.
 //
 // What bounds it. Few rows: memory (one token of 64 sequences, contexts to 8192, 8
-// key heads of 4 query heads: 102 us, 5.4 TB/s of keys and weights; 100 with five
+// key heads of 4 query heads: 103 us, 5.4 TB/s of keys and weights; 100 with five
 // stages and two chunks). Accepted paths of 1 to 7 nodes, 16 sequences, 300-4000
-// positions, 8 x 8 heads: 23.4 us, of which the keys at that rate would take 13; the
+// positions, 8 x 8 heads: 23.7 us, of which the keys at that rate would take 13; the
 // rest are the first lookups of a launch and of each stay. Many rows: the latency
 // of a chunk's way (wait, tensor memory, exponentials, release; tensor pipe and
 // exponential unit are a quarter busy, the schedulers a third): a chunk of 500 nodes
-// at 4000 positions, 8 x 4 heads 33.2 us, 0.52 PFLOP/s (0.8 more with two chunks of rows
+// at 4000 positions, 8 x 4 heads 33.4 us, 0.52 PFLOP/s (0.8 more with two chunks of rows
 // in shared memory; 44.9 with the chunks brought by 16-byte copies, whose addresses
 // took two warps longer than the products; 0.7 more with scalar in the place of packed
 // arithmetic; the second 32 columns fetched beside the first ones' sums or after them, the same).
@@ -451,10 +451,10 @@ struct Group {
 
 // Clears the statuses, which the weighing's CTAs only raise: a plain store of a good one by a
 // CTA that began late, behind another stream's work, would take back what one that gave up
-// reported. The weighing starts beside it and waits for it before it raises any. (Paths of
-// 16 sequences: 23.4 us, 22.6 with the plain stores, 26.6 with a memset. With the checks in
-// this kernel too, 23.5, but one token over 100003 positions in pages of 8 63.6 for 60.7, as
-// its blocks keep the weighing's from their SMs, and of 4000 sequences 668 for 580.)
+// reported. The weighing's blocks are launched beside it. (Paths of 16 sequences: 23.7 us,
+// 22.6 with the plain stores, 26.6 with a memset. With the checks in this kernel too, one
+// token over 100003 positions in pages of 8 took 63.6 for 61.0, as its blocks keep the
+// weighing's from their SMs, and of 4000 sequences 668 for 595.)
 __global__ void __launch_bounds__(256) weigh_clear_kernel(int32_t* status, int B) {
     asm volatile("griddepcontrol.launch_dependents;");
     const int b = blockIdx.x * 256 + threadIdx.x;
@@ -471,6 +471,9 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t qs = smem_u32(mem) + 2048, stages = qs + kChunks * Shape<D>::kTile;
     const int tid = threadIdx.x, warp = tid >> 5;
 
+    // (nothing is read before the kernel that clears the statuses is done: what another thread
+    // has put on the stream between the two is done then too)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const WeighPart part = weigh_locate<kKv, kRows, NT>(p, &c->scan);
     if (tid == 0) {
         for (int i = 0; i < Shape<D>::kStages; ++i) {
@@ -510,10 +513,7 @@ __global__ void __launch_bounds__(NT, 1)
     } else {
         Loader<D> l{p, c, &mq, qs, warp - 10};
         l.run(way);
-        if (warp == 11) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // (the statuses are cleared; the block's end follows)
-            weigh_statuses<true>(p, blockIdx.x, gridDim.x);
-        }
+        if (warp == 11) weigh_statuses<true>(p, blockIdx.x, gridDim.x);
     }
     __syncwarp();
     tc_fence_before();
