@@ -625,7 +625,7 @@ spec_status spec_cache_weigh(const void* q, const float* lse, const spec_cache* 
  *                 budget - 1 of a sequence to be shortened whose count is not 1
  *                 (nothing moves); NULL allowed
  *   workspace     >= spec_cache_evict_workspace_size(layers, B, kv_heads,
- *                 capacity) bytes
+ *                 capacity) bytes (about a word for each weight)
  * layers x B x kv_heads < 2^30.
  * ---------------------------------------------------------------------- */
 size_t spec_cache_evict_workspace_size(int layers, int B, int kv_heads, int64_t capacity);
